@@ -88,6 +88,10 @@ typedef enum vce_dtype {
  * 16-byte aligned; that access was skipped instead of made. */
 #define VCE_DEVSTATUS_BOUNDS 4
 
+/* Formats of microscaled tensors: one power-of-two scale per 32 columns. */
+#define VCE_MX_E4M3 0 /* 8-bit values, at most 448 */
+#define VCE_MX_E2M1 1 /* 4-bit values: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives */
+
 /* reduce_loss values */
 #define VCE_REDUCE_NONE 0 /* per-row loss */
 #define VCE_REDUCE_MEAN 1 /* sum over rows / N_v (the API card's reduce_loss=True) */
@@ -329,6 +333,104 @@ vce_status lce_backward(const void* X, const void* W, int64_t n, int64_t h, int6
  */
 vce_status shift_targets(const int64_t* target, int64_t n, int64_t seq_len, int64_t ignore_idx,
                          int64_t* shifted, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* the norm before the classifier                                           */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * Root-mean-square norm of hidden states with the residual's addition:
+ *     h = round(x + residual)   (h = x when residual is NULL)
+ *     r = 1 / sqrt(mean_i h_i^2 + eps),  y_i = h_i r w_i
+ * The sum is rounded to the tensors' type before the norm is taken, so that the
+ * norm, the residual stream the caller keeps and the backward pass all see the
+ * same numbers.  Arithmetic and sums are FP32.
+ *
+ *   x         [n, hidden], dtype BF16 or F32, rows x_stride elements apart (>= hidden).
+ *   residual  NULL or [n, hidden] of the same type, rows residual_stride apart.
+ *   weight    [hidden], weight_dtype BF16 or F32.
+ *   eps       >= 0.  A row of zeros with eps 0 gives NaN (0 times infinity).
+ *   h         [n, hidden], rows h_stride apart; written (and required) when residual is
+ *             given, ignored otherwise.  May equal x or residual (same stride).
+ *   y         [n, hidden], rows y_stride apart, of x's type.  May equal x, or residual when
+ *             h does not (same stride); any other overlap of the operands is undefined.
+ *   rstd      F32 [n]: r of every row, or NULL.
+ *
+ * All pointers and strides need only element alignment; rows whose pointers,
+ * strides and length allow 16-byte accesses are read by them.
+ */
+vce_status rms_norm_forward(const void* x, int dtype, int64_t n, int64_t hidden, int64_t x_stride,
+                            const void* residual, int64_t residual_stride, const void* weight,
+                            int weight_dtype, float eps, void* h, int64_t h_stride, void* y,
+                            int64_t y_stride, float* rstd, int* dev_status, void* stream);
+
+/*
+ * The same norm with y as a microscaled E4M3 tensor (see mx_quantize for the layout
+ * and the rule of the scales), quantised from the FP32 values without a rounding to
+ * x's type in between: the input of mx_linear.
+ *   codes, scales  mx_codes_size / mx_scales_size bytes, 16-byte aligned; fully written.
+ */
+vce_status rms_norm_mx(const void* x, int dtype, int64_t n, int64_t hidden, int64_t x_stride,
+                       const void* residual, int64_t residual_stride, const void* weight,
+                       int weight_dtype, float eps, void* h, int64_t h_stride, void* codes,
+                       void* scales, float* rstd, int* dev_status, void* stream);
+
+/* Bytes of workspace rms_norm_backward needs (FP32 partial sums of the weight's
+ * gradient: at most four rows of ``hidden`` per SM), on the current device. */
+size_t rms_norm_workspace_size(int64_t n, int64_t hidden);
+
+/*
+ * Backward of the norm, with g_i = w_i dy_i:
+ *     dx_i = r (g_i - h_i r^2 mean_j (g_j h_j)) + dh_i
+ *     dweight_i = sum over rows of dy_i h_i r
+ * dx is the gradient of x and of the residual alike.  The sums run in a fixed order
+ * (no atomics): equal inputs on equal devices give equal bits.
+ *
+ *   dy        [n, hidden] of ``dtype``, rows dy_stride apart.
+ *   h, rstd   from the forward call (h = x where there was no residual).
+ *   dh        NULL, or the gradient that reaches h by the residual stream.
+ *   dx        [n, hidden] of ``dtype``; may equal dy or dh (same stride), not h.
+ *   dweight   [hidden] of weight_dtype; all zeros for n = 0.
+ *   ws        rms_norm_workspace_size bytes, 256-byte aligned (may be NULL for n = 0).
+ */
+vce_status rms_norm_backward(const void* dy, int dtype, int64_t n, int64_t hidden, int64_t dy_stride,
+                             const void* h, int64_t h_stride, const void* weight, int weight_dtype,
+                             const float* rstd, const void* dh, int64_t dh_stride, void* dx,
+                             int64_t dx_stride, void* dweight, void* ws, size_t ws_bytes,
+                             int* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* microscaled tensors                                                      */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * A microscaled tensor [rows, cols] is a buffer of codes and a buffer of scales.
+ *   codes   rows of padded columns (cols rounded up to 128, the rest 0).  E4M3: one
+ *           byte a value.  E2M1: two values a byte, the even column in the low
+ *           four bits (sign, two exponent bits, one mantissa bit).
+ *   scales  E8M0 bytes (2^(byte - 127); 255 is NaN), one per row and 32 columns, in
+ *           tiles of 128 rows x 4 blocks: the scale of (row, block) is byte
+ *           ((row / 128) * (padded / 128) + block / 4) * 512
+ *             + (row % 32) * 16 + (row % 128) / 32 * 4 + block % 4.
+ *           Rows and blocks past the tensor are 0.
+ */
+size_t mx_codes_size(int64_t rows, int64_t cols, int fmt);
+size_t mx_scales_size(int64_t rows, int64_t cols);
+
+/*
+ * Quantise x [rows, cols] (BF16 or F32, rows ``row_stride`` elements apart).  A block's
+ * scale is the least power of two (at least 2^-127) under which none of its values
+ * saturates; values are rounded to nearest, ties to even.  A block that holds an
+ * infinity or a NaN gets the scale NaN and codes 0.  codes and scales must be
+ * 16-byte aligned; both are fully written.
+ */
+vce_status mx_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int64_t row_stride, int fmt,
+                       void* codes, void* scales, int* dev_status, void* stream);
+
+/* The values a microscaled tensor stands for, as BF16 or F32 [rows, cols] (exact, but for
+ * BF16 values below 2^-126, which are rounded). */
+vce_status mx_dequantize(const void* codes, const void* scales, int fmt, int64_t rows, int64_t cols,
+                         void* out, int dtype, int64_t row_stride, int* dev_status, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* diagnostics                                                              */

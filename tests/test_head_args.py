@@ -1,0 +1,140 @@
+"""Refusals of the operators around the cross entropy, and their FP64 definitions pinned to
+torch, without a GPU: a wrong argument is an error before any launch."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import vocabulary_cross_entropy_gb300 as vce
+from oracle import head
+
+OK, INVALID, DTYPE, ALIGN, WORKSPACE, ARCH, CUDA = range(7)
+FAKE = 0x10000  # never dereferenced: host validation fails first
+P, I64, I, F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from vocabulary_cross_entropy_gb300 import build
+    build.build()
+
+
+def _norm(x=FAKE, dtype=0, n=4, h=64, xs=64, res=None, rs=64, w=FAKE, wd=0, eps=1e-6, hp=None, hs=64, y=FAKE,
+          ys=64, rstd=FAKE):
+    return vce.library().rms_norm_forward(x, dtype, n, h, xs, res, rs, w, wd, eps, hp, hs, y, ys, rstd, None, None)
+
+
+def test_norm_forward_refusals():
+    assert _norm(dtype=2) == DTYPE and _norm(wd=9) == DTYPE
+    for bad in (dict(n=-1), dict(h=0), dict(xs=63), dict(eps=-1.0), dict(eps=float("nan")), dict(x=None),
+                dict(w=None), dict(y=None), dict(ys=63), dict(res=FAKE, hp=None), dict(res=FAKE, hp=FAKE, rs=3),
+                dict(res=FAKE, hp=FAKE, hs=3), dict(n=1 << 40), dict(h=1 << 40, xs=1 << 40, ys=1 << 40)):
+        assert _norm(**bad) == INVALID, bad
+    for bad in (dict(x=FAKE + 1), dict(y=FAKE + 1), dict(w=FAKE + 1), dict(rstd=FAKE + 2), dict(wd=1, w=FAKE + 2)):
+        assert _norm(**bad) == ALIGN, bad
+
+
+def test_norm_mx_refusals():
+    f = vce.library().rms_norm_mx
+
+    def call(codes=FAKE, scales=FAKE, dtype=0):
+        return f(FAKE, dtype, 4, 64, 64, None, 0, FAKE, 0, 1e-6, None, 0, codes, scales, None, None, None)
+
+    assert call(dtype=5) == DTYPE
+    assert call(codes=None) == INVALID and call(scales=None) == INVALID
+    assert call(codes=FAKE + 8) == ALIGN and call(scales=FAKE + 4) == ALIGN
+
+
+def test_norm_backward_refusals():
+    f = vce.library().rms_norm_backward
+
+    def call(dy=FAKE, dtype=0, n=4, h=64, gs=64, hp=FAKE + 256, hs=64, w=FAKE, wd=0, rstd=FAKE, dh=None, ds=64,
+             dx=FAKE, xs=64, dw=FAKE, ws=FAKE, size=1 << 30):
+        return f(dy, dtype, n, h, gs, hp, hs, w, wd, rstd, dh, ds, dx, xs, dw, ws, size, None, None)
+
+    assert call(dtype=3) == DTYPE and call(wd=3) == DTYPE
+    for bad in (dict(n=-1), dict(h=0), dict(gs=1), dict(hs=1), dict(xs=1), dict(dh=FAKE, ds=1), dict(dy=None),
+                dict(hp=None), dict(w=None), dict(rstd=None), dict(dx=None), dict(dw=None), dict(dx=FAKE + 256)):
+        assert call(**bad) == INVALID, bad
+    assert call(dy=FAKE + 1) == ALIGN and call(ws=FAKE + 128) == ALIGN
+    assert call(ws=None) == WORKSPACE
+
+
+def test_mx_refusals():
+    lib = vce.library()
+
+    def q(x=FAKE, dtype=0, n=4, c=64, s=64, fmt=0, codes=FAKE, scales=FAKE, fn=lib.mx_quantize):
+        if fn is lib.mx_quantize:
+            return fn(x, dtype, n, c, s, fmt, codes, scales, None, None)
+        return fn(codes, scales, fmt, n, c, x, dtype, s, None, None)
+
+    for fn in (lib.mx_quantize, lib.mx_dequantize):
+        assert q(dtype=2, fn=fn) == DTYPE and q(fmt=2, fn=fn) == DTYPE
+        for bad in (dict(n=-1), dict(c=0), dict(s=63), dict(x=None), dict(codes=None), dict(scales=None)):
+            assert q(**bad, fn=fn) == INVALID, bad
+        for bad in (dict(x=FAKE + 1), dict(codes=FAKE + 8), dict(scales=FAKE + 8)):
+            assert q(**bad, fn=fn) == ALIGN, bad
+    assert vce.mx_codes_size(3, 129, "e4m3") == 3 * 256 and vce.mx_codes_size(3, 129, "e2m1") == 3 * 128
+    assert vce.mx_scales_size(129, 129) == 256 * 8 and vce.mx_scales_size(0, 5) == 0
+
+
+def test_python_refusals():
+    x, w = torch.zeros(4, 64), torch.ones(64)
+    with pytest.raises(ValueError, match="CUDA"):
+        vce.rms_norm_forward(x, w)
+    with pytest.raises(ValueError, match="CUDA"):
+        vce.mx_quantize(x)
+    with pytest.raises(TypeError):
+        vce.rms_norm_forward(x.half(), w)
+    with pytest.raises(TypeError):
+        vce.rms_norm_forward(x, w.half())
+    with pytest.raises(ValueError):
+        vce.rms_norm_forward(x, w[:63])
+    with pytest.raises(ValueError):
+        vce.rms_norm_forward(x.t(), w)
+    with pytest.raises(ValueError):
+        vce.rms_norm_forward(x, w, residual=x[:1])          # no broadcasting
+    with pytest.raises(TypeError):
+        vce.rms_norm_forward(x, w, residual=x.bfloat16())
+    with pytest.raises(ValueError):
+        vce.rms_norm_forward(x, w, y=torch.zeros(1, 64).expand(4, 64))
+    with pytest.raises(ValueError):
+        vce.rms_norm_forward(x, w, h=x)                     # h without a residual
+    with pytest.raises(ValueError):
+        vce.rms_norm(x, w, residual=x[:1])
+    with pytest.raises(ValueError):
+        vce.linear_cross_entropy(x.bfloat16(), x.bfloat16(), torch.zeros(4, dtype=torch.int64), residual=x)
+    with pytest.raises(ValueError):
+        vce.mx_quantize(x, "e5m2")
+    with pytest.raises(ValueError):
+        vce.rms_norm_backward(x, x, w, torch.zeros(3))
+    bad = vce.MXTensor(torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8), 4, 64, "e4m3")
+    with pytest.raises(ValueError, match="codes"):          # codes are padded to 128 columns
+        vce.mx_dequantize(bad)
+
+
+def test_formats_against_torch():
+    vals = head.mx_values("e4m3")
+    all8 = torch.arange(127, dtype=torch.uint8).view(torch.float8_e4m3fn).double().numpy()
+    assert np.array_equal(vals, all8)
+    assert np.array_equal(head.mx_values("e2m1"), [0, 0.5, 1, 1.5, 2, 3, 4, 6])
+    x = torch.randn(1, 32 * 500, generator=torch.Generator().manual_seed(0)).double()
+    codes, e = head.mx_quantize(x.numpy(), "e4m3")
+    scaled = x.view(1, -1, 32) * 2.0 ** -torch.from_numpy(e).double()[:, :, None]
+    assert scaled.abs().max() <= 448
+    want = scaled.float().to(torch.float8_e4m3fn).view(torch.uint8).numpy().reshape(1, -1)
+    assert np.array_equal(codes, want)
+    assert np.all(np.abs(head.mx_dequantize(codes, e, "e4m3") - x.numpy()) <= 2.0 ** -4 * np.abs(x.numpy()) + 1e-3)
+
+
+def test_norm_definition_against_torch():
+    h = torch.randn(5, 48, dtype=torch.float64, generator=torch.Generator().manual_seed(1), requires_grad=True)
+    w = torch.randn(48, dtype=torch.float64, generator=torch.Generator().manual_seed(2), requires_grad=True)
+    y = torch.nn.functional.rms_norm(h, (48,), w, 1e-5)
+    dy = torch.randn(5, 48, dtype=torch.float64, generator=torch.Generator().manual_seed(3))
+    y.backward(dy)
+    got, r = head.rms_norm(h.detach().numpy(), w.detach().numpy(), 1e-5)
+    dx, dw = head.rms_norm_backward(dy.numpy(), h.detach().numpy(), w.detach().numpy(), r)
+    assert np.allclose(got, y.detach().numpy(), rtol=1e-12) and np.allclose(dx, h.grad.numpy(), rtol=1e-10)
+    assert np.allclose(dw, w.grad.numpy(), rtol=1e-10)

@@ -38,4 +38,17 @@ from ._binding import (  # noqa: F401
     selftest_lce_forward_timeout,
     selftest_ce_fused_timeout,
 )
-from .autograd import parallel_cross_entropy, linear_cross_entropy  # noqa: F401,E402
+from ._head import (  # noqa: F401,E402
+    MX_E4M3,
+    MX_E2M1,
+    MXTensor,
+    mx_codes_size,
+    mx_scales_size,
+    mx_quantize,
+    mx_dequantize,
+    rms_norm_forward,
+    rms_norm_mx,
+    rms_norm_workspace_size,
+    rms_norm_backward,
+)
+from .autograd import parallel_cross_entropy, linear_cross_entropy, rms_norm  # noqa: F401,E402

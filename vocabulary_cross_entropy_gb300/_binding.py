@@ -79,6 +79,25 @@ def library() -> ctypes.CDLL:
     lib.lce_backward.argtypes = [_c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_f32,
                                  _c_int, _c_i64, _c_p, _c_p, _c_p, _c_size, _c_p, _c_p]
     lib.lce_backward.restype = _c_int
+    lib.rms_norm_forward.argtypes = [_c_p, _c_int, _c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_p, _c_int, _c_f32,
+                                     _c_p, _c_i64, _c_p, _c_i64, _c_p, _c_p, _c_p]
+    lib.rms_norm_forward.restype = _c_int
+    lib.rms_norm_mx.argtypes = [_c_p, _c_int, _c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_p, _c_int, _c_f32,
+                                _c_p, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_p]
+    lib.rms_norm_mx.restype = _c_int
+    lib.rms_norm_workspace_size.argtypes = [_c_i64, _c_i64]
+    lib.rms_norm_workspace_size.restype = _c_size
+    lib.rms_norm_backward.argtypes = [_c_p, _c_int, _c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_p, _c_int, _c_p,
+                                      _c_p, _c_i64, _c_p, _c_i64, _c_p, _c_p, _c_size, _c_p, _c_p]
+    lib.rms_norm_backward.restype = _c_int
+    lib.mx_codes_size.argtypes = [_c_i64, _c_i64, _c_int]
+    lib.mx_codes_size.restype = _c_size
+    lib.mx_scales_size.argtypes = [_c_i64, _c_i64]
+    lib.mx_scales_size.restype = _c_size
+    lib.mx_quantize.argtypes = [_c_p, _c_int, _c_i64, _c_i64, _c_i64, _c_int, _c_p, _c_p, _c_p, _c_p]
+    lib.mx_quantize.restype = _c_int
+    lib.mx_dequantize.argtypes = [_c_p, _c_p, _c_int, _c_i64, _c_i64, _c_p, _c_int, _c_i64, _c_p, _c_p]
+    lib.mx_dequantize.restype = _c_int
     lib.vce_selftest_wait_timeout.argtypes = [ctypes.c_uint64, _c_p, _c_p, _c_p]
     lib.vce_selftest_wait_timeout.restype = _c_int
     lib.vce_selftest_lce_forward_timeout.argtypes = [_c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_p, ctypes.c_uint64,

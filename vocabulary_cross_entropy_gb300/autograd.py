@@ -9,13 +9,17 @@ parallel_cross_entropy  the logits form, with the call shape of Transformer
 linear_cross_entropy    the linear form, loss from embeddings [..., H] and the
                         classifier [V, H] (Cut Cross-Entropy card
                         "what_it_does"), with optional token shifting and
-                        per-token entropy.
+                        per-token entropy, and optionally the norm before
+                        the classifier.
+rms_norm                that norm with the residual's addition, by itself.
 """
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _binding as b
+from . import _head
 
 
 def _grad_tensor(grad, reduce_code, n, device):
@@ -80,15 +84,67 @@ class _LinearCE(torch.autograd.Function):
         return r.dX, r.dW, None, None, None, None, None
 
 
+def _rows(t):
+    """``t`` [..., H] as [rows, H] with contiguous rows that do not overlap (a gradient may be
+    expanded, an input transposed)."""
+    flat = t.reshape(-1, t.shape[-1])
+    return flat if flat.stride(-1) == 1 and flat.stride(0) >= flat.shape[1] else flat.contiguous()
+
+
+class _RMSNorm(torch.autograd.Function):
+    # takes and gives back x's own shape: the gradient of x and of the residual is then one
+    # tensor with two owners, which autograd copies before it makes it a leaf's .grad (views
+    # made outside would each look like the only owner)
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps):
+        f = _head.rms_norm_forward(_rows(x), weight, eps, None if residual is None else _rows(residual))
+        ctx.save_for_backward(f.h, weight, f.rstd)
+        ctx.set_materialize_grads(False)
+        ctx.with_residual = residual is not None
+        y = f.y.view(x.shape)
+        return (y, f.h.view(x.shape)) if residual is not None else y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh=None):
+        h, weight, rstd = ctx.saved_tensors
+        if dy is None:  # only the residual stream was used, or nothing
+            dx, dweight = dh, None
+        else:
+            dx, dweight = _head.rms_norm_backward(_rows(dy), h, weight, rstd, None if dh is None else _rows(dh))
+            dx = dx.view(dy.shape)
+        return dx, dweight, dx if ctx.with_residual else None, None
+
+
+def rms_norm(x, weight, eps: float = 1e-6, residual=None):
+    """Root-mean-square norm of ``x`` [..., H] (plus ``residual``, of the same shape) over its
+    last dimension, times ``weight`` [H].
+
+    Returns y, or (y, x + residual) when a residual is given; both take part in the backward
+    pass.  x and residual are BF16 or FP32, weight either.
+    """
+    if residual is not None and residual.shape != x.shape:
+        raise ValueError("residual must have the shape of x")
+    return _RMSNorm.apply(x, weight, residual, float(eps))
+
+
 def linear_cross_entropy(embeddings, classifier, labels, ignore_index: int = -100, reduction: str = "mean",
-                         label_smoothing: float = 0.0, shift: bool = False, return_entropy: bool = False):
+                         label_smoothing: float = 0.0, shift: bool = False, return_entropy: bool = False,
+                         norm_weight=None, norm_eps: float = 1e-6, residual=None):
     """Cross entropy of ``embeddings @ classifier.T`` against ``labels`` without the logits.
 
     embeddings [..., H] and classifier [V, H] are BF16; labels [...] int64.  ``reduction``
     is 'mean' (over non-ignored tokens), 'sum' or 'none'.  ``shift`` scores position t
     of each sequence (the last dimension of ``labels``) against label t + 1.  With
-    ``return_entropy`` the per-token entropy of the softmax is returned as well.
+    ``return_entropy`` the per-token entropy of the softmax is returned as well.  With
+    ``norm_weight`` [H] the classifier takes rms_norm(embeddings, norm_weight, norm_eps,
+    residual): the last norm of a model, whose gradients are part of the backward pass.
     """
+    if norm_weight is not None:
+        out = rms_norm(embeddings, norm_weight, norm_eps, residual)
+        embeddings = out if residual is None else out[0]
+    elif residual is not None:
+        raise ValueError("residual is added by the norm: it needs norm_weight")
     lead = embeddings.shape[:-1]
     h = embeddings.shape[-1]
     x = embeddings.reshape(-1, h)

@@ -1,0 +1,548 @@
+// Root-mean-square norm of hidden states with the residual's addition, its 8-bit
+// microscaled form, and its backward pass.
+//
+//   h = round(x + residual)      (h = x without a residual)
+//   r = 1 / sqrt(mean_i h_i^2 + eps)
+//   y_i = h_i r w_i
+//
+//   g_i = w_i dy_i,  c = r^2 mean_i (g_i h_i)
+//   dx_i = r (g_i - h_i c) + dh_i  (the gradient of x and of the residual)
+//   dw_i = sum over rows of dy_i h_i r
+//
+// The norm is taken of the rounded sum, the value the caller keeps as the residual
+// stream, so that the backward pass differentiates the very numbers the forward
+// pass used.  All arithmetic and every sum is FP32; the one rounding to fewer bits
+// besides h is the store of y (dx, dw).
+//
+// All three are bound by memory: a row is read once into registers, reduced over
+// its threads and written from registers.
+
+#include "vce_internal.cuh"
+#include "mx_format.cuh"
+
+#include <math.h>
+
+namespace vce {
+namespace {
+
+constexpr int kMaxThreads = 512;
+
+template <typename T, int VE>
+struct alignas(sizeof(T) * VE) Vec {
+    T e[VE];
+};
+
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f(float v);
+template <>
+__device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+template <int VE>
+__device__ __forceinline__ void load_weight(const void* w, int w_f32, int64_t at, float (&out)[VE]) {
+    if (w_f32) {
+        if constexpr (VE == 8) {  // two 16-byte loads
+            const Vec<float, 4> a = *reinterpret_cast<const Vec<float, 4>*>(static_cast<const float*>(w) + at);
+            const Vec<float, 4> b = *reinterpret_cast<const Vec<float, 4>*>(static_cast<const float*>(w) + at + 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) out[i] = a.e[i], out[i + 4] = b.e[i];
+        } else {
+            const Vec<float, VE> a = *reinterpret_cast<const Vec<float, VE>*>(static_cast<const float*>(w) + at);
+#pragma unroll
+            for (int i = 0; i < VE; ++i) out[i] = a.e[i];
+        }
+    } else {
+        const Vec<__nv_bfloat16, VE> a =
+            *reinterpret_cast<const Vec<__nv_bfloat16, VE>*>(static_cast<const __nv_bfloat16*>(w) + at);
+#pragma unroll
+        for (int i = 0; i < VE; ++i) out[i] = to_f(a.e[i]);
+    }
+}
+
+// Sum over the ``tpr`` threads of a row (a warp, or the whole block); every thread
+// gets it.  ``slot`` holds one float per warp and is not reused before the next barrier.
+__device__ __forceinline__ float row_sum(float v, int tpr, float* slot) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (tpr == 32) return v;
+    if ((threadIdx.x & 31) == 0) slot[threadIdx.x >> 5] = v;
+    __syncthreads();
+    const int warps = tpr >> 5;
+    v = (threadIdx.x & 31) < warps ? slot[threadIdx.x & 31] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+struct NormArgs {
+    const void *x, *residual, *weight;
+    int w_f32;
+    int64_t n, hidden, x_stride, r_stride, h_stride, y_stride;
+    float eps;
+    void *h, *y;
+    float* rstd;
+    uint8_t *codes, *scales;  // 8-bit form: [n, padded], scale tiles
+    int64_t padded, rows_padded;
+    int tpr;  // threads per row: 32, or the block
+    int* dev_status;
+};
+
+// The 8-bit form's stores of VE consecutive values at column ``col`` (a multiple of
+// VE).  The 32 / VE lanes that hold one block find its largest magnitude together;
+// every lane of the warp calls.
+template <int VE>
+__device__ __forceinline__ void store_mx(const NormArgs& a, int64_t row, int64_t col, const float (&y)[VE]) {
+    constexpr int kLanes = mx::kBlock / VE;
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < VE; ++i) m = max(m, __float_as_uint(y[i]) & 0x7fffffffu);
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const uint32_t sb = mx::scale_byte<VCE_MX_E4M3>(m);
+    // without a branch on the NaN code: inverse_scale of it is not used
+    const float inv = sb == mx::kNanScale ? 0.f : mx::inverse_scale(sb);
+    if (col >= a.padded) return;
+    const bool bad = sb == mx::kNanScale;
+    uint8_t* dst = a.codes + row * a.padded + col;
+    if (!VCE_BOUNDS(row >= 0 && row < a.n && col >= 0 && col + VE <= a.padded, a.dev_status)) return;
+    if constexpr (VE == 1) {
+        *dst = bad ? 0 : uint8_t(mx::e4m3x2(y[0] * inv, 0.f) & 0xff);
+    } else {
+        uint16_t c[VE / 2];
+#pragma unroll
+        for (int i = 0; i < VE / 2; ++i) c[i] = bad ? 0 : uint16_t(mx::e4m3x2(y[2 * i] * inv, y[2 * i + 1] * inv));
+        if constexpr (VE == 8)
+            *reinterpret_cast<uint2*>(dst) = make_uint2(c[0] | uint32_t(c[1]) << 16, c[2] | uint32_t(c[3]) << 16);
+        else if constexpr (VE == 4)
+            *reinterpret_cast<uint32_t*>(dst) = c[0] | uint32_t(c[1]) << 16;
+        else
+            *reinterpret_cast<uint16_t*>(dst) = c[0];
+    }
+    if (col % mx::kBlock == 0)
+        a.scales[mx::scale_offset(row, col / mx::kBlock, a.padded / mx::kColTile)] = uint8_t(sb);
+}
+
+// Scales of the rows past the last one in the last tile.
+__device__ __forceinline__ void zero_scale_row(const NormArgs& a, int64_t row, int t, int tpr) {
+    for (int64_t b = t; b < a.padded / mx::kBlock; b += tpr)
+        a.scales[mx::scale_offset(row, b, a.padded / mx::kColTile)] = 0;
+}
+
+// One row per ``tpr`` threads, NV vectors of VE elements per thread in registers.
+template <typename T, int VE, int NV, bool kMx>
+__global__ void __launch_bounds__(kMaxThreads) rms_norm_rows(const NormArgs a) {
+    __shared__ float slot[32];
+    const int tpr = a.tpr;
+    const int t = threadIdx.x % tpr;
+    const int64_t row = int64_t(blockIdx.x) * (blockDim.x / tpr) + threadIdx.x / tpr;
+    if (kMx && row >= a.n) {  // (whole warps: a row's threads are whole warps)
+        if (row < a.rows_padded) zero_scale_row(a, row, t, tpr);
+        return;
+    }
+    if (row >= a.n) return;
+    using V = Vec<T, VE>;
+    const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+    const T* res = a.residual ? static_cast<const T*>(a.residual) + row * a.r_stride : nullptr;
+    T* h = a.residual ? static_cast<T*>(a.h) + row * a.h_stride : nullptr;
+    V v[NV], u[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int64_t col = int64_t(j * tpr + t) * VE;
+        if (col < a.hidden) v[j] = *reinterpret_cast<const V*>(x + col);
+    }
+    if (res) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int64_t col = int64_t(j * tpr + t) * VE;
+            if (col < a.hidden) u[j] = *reinterpret_cast<const V*>(res + col);
+        }
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int64_t col = int64_t(j * tpr + t) * VE;
+        if (col < a.hidden) {
+            if (res) {
+#pragma unroll
+                for (int i = 0; i < VE; ++i) v[j].e[i] = from_f<T>(to_f(v[j].e[i]) + to_f(u[j].e[i]));
+                if (VCE_BOUNDS(col >= 0 && col + VE <= a.hidden && row < a.n, a.dev_status))
+                    *reinterpret_cast<V*>(h + col) = v[j];
+            }
+#pragma unroll
+            for (int i = 0; i < VE; ++i) ss = fmaf(to_f(v[j].e[i]), to_f(v[j].e[i]), ss);
+        }
+    }
+    ss = row_sum(ss, tpr, slot);
+    const float r = 1.f / sqrtf(ss / float(a.hidden) + a.eps);
+    if (t == 0 && a.rstd) a.rstd[row] = r;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int64_t col = int64_t(j * tpr + t) * VE;
+        float y[VE];
+        if (col < a.hidden) {
+            load_weight<VE>(a.weight, a.w_f32, col, y);
+#pragma unroll
+            for (int i = 0; i < VE; ++i) y[i] = to_f(v[j].e[i]) * r * y[i];
+            if (!kMx) {
+                V o;
+#pragma unroll
+                for (int i = 0; i < VE; ++i) o.e[i] = from_f<T>(y[i]);
+                if (VCE_BOUNDS(col >= 0 && col + VE <= a.hidden && row < a.n, a.dev_status))
+                    *reinterpret_cast<V*>(static_cast<T*>(a.y) + row * a.y_stride + col) = o;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VE; ++i) y[i] = 0.f;
+        }
+        if constexpr (kMx) store_mx<VE>(a, row, col, y);
+    }
+}
+
+// Rows longer than the registers hold: two passes over the row, one block per row,
+// one element per thread and step.  Each thread reads back only what it wrote.
+template <typename T, bool kMx>
+__global__ void __launch_bounds__(kMaxThreads) rms_norm_long(const NormArgs a) {
+    __shared__ float slot[32];
+    const int64_t row = blockIdx.x;
+    if (row >= a.n) {
+        if (kMx && row < a.rows_padded) zero_scale_row(a, row, threadIdx.x, blockDim.x);
+        return;
+    }
+    const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+    const T* res = a.residual ? static_cast<const T*>(a.residual) + row * a.r_stride : nullptr;
+    T* h = a.residual ? static_cast<T*>(a.h) + row * a.h_stride : nullptr;
+    float ss = 0.f, comp = 0.f;  // compensated: one thread adds many terms
+    for (int64_t col = threadIdx.x; col < a.hidden; col += blockDim.x) {
+        T v = x[col];
+        if (res) {
+            v = from_f<T>(to_f(v) + to_f(res[col]));
+            h[col] = v;
+        }
+        const float q = fmaf(to_f(v), to_f(v), -comp);
+        const float s = ss + q;
+        comp = (s - ss) - q;
+        ss = s;
+    }
+    ss = row_sum(ss, blockDim.x, slot);
+    const float r = 1.f / sqrtf(ss / float(a.hidden) + a.eps);
+    if (threadIdx.x == 0 && a.rstd) a.rstd[row] = r;
+    const T* src = res ? h : x;
+    const int64_t end = kMx ? a.padded : a.hidden;  // both passes give a thread the same columns
+    for (int64_t c0 = 0; c0 < end; c0 += blockDim.x) {
+        const int64_t col = c0 + threadIdx.x;
+        float y[1] = {0.f}, w[1];
+        if (col < a.hidden) {
+            load_weight<1>(a.weight, a.w_f32, col, w);
+            y[0] = to_f(src[col]) * r * w[0];
+            if (!kMx) static_cast<T*>(a.y)[row * a.y_stride + col] = from_f<T>(y[0]);
+        }
+        if constexpr (kMx) store_mx<1>(a, row, col, y);
+    }
+}
+
+struct NormBwdArgs {
+    const void *dy, *h, *weight, *dh;
+    const float* rstd;
+    int w_f32;
+    int64_t n, hidden, dy_stride, h_stride, dh_stride, dx_stride;
+    void* dx;
+    float* part;  // [parts][hidden] partial sums of dw
+    int parts;
+    int tpr;
+    int* dev_status;
+};
+
+// Rows blockIdx.x, blockIdx.x + gridDim.x, ...: a thread keeps the same columns for
+// all of them and sums their dw in registers; the block writes one partial row.
+template <typename T, int VE, int NV>
+__global__ void __launch_bounds__(kMaxThreads) rms_norm_backward_rows(const NormBwdArgs a) {
+    extern __shared__ float smem[];  // [2][32] reduction slots, then [hidden] (several rows per block)
+    using V = Vec<T, VE>;
+    const int tpr = a.tpr, groups = blockDim.x / tpr;
+    const int t = threadIdx.x % tpr, g = threadIdx.x / tpr;
+    float acc[NV][VE];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < VE; ++i) acc[j][i] = 0.f;
+    int parity = 0;
+    const float inv_h = 1.f / float(a.hidden);
+    for (int64_t row = int64_t(blockIdx.x) * groups + g; row < a.n; row += int64_t(gridDim.x) * groups) {
+        const T* dy = static_cast<const T*>(a.dy) + row * a.dy_stride;
+        const T* h = static_cast<const T*>(a.h) + row * a.h_stride;
+        const T* dh = a.dh ? static_cast<const T*>(a.dh) + row * a.dh_stride : nullptr;
+        T* dx = static_cast<T*>(a.dx) + row * a.dx_stride;
+        V vg[NV], vh[NV], ve[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int64_t col = int64_t(j * tpr + t) * VE;
+            if (col < a.hidden) {
+                vg[j] = *reinterpret_cast<const V*>(dy + col);
+                vh[j] = *reinterpret_cast<const V*>(h + col);
+                if (dh) ve[j] = *reinterpret_cast<const V*>(dh + col);
+            }
+        }
+        const float r = a.rstd[row];
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int64_t col = int64_t(j * tpr + t) * VE;
+            if (col < a.hidden) {
+                float w[VE];
+                load_weight<VE>(a.weight, a.w_f32, col, w);
+#pragma unroll
+                for (int i = 0; i < VE; ++i) {
+                    const float hat = to_f(vh[j].e[i]) * r, d = to_f(vg[j].e[i]);
+                    acc[j][i] = fmaf(d, hat, acc[j][i]);
+                    s = fmaf(d * w[i], hat, s);
+                }
+            }
+        }
+        s = row_sum(s, tpr, smem + parity * 32) * inv_h;
+        parity ^= 1;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int64_t col = int64_t(j * tpr + t) * VE;
+            if (col < a.hidden) {
+                float w[VE];
+                load_weight<VE>(a.weight, a.w_f32, col, w);
+                V o;
+#pragma unroll
+                for (int i = 0; i < VE; ++i) {
+                    const float hat = to_f(vh[j].e[i]) * r;
+                    float d = r * (to_f(vg[j].e[i]) * w[i] - hat * s);
+                    if (dh) d += to_f(ve[j].e[i]);
+                    o.e[i] = from_f<T>(d);
+                }
+                if (VCE_BOUNDS(col >= 0 && col + VE <= a.hidden && row < a.n, a.dev_status))
+                    *reinterpret_cast<V*>(dx + col) = o;
+            }
+        }
+    }
+    float* out = a.part + int64_t(blockIdx.x) * a.hidden;
+    if (groups == 1) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int64_t col = int64_t(j * tpr + t) * VE;
+            if (col < a.hidden && VCE_BOUNDS(int(blockIdx.x) < a.parts, a.dev_status))
+#pragma unroll
+                for (int i = 0; i < VE; ++i) out[col + i] = acc[j][i];
+        }
+        return;
+    }
+    float* sum = smem + 64;  // the block's row groups add theirs in turn: a fixed order
+    for (int k = 0; k < groups; ++k) {
+        if (g == k) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int64_t col = int64_t(j * tpr + t) * VE;
+                if (col < a.hidden)
+#pragma unroll
+                    for (int i = 0; i < VE; ++i) sum[col + i] = (k == 0 ? 0.f : sum[col + i]) + acc[j][i];
+            }
+        }
+        __syncthreads();
+    }
+    for (int64_t c = threadIdx.x; c < a.hidden; c += blockDim.x)
+        if (VCE_BOUNDS(int(blockIdx.x) < a.parts, a.dev_status)) out[c] = sum[c];
+}
+
+// Rows longer than the registers hold: dx by one block per row (after dw: dx may
+// be written over dy) ...
+template <typename T>
+__global__ void __launch_bounds__(kMaxThreads) rms_norm_backward_long(const NormBwdArgs a) {
+    __shared__ float slot[32];
+    const int64_t row = blockIdx.x;
+    const T* dy = static_cast<const T*>(a.dy) + row * a.dy_stride;
+    const T* h = static_cast<const T*>(a.h) + row * a.h_stride;
+    const T* dh = a.dh ? static_cast<const T*>(a.dh) + row * a.dh_stride : nullptr;
+    const float r = a.rstd[row];
+    float s = 0.f, comp = 0.f, w[1];
+    for (int64_t col = threadIdx.x; col < a.hidden; col += blockDim.x) {
+        load_weight<1>(a.weight, a.w_f32, col, w);
+        const float q = fmaf(to_f(dy[col]) * w[0], to_f(h[col]) * r, -comp);
+        const float n = s + q;
+        comp = (n - s) - q;
+        s = n;
+    }
+    s = row_sum(s, blockDim.x, slot) / float(a.hidden);
+    for (int64_t col = threadIdx.x; col < a.hidden; col += blockDim.x) {
+        load_weight<1>(a.weight, a.w_f32, col, w);
+        float d = r * (to_f(dy[col]) * w[0] - to_f(h[col]) * r * s);
+        if (dh) d += to_f(dh[col]);
+        static_cast<T*>(a.dx)[row * a.dx_stride + col] = from_f<T>(d);
+    }
+}
+
+// ... and dw by columns: block (x, y) sums rows y, y + parts, ... of 256 columns.
+template <typename T>
+__global__ void __launch_bounds__(256) rms_norm_dweight_long(const NormBwdArgs a) {
+    const int64_t col = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    if (col >= a.hidden) return;
+    float s = 0.f;
+    for (int64_t row = blockIdx.y; row < a.n; row += a.parts)
+        s = fmaf(to_f(static_cast<const T*>(a.dy)[row * a.dy_stride + col]),
+                 to_f(static_cast<const T*>(a.h)[row * a.h_stride + col]) * a.rstd[row], s);
+    a.part[int64_t(blockIdx.y) * a.hidden + col] = s;
+}
+
+// dw = the sum of the partial rows, in a fixed order: 32 columns per block, 8 threads
+// per column, each over every eighth partial.
+__global__ void __launch_bounds__(256) rms_norm_dweight_sum(const float* __restrict__ part, int parts,
+                                                            int64_t hidden, void* dw, int w_f32) {
+    __shared__ float sm[8][32];
+    const int lc = threadIdx.x & 31, sp = threadIdx.x >> 5;
+    const int64_t col = int64_t(blockIdx.x) * 32 + lc;
+    float s = 0.f;
+    if (col < hidden) {
+#pragma unroll 8
+        for (int p = sp; p < parts; p += 8) s += part[int64_t(p) * hidden + col];
+    }
+    sm[sp][lc] = s;
+    __syncthreads();
+    if (sp != 0 || col >= hidden) return;
+    for (int k = 1; k < 8; ++k) s += sm[k][lc];
+    if (w_f32) static_cast<float*>(dw)[col] = s;
+    else static_cast<__nv_bfloat16*>(dw)[col] = __float2bfloat16_rn(s);
+}
+
+// Elements per access: the widest of the kernel's choices that divides the row length and
+// every stride and to which every pointer is aligned.
+int pick_ve(int full, int64_t hidden, size_t es, std::initializer_list<const void*> ptrs,
+            std::initializer_list<int64_t> strides, const void* weight, int w_f32) {
+    for (int ve : {full, 2}) {
+        bool ok = hidden % ve == 0;
+        for (const void* p : ptrs) ok = ok && reinterpret_cast<uintptr_t>(p) % (ve * es) == 0;
+        for (int64_t s : strides) ok = ok && s % ve == 0;
+        const size_t wa = w_f32 ? (ve * 4 > 16 ? 16 : ve * 4) : ve * 2;
+        ok = ok && reinterpret_cast<uintptr_t>(weight) % wa == 0;
+        if (ok) return ve;
+    }
+    return 1;
+}
+
+int pow2_at_least(int64_t x) {
+    int p = 32;
+    while (p < x) p *= 2;
+    return p;
+}
+
+template <typename T, bool kMx>
+vce_status norm_forward(NormArgs a, int ve, cudaStream_t s, const DeviceInfo& dev) {
+    constexpr int kFull = 16 / sizeof(T);
+    const int64_t cols = kMx ? a.padded : a.hidden;
+    const int64_t nvec = (cols + ve - 1) / ve;
+    const int64_t rows = kMx ? a.rows_padded : a.n;
+    count_launch();
+    // Four vectors per thread keep enough loads in flight from few threads; with fewer
+    // rows than fill the SMs, one vector per thread finishes a row sooner.
+    int nv = a.n < 2 * dev.num_sms ? 1 : 4;
+    if (ve != kFull) nv = 8;
+    while (nv < 8 && nvec > int64_t(kMaxThreads) * nv) nv *= 2;
+    if (nvec > int64_t(kMaxThreads) * nv) {
+        rms_norm_long<T, kMx><<<unsigned(rows), kMaxThreads, 0, s>>>(a);
+        return cudaGetLastError() == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
+    }
+    a.tpr = pow2_at_least((nvec + nv - 1) / nv);
+    const int block = a.tpr == 32 ? 128 : a.tpr;  // four rows of one warp each, or one row
+    const unsigned grid = unsigned((rows + block / a.tpr - 1) / (block / a.tpr));
+    if (ve == kFull) {
+        if (nv == 1) rms_norm_rows<T, kFull, 1, kMx><<<grid, block, 0, s>>>(a);
+        else if (nv == 2) rms_norm_rows<T, kFull, 2, kMx><<<grid, block, 0, s>>>(a);
+        else if (nv == 4) rms_norm_rows<T, kFull, 4, kMx><<<grid, block, 0, s>>>(a);
+        else rms_norm_rows<T, kFull, 8, kMx><<<grid, block, 0, s>>>(a);
+    } else if (ve == 2) {
+        rms_norm_rows<T, 2, 8, kMx><<<grid, block, 0, s>>>(a);
+    } else {
+        rms_norm_rows<T, 1, 8, kMx><<<grid, block, 0, s>>>(a);
+    }
+    return cudaGetLastError() == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
+}
+
+template <typename T>
+vce_status norm_backward(NormBwdArgs a, int ve, int parts, cudaStream_t s) {
+    constexpr int kFull = 16 / sizeof(T);
+    constexpr int kNv = 32 / kFull;  // 32 sums of dw per thread
+    const int64_t nvec = (a.hidden + ve - 1) / ve;
+    int nv = ve == kFull ? kNv : 16;
+    a.parts = parts;
+    if (a.n > 0 && nvec > int64_t(kMaxThreads) * nv) {
+        count_launch();  // dw first: dx may be written over dy
+        rms_norm_dweight_long<T><<<dim3(unsigned((a.hidden + 255) / 256), unsigned(parts)), 256, 0, s>>>(a);
+        count_launch();
+        rms_norm_backward_long<T><<<unsigned(a.n), kMaxThreads, 0, s>>>(a);
+    } else if (a.n > 0) {
+        while (nv > 1 && nvec <= 32 * (nv / 2) && ve == kFull) nv /= 2;
+        a.tpr = pow2_at_least((nvec + nv - 1) / nv);
+        const int block = a.tpr == 32 ? 128 : a.tpr;
+        const size_t smem = 64 * sizeof(float) + (block == a.tpr ? 0 : size_t(a.hidden) * sizeof(float));
+        count_launch();
+        if (ve == kFull) {
+            if (nv == kNv) rms_norm_backward_rows<T, kFull, kNv><<<parts, block, smem, s>>>(a);
+            else if (nv == kNv / 2) rms_norm_backward_rows<T, kFull, kNv / 2><<<parts, block, smem, s>>>(a);
+            else rms_norm_backward_rows<T, kFull, kNv / 4><<<parts, block, smem, s>>>(a);
+        } else if (ve == 2) {
+            rms_norm_backward_rows<T, 2, 16><<<parts, block, smem, s>>>(a);
+        } else {
+            rms_norm_backward_rows<T, 1, 16><<<parts, block, smem, s>>>(a);
+        }
+    }
+    return cudaGetLastError() == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
+}
+
+}  // namespace
+
+// Partial rows of dw: four blocks per SM, or one per row.
+int rms_norm_parts(int64_t n, int num_sms) {
+    const int64_t most = int64_t(num_sms) * 4;
+    return int(n < most ? n : most);
+}
+
+vce_status launch_rms_norm(const void* x, const void* residual, const void* weight, int dtype, int w_dtype,
+                           int64_t n, int64_t hidden, int64_t x_stride, int64_t r_stride, int64_t h_stride,
+                           int64_t y_stride, float eps, void* h, void* y, float* rstd, uint8_t* codes,
+                           uint8_t* scales, int* dev_status, cudaStream_t s, const DeviceInfo& dev) {
+    if (n == 0) return VCE_OK;
+    NormArgs a{};
+    a.x = x; a.residual = residual; a.weight = weight; a.w_f32 = w_dtype == VCE_F32;
+    a.n = n; a.hidden = hidden; a.x_stride = x_stride; a.r_stride = r_stride; a.h_stride = h_stride;
+    a.y_stride = y_stride; a.eps = eps; a.h = h; a.y = y; a.rstd = rstd; a.codes = codes; a.scales = scales;
+    a.padded = mx::padded(hidden); a.rows_padded = mx::padded(n); a.dev_status = dev_status;
+    const size_t es = dtype == VCE_BF16 ? 2 : 4;
+    const void* any = x;  // absent operands do not limit the access width
+    const int ve = pick_ve(int(16 / es), hidden, es,
+                           {x, residual ? residual : any, residual ? h : any, codes ? any : y},
+                           {x_stride, residual ? r_stride : 0, residual ? h_stride : 0, codes ? 0 : y_stride},
+                           weight, a.w_f32);
+    if (dtype == VCE_BF16)
+        return codes ? norm_forward<__nv_bfloat16, true>(a, ve, s, dev)
+                     : norm_forward<__nv_bfloat16, false>(a, ve, s, dev);
+    return codes ? norm_forward<float, true>(a, ve, s, dev) : norm_forward<float, false>(a, ve, s, dev);
+}
+
+vce_status launch_rms_norm_backward(const void* dy, const void* h, const void* weight, const float* rstd,
+                                    const void* dh, int dtype, int w_dtype, int64_t n, int64_t hidden,
+                                    int64_t dy_stride, int64_t h_stride, int64_t dh_stride, int64_t dx_stride,
+                                    void* dx, void* dweight, void* ws, int* dev_status, cudaStream_t s,
+                                    const DeviceInfo& dev) {
+    NormBwdArgs a{};
+    a.dy = dy; a.h = h; a.weight = weight; a.dh = dh; a.rstd = rstd; a.w_f32 = w_dtype == VCE_F32;
+    a.n = n; a.hidden = hidden; a.dy_stride = dy_stride; a.h_stride = h_stride; a.dh_stride = dh_stride;
+    a.dx_stride = dx_stride; a.dx = dx; a.part = static_cast<float*>(ws); a.dev_status = dev_status;
+    const size_t es = dtype == VCE_BF16 ? 2 : 4;
+    const int parts = rms_norm_parts(n, dev.num_sms);
+    const int ve = n == 0 ? 1
+                          : pick_ve(int(16 / es), hidden, es, {dy, h, dh ? dh : h, dx},
+                                    {dy_stride, h_stride, dh ? dh_stride : 0, dx_stride}, weight, a.w_f32);
+    vce_status st = dtype == VCE_BF16 ? norm_backward<__nv_bfloat16>(a, ve, parts, s)
+                                      : norm_backward<float>(a, ve, parts, s);
+    if (st) return st;
+    count_launch();
+    rms_norm_dweight_sum<<<unsigned((hidden + 31) / 32), 256, 0, s>>>(a.part, parts, hidden, dweight, a.w_f32);
+    return cudaGetLastError() == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
+}
+
+}  // namespace vce

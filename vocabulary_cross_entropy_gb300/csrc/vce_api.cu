@@ -3,6 +3,7 @@
 // allocates, frees or synchronises.
 
 #include "vce_internal.cuh"
+#include "mx_format.cuh"
 
 #include <atomic>
 #include <mutex>
@@ -56,6 +57,30 @@ bool eps_ok(float eps) { return eps >= 0.f && eps <= 1.f; }  // false for NaN to
 bool reduce_ok(int r) { return r == VCE_REDUCE_NONE || r == VCE_REDUCE_MEAN || r == VCE_REDUCE_SUM; }
 
 size_t elem_size(int dtype) { return dtype == VCE_BF16 ? 2 : 4; }
+
+bool dtype_ok(int dtype) { return dtype == VCE_BF16 || dtype == VCE_F32; }
+
+bool mx_ok(int fmt) { return fmt == VCE_MX_E4M3 || fmt == VCE_MX_E2M1; }
+
+// Row counts and lengths the row kernels index with: a grid dimension of rows (and of
+// the rows that fill a scale tile), 32-bit columns inside a row.
+constexpr int64_t kMaxRows = 0x7fffff00;
+constexpr int64_t kMaxCols = int64_t(1) << 28;
+
+vce_status check_norm(int dtype, int64_t n, int64_t hidden, const void* x, int64_t x_stride, const void* residual,
+                      int64_t residual_stride, const void* weight, int weight_dtype, float eps, const void* h,
+                      int64_t h_stride, const float* rstd) {
+    if (!dtype_ok(dtype) || !dtype_ok(weight_dtype)) return VCE_ERR_DTYPE;
+    if (n < 0 || n > kMaxRows || hidden < 1 || hidden > kMaxCols || x_stride < hidden || !(eps >= 0.f))
+        return VCE_ERR_INVALID_ARG;
+    if (n > 0 && (!x || !weight)) return VCE_ERR_INVALID_ARG;
+    if (n > 0 && residual && (!h || residual_stride < hidden || h_stride < hidden)) return VCE_ERR_INVALID_ARG;
+    const size_t es = elem_size(dtype);
+    if (!aligned(x, es) || !aligned(residual, es) || !aligned(h, es) || !aligned(weight, elem_size(weight_dtype)) ||
+        !aligned(rstd, 4))
+        return VCE_ERR_ALIGN;
+    return VCE_OK;
+}
 
 }  // namespace
 
@@ -224,6 +249,102 @@ vce_status lce_backward(const void* X, const void* W, int64_t n, int64_t h, int6
     return launch_lce_backward(X, W, n, h, v, target, lse, n_valid, grad_output, label_smoothing,
                                reduce_loss, ignore_idx, dX, dW, ws, slab, dev_status,
                                static_cast<cudaStream_t>(stream), dev);
+}
+
+vce_status rms_norm_forward(const void* x, int dtype, int64_t n, int64_t hidden, int64_t x_stride,
+                            const void* residual, int64_t residual_stride, const void* weight,
+                            int weight_dtype, float eps, void* h, int64_t h_stride, void* y,
+                            int64_t y_stride, float* rstd, int* dev_status, void* stream) {
+    if (vce_status st = check_norm(dtype, n, hidden, x, x_stride, residual, residual_stride, weight, weight_dtype,
+                                   eps, h, h_stride, rstd))
+        return st;
+    if (n > 0 && (!y || y_stride < hidden)) return VCE_ERR_INVALID_ARG;
+    if (!aligned(y, elem_size(dtype))) return VCE_ERR_ALIGN;
+    DeviceInfo dev;
+    if (vce_status st = current_device(dev)) return st;
+    return launch_rms_norm(x, residual, weight, dtype, weight_dtype, n, hidden, x_stride, residual_stride, h_stride,
+                           y_stride, eps, h, y, rstd, nullptr, nullptr, dev_status,
+                           static_cast<cudaStream_t>(stream), dev);
+}
+
+vce_status rms_norm_mx(const void* x, int dtype, int64_t n, int64_t hidden, int64_t x_stride,
+                       const void* residual, int64_t residual_stride, const void* weight,
+                       int weight_dtype, float eps, void* h, int64_t h_stride, void* codes,
+                       void* scales, float* rstd, int* dev_status, void* stream) {
+    if (vce_status st = check_norm(dtype, n, hidden, x, x_stride, residual, residual_stride, weight, weight_dtype,
+                                   eps, h, h_stride, rstd))
+        return st;
+    if (n > 0 && (!codes || !scales)) return VCE_ERR_INVALID_ARG;
+    if (!aligned(codes, 16) || !aligned(scales, 16)) return VCE_ERR_ALIGN;
+    DeviceInfo dev;
+    if (vce_status st = current_device(dev)) return st;
+    return launch_rms_norm(x, residual, weight, dtype, weight_dtype, n, hidden, x_stride, residual_stride, h_stride,
+                           0, eps, h, nullptr, rstd, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales),
+                           dev_status, static_cast<cudaStream_t>(stream), dev);
+}
+
+size_t rms_norm_workspace_size(int64_t n, int64_t hidden) {
+    DeviceInfo dev;
+    if (n <= 0 || hidden <= 0 || current_device(dev) != VCE_OK) return 0;
+    return align256(size_t(rms_norm_parts(n, dev.num_sms)) * size_t(hidden) * sizeof(float));
+}
+
+vce_status rms_norm_backward(const void* dy, int dtype, int64_t n, int64_t hidden, int64_t dy_stride,
+                             const void* h, int64_t h_stride, const void* weight, int weight_dtype,
+                             const float* rstd, const void* dh, int64_t dh_stride, void* dx,
+                             int64_t dx_stride, void* dweight, void* ws, size_t ws_bytes,
+                             int* dev_status, void* stream) {
+    if (!dtype_ok(dtype) || !dtype_ok(weight_dtype)) return VCE_ERR_DTYPE;
+    if (n < 0 || n > kMaxRows || hidden < 1 || hidden > kMaxCols || !dweight) return VCE_ERR_INVALID_ARG;
+    if (n > 0 && (!dy || !h || !weight || !rstd || !dx || dy_stride < hidden || h_stride < hidden ||
+                  dx_stride < hidden || (dh && dh_stride < hidden) || dx == h))
+        return VCE_ERR_INVALID_ARG;
+    const size_t es = elem_size(dtype), ews = elem_size(weight_dtype);
+    if (!aligned(dy, es) || !aligned(h, es) || !aligned(dh, es) || !aligned(dx, es) || !aligned(weight, ews) ||
+        !aligned(dweight, ews) || !aligned(rstd, 4))
+        return VCE_ERR_ALIGN;
+    DeviceInfo dev;
+    if (n > 0 && !ws) return VCE_ERR_WORKSPACE;
+    if (!aligned(ws, 256)) return VCE_ERR_ALIGN;
+    if (vce_status st = current_device(dev)) return st;
+    if (n > 0 && ws_bytes < rms_norm_workspace_size(n, hidden)) return VCE_ERR_WORKSPACE;
+    return launch_rms_norm_backward(dy, h, weight, rstd, dh, dtype, weight_dtype, n, hidden, dy_stride, h_stride,
+                                    dh_stride, dx_stride, dx, dweight, ws, dev_status,
+                                    static_cast<cudaStream_t>(stream), dev);
+}
+
+size_t mx_codes_size(int64_t rows, int64_t cols, int fmt) {
+    if (rows <= 0 || cols <= 0 || !mx_ok(fmt)) return 0;
+    return size_t(rows) * size_t(mx::padded(cols)) / (fmt == VCE_MX_E2M1 ? 2 : 1);
+}
+
+size_t mx_scales_size(int64_t rows, int64_t cols) {
+    if (rows <= 0 || cols <= 0) return 0;
+    return size_t(mx::padded(rows)) * size_t(mx::padded(cols)) / mx::kBlock;
+}
+
+vce_status mx_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int64_t row_stride, int fmt,
+                       void* codes, void* scales, int* dev_status, void* stream) {
+    if (!dtype_ok(dtype) || !mx_ok(fmt)) return VCE_ERR_DTYPE;
+    if (rows < 0 || rows > kMaxRows || cols < 1 || cols > kMaxCols || row_stride < cols) return VCE_ERR_INVALID_ARG;
+    if (rows > 0 && (!x || !codes || !scales)) return VCE_ERR_INVALID_ARG;
+    if (!aligned(x, elem_size(dtype)) || !aligned(codes, 16) || !aligned(scales, 16)) return VCE_ERR_ALIGN;
+    DeviceInfo dev;
+    if (vce_status st = current_device(dev)) return st;
+    return launch_mx_quantize(x, dtype, rows, cols, row_stride, fmt, static_cast<uint8_t*>(codes),
+                              static_cast<uint8_t*>(scales), dev_status, static_cast<cudaStream_t>(stream));
+}
+
+vce_status mx_dequantize(const void* codes, const void* scales, int fmt, int64_t rows, int64_t cols,
+                         void* out, int dtype, int64_t row_stride, int* dev_status, void* stream) {
+    if (!dtype_ok(dtype) || !mx_ok(fmt)) return VCE_ERR_DTYPE;
+    if (rows < 0 || rows > kMaxRows || cols < 1 || cols > kMaxCols || row_stride < cols) return VCE_ERR_INVALID_ARG;
+    if (rows > 0 && (!out || !codes || !scales)) return VCE_ERR_INVALID_ARG;
+    if (!aligned(out, elem_size(dtype)) || !aligned(codes, 16) || !aligned(scales, 16)) return VCE_ERR_ALIGN;
+    DeviceInfo dev;
+    if (vce_status st = current_device(dev)) return st;
+    return launch_mx_dequantize(static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), fmt, rows,
+                                cols, out, dtype, row_stride, dev_status, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
