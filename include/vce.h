@@ -432,6 +432,20 @@ vce_status mx_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int
 vce_status mx_dequantize(const void* codes, const void* scales, int fmt, int64_t rows, int64_t cols,
                          void* out, int dtype, int64_t row_stride, int* dev_status, void* stream);
 
+/*
+ * Logits of a quantised classifier: out[i, j] = sum_k x[i, k] w[j, k] of the values the
+ * two microscaled tensors stand for, in one pass of the block-scaled tensor-core
+ * instruction (exact products, FP32 sums).  What lce_forward folds into a loss is
+ * stored here, for sampling (ce_sample) or scoring (ce_forward).
+ *
+ *   x  E4M3 [n, h] (mx_quantize or rms_norm_mx); w  E2M1 [v, h].
+ *   out  BF16 or F32 [n, v], rows out_stride elements apart (>= v), aligned to its type.
+ * A NaN scale makes the outputs of its row of x (of w) NaN.
+ */
+vce_status mx_linear(const void* x_codes, const void* x_scales, const void* w_codes, const void* w_scales,
+                     int64_t n, int64_t h, int64_t v, void* out, int out_dtype, int64_t out_stride,
+                     int* dev_status, void* stream);
+
 /* ------------------------------------------------------------------------ */
 /* diagnostics                                                              */
 /* ------------------------------------------------------------------------ */

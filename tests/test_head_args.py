@@ -79,6 +79,28 @@ def test_mx_refusals():
     assert vce.mx_scales_size(129, 129) == 256 * 8 and vce.mx_scales_size(0, 5) == 0
 
 
+def test_mx_linear_refusals():
+    f = vce.library().mx_linear
+
+    def call(xc=FAKE, xs=FAKE, wc=FAKE, ws=FAKE, n=4, h=64, v=100, out=FAKE, dtype=0, stride=100):
+        return f(xc, xs, wc, ws, n, h, v, out, dtype, stride, None, None)
+
+    assert call(dtype=2) == DTYPE
+    for bad in (dict(n=-1), dict(h=0), dict(v=0), dict(stride=99), dict(xc=None), dict(xs=None), dict(wc=None),
+                dict(ws=None), dict(out=None), dict(n=1 << 40), dict(v=1 << 40, stride=1 << 40)):
+        assert call(**bad) == INVALID, bad
+    for bad in (dict(xc=FAKE + 8), dict(xs=FAKE + 8), dict(wc=FAKE + 8), dict(ws=FAKE + 8), dict(out=FAKE + 1)):
+        assert call(**bad) == ALIGN, bad
+    x, w = vce.MXTensor.empty(4, 64, "e4m3", "cpu"), vce.MXTensor.empty(9, 64, "e2m1", "cpu")
+    with pytest.raises(ValueError, match="CUDA"):
+        vce.mx_linear(x, w)
+    for pair in ((w, w), (x, x), (x, vce.MXTensor.empty(9, 65, "e2m1", "cpu"))):
+        with pytest.raises(ValueError):
+            vce.mx_linear(*pair)
+    with pytest.raises(ValueError):
+        vce.mx_linear(x, w, out=torch.zeros(4, 8, dtype=torch.bfloat16))
+
+
 def test_python_refusals():
     x, w = torch.zeros(4, 64), torch.ones(64)
     with pytest.raises(ValueError, match="CUDA"):

@@ -46,6 +46,7 @@ from ._head import (  # noqa: F401,E402
     mx_scales_size,
     mx_quantize,
     mx_dequantize,
+    mx_linear,
     rms_norm_forward,
     rms_norm_mx,
     rms_norm_workspace_size,

@@ -98,6 +98,8 @@ def library() -> ctypes.CDLL:
     lib.mx_quantize.restype = _c_int
     lib.mx_dequantize.argtypes = [_c_p, _c_p, _c_int, _c_i64, _c_i64, _c_p, _c_int, _c_i64, _c_p, _c_p]
     lib.mx_dequantize.restype = _c_int
+    lib.mx_linear.argtypes = [_c_p, _c_p, _c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_int, _c_i64, _c_p, _c_p]
+    lib.mx_linear.restype = _c_int
     lib.vce_selftest_wait_timeout.argtypes = [ctypes.c_uint64, _c_p, _c_p, _c_p]
     lib.vce_selftest_wait_timeout.restype = _c_int
     lib.vce_selftest_lce_forward_timeout.argtypes = [_c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_p, ctypes.c_uint64,

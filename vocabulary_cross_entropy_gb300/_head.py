@@ -178,6 +178,28 @@ def mx_dequantize(t: MXTensor, dtype=torch.bfloat16, *, out=None, dev_status=Non
     return out
 
 
+def mx_linear(x: MXTensor, w: MXTensor, out_dtype=torch.bfloat16, *, out=None, dev_status=None, stream=None):
+    """``x @ w.T`` of the values of x (e4m3, [n, h]) and the classifier w (e2m1, [v, h]):
+    logits [n, v] in bfloat16 or float32.  dev_status is None or an int32 [1] tensor."""
+    lib = b.library()
+    _check_mx(x, "x")
+    _check_mx(w, "w")
+    dev = x.codes.device
+    if x.fmt != "e4m3" or w.fmt != "e2m1":
+        raise ValueError(f"x must be e4m3 and w e2m1, got {x.fmt} and {w.fmt}")
+    if x.cols != w.cols or w.rows < 1:
+        raise ValueError("x and w must share the hidden dimension, and w have rows")
+    if w.codes.device != dev:
+        raise ValueError("x and w are on different devices")
+    if out is None:
+        with _on_stream(stream):
+            out = torch.empty(x.rows, w.rows, dtype=out_dtype, device=dev)
+    stride = _written(out, "out", (x.rows, w.rows), out_dtype, dev)
+    _launch("mx_linear", dev, lib.mx_linear, b._ptr(x.codes), b._ptr(x.scales), b._ptr(w.codes), b._ptr(w.scales),
+            x.rows, x.cols, w.rows, b._ptr(out), _float_code(out, "out"), stride, _status(dev_status, dev), stream)
+    return out
+
+
 # ---------------------------------------------------------------------------
 # the norm before the classifier
 # ---------------------------------------------------------------------------

@@ -347,4 +347,20 @@ vce_status mx_dequantize(const void* codes, const void* scales, int fmt, int64_t
                                 cols, out, dtype, row_stride, dev_status, static_cast<cudaStream_t>(stream));
 }
 
+vce_status mx_linear(const void* x_codes, const void* x_scales, const void* w_codes, const void* w_scales,
+                     int64_t n, int64_t h, int64_t v, void* out, int out_dtype, int64_t out_stride,
+                     int* dev_status, void* stream) {
+    if (!dtype_ok(out_dtype)) return VCE_ERR_DTYPE;
+    if (n < 0 || n > kMaxRows || v < 1 || v > kMaxRows || h < 1 || h > kMaxCols || out_stride < v)
+        return VCE_ERR_INVALID_ARG;
+    if (n > 0 && (!x_codes || !x_scales || !w_codes || !w_scales || !out)) return VCE_ERR_INVALID_ARG;
+    if (!aligned(x_codes, 16) || !aligned(x_scales, 16) || !aligned(w_codes, 16) || !aligned(w_scales, 16) ||
+        !aligned(out, elem_size(out_dtype)))
+        return VCE_ERR_ALIGN;
+    DeviceInfo dev;
+    if (vce_status st = current_device(dev)) return st;
+    return launch_mx_linear(x_codes, x_scales, w_codes, w_scales, n, v, h, out, out_dtype, out_stride, dev_status,
+                            static_cast<cudaStream_t>(stream), dev);
+}
+
 }  // extern "C"

@@ -161,4 +161,9 @@ vce_status launch_mx_quantize(const void* x, int dtype, int64_t rows, int64_t co
 vce_status launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int fmt, int64_t rows, int64_t cols,
                                 void* out, int dtype, int64_t stride, int* dev_status, cudaStream_t s);
 
+// ---- product of microscaled matrices (mx_linear.cu) ----
+vce_status launch_mx_linear(const void* x_codes, const void* x_scales, const void* w_codes, const void* w_scales,
+                            int64_t n, int64_t v, int64_t h, void* out, int out_dtype, int64_t out_stride,
+                            int* dev_status, cudaStream_t s, const DeviceInfo& dev);
+
 }  // namespace vce
