@@ -88,6 +88,10 @@ typedef enum vce_dtype {
  * 16-byte aligned; that access was skipped instead of made. */
 #define VCE_DEVSTATUS_BOUNDS 4
 
+/* ce_sample: a row from which no token can be drawn (every logit -inf, a NaN or +inf
+ * among the logits, or a NaN parameter); its token is -1. */
+#define VCE_DEVSTATUS_BAD_ROW 8
+
 /* Formats of microscaled tensors: one power-of-two scale per 32 columns. */
 #define VCE_MX_E4M3 0 /* 8-bit values, at most 448 */
 #define VCE_MX_E2M1 1 /* 4-bit values: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives */
@@ -234,6 +238,40 @@ vce_status ce_forward_noalloc(const void* logits, int dtype, int64_t n_rows, int
                               int64_t row_stride, const int64_t* target, float label_smoothing,
                               int reduce_loss, int64_t ignore_idx, float* loss, float* stats,
                               int64_t* n_valid, int* dev_status, void* stream);
+
+/*
+ * One token per row of logits, from a given uniform number.  The tokens of a row are
+ * ordered by (logit descending, index ascending), with weights
+ *     w_i = exp((z_i - max z) / temperature),
+ * and the head of that order is kept which all of these keep:
+ *     top_k   the first k tokens;
+ *     top_p   the shortest head whose weight is at least top_p times the weight of
+ *             what top_k kept (always the first token);
+ *     min_p   the tokens of weight at least min_p (of at least min_p times the
+ *             likeliest token's probability).
+ * The token is the first one at which the cumulated weight exceeds uniform times the
+ * weight of all kept ones.  A temperature of 0 or less takes the first token.  The
+ * choice is made in whole-number weights of 43 to 46 fractional bits, summed exactly:
+ * it does not depend on how a row is split, and a token whose weight is below
+ * 2^-(bits + 1) is never drawn.
+ *
+ *   logits       as in ce_forward, with 1 <= vocab <= VCE_SAMPLE_MAX_VOCAB; -inf marks a
+ *                token that is not allowed.
+ *   uniform      F32 [n_rows], in [0, 1) (smaller counts as 0, larger takes the last kept).
+ *   temperature, top_p, min_p  F32 [n_rows], top_k int32 [n_rows]; each may be NULL:
+ *                temperature 1, no filter.  top_k <= 0 or >= vocab, top_p >= 1 and
+ *                min_p <= 0 leave their filter out; min_p above 1 counts as 1;
+ *                temperatures above 0 are taken between 1e-30 and 1e30.
+ *   token        int64 [n_rows].
+ *   logprob      F32 [n_rows] or NULL: log(w_token / weight of all kept tokens).
+ * A row from which nothing can be drawn (every logit -inf, a NaN or +inf among them, or
+ * a NaN parameter) gets token -1, logprob NaN and VCE_DEVSTATUS_BAD_ROW.
+ */
+#define VCE_SAMPLE_MAX_VOCAB 1048576
+vce_status ce_sample(const void* logits, int dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
+                     const float* uniform, const float* temperature, const int32_t* top_k,
+                     const float* top_p, const float* min_p, int64_t* token, float* logprob,
+                     int* dev_status, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* linear form (X, W and the gradients are BF16; accumulation is FP32)      */

@@ -96,3 +96,30 @@ def mx_pack(codes, e, cols, fmt):
         for b in range(e.shape[1]):
             tiles[r // 128, b // 4, r % 32 * 16 + r % 128 // 32 * 4 + b % 4] = e[r, b] + 127
     return packed, tiles
+
+
+# ---------------------------------------------------------------------------
+# sampling
+# ---------------------------------------------------------------------------
+
+def sample_row(z, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
+    """(token, log probability) of one row of FP64 logits; (-1, nan) where nothing can be drawn."""
+    z = np.asarray(z, np.float64)
+    if np.isnan(z).any() or np.isnan([u, temperature, top_p, min_p]).any() or not np.isfinite(z.max()):
+        return -1, np.nan
+    order = np.lexsort((np.arange(len(z)), -z))       # logit descending, index ascending
+    if temperature <= 0:
+        return int(order[0]), 0.0
+    with np.errstate(over="ignore", under="ignore"):
+        w = np.exp((z[order] - z.max()) / np.float64(np.clip(temperature, 1e-30, 1e30)))
+    w = w[:int((w > 0).sum())]
+    if 0 < top_k < len(z):
+        w = w[:top_k]
+    c = np.cumsum(w)
+    kept = len(w)
+    if top_p < 1:
+        kept = max(1, int((c - w < top_p * c[-1]).sum()))
+    if min_p > 0:
+        kept = min(kept, int((w >= min(min_p, 1.0)).sum()))
+    at = min(int((c[:kept] <= max(u, 0.0) * c[kept - 1]).sum()), kept - 1)
+    return int(order[at]), float(np.log(w[at] / c[kept - 1]))

@@ -101,6 +101,56 @@ def test_mx_linear_refusals():
         vce.mx_linear(x, w, out=torch.zeros(4, 8, dtype=torch.bfloat16))
 
 
+def test_sample_refusals():
+    f = vce.library().ce_sample
+
+    def call(z=FAKE, dtype=0, n=4, v=100, stride=100, u=FAKE, t=None, k=None, p=None, m=None, tok=FAKE, lp=None):
+        return f(z, dtype, n, v, stride, u, t, k, p, m, tok, lp, None, None)
+
+    assert call(dtype=2) == DTYPE
+    for bad in (dict(n=-1), dict(v=0), dict(stride=99), dict(z=None), dict(u=None), dict(tok=None),
+                dict(v=(1 << 20) + 1, stride=1 << 21)):
+        assert call(**bad) == INVALID, bad
+    for bad in (dict(z=FAKE + 1), dict(u=FAKE + 2), dict(t=FAKE + 1), dict(k=FAKE + 1), dict(p=FAKE + 1),
+                dict(m=FAKE + 1), dict(tok=FAKE + 4), dict(lp=FAKE + 1)):
+        assert call(**bad) == ALIGN, bad
+    z, u = torch.zeros(4, 10), torch.zeros(4)
+    with pytest.raises(ValueError, match="CUDA"):
+        vce.ce_sample(z, u)
+    for kw in (dict(temperature=torch.zeros(3)), dict(top_k=torch.zeros(4)), dict(top_p=torch.zeros(4).double()),
+               dict(min_p=torch.zeros(4, 2)[:, 0]), dict(token=torch.zeros(4, dtype=torch.int32))):
+        with pytest.raises(ValueError):
+            vce.ce_sample(z, u, **kw)
+    with pytest.raises(ValueError):
+        vce.ce_sample(z, u[:3])
+    with pytest.raises(TypeError):
+        vce.ce_sample(z.double(), u)
+    with pytest.raises(ValueError):
+        vce.linear_sample(z, vce.MXTensor.empty(9, 10, "e2m1", "cpu"), u, residual=z)
+
+
+def test_sampling_definition():
+    rng = np.random.default_rng(0)
+    z = rng.normal(size=50) * 2
+    p = np.exp(z - z.max())
+    p /= p.sum()
+    order = np.argsort(-z, kind="stable")
+    us = (np.arange(20000) + 0.5) / 20000
+    share = np.bincount([head.sample_row(z, u)[0] for u in us], minlength=50) / len(us)
+    assert np.abs(share - p).max() <= 1 / len(us)
+    for u in (0.0, 0.3, 0.999999):
+        assert head.sample_row(z, u, 0.0)[0] == order[0] and head.sample_row(z, u, top_k=1)[0] == order[0]
+        assert head.sample_row(z, u, top_p=0.5)[0] in order[:np.searchsorted(np.cumsum(p[order]), 0.5) + 1]
+        assert p[head.sample_row(z, u, min_p=0.2)[0]] >= 0.2 * p.max() * (1 - 1e-12)
+    assert head.sample_row(z, 0.999999, top_k=7)[0] == order[6]
+    t, lp = head.sample_row(z, 0.6)
+    assert abs(lp - np.log(p[t])) <= 1e-12
+    assert head.sample_row(np.array([1.0, 1.0, 1.0, 1.0]), 0.5)[0] == 2
+    assert head.sample_row(np.array([-np.inf, -np.inf]), 0.5)[0] == -1
+    assert head.sample_row(np.array([0.0, np.nan]), 0.5)[0] == -1
+    assert head.sample_row(np.array([0.0, np.inf]), 0.5)[0] == -1
+
+
 def test_python_refusals():
     x, w = torch.zeros(4, 64), torch.ones(64)
     with pytest.raises(ValueError, match="CUDA"):

@@ -15,6 +15,7 @@ from ._binding import (  # noqa: F401
     DEVSTATUS_BAD_TARGET,
     DEVSTATUS_TIMEOUT,
     DEVSTATUS_BOUNDS,
+    DEVSTATUS_BAD_ROW,
     DEFAULT_SLAB_BYTES,
     SLAB_UNCAPPED,
     REDUCE_NONE,
@@ -41,6 +42,7 @@ from ._binding import (  # noqa: F401
 from ._head import (  # noqa: F401,E402
     MX_E4M3,
     MX_E2M1,
+    SAMPLE_MAX_VOCAB,
     MXTensor,
     mx_codes_size,
     mx_scales_size,
@@ -51,5 +53,7 @@ from ._head import (  # noqa: F401,E402
     rms_norm_mx,
     rms_norm_workspace_size,
     rms_norm_backward,
+    ce_sample,
+    linear_sample,
 )
 from .autograd import parallel_cross_entropy, linear_cross_entropy, rms_norm  # noqa: F401,E402

@@ -17,6 +17,7 @@ F32 = 1
 DEVSTATUS_BAD_TARGET = 1
 DEVSTATUS_TIMEOUT = 2
 DEVSTATUS_BOUNDS = 4
+DEVSTATUS_BAD_ROW = 8
 # max_slab_bytes: 0 selects the library's default cap (VCE_DEFAULT_SLAB_BYTES);
 # SLAB_UNCAPPED lets one dZ slab cover the whole vocabulary
 DEFAULT_SLAB_BYTES = 256 << 20
@@ -100,6 +101,9 @@ def library() -> ctypes.CDLL:
     lib.mx_dequantize.restype = _c_int
     lib.mx_linear.argtypes = [_c_p, _c_p, _c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_int, _c_i64, _c_p, _c_p]
     lib.mx_linear.restype = _c_int
+    lib.ce_sample.argtypes = [_c_p, _c_int, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p,
+                              _c_p]
+    lib.ce_sample.restype = _c_int
     lib.vce_selftest_wait_timeout.argtypes = [ctypes.c_uint64, _c_p, _c_p, _c_p]
     lib.vce_selftest_wait_timeout.restype = _c_int
     lib.vce_selftest_lce_forward_timeout.argtypes = [_c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_p, ctypes.c_uint64,

@@ -1,5 +1,5 @@
 """ctypes marshalling for the operators around the vocabulary cross entropy: the norm
-before the classifier and microscaled tensors (see include/vce.h for what each
+before the classifier, microscaled tensors and their product, and sampling (see include/vce.h for what each
 computes).  As in ``_binding``, torch tensors supply memory and the current stream.
 
 A call given ``stream`` allocates what it was not given (outputs and workspace) from
@@ -15,11 +15,13 @@ import torch
 from . import _binding as b
 
 MX_E4M3, MX_E2M1 = 0, 1
+SAMPLE_MAX_VOCAB = 1 << 20
 _FMT = {"e4m3": MX_E4M3, "e2m1": MX_E2M1}
 
 RMSNormForward = namedtuple("RMSNormForward", "y h rstd")
 RMSNormMX = namedtuple("RMSNormMX", "y h rstd")
 RMSNormBackward = namedtuple("RMSNormBackward", "dx dweight")
+CESample = namedtuple("CESample", "token logprob dev_status")
 
 
 def _on_stream(stream):
@@ -296,3 +298,67 @@ def rms_norm_backward(dy, h, weight, rstd, dh=None, *, dx=None, dweight=None, wo
             b._ptr(dweight), b._ptr(workspace), workspace.numel() * workspace.element_size(),
             _status(dev_status, dev), stream)
     return RMSNormBackward(dx, dweight)
+
+
+# ---------------------------------------------------------------------------
+# sampling
+# ---------------------------------------------------------------------------
+
+def _per_row(value, name, n, dtype, device):
+    """A sampling parameter: None, a number for all rows, or a tensor with one entry per row."""
+    if value is None:
+        return None
+    if isinstance(value, torch.Tensor):
+        return _vector(value, name, n, dtype, device)
+    return torch.full((n,), value, dtype=dtype, device=device)
+
+
+def ce_sample(logits, uniform, temperature=None, top_k=None, top_p=None, min_p=None, *, token=None, logprob=None,
+              dev_status=None, stream=None):
+    """One token per row of ``logits`` [..., V] (bfloat16 or float32) from ``uniform`` (float32 in
+    [0, 1), one per row).  temperature, top_p, min_p (float32) and top_k (int32) are None, a
+    number, or a tensor with one entry per row.  Returns (token int64, logprob, dev_status), the
+    first two shaped like the leading dimensions; logprob is the logarithm of the probability
+    the token was drawn with.  A row from which nothing can be drawn gives -1 and NaN."""
+    lib = b.library()
+    dev = logits.device
+    code = _float_code(logits, "logits")
+    n, vocab, stride = b._rows_view(logits)
+    lead = logits.shape[:-1]
+    _vector(uniform, "uniform", n, torch.float32, dev)
+    with _on_stream(stream):
+        temperature = _per_row(temperature, "temperature", n, torch.float32, dev)
+        top_k = _per_row(top_k, "top_k", n, torch.int32, dev)
+        top_p = _per_row(top_p, "top_p", n, torch.float32, dev)
+        min_p = _per_row(min_p, "min_p", n, torch.float32, dev)
+        if token is None:
+            token = torch.empty(lead, dtype=torch.int64, device=dev)
+        if logprob is None:
+            logprob = torch.empty(lead, dtype=torch.float32, device=dev)
+        if dev_status is None:
+            dev_status = torch.zeros(1, dtype=torch.int32, device=dev)
+    _vector(token, "token", n, torch.int64, dev)
+    _vector(logprob, "logprob", n, torch.float32, dev)
+    _launch("ce_sample", dev, lib.ce_sample, b._ptr(logits), code, n, vocab, stride, b._ptr(uniform),
+            b._ptr(temperature), b._ptr(top_k), b._ptr(top_p), b._ptr(min_p), b._ptr(token), b._ptr(logprob),
+            _status(dev_status, dev), stream)
+    return CESample(token, logprob, dev_status)
+
+
+def linear_sample(embeddings, classifier: MXTensor, uniform, temperature=None, top_k=None, top_p=None, min_p=None, *,
+                  norm_weight=None, norm_eps=1e-6, residual=None, stream=None):
+    """The next token after ``embeddings`` [..., H], the counterpart of linear_cross_entropy when a
+    model answers: the norm (with ``norm_weight`` [H]; plus ``residual``) in 8 bits, the product
+    with the 4-bit ``classifier``, and ce_sample of the logits.  Returns ce_sample's results."""
+    lead, h = embeddings.shape[:-1], embeddings.shape[-1]
+    x = embeddings.reshape(-1, h)
+    if norm_weight is not None:
+        res = None if residual is None else residual.reshape(-1, h)
+        q = rms_norm_mx(x, norm_weight, norm_eps, res, stream=stream).y
+    elif residual is not None:
+        raise ValueError("residual is added by the norm: it needs norm_weight")
+    else:
+        q = mx_quantize(x, "e4m3", stream=stream)
+    logits = mx_linear(q, classifier, torch.float32, stream=stream)
+    r = ce_sample(logits, uniform, temperature, top_k, top_p, min_p, stream=stream)
+    return CESample(r.token.view(lead), r.logprob.view(lead), r.dev_status)

@@ -363,4 +363,21 @@ vce_status mx_linear(const void* x_codes, const void* x_scales, const void* w_co
                             static_cast<cudaStream_t>(stream), dev);
 }
 
+vce_status ce_sample(const void* logits, int dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
+                     const float* uniform, const float* temperature, const int32_t* top_k,
+                     const float* top_p, const float* min_p, int64_t* token, float* logprob,
+                     int* dev_status, void* stream) {
+    if (!dtype_ok(dtype)) return VCE_ERR_DTYPE;
+    if (n_rows < 0 || n_rows > kMaxRows || vocab < 1 || vocab > VCE_SAMPLE_MAX_VOCAB || row_stride < vocab)
+        return VCE_ERR_INVALID_ARG;
+    if (n_rows > 0 && (!logits || !uniform || !token)) return VCE_ERR_INVALID_ARG;
+    if (!aligned(logits, elem_size(dtype)) || !aligned(uniform, 4) || !aligned(temperature, 4) ||
+        !aligned(top_k, 4) || !aligned(top_p, 4) || !aligned(min_p, 4) || !aligned(token, 8) || !aligned(logprob, 4))
+        return VCE_ERR_ALIGN;
+    DeviceInfo dev;
+    if (vce_status st = current_device(dev)) return st;
+    return launch_ce_sample(logits, dtype, n_rows, vocab, row_stride, uniform, temperature, top_k, top_p, min_p,
+                            token, logprob, dev_status, static_cast<cudaStream_t>(stream), dev);
+}
+
 }  // extern "C"

@@ -143,6 +143,12 @@ vce_status launch_lce_backward(const void* X, const void* W, int64_t n, int64_t 
                                int64_t ignore_idx, void* dX, void* dW, void* ws, int64_t slab,
                                int* dev_status, cudaStream_t s, const DeviceInfo& dev);
 
+// ---- sampling (ce_sample.cu) ----
+vce_status launch_ce_sample(const void* logits, int dtype, int64_t n, int64_t vocab, int64_t stride,
+                            const float* uniform, const float* temperature, const int* top_k, const float* top_p,
+                            const float* min_p, int64_t* token, float* logprob, int* dev_status, cudaStream_t s,
+                            const DeviceInfo& dev);
+
 // ---- the norm before the classifier (rms_norm.cu) ----
 int rms_norm_parts(int64_t n, int num_sms);
 vce_status launch_rms_norm(const void* x, const void* residual, const void* weight, int dtype, int w_dtype,
