@@ -167,7 +167,7 @@ def test_python_refusals():
         vce.rms_norm_forward(x.t(), w)
     with pytest.raises(ValueError):
         vce.rms_norm_forward(x, w, residual=x[:1])          # no broadcasting
-    with pytest.raises(TypeError):
+    with pytest.raises(ValueError):
         vce.rms_norm_forward(x, w, residual=x.bfloat16())
     with pytest.raises(ValueError):
         vce.rms_norm_forward(x, w, y=torch.zeros(1, 64).expand(4, 64))

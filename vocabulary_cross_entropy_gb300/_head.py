@@ -24,43 +24,60 @@ RMSNormBackward = namedtuple("RMSNormBackward", "dx dweight")
 CESample = namedtuple("CESample", "token logprob dev_status")
 
 
+_CODES = {torch.bfloat16: b.BF16, torch.float32: b.F32}
+_no_stream = contextlib.nullcontext()
+
+
 def _on_stream(stream):
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _no_stream if stream is None else torch.cuda.stream(stream)
 
 
-def _float_code(t, name):
-    if t.dtype is torch.bfloat16:
-        return b.BF16
-    if t.dtype is torch.float32:
-        return b.F32
-    raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+def _float_code(dtype, name):
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"{name} must be bfloat16 or float32, got {dtype}")
+    return code
 
 
-def _matrix(t, name, shape=None, dtype=None, device=None):
-    """Row stride of a [rows, cols] tensor with contiguous rows that do not overlap."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+def _rows_of(t, name):
+    """(rows, cols, row stride) of a 2-D tensor with contiguous rows."""
+    if t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D tensor with contiguous rows")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    n, c = t.shape
+    rs, cs = t.stride()
+    if cs != 1 and c > 1:
+        raise ValueError(f"{name} must be a 2-D tensor with contiguous rows")
+    return n, c, rs if n > 1 else c
 
 
-def _written(t, name, shape, dtype, device):
-    """_matrix of an output: its rows must not overlap."""
-    stride = _matrix(t, name, shape, dtype, device)
-    if stride < t.shape[1]:
+def _same_rows(t, name, like):
+    """Row stride of a tensor that has to match ``like`` in shape, type and device."""
+    if t.shape != like.shape or t.dtype is not like.dtype or t.get_device() != like.get_device():
+        raise ValueError(f"{name} must be a {like.dtype} tensor of shape {tuple(like.shape)} on {like.device}, got "
+                         f"{t.dtype}, {tuple(t.shape)} on {t.device}")
+    return _rows_of(t, name)[2]
+
+
+def _written_rows(t, name, shape, dtype, index):
+    """Row stride of an output the caller gave: its rows must not overlap."""
+    if tuple(t.shape) != shape or t.dtype is not dtype or t.get_device() != index:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {shape} on the inputs' device")
+    n, c, stride = _rows_of(t, name)
+    if stride < c:
         raise ValueError(f"the rows of {name} overlap")
     return stride
 
 
-def _vector(t, name, n, dtype, device):
-    if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements on {device}")
+def _vector(t, name, n, dtype, index):
+    if t.dtype is not dtype or t.numel() != n or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements on the inputs' device")
     return t
+
+
+def _weight(t, hidden, index):
+    code = _float_code(t.dtype, "weight")
+    _vector(t, "weight", hidden, t.dtype, index)
+    return code
 
 
 def _launch(name, device, fn, *args):
@@ -68,13 +85,13 @@ def _launch(name, device, fn, *args):
     if device.type != "cuda":
         raise ValueError(f"{name}: tensors must be on a CUDA device, got {device}")
     *args, stream = args
-    b._check(name, b._on(device, fn, *args, b._stream(device, stream)))
+    st = b._on(device, fn, *args, b._stream(device, stream))
+    if st:
+        b._check(name, st)
 
 
-def _status(t, device):
-    if t is None:
-        return None
-    return b._ptr(_vector(t, "dev_status", 1, torch.int32, device))
+def _status(t, index):
+    return None if t is None else _vector(t, "dev_status", 1, torch.int32, index).data_ptr()
 
 
 # ---------------------------------------------------------------------------
@@ -127,15 +144,17 @@ def _fmt(fmt) -> int:
 
 
 def _check_mx(t, name):
-    code = _fmt(t.fmt)
-    n, c = t.codes, t.scales
-    if t.rows < 0 or t.cols < 1:
+    """Format code of a microscaled tensor whose buffers have the sizes its shape needs."""
+    codes, scales, rows, cols, fmt = t
+    code = _fmt(fmt)
+    if rows < 0 or cols < 1:
         raise ValueError(f"{name}: rows and cols must be positive")
-    for part, what, size in ((n, "codes", mx_codes_size(t.rows, t.cols, t.fmt)),
-                             (c, "scales", mx_scales_size(t.rows, t.cols))):
-        if part.dtype != torch.uint8 or not part.is_contiguous() or part.numel() != size:
+    padded = -(-cols // 128) * 128
+    for part, what, size in ((codes, "codes", rows * padded >> code),
+                             (scales, "scales", -(-rows // 128) * padded * 4)):
+        if part.dtype is not torch.uint8 or part.numel() != size or not part.is_contiguous():
             raise ValueError(f"{name}.{what} must be a contiguous uint8 tensor of {size} bytes")
-    if n.device != c.device:
+    if codes.get_device() != scales.get_device():
         raise ValueError(f"{name}: codes and scales are on different devices")
     return code
 
@@ -150,55 +169,57 @@ def mx_scales_size(rows: int, cols: int) -> int:
 
 def mx_quantize(x, fmt="e2m1", *, out=None, dev_status=None, stream=None) -> MXTensor:
     """``x`` [rows, cols] (bfloat16 or float32) as a microscaled tensor."""
-    lib = b.library()
-    code, fcode = _float_code(x, "x"), _fmt(fmt)
-    stride = _matrix(x, "x")
-    rows, cols = x.shape
+    code, fcode = _float_code(x.dtype, "x"), _fmt(fmt)
+    rows, cols, stride = _rows_of(x, "x")
+    dev, index = x.device, x.get_device()
     if out is None:
         with _on_stream(stream):
-            out = MXTensor.empty(rows, cols, fmt, x.device)
+            out = MXTensor.empty(rows, cols, fmt, dev)
     else:
         _check_mx(out, "out")
-        if (out.rows, out.cols, out.fmt) != (rows, cols, fmt) or out.codes.device != x.device:
+        if out[2:] != (rows, cols, fmt) or out.codes.get_device() != index:
             raise ValueError("out must have x's shape and device, and the format asked for")
-    _launch("mx_quantize", x.device, lib.mx_quantize, b._ptr(x), code, rows, cols, stride, fcode, b._ptr(out.codes),
-            b._ptr(out.scales), _status(dev_status, x.device), stream)
+    _launch("mx_quantize", dev, b.library().mx_quantize, x.data_ptr(), code, rows, cols, stride, fcode,
+            out.codes.data_ptr(), out.scales.data_ptr(), _status(dev_status, index), stream)
     return out
 
 
 def mx_dequantize(t: MXTensor, dtype=torch.bfloat16, *, out=None, dev_status=None, stream=None):
     """The values of a microscaled tensor, [rows, cols] in bfloat16 or float32."""
-    lib = b.library()
-    fcode = _check_mx(t, "t")
-    dev = t.codes.device
+    fcode, code = _check_mx(t, "t"), _float_code(dtype, "dtype")
+    codes, scales, rows, cols, _ = t
+    dev, index = codes.device, codes.get_device()
+    stride = cols
     if out is None:
         with _on_stream(stream):
-            out = torch.empty(t.rows, t.cols, dtype=dtype, device=dev)
-    stride = _written(out, "out", (t.rows, t.cols), dtype, dev)
-    _launch("mx_dequantize", dev, lib.mx_dequantize, b._ptr(t.codes), b._ptr(t.scales), fcode, t.rows, t.cols,
-            b._ptr(out), _float_code(out, "out"), stride, _status(dev_status, dev), stream)
+            out = torch.empty(rows, cols, dtype=dtype, device=dev)
+    else:
+        stride = _written_rows(out, "out", (rows, cols), dtype, index)
+    _launch("mx_dequantize", dev, b.library().mx_dequantize, codes.data_ptr(), scales.data_ptr(), fcode, rows, cols,
+            out.data_ptr(), code, stride, _status(dev_status, index), stream)
     return out
 
 
 def mx_linear(x: MXTensor, w: MXTensor, out_dtype=torch.bfloat16, *, out=None, dev_status=None, stream=None):
     """``x @ w.T`` of the values of x (e4m3, [n, h]) and the classifier w (e2m1, [v, h]):
     logits [n, v] in bfloat16 or float32.  dev_status is None or an int32 [1] tensor."""
-    lib = b.library()
-    _check_mx(x, "x")
-    _check_mx(w, "w")
-    dev = x.codes.device
-    if x.fmt != "e4m3" or w.fmt != "e2m1":
+    if (_check_mx(x, "x"), _check_mx(w, "w")) != (MX_E4M3, MX_E2M1):
         raise ValueError(f"x must be e4m3 and w e2m1, got {x.fmt} and {w.fmt}")
-    if x.cols != w.cols or w.rows < 1:
+    xc, xs, n, h, _ = x
+    wc, ws, v, wh, _ = w
+    dev, index = xc.device, xc.get_device()
+    if h != wh or v < 1:
         raise ValueError("x and w must share the hidden dimension, and w have rows")
-    if w.codes.device != dev:
+    if wc.get_device() != index:
         raise ValueError("x and w are on different devices")
+    code, stride = _float_code(out_dtype, "out_dtype"), v
     if out is None:
         with _on_stream(stream):
-            out = torch.empty(x.rows, w.rows, dtype=out_dtype, device=dev)
-    stride = _written(out, "out", (x.rows, w.rows), out_dtype, dev)
-    _launch("mx_linear", dev, lib.mx_linear, b._ptr(x.codes), b._ptr(x.scales), b._ptr(w.codes), b._ptr(w.scales),
-            x.rows, x.cols, w.rows, b._ptr(out), _float_code(out, "out"), stride, _status(dev_status, dev), stream)
+            out = torch.empty(n, v, dtype=out_dtype, device=dev)
+    else:
+        stride = _written_rows(out, "out", (n, v), out_dtype, index)
+    _launch("mx_linear", dev, b.library().mx_linear, xc.data_ptr(), xs.data_ptr(), wc.data_ptr(), ws.data_ptr(), n, h,
+            v, out.data_ptr(), code, stride, _status(dev_status, index), stream)
     return out
 
 
@@ -207,61 +228,63 @@ def mx_linear(x: MXTensor, w: MXTensor, out_dtype=torch.bfloat16, *, out=None, d
 # ---------------------------------------------------------------------------
 
 def _norm_inputs(x, weight, residual, h, stream):
-    code = _float_code(x, "x")
-    xs = _matrix(x, "x")
-    n, hidden = x.shape
-    if weight.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"weight must be bfloat16 or float32, got {weight.dtype}")
-    _vector(weight, "weight", hidden, weight.dtype, x.device)
-    rs = hs = hidden
-    if residual is not None:
-        rs = _matrix(residual, "residual", x.shape, x.dtype, x.device)
-        if h is None:
-            with _on_stream(stream):
-                h = torch.empty(n, hidden, dtype=x.dtype, device=x.device)
-        hs = _written(h, "h", x.shape, x.dtype, x.device)
-    elif h is not None:
-        raise ValueError("h is written only when a residual is given")
-    return code, n, hidden, xs, rs, hs, h
+    """What both norms hand to the library, and h: (code, n, hidden, x stride, residual, its stride,
+    weight code, h's pointer, its stride), device index, h."""
+    code = _float_code(x.dtype, "x")
+    n, hidden, xs = _rows_of(x, "x")
+    index = x.get_device()
+    wcode = _weight(weight, hidden, index)
+    if residual is None:
+        if h is not None:
+            raise ValueError("h is written only when a residual is given")
+        return (code, n, hidden, xs, None, hidden, weight.data_ptr(), wcode), None, hidden, index, x
+    rs, hs = _same_rows(residual, "residual", x), hidden
+    if h is None:
+        with _on_stream(stream):
+            h = torch.empty(n, hidden, dtype=x.dtype, device=x.device)
+    else:
+        hs = _written_rows(h, "h", (n, hidden), x.dtype, index)
+    return (code, n, hidden, xs, residual.data_ptr(), rs, weight.data_ptr(), wcode), h.data_ptr(), hs, index, h
 
 
 def rms_norm_forward(x, weight, eps=1e-6, residual=None, *, h=None, y=None, rstd=None, dev_status=None,
                      stream=None):
     """Norm of x + residual over the last dimension of ``x`` [n, hidden].  Returns (y, h, rstd):
     h is the rounded sum (``x`` itself without a residual), rstd FP32 [n]."""
-    lib = b.library()
-    code, n, hidden, xs, rs, hs, h = _norm_inputs(x, weight, residual, h, stream)
+    args, hp, hs, index, h = _norm_inputs(x, weight, residual, h, stream)
+    n, hidden = args[1], args[2]
+    dev, ys = x.device, hidden
     with _on_stream(stream):
         if y is None:
-            y = torch.empty(n, hidden, dtype=x.dtype, device=x.device)
+            y = torch.empty(n, hidden, dtype=x.dtype, device=dev)
+        else:
+            ys = _written_rows(y, "y", (n, hidden), x.dtype, index)
         if rstd is None:
-            rstd = torch.empty(n, dtype=torch.float32, device=x.device)
-    ys = _written(y, "y", x.shape, x.dtype, x.device)
-    _vector(rstd, "rstd", n, torch.float32, x.device)
-    _launch("rms_norm_forward", x.device, lib.rms_norm_forward, b._ptr(x), code, n, hidden, xs, b._ptr(residual),
-            rs, b._ptr(weight), _float_code(weight, "weight"), float(eps), b._ptr(h), hs, b._ptr(y), ys,
-            b._ptr(rstd), _status(dev_status, x.device), stream)
-    return RMSNormForward(y, x if h is None else h, rstd)
+            rstd = torch.empty(n, dtype=torch.float32, device=dev)
+        else:
+            _vector(rstd, "rstd", n, torch.float32, index)
+    _launch("rms_norm_forward", dev, b.library().rms_norm_forward, x.data_ptr(), *args, eps, hp, hs, y.data_ptr(), ys,
+            rstd.data_ptr(), _status(dev_status, index), stream)
+    return RMSNormForward(y, h, rstd)
 
 
 def rms_norm_mx(x, weight, eps=1e-6, residual=None, *, h=None, out=None, rstd=None, dev_status=None, stream=None):
     """rms_norm_forward with y as an E4M3 microscaled tensor, mx_linear's input.  Returns
     (y: MXTensor, h, rstd); rstd only when a tensor is passed for it."""
-    lib = b.library()
-    code, n, hidden, xs, rs, hs, h = _norm_inputs(x, weight, residual, h, stream)
+    args, hp, hs, index, h = _norm_inputs(x, weight, residual, h, stream)
+    n, hidden = args[1], args[2]
     if out is None:
         with _on_stream(stream):
             out = MXTensor.empty(n, hidden, "e4m3", x.device)
     else:
         _check_mx(out, "out")
-        if (out.rows, out.cols, out.fmt) != (n, hidden, "e4m3") or out.codes.device != x.device:
+        if out[2:] != (n, hidden, "e4m3") or out.codes.get_device() != index:
             raise ValueError("out must be an e4m3 tensor of x's shape and device")
     if rstd is not None:
-        _vector(rstd, "rstd", n, torch.float32, x.device)
-    _launch("rms_norm_mx", x.device, lib.rms_norm_mx, b._ptr(x), code, n, hidden, xs, b._ptr(residual), rs,
-            b._ptr(weight), _float_code(weight, "weight"), float(eps), b._ptr(h), hs, b._ptr(out.codes),
-            b._ptr(out.scales), b._ptr(rstd), _status(dev_status, x.device), stream)
-    return RMSNormMX(out, x if h is None else h, rstd)
+        _vector(rstd, "rstd", n, torch.float32, index)
+    _launch("rms_norm_mx", x.device, b.library().rms_norm_mx, x.data_ptr(), *args, eps, hp, hs, out.codes.data_ptr(),
+            out.scales.data_ptr(), b._ptr(rstd), _status(dev_status, index), stream)
+    return RMSNormMX(out, h, rstd)
 
 
 def rms_norm_workspace_size(n: int, hidden: int) -> int:
@@ -273,30 +296,31 @@ def rms_norm_backward(dy, h, weight, rstd, dh=None, *, dx=None, dweight=None, wo
     """Backward of rms_norm_forward.  Returns (dx, dweight): dx is the gradient of x and of the
     residual; ``dh`` is the gradient that reaches h by another way."""
     lib = b.library()
-    dev = dy.device
-    code = _float_code(dy, "dy")
-    gs = _matrix(dy, "dy")
-    n, hidden = dy.shape
-    hs = _matrix(h, "h", dy.shape, dy.dtype, dev)
-    ds = hidden if dh is None else _matrix(dh, "dh", dy.shape, dy.dtype, dev)
-    if weight.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"weight must be bfloat16 or float32, got {weight.dtype}")
-    _vector(weight, "weight", hidden, weight.dtype, dev)
-    _vector(rstd, "rstd", n, torch.float32, dev)
+    dev, index = dy.device, dy.get_device()
+    code = _float_code(dy.dtype, "dy")
+    n, hidden, gs = _rows_of(dy, "dy")
+    hs = _same_rows(h, "h", dy)
+    ds = hidden if dh is None else _same_rows(dh, "dh", dy)
+    wcode = _weight(weight, hidden, index)
+    _vector(rstd, "rstd", n, torch.float32, index)
+    xs = hidden
     with _on_stream(stream):
         if dx is None:
             dx = torch.empty(n, hidden, dtype=dy.dtype, device=dev)
+        else:
+            xs = _written_rows(dx, "dx", (n, hidden), dy.dtype, index)
         if dweight is None:
             dweight = torch.empty(hidden, dtype=weight.dtype, device=dev)
+        else:
+            _vector(dweight, "dweight", hidden, weight.dtype, index)
         if workspace is None:
             size = b._on(dev, lib.rms_norm_workspace_size, n, hidden)
-            workspace = torch.empty(max(1, size), dtype=torch.uint8, device=dev)
-    xs = _written(dx, "dx", dy.shape, dy.dtype, dev)
-    _vector(dweight, "dweight", hidden, weight.dtype, dev)
-    _launch("rms_norm_backward", dev, lib.rms_norm_backward, b._ptr(dy), code, n, hidden, gs, b._ptr(h), hs,
-            b._ptr(weight), _float_code(weight, "weight"), b._ptr(rstd), b._ptr(dh), ds, b._ptr(dx), xs,
-            b._ptr(dweight), b._ptr(workspace), workspace.numel() * workspace.element_size(),
-            _status(dev_status, dev), stream)
+            workspace = torch.empty(size or 1, dtype=torch.uint8, device=dev)
+        elif workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+    _launch("rms_norm_backward", dev, lib.rms_norm_backward, dy.data_ptr(), code, n, hidden, gs, h.data_ptr(), hs,
+            weight.data_ptr(), wcode, rstd.data_ptr(), b._ptr(dh), ds, dx.data_ptr(), xs, dweight.data_ptr(),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), _status(dev_status, index), stream)
     return RMSNormBackward(dx, dweight)
 
 
@@ -304,12 +328,12 @@ def rms_norm_backward(dy, h, weight, rstd, dh=None, *, dx=None, dweight=None, wo
 # sampling
 # ---------------------------------------------------------------------------
 
-def _per_row(value, name, n, dtype, device):
+def _per_row(value, name, n, dtype, index, device):
     """A sampling parameter: None, a number for all rows, or a tensor with one entry per row."""
     if value is None:
         return None
     if isinstance(value, torch.Tensor):
-        return _vector(value, name, n, dtype, device)
+        return _vector(value, name, n, dtype, index)
     return torch.full((n,), value, dtype=dtype, device=device)
 
 
@@ -319,34 +343,35 @@ def ce_sample(logits, uniform, temperature=None, top_k=None, top_p=None, min_p=N
     [0, 1), one per row).  temperature, top_p, min_p (float32) and top_k (int32) are None, a
     number, or a tensor with one entry per row.  Returns (token int64, logprob, dev_status), the
     first two shaped like the leading dimensions; logprob is the logarithm of the probability
-    the token was drawn with.  A row from which nothing can be drawn gives -1 and NaN."""
-    lib = b.library()
-    dev = logits.device
-    code = _float_code(logits, "logits")
+    the token was drawn with.  A row from which nothing can be drawn gives -1 and NaN, and sets
+    a bit of ``dev_status`` (int32 [1]) where one is passed."""
+    dev, index = logits.device, logits.get_device()
+    code = _float_code(logits.dtype, "logits")
     n, vocab, stride = b._rows_view(logits)
     lead = logits.shape[:-1]
-    _vector(uniform, "uniform", n, torch.float32, dev)
+    _vector(uniform, "uniform", n, torch.float32, index)
     with _on_stream(stream):
-        temperature = _per_row(temperature, "temperature", n, torch.float32, dev)
-        top_k = _per_row(top_k, "top_k", n, torch.int32, dev)
-        top_p = _per_row(top_p, "top_p", n, torch.float32, dev)
-        min_p = _per_row(min_p, "min_p", n, torch.float32, dev)
+        temperature = _per_row(temperature, "temperature", n, torch.float32, index, dev)
+        top_k = _per_row(top_k, "top_k", n, torch.int32, index, dev)
+        top_p = _per_row(top_p, "top_p", n, torch.float32, index, dev)
+        min_p = _per_row(min_p, "min_p", n, torch.float32, index, dev)
         if token is None:
             token = torch.empty(lead, dtype=torch.int64, device=dev)
+        else:
+            _vector(token, "token", n, torch.int64, index)
         if logprob is None:
             logprob = torch.empty(lead, dtype=torch.float32, device=dev)
-        if dev_status is None:
-            dev_status = torch.zeros(1, dtype=torch.int32, device=dev)
-    _vector(token, "token", n, torch.int64, dev)
-    _vector(logprob, "logprob", n, torch.float32, dev)
-    _launch("ce_sample", dev, lib.ce_sample, b._ptr(logits), code, n, vocab, stride, b._ptr(uniform),
-            b._ptr(temperature), b._ptr(top_k), b._ptr(top_p), b._ptr(min_p), b._ptr(token), b._ptr(logprob),
-            _status(dev_status, dev), stream)
+        else:
+            _vector(logprob, "logprob", n, torch.float32, index)
+    ptr = b._ptr
+    _launch("ce_sample", dev, b.library().ce_sample, logits.data_ptr(), code, n, vocab, stride, uniform.data_ptr(),
+            ptr(temperature), ptr(top_k), ptr(top_p), ptr(min_p), token.data_ptr(), logprob.data_ptr(),
+            _status(dev_status, index), stream)
     return CESample(token, logprob, dev_status)
 
 
 def linear_sample(embeddings, classifier: MXTensor, uniform, temperature=None, top_k=None, top_p=None, min_p=None, *,
-                  norm_weight=None, norm_eps=1e-6, residual=None, stream=None):
+                  norm_weight=None, norm_eps=1e-6, residual=None, dev_status=None, stream=None):
     """The next token after ``embeddings`` [..., H], the counterpart of linear_cross_entropy when a
     model answers: the norm (with ``norm_weight`` [H]; plus ``residual``) in 8 bits, the product
     with the 4-bit ``classifier``, and ce_sample of the logits.  Returns ce_sample's results."""
@@ -359,6 +384,6 @@ def linear_sample(embeddings, classifier: MXTensor, uniform, temperature=None, t
         raise ValueError("residual is added by the norm: it needs norm_weight")
     else:
         q = mx_quantize(x, "e4m3", stream=stream)
-    logits = mx_linear(q, classifier, torch.float32, stream=stream)
-    r = ce_sample(logits, uniform, temperature, top_k, top_p, min_p, stream=stream)
-    return CESample(r.token.view(lead), r.logprob.view(lead), r.dev_status)
+    logits = mx_linear(q, classifier, torch.float32, dev_status=dev_status, stream=stream)
+    r = ce_sample(logits, uniform, temperature, top_k, top_p, min_p, dev_status=dev_status, stream=stream)
+    return CESample(r.token.view(lead), r.logprob.view(lead), dev_status)
