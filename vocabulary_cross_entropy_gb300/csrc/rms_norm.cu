@@ -21,6 +21,8 @@
 #include "mx_format.cuh"
 
 #include <math.h>
+#include <initializer_list>
+#include <mutex>
 
 namespace vce {
 namespace {
@@ -350,6 +352,110 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_backward_rows(const Norm
         if (VCE_BOUNDS(int(blockIdx.x) < a.parts, a.dev_status)) out[c] = sum[c];
 }
 
+__device__ __forceinline__ void copy16_async(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src)
+                 : "memory");
+}
+
+// The same for 16-byte aligned rows of one block each, with the loads of the next kStages
+// - 1 rows in flight: a thread copies its own vectors to its own slots of shared memory
+// and reads them back itself, so the ring needs no barrier.
+template <typename T, int NV, int kStages>
+__global__ void __launch_bounds__(kMaxThreads) rms_norm_backward_ring(const NormBwdArgs a) {
+    constexpr int VE = 16 / sizeof(T);
+    using V = Vec<T, VE>;
+    extern __shared__ __align__(16) uint8_t ring_raw[];
+    float* slots = reinterpret_cast<float*>(ring_raw);        // [2][32]
+    V* ring = reinterpret_cast<V*>(ring_raw + 64 * sizeof(float));  // [kStages][streams][NV][threads]
+    const int t = threadIdx.x, tpr = blockDim.x, streams = a.dh ? 3 : 2;
+    const int stage_vecs = streams * NV * tpr;
+    float acc[NV][VE];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < VE; ++i) acc[j][i] = 0.f;
+    auto prefetch = [&](int64_t row, int stage) {
+        if (row < a.n) {
+            const T* dy = static_cast<const T*>(a.dy) + row * a.dy_stride;
+            const T* h = static_cast<const T*>(a.h) + row * a.h_stride;
+            const T* dh = static_cast<const T*>(a.dh) + row * a.dh_stride;
+            V* dst = ring + stage * stage_vecs + t;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int64_t col = int64_t(j * tpr + t) * VE;
+                if (col < a.hidden && VCE_BOUNDS(aligned16(dy + col) && aligned16(h + col), a.dev_status)) {
+                    copy16_async(dst + j * tpr, dy + col);
+                    copy16_async(dst + (NV + j) * tpr, h + col);
+                    if (streams == 3) copy16_async(dst + (2 * NV + j) * tpr, dh + col);
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");  // one group per row, empty past the end
+    };
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) prefetch(int64_t(blockIdx.x) + int64_t(s) * gridDim.x, s);
+    const float inv_h = 1.f / float(a.hidden);
+    int stage = 0, parity = 0;
+    for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
+        // the slots of the row before this one have been read (by this thread)
+        prefetch(row + int64_t(kStages - 1) * gridDim.x, stage == 0 ? kStages - 1 : stage - 1);
+        const float r = a.rstd[row];
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        const V* src = ring + stage * stage_vecs + t;
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int64_t col = int64_t(j * tpr + t) * VE;
+            if (col < a.hidden) {
+                const V vg = src[j * tpr], vh = src[(NV + j) * tpr];
+                float w[VE];
+                load_weight<VE>(a.weight, a.w_f32, col, w);
+#pragma unroll
+                for (int i = 0; i < VE; ++i) {
+                    const float hat = to_f(vh.e[i]) * r, d = to_f(vg.e[i]);
+                    acc[j][i] = fmaf(d, hat, acc[j][i]);
+                    s = fmaf(d * w[i], hat, s);
+                }
+            }
+        }
+        s = row_sum(s, tpr, slots + parity * 32) * inv_h;
+        parity ^= 1;
+        T* dx = static_cast<T*>(a.dx) + row * a.dx_stride;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int64_t col = int64_t(j * tpr + t) * VE;
+            if (col < a.hidden) {
+                const V vg = src[j * tpr], vh = src[(NV + j) * tpr];
+                float w[VE];
+                load_weight<VE>(a.weight, a.w_f32, col, w);
+                V o, ve;
+                if (streams == 3) ve = src[(2 * NV + j) * tpr];
+#pragma unroll
+                for (int i = 0; i < VE; ++i) {
+                    const float hat = to_f(vh.e[i]) * r;
+                    float d = r * (to_f(vg.e[i]) * w[i] - hat * s);
+                    if (streams == 3) d += to_f(ve.e[i]);
+                    o.e[i] = from_f<T>(d);
+                }
+                if (VCE_BOUNDS(col >= 0 && col + VE <= a.hidden && row < a.n, a.dev_status))
+                    *reinterpret_cast<V*>(dx + col) = o;
+            }
+        }
+        if (++stage == kStages) stage = 0;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    float* out = a.part + int64_t(blockIdx.x) * a.hidden;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int64_t col = int64_t(j * tpr + t) * VE;
+        if (col < a.hidden && VCE_BOUNDS(int(blockIdx.x) < a.parts, a.dev_status))
+#pragma unroll
+            for (int i = 0; i < VE; ++i) out[col + i] = acc[j][i];
+    }
+}
+
 // Rows longer than the registers hold: dx by one block per row (after dw: dx may
 // be written over dy) ...
 template <typename T>
@@ -462,13 +568,44 @@ vce_status norm_forward(NormArgs a, int ve, cudaStream_t s, const DeviceInfo& de
     return cudaGetLastError() == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
 }
 
+constexpr int kRingStages = 3;
+constexpr size_t kRingMost = 148 << 10;  // of shared memory per block
+
+template <typename T, int NV>
+vce_status launch_ring(const NormBwdArgs& a, int threads, size_t smem, cudaStream_t s, int device) {
+    static std::mutex mu;
+    static bool ready[64];
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!ready[device]) {
+            if (cudaFuncSetAttribute(rms_norm_backward_ring<T, NV, kRingStages>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, int(kRingMost)) != cudaSuccess)
+                return VCE_ERR_CUDA;
+            ready[device] = true;
+        }
+    }
+    count_launch();
+    rms_norm_backward_ring<T, NV, kRingStages><<<a.parts, threads, smem, s>>>(a);
+    return cudaGetLastError() == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
+}
+
 template <typename T>
-vce_status norm_backward(NormBwdArgs a, int ve, int parts, cudaStream_t s) {
+vce_status norm_backward(NormBwdArgs a, int ve, int& parts, cudaStream_t s, const DeviceInfo& dev) {
     constexpr int kFull = 16 / sizeof(T);
     constexpr int kNv = 32 / kFull;  // 32 sums of dw per thread
     const int64_t nvec = (a.hidden + ve - 1) / ve;
     int nv = ve == kFull ? kNv : 16;
     a.parts = parts;
+    // The ring where a row is longer than 128 vectors and three stages of it fit: as many
+    // blocks as shared memory lets an SM hold, so that all run at once.
+    const int threads = nvec > 512 ? 512 : 256;
+    const size_t ring = 64 * sizeof(float) + size_t(kRingStages) * (a.dh ? 3 : 2) * 2 * threads * 16;
+    if (a.n > 0 && ve == kFull && nvec > 128 && nvec <= 2 * threads && ring <= kRingMost) {
+        const int64_t fit = int64_t(dev.num_sms) * int64_t((228 << 10) / (ring + 1024));
+        if (parts > fit) parts = int(fit);
+        a.parts = parts;
+        return launch_ring<T, 2>(a, threads, ring, s, dev.ordinal);
+    }
     if (a.n > 0 && nvec > int64_t(kMaxThreads) * nv) {
         count_launch();  // dw first: dx may be written over dy
         rms_norm_dweight_long<T><<<dim3(unsigned((a.hidden + 255) / 256), unsigned(parts)), 256, 0, s>>>(a);
@@ -533,12 +670,12 @@ vce_status launch_rms_norm_backward(const void* dy, const void* h, const void* w
     a.n = n; a.hidden = hidden; a.dy_stride = dy_stride; a.h_stride = h_stride; a.dh_stride = dh_stride;
     a.dx_stride = dx_stride; a.dx = dx; a.part = static_cast<float*>(ws); a.dev_status = dev_status;
     const size_t es = dtype == VCE_BF16 ? 2 : 4;
-    const int parts = rms_norm_parts(n, dev.num_sms);
+    int parts = rms_norm_parts(n, dev.num_sms);
     const int ve = n == 0 ? 1
                           : pick_ve(int(16 / es), hidden, es, {dy, h, dh ? dh : h, dx},
                                     {dy_stride, h_stride, dh ? dh_stride : 0, dx_stride}, weight, a.w_f32);
-    vce_status st = dtype == VCE_BF16 ? norm_backward<__nv_bfloat16>(a, ve, parts, s)
-                                      : norm_backward<float>(a, ve, parts, s);
+    vce_status st = dtype == VCE_BF16 ? norm_backward<__nv_bfloat16>(a, ve, parts, s, dev)
+                                      : norm_backward<float>(a, ve, parts, s, dev);
     if (st) return st;
     count_launch();
     rms_norm_dweight_sum<<<unsigned((hidden + 31) / 32), 256, 0, s>>>(a.part, parts, hidden, dweight, a.w_f32);
