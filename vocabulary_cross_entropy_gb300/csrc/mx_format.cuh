@@ -16,9 +16,6 @@
 
 #include "vce_internal.cuh"
 
-#include <cuda_fp4.h>
-#include <cuda_fp8.h>
-
 namespace vce {
 namespace mx {
 
@@ -56,11 +53,44 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
     return __uint_as_float(byte == 0 ? 0x00400000u : byte << 23);
 }
 
+// Two values as codes, the first in the low bits: round to nearest even, saturating.
+// (The conversion instructions by name: the toolkit's wrappers cost several times as many
+// instructions, which at eight columns per thread was what bound the quantisation.)
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-    return uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3));
+    uint16_t c;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(hi), "f"(lo));
+    return c;
 }
 __device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
-    return uint32_t(__nv_cvt_float2_to_fp4x2(make_float2(lo, hi), __NV_E2M1, cudaRoundNearest));
+    uint32_t c;
+    asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u32.u8 %0, t;\n\t}"
+        : "=r"(c)
+        : "f"(hi), "f"(lo));
+    return c;
+}
+
+// max(m, |x|) that keeps a NaN
+__device__ __forceinline__ float max_abs(float m, float x) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(x)));
+    return r;
+}
+
+// Decoding by bits: a code's exponent and mantissa put at the same places of a BF16 are
+// the value times 2^-126 (E2M1, exponent bias 1) or 2^-120 (E4M3, bias 7), subnormals
+// among them.  Two codes (bits 0-3 and 4-7, or 0-7 and 8-15 of ``c``) to a BF16 pair:
+template <int kFmt>
+__device__ __forceinline__ uint32_t decode_pair(uint32_t c) {
+    if (kFmt == VCE_MX_E2M1) {
+        const uint32_t t = (c & 0xfu) | (c & 0xf0u) << 12;
+        return (t & 0x00070007u) << 6 | (t & 0x00080008u) << 12;
+    }
+    const uint32_t t = (c & 0xffu) | (c & 0xff00u) << 8;
+    return (t & 0x007f007fu) << 4 | (t & 0x00800080u) << 8;
+}
+template <int kFmt>
+__device__ __forceinline__ float decode_factor() {
+    return kFmt == VCE_MX_E2M1 ? 0x1p126f : 0x1p120f;
 }
 
 }  // namespace mx

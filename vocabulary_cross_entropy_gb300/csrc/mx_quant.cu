@@ -10,82 +10,116 @@ namespace vce {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kUnroll = 4;
 
 struct QuantArgs {
     const void* x;
     int64_t rows, cols, stride, padded, rows_padded;
     uint8_t *codes, *scales;
-    int vector_ok;  // rows start 16-byte aligned and cols is a multiple of 8
     int tpr;        // threads per row: a power of two, 16 .. kThreads
     int* dev_status;
 };
 
+// Eight columns as loaded.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&v)[8]);
+struct Raw8;
 template <>
-__device__ __forceinline__ void load8<float>(const float* p, float (&v)[8]) {
-    const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&v)[8]) {
-    const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
-    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(u[i] << 16);
-        v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+struct Raw8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = __ldcs(reinterpret_cast<const float4*>(p));
+        b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
     }
-}
-__device__ __forceinline__ float load1(const float* p) { return *p; }
-__device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+    __device__ __forceinline__ void load_some(const float* p, int n) {  // the first n, then zeros
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = k < n ? p[k] : 0.f;
+        a = make_float4(v[0], v[1], v[2], v[3]);
+        b = make_float4(v[4], v[5], v[6], v[7]);
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+};
+template <>
+struct Raw8<__nv_bfloat16> {
+    uint4 a;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = __ldcs(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void load_some(const __nv_bfloat16* p, int n) {
+        const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            w[k] = (2 * k < n ? uint32_t(q[2 * k]) : 0u) | (2 * k + 1 < n ? uint32_t(q[2 * k + 1]) : 0u) << 16;
+        a = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(u[i] << 16);
+            v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
+    }
+};
 
-// One thread per eight columns and step; ``tpr`` threads walk one row.  The grid covers the
-// scale rows that fill the last tile too.
-template <typename T, int kFmt>
+// One thread per eight columns and step, kUnroll steps loaded ahead; ``tpr`` threads walk
+// one row.  The grid covers the scale rows that fill the last tile too.
+template <typename T, int kFmt, bool kVector>
 __global__ void __launch_bounds__(kThreads) mx_quantize_kernel(const QuantArgs a) {
     const int units = int(a.padded / 8);  // per row, a multiple of 16: half warps share a scale tile
     const int64_t row = int64_t(blockIdx.x) * (kThreads / a.tpr) + threadIdx.x / a.tpr;
     if (row >= a.rows_padded) return;
-    const bool live = row < a.rows;
-    const T* x = static_cast<const T*>(a.x) + row * a.stride;
-    const int64_t tile_row = mx::scale_offset(row, 0, a.padded / mx::kColTile);
-#pragma unroll 2
-    for (int u = threadIdx.x % a.tpr; u < units; u += a.tpr) {  // whole half warps
-        const int col = u * 8;
-        float v[8];
-        if (live && a.vector_ok && col < a.cols) {
-            load8<T>(x + col, v);
-        } else {
+    const int cols = row < a.rows ? int(a.cols) : 0;
+    const T* x = static_cast<const T*>(a.x) + (cols ? row : 0) * a.stride;
+    uint8_t* codes = a.codes + row * (kFmt == VCE_MX_E4M3 ? a.padded : a.padded / 2);
+    uint8_t* scales = a.scales + mx::scale_offset(row, 0, a.padded / mx::kColTile);
+    const unsigned lanes = 0xffffu << (threadIdx.x & 16);
+    for (int u0 = threadIdx.x % a.tpr; u0 < units; u0 += kUnroll * a.tpr) {  // whole half warps
+        Raw8<T> raw[kUnroll];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = live && col + k < a.cols ? load1(x + col + k) : 0.f;
+        for (int k = 0; k < kUnroll; ++k) {
+            const int col = (u0 + k * a.tpr) * 8;
+            if (kVector) {
+                if (col < cols) raw[k].load(x + col);
+                else raw[k].load_some(x, 0);
+            } else {
+                raw[k].load_some(x + col, cols - col);
+            }
         }
-        uint32_t m = 0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(v[k]) & 0x7fffffffu);
-        const unsigned lanes = 0xffffu << (threadIdx.x & 16);
-        m = max(m, __shfl_xor_sync(lanes, m, 1));
-        m = max(m, __shfl_xor_sync(lanes, m, 2));
-        const uint32_t sb = mx::scale_byte<kFmt>(m);
-        const bool bad = sb == mx::kNanScale;
-        const float inv = bad ? 0.f : mx::inverse_scale(sb);
-        // the four scales of a tile's row as one word
-        uint32_t word = sb | __shfl_down_sync(lanes, sb, 4, 16) << 8;
-        word |= __shfl_down_sync(lanes, word, 8, 16) << 16;
-        if ((threadIdx.x & 15) == 0 && VCE_BOUNDS(col % mx::kColTile == 0 && col < a.padded, a.dev_status))
-            *reinterpret_cast<uint32_t*>(a.scales + tile_row + int64_t(col / mx::kColTile) * mx::kTileBytes) = word;
-        if (!live || !VCE_BOUNDS(row >= 0 && col + 8 <= a.padded, a.dev_status)) continue;
-        if (kFmt == VCE_MX_E4M3) {
-            uint32_t c[4];
+        for (int k = 0; k < kUnroll; ++k) {
+            const int u = u0 + k * a.tpr, col = u * 8;
+            if (u >= units) break;
+            float v[8];
+            raw[k].get(v);
+            float top = 0.f;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) c[k] = bad ? 0u : mx::e4m3x2(v[2 * k] * inv, v[2 * k + 1] * inv);
-            *reinterpret_cast<uint2*>(a.codes + row * a.padded + col) =
-                make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
-        } else {
-            uint32_t c = 0;
+            for (int i = 0; i < 8; ++i) top = mx::max_abs(top, v[i]);
+            uint32_t m = __float_as_uint(top);  // bits order magnitudes, a NaN above all
+            m = max(m, __shfl_xor_sync(lanes, m, 1));
+            m = max(m, __shfl_xor_sync(lanes, m, 2));
+            const uint32_t sb = mx::scale_byte<kFmt>(m);
+            const bool bad = sb == mx::kNanScale;
+            const float inv = mx::inverse_scale(bad ? 0u : sb);
+            // the four scales of a tile's row as one word
+            uint32_t word = sb | __shfl_down_sync(lanes, sb, 4, 16) << 8;
+            word |= __shfl_down_sync(lanes, word, 8, 16) << 16;
+            if ((threadIdx.x & 15) == 0 && VCE_BOUNDS(col % mx::kColTile == 0 && col < a.padded, a.dev_status))
+                *reinterpret_cast<uint32_t*>(scales + (col / mx::kColTile) * mx::kTileBytes) = word;
+            if (row >= a.rows || !VCE_BOUNDS(row >= 0 && col + 8 <= a.padded, a.dev_status)) continue;
+            if (kFmt == VCE_MX_E4M3) {
+                uint32_t c[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) c |= (bad ? 0u : mx::e2m1x2(v[2 * k] * inv, v[2 * k + 1] * inv)) << (8 * k);
-            *reinterpret_cast<uint32_t*>(a.codes + (row * a.padded + col) / 2) = c;
+                for (int i = 0; i < 4; ++i) c[i] = mx::e4m3x2(v[2 * i] * inv, v[2 * i + 1] * inv);
+                const uint2 w = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+                *reinterpret_cast<uint2*>(codes + col) = bad ? make_uint2(0, 0) : w;
+            } else {
+                uint32_t c = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) c |= mx::e2m1x2(v[2 * i] * inv, v[2 * i + 1] * inv) << (8 * i);
+                *reinterpret_cast<uint32_t*>(codes + col / 2) = bad ? 0u : c;
+            }
         }
     }
 }
@@ -94,7 +128,6 @@ struct DequantArgs {
     const uint8_t *codes, *scales;
     int64_t rows, cols, stride, padded;
     void* out;
-    int vector_ok;
     int tpr;
     int* dev_status;
 };
@@ -117,53 +150,58 @@ __device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float
 
 // A value of either format fits 4 significant bits, so its product with the scale is
 // exact in FP32, and in BF16 unless it is subnormal there.
-template <typename T, int kFmt>
+template <typename T, int kFmt, bool kVector>
 __global__ void __launch_bounds__(kThreads) mx_dequantize_kernel(const DequantArgs a) {
-    const int units = int((a.cols + 7) / 8);
+    const int cols = int(a.cols), units = (cols + 7) / 8;
     const int64_t row = int64_t(blockIdx.x) * (kThreads / a.tpr) + threadIdx.x / a.tpr;
     if (row >= a.rows) return;
+    const uint8_t* codes = a.codes + row * (kFmt == VCE_MX_E4M3 ? a.padded : a.padded / 2);
     const uint8_t* scales = a.scales + mx::scale_offset(row, 0, a.padded / mx::kColTile);
     T* out = static_cast<T*>(a.out) + row * a.stride;
-#pragma unroll 2
-    for (int u = threadIdx.x % a.tpr; u < units; u += a.tpr) {
-        const int col = u * 8;
-        if (!VCE_BOUNDS(row >= 0 && col + 8 <= a.padded, a.dev_status)) continue;
-        const float s = mx::scale_value(scales[(col / mx::kColTile) * mx::kTileBytes + (col / mx::kBlock & 3)]);
-        float v[8];
-        if (kFmt == VCE_MX_E4M3) {
-            const uint2 c = __ldcs(reinterpret_cast<const uint2*>(a.codes + row * a.padded + col));
+    for (int u0 = threadIdx.x % a.tpr; u0 < units; u0 += kUnroll * a.tpr) {
+        uint2 c[kUnroll];
+        uint32_t sb[kUnroll];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t w = (k < 2 ? c.x : c.y) >> (16 * (k & 1));
-                const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w & 0xffff), __NV_E4M3);
-                const float2 f = __half22float2(__half2(h));
-                v[2 * k] = f.x * s, v[2 * k + 1] = f.y * s;
-            }
-        } else {
-            const uint32_t c = __ldcs(reinterpret_cast<const uint32_t*>(a.codes + (row * a.padded + col) / 2));
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const __half2_raw h =
-                    __nv_cvt_fp4x2_to_halfraw2(__nv_fp4x2_storage_t(c >> (8 * k) & 0xff), __NV_E2M1);
-                const float2 f = __half22float2(__half2(h));
-                v[2 * k] = f.x * s, v[2 * k + 1] = f.y * s;
-            }
+        for (int k = 0; k < kUnroll; ++k) {
+            const int u = u0 + k * a.tpr, col = u * 8;
+            if (u >= units || !VCE_BOUNDS(row >= 0 && col + 8 <= a.padded, a.dev_status)) break;
+            if (kFmt == VCE_MX_E4M3) c[k] = __ldcs(reinterpret_cast<const uint2*>(codes + col));
+            else c[k].x = __ldcs(reinterpret_cast<const uint32_t*>(codes + col / 2));
+            sb[k] = scales[(col / mx::kColTile) * mx::kTileBytes + (col / mx::kBlock & 3)];
         }
-        if (a.vector_ok) {
-            store8(out + col, v);
-        } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (col + k < a.cols) store1(out + col + k, v[k]);
+        for (int k = 0; k < kUnroll; ++k) {
+            const int u = u0 + k * a.tpr, col = u * 8;
+            if (u >= units || !VCE_BOUNDS(row >= 0 && col + 8 <= a.padded, a.dev_status)) break;
+            const float s = mx::scale_value(sb[k]);
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {  // a BF16 pair of the values times 1 / decode_factor
+                const uint32_t pair =
+                    kFmt == VCE_MX_E4M3 ? mx::decode_pair<kFmt>((i < 2 ? c[k].x : c[k].y) >> (16 * (i & 1)) & 0xffffu)
+                                        : mx::decode_pair<kFmt>(c[k].x >> (8 * i) & 0xffu);
+                // the first product is exact, the second but for results below 2^-126
+                v[2 * i] = __uint_as_float(pair << 16) * mx::decode_factor<kFmt>() * s;
+                v[2 * i + 1] = __uint_as_float(pair & 0xffff0000u) * mx::decode_factor<kFmt>() * s;
+            }
+            if (kVector) {
+                store8(out + col, v);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (col + i < cols) store1(out + col + i, v[i]);
+            }
         }
     }
 }
 
-// Threads per row: the least power of two that covers its units of eight columns, at
-// most a block.
+// Threads per row: few enough that a thread has several units of eight columns over
+// which its set-up is spread (two units per thread took 1.6 times as long as eight at
+// 4096 columns: the kernels were bound by instructions), at least the half warp that
+// shares a scale tile.
 int threads_per_row(int64_t units) {
     int t = 16;
-    while (t < kThreads && t < units) t *= 2;
+    while (t < kThreads && t * 8 < units) t *= 2;
     return t;
 }
 
@@ -171,23 +209,36 @@ bool vectors_fit(const void* p, int64_t cols, int64_t stride, size_t es) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && cols % 8 == 0 && (stride * int64_t(es)) % 16 == 0;
 }
 
+template <typename T, int kFmt>
+void quantize(const QuantArgs& a, bool vector, unsigned grid, cudaStream_t s) {
+    if (vector) mx_quantize_kernel<T, kFmt, true><<<grid, kThreads, 0, s>>>(a);
+    else mx_quantize_kernel<T, kFmt, false><<<grid, kThreads, 0, s>>>(a);
+}
+
+template <typename T, int kFmt>
+void dequantize(const DequantArgs& a, bool vector, unsigned grid, cudaStream_t s) {
+    if (vector) mx_dequantize_kernel<T, kFmt, true><<<grid, kThreads, 0, s>>>(a);
+    else mx_dequantize_kernel<T, kFmt, false><<<grid, kThreads, 0, s>>>(a);
+}
+
 }  // namespace
 
 vce_status launch_mx_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int64_t stride, int fmt,
                               uint8_t* codes, uint8_t* scales, int* dev_status, cudaStream_t s) {
     if (rows == 0) return VCE_OK;
-    QuantArgs a{x, rows, cols, stride, mx::padded(cols), mx::padded(rows), codes, scales, 0, 0, dev_status};
-    a.vector_ok = vectors_fit(x, cols, stride, dtype == VCE_BF16 ? 2 : 4);
-    a.tpr = threads_per_row(a.padded / 8);
+    const int64_t padded = mx::padded(cols);
+    const QuantArgs a{x, rows, cols, stride, padded, mx::padded(rows), codes, scales, threads_per_row(padded / 8),
+                      dev_status};
+    const bool vec = vectors_fit(x, cols, stride, dtype == VCE_BF16 ? 2 : 4);
     const int per = kThreads / a.tpr;
     const unsigned g = unsigned((a.rows_padded + per - 1) / per);
     count_launch();
     if (dtype == VCE_BF16) {
-        if (fmt == VCE_MX_E4M3) mx_quantize_kernel<__nv_bfloat16, VCE_MX_E4M3><<<g, kThreads, 0, s>>>(a);
-        else mx_quantize_kernel<__nv_bfloat16, VCE_MX_E2M1><<<g, kThreads, 0, s>>>(a);
+        if (fmt == VCE_MX_E4M3) quantize<__nv_bfloat16, VCE_MX_E4M3>(a, vec, g, s);
+        else quantize<__nv_bfloat16, VCE_MX_E2M1>(a, vec, g, s);
     } else {
-        if (fmt == VCE_MX_E4M3) mx_quantize_kernel<float, VCE_MX_E4M3><<<g, kThreads, 0, s>>>(a);
-        else mx_quantize_kernel<float, VCE_MX_E2M1><<<g, kThreads, 0, s>>>(a);
+        if (fmt == VCE_MX_E4M3) quantize<float, VCE_MX_E4M3>(a, vec, g, s);
+        else quantize<float, VCE_MX_E2M1>(a, vec, g, s);
     }
     return cudaGetLastError() == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
 }
@@ -195,18 +246,18 @@ vce_status launch_mx_quantize(const void* x, int dtype, int64_t rows, int64_t co
 vce_status launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int fmt, int64_t rows, int64_t cols,
                                 void* out, int dtype, int64_t stride, int* dev_status, cudaStream_t s) {
     if (rows == 0) return VCE_OK;
-    DequantArgs a{codes, scales, rows, cols, stride, mx::padded(cols), out, 0, 0, dev_status};
-    a.vector_ok = vectors_fit(out, cols, stride, dtype == VCE_BF16 ? 2 : 4);
-    a.tpr = threads_per_row((cols + 7) / 8);
+    const DequantArgs a{codes, scales, rows, cols, stride, mx::padded(cols), out, threads_per_row((cols + 7) / 8),
+                        dev_status};
+    const bool vec = vectors_fit(out, cols, stride, dtype == VCE_BF16 ? 2 : 4);
     const int per = kThreads / a.tpr;
     const unsigned g = unsigned((rows + per - 1) / per);
     count_launch();
     if (dtype == VCE_BF16) {
-        if (fmt == VCE_MX_E4M3) mx_dequantize_kernel<__nv_bfloat16, VCE_MX_E4M3><<<g, kThreads, 0, s>>>(a);
-        else mx_dequantize_kernel<__nv_bfloat16, VCE_MX_E2M1><<<g, kThreads, 0, s>>>(a);
+        if (fmt == VCE_MX_E4M3) dequantize<__nv_bfloat16, VCE_MX_E4M3>(a, vec, g, s);
+        else dequantize<__nv_bfloat16, VCE_MX_E2M1>(a, vec, g, s);
     } else {
-        if (fmt == VCE_MX_E4M3) mx_dequantize_kernel<float, VCE_MX_E4M3><<<g, kThreads, 0, s>>>(a);
-        else mx_dequantize_kernel<float, VCE_MX_E2M1><<<g, kThreads, 0, s>>>(a);
+        if (fmt == VCE_MX_E4M3) dequantize<float, VCE_MX_E4M3>(a, vec, g, s);
+        else dequantize<float, VCE_MX_E2M1>(a, vec, g, s);
     }
     return cudaGetLastError() == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
 }

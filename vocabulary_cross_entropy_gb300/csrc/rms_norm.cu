@@ -98,9 +98,10 @@ struct NormArgs {
 template <int VE>
 __device__ __forceinline__ void store_mx(const NormArgs& a, int64_t row, int64_t col, const float (&y)[VE]) {
     constexpr int kLanes = mx::kBlock / VE;
-    uint32_t m = 0;
+    float top = 0.f;
 #pragma unroll
-    for (int i = 0; i < VE; ++i) m = max(m, __float_as_uint(y[i]) & 0x7fffffffu);
+    for (int i = 0; i < VE; ++i) top = mx::max_abs(top, y[i]);
+    uint32_t m = __float_as_uint(top);
 #pragma unroll
     for (int o = 1; o < kLanes; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     const uint32_t sb = mx::scale_byte<VCE_MX_E4M3>(m);
