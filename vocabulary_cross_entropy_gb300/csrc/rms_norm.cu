@@ -43,6 +43,44 @@ __device__ __forceinline__ float from_f<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
+// A vector's values as FP32, and back (BF16: two values per conversion instruction).
+template <int VE>
+__device__ __forceinline__ void unpack(const Vec<float, VE>& v, float (&f)[VE]) {
+#pragma unroll
+    for (int i = 0; i < VE; ++i) f[i] = v.e[i];
+}
+template <int VE>
+__device__ __forceinline__ void unpack(const Vec<__nv_bfloat16, VE>& v, float (&f)[VE]) {
+    if constexpr (VE == 1) {
+        f[0] = to_f(v.e[0]);
+    } else {
+        const uint32_t* u = reinterpret_cast<const uint32_t*>(&v);
+#pragma unroll
+        for (int i = 0; i < VE / 2; ++i) {
+            f[2 * i] = __uint_as_float(u[i] << 16);
+            f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
+    }
+}
+template <int VE>
+__device__ __forceinline__ void pack(const float (&f)[VE], Vec<float, VE>& v) {
+#pragma unroll
+    for (int i = 0; i < VE; ++i) v.e[i] = f[i];
+}
+template <int VE>
+__device__ __forceinline__ void pack(const float (&f)[VE], Vec<__nv_bfloat16, VE>& v) {
+    if constexpr (VE == 1) {
+        v.e[0] = __float2bfloat16_rn(f[0]);
+    } else {
+        uint32_t* u = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+        for (int i = 0; i < VE / 2; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+    }
+}
+
 template <int VE>
 __device__ __forceinline__ void load_weight(const void* w, int w_f32, int64_t at, float (&out)[VE]) {
     if (w_f32) {
@@ -59,8 +97,7 @@ __device__ __forceinline__ void load_weight(const void* w, int w_f32, int64_t at
     } else {
         const Vec<__nv_bfloat16, VE> a =
             *reinterpret_cast<const Vec<__nv_bfloat16, VE>*>(static_cast<const __nv_bfloat16*>(w) + at);
-#pragma unroll
-        for (int i = 0; i < VE; ++i) out[i] = to_f(a.e[i]);
+        unpack<VE>(a, out);
     }
 }
 
@@ -93,10 +130,12 @@ struct NormArgs {
 };
 
 // The 8-bit form's stores of VE consecutive values at column ``col`` (a multiple of
-// VE).  The 32 / VE lanes that hold one block find its largest magnitude together;
-// every lane of the warp calls.
+// VE) of the row whose codes and scales start at ``codes`` and ``scales``.  The 32 / VE
+// lanes that hold one block find its largest magnitude together; every lane of the
+// warp calls.
 template <int VE>
-__device__ __forceinline__ void store_mx(const NormArgs& a, int64_t row, int64_t col, const float (&y)[VE]) {
+__device__ __forceinline__ void store_mx(const NormArgs& a, uint8_t* codes, uint8_t* scales, int col,
+                                         const float (&y)[VE]) {
     constexpr int kLanes = mx::kBlock / VE;
     float top = 0.f;
 #pragma unroll
@@ -105,27 +144,31 @@ __device__ __forceinline__ void store_mx(const NormArgs& a, int64_t row, int64_t
 #pragma unroll
     for (int o = 1; o < kLanes; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     const uint32_t sb = mx::scale_byte<VCE_MX_E4M3>(m);
-    // without a branch on the NaN code: inverse_scale of it is not used
-    const float inv = sb == mx::kNanScale ? 0.f : mx::inverse_scale(sb);
-    if (col >= a.padded) return;
     const bool bad = sb == mx::kNanScale;
-    uint8_t* dst = a.codes + row * a.padded + col;
-    if (!VCE_BOUNDS(row >= 0 && row < a.n && col >= 0 && col + VE <= a.padded, a.dev_status)) return;
+    const float inv = mx::inverse_scale(bad ? 0u : sb);
+    uint32_t word = sb;
+    if constexpr (VE >= 4) {  // a warp holds whole scale tiles: four scales to a word
+        word |= __shfl_down_sync(0xffffffffu, word, kLanes) << 8;
+        word |= __shfl_down_sync(0xffffffffu, word, 2 * kLanes) << 16;
+    }
+    if (col >= a.padded || !VCE_BOUNDS(col >= 0 && col + VE <= a.padded, a.dev_status)) return;
+    uint8_t* dst = codes + col;
     if constexpr (VE == 1) {
         *dst = bad ? 0 : uint8_t(mx::e4m3x2(y[0] * inv, 0.f) & 0xff);
     } else {
-        uint16_t c[VE / 2];
+        uint32_t c[VE / 2];
 #pragma unroll
-        for (int i = 0; i < VE / 2; ++i) c[i] = bad ? 0 : uint16_t(mx::e4m3x2(y[2 * i] * inv, y[2 * i + 1] * inv));
-        if constexpr (VE == 8)
-            *reinterpret_cast<uint2*>(dst) = make_uint2(c[0] | uint32_t(c[1]) << 16, c[2] | uint32_t(c[3]) << 16);
-        else if constexpr (VE == 4)
-            *reinterpret_cast<uint32_t*>(dst) = c[0] | uint32_t(c[1]) << 16;
-        else
-            *reinterpret_cast<uint16_t*>(dst) = c[0];
+        for (int i = 0; i < VE / 2; ++i) c[i] = bad ? 0 : mx::e4m3x2(y[2 * i] * inv, y[2 * i + 1] * inv);
+        if constexpr (VE == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+        else if constexpr (VE == 4) *reinterpret_cast<uint32_t*>(dst) = c[0] | c[1] << 16;
+        else *reinterpret_cast<uint16_t*>(dst) = uint16_t(c[0]);
     }
-    if (col % mx::kBlock == 0)
-        a.scales[mx::scale_offset(row, col / mx::kBlock, a.padded / mx::kColTile)] = uint8_t(sb);
+    uint8_t* at = scales + (col / mx::kColTile) * mx::kTileBytes;
+    if (VE >= 4) {
+        if (col % mx::kColTile == 0) *reinterpret_cast<uint32_t*>(at) = word;
+    } else if (col % mx::kBlock == 0) {
+        at[col / mx::kBlock & 3] = uint8_t(sb);
+    }
 }
 
 // Scales of the rows past the last one in the last tile.
@@ -137,6 +180,7 @@ __device__ __forceinline__ void zero_scale_row(const NormArgs& a, int64_t row, i
 // One row per ``tpr`` threads, NV vectors of VE elements per thread in registers.
 template <typename T, int VE, int NV, bool kMx>
 __global__ void __launch_bounds__(kMaxThreads) rms_norm_rows(const NormArgs a) {
+    uint8_t *codes = nullptr, *scales = nullptr;
     __shared__ float slot[32];
     const int tpr = a.tpr;
     const int t = threadIdx.x % tpr;
@@ -146,53 +190,65 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_rows(const NormArgs a) {
         return;
     }
     if (row >= a.n) return;
+    if (kMx) {
+        codes = a.codes + row * a.padded;
+        scales = a.scales + mx::scale_offset(row, 0, a.padded / mx::kColTile);
+    }
     using V = Vec<T, VE>;
+    const int hidden = int(a.hidden);
     const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
     const T* res = a.residual ? static_cast<const T*>(a.residual) + row * a.r_stride : nullptr;
     T* h = a.residual ? static_cast<T*>(a.h) + row * a.h_stride : nullptr;
     V v[NV], u[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int64_t col = int64_t(j * tpr + t) * VE;
-        if (col < a.hidden) v[j] = *reinterpret_cast<const V*>(x + col);
+        const int col = (j * tpr + t) * VE;
+        if (col < hidden) v[j] = *reinterpret_cast<const V*>(x + col);
     }
     if (res) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int64_t col = int64_t(j * tpr + t) * VE;
-            if (col < a.hidden) u[j] = *reinterpret_cast<const V*>(res + col);
+            const int col = (j * tpr + t) * VE;
+            if (col < hidden) u[j] = *reinterpret_cast<const V*>(res + col);
         }
     }
     float ss = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int64_t col = int64_t(j * tpr + t) * VE;
-        if (col < a.hidden) {
+        const int col = (j * tpr + t) * VE;
+        if (col < hidden) {
+            float f[VE];
+            unpack<VE>(v[j], f);
             if (res) {
+                float g[VE];
+                unpack<VE>(u[j], g);
 #pragma unroll
-                for (int i = 0; i < VE; ++i) v[j].e[i] = from_f<T>(to_f(v[j].e[i]) + to_f(u[j].e[i]));
+                for (int i = 0; i < VE; ++i) f[i] += g[i];
+                pack<VE>(f, v[j]);
+                unpack<VE>(v[j], f);
                 if (VCE_BOUNDS(col >= 0 && col + VE <= a.hidden && row < a.n, a.dev_status))
                     *reinterpret_cast<V*>(h + col) = v[j];
             }
 #pragma unroll
-            for (int i = 0; i < VE; ++i) ss = fmaf(to_f(v[j].e[i]), to_f(v[j].e[i]), ss);
+            for (int i = 0; i < VE; ++i) ss = fmaf(f[i], f[i], ss);
         }
     }
     ss = row_sum(ss, tpr, slot);
-    const float r = 1.f / sqrtf(ss / float(a.hidden) + a.eps);
+    const float r = __frsqrt_rn(ss / float(a.hidden) + a.eps);
     if (t == 0 && a.rstd) a.rstd[row] = r;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int64_t col = int64_t(j * tpr + t) * VE;
+        const int col = (j * tpr + t) * VE;
         float y[VE];
-        if (col < a.hidden) {
+        if (col < hidden) {
+            float f[VE];
             load_weight<VE>(a.weight, a.w_f32, col, y);
+            unpack<VE>(v[j], f);
 #pragma unroll
-            for (int i = 0; i < VE; ++i) y[i] = to_f(v[j].e[i]) * r * y[i];
+            for (int i = 0; i < VE; ++i) y[i] = f[i] * r * y[i];
             if (!kMx) {
                 V o;
-#pragma unroll
-                for (int i = 0; i < VE; ++i) o.e[i] = from_f<T>(y[i]);
+                pack<VE>(y, o);
                 if (VCE_BOUNDS(col >= 0 && col + VE <= a.hidden && row < a.n, a.dev_status))
                     *reinterpret_cast<V*>(static_cast<T*>(a.y) + row * a.y_stride + col) = o;
             }
@@ -200,7 +256,7 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_rows(const NormArgs a) {
 #pragma unroll
             for (int i = 0; i < VE; ++i) y[i] = 0.f;
         }
-        if constexpr (kMx) store_mx<VE>(a, row, col, y);
+        if constexpr (kMx) store_mx<VE>(a, codes, scales, col, y);
     }
 }
 
@@ -230,10 +286,12 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_long(const NormArgs a) {
         ss = s;
     }
     ss = row_sum(ss, blockDim.x, slot);
-    const float r = 1.f / sqrtf(ss / float(a.hidden) + a.eps);
+    const float r = __frsqrt_rn(ss / float(a.hidden) + a.eps);
     if (threadIdx.x == 0 && a.rstd) a.rstd[row] = r;
     const T* src = res ? h : x;
     const int64_t end = kMx ? a.padded : a.hidden;  // both passes give a thread the same columns
+    uint8_t* codes = a.codes + row * a.padded;
+    uint8_t* scales = a.scales + mx::scale_offset(row, 0, a.padded / mx::kColTile);
     for (int64_t c0 = 0; c0 < end; c0 += blockDim.x) {
         const int64_t col = c0 + threadIdx.x;
         float y[1] = {0.f}, w[1];
@@ -242,7 +300,7 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_long(const NormArgs a) {
             y[0] = to_f(src[col]) * r * w[0];
             if (!kMx) static_cast<T*>(a.y)[row * a.y_stride + col] = from_f<T>(y[0]);
         }
-        if constexpr (kMx) store_mx<1>(a, row, col, y);
+        if constexpr (kMx) store_mx<1>(a, codes, scales, int(col), y);
     }
 }
 
@@ -281,7 +339,7 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_backward_rows(const Norm
         V vg[NV], vh[NV], ve[NV];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int64_t col = int64_t(j * tpr + t) * VE;
+            const int col = (j * tpr + t) * VE;
             if (col < a.hidden) {
                 vg[j] = *reinterpret_cast<const V*>(dy + col);
                 vh[j] = *reinterpret_cast<const V*>(h + col);
@@ -292,15 +350,17 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_backward_rows(const Norm
         float s = 0.f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int64_t col = int64_t(j * tpr + t) * VE;
+            const int col = (j * tpr + t) * VE;
             if (col < a.hidden) {
-                float w[VE];
+                float w[VE], d[VE], f[VE];
                 load_weight<VE>(a.weight, a.w_f32, col, w);
+                unpack<VE>(vg[j], d);
+                unpack<VE>(vh[j], f);
 #pragma unroll
                 for (int i = 0; i < VE; ++i) {
-                    const float hat = to_f(vh[j].e[i]) * r, d = to_f(vg[j].e[i]);
-                    acc[j][i] = fmaf(d, hat, acc[j][i]);
-                    s = fmaf(d * w[i], hat, s);
+                    const float hat = f[i] * r;
+                    acc[j][i] = fmaf(d[i], hat, acc[j][i]);
+                    s = fmaf(d[i] * w[i], hat, s);
                 }
             }
         }
@@ -308,18 +368,21 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_backward_rows(const Norm
         parity ^= 1;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int64_t col = int64_t(j * tpr + t) * VE;
+            const int col = (j * tpr + t) * VE;
             if (col < a.hidden) {
-                float w[VE];
+                float w[VE], d[VE], f[VE];
                 load_weight<VE>(a.weight, a.w_f32, col, w);
-                V o;
+                unpack<VE>(vg[j], d);
+                unpack<VE>(vh[j], f);
 #pragma unroll
-                for (int i = 0; i < VE; ++i) {
-                    const float hat = to_f(vh[j].e[i]) * r;
-                    float d = r * (to_f(vg[j].e[i]) * w[i] - hat * s);
-                    if (dh) d += to_f(ve[j].e[i]);
-                    o.e[i] = from_f<T>(d);
+                for (int i = 0; i < VE; ++i) d[i] = r * (d[i] * w[i] - f[i] * r * s);
+                if (dh) {
+                    unpack<VE>(ve[j], f);
+#pragma unroll
+                    for (int i = 0; i < VE; ++i) d[i] += f[i];
                 }
+                V o;
+                pack<VE>(d, o);
                 if (VCE_BOUNDS(col >= 0 && col + VE <= a.hidden && row < a.n, a.dev_status))
                     *reinterpret_cast<V*>(dx + col) = o;
             }
@@ -329,7 +392,7 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_backward_rows(const Norm
     if (groups == 1) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int64_t col = int64_t(j * tpr + t) * VE;
+            const int col = (j * tpr + t) * VE;
             if (col < a.hidden && VCE_BOUNDS(int(blockIdx.x) < a.parts, a.dev_status))
 #pragma unroll
                 for (int i = 0; i < VE; ++i) out[col + i] = acc[j][i];
@@ -341,7 +404,7 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_backward_rows(const Norm
         if (g == k) {
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                const int64_t col = int64_t(j * tpr + t) * VE;
+                const int col = (j * tpr + t) * VE;
                 if (col < a.hidden)
 #pragma unroll
                     for (int i = 0; i < VE; ++i) sum[col + i] = (k == 0 ? 0.f : sum[col + i]) + acc[j][i];
@@ -385,7 +448,7 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_backward_ring(const Norm
             V* dst = ring + stage * stage_vecs + t;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                const int64_t col = int64_t(j * tpr + t) * VE;
+                const int col = (j * tpr + t) * VE;
                 if (col < a.hidden && VCE_BOUNDS(aligned16(dy + col) && aligned16(h + col), a.dev_status)) {
                     copy16_async(dst + j * tpr, dy + col);
                     copy16_async(dst + (NV + j) * tpr, h + col);
@@ -408,16 +471,18 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_backward_ring(const Norm
         float s = 0.f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int64_t col = int64_t(j * tpr + t) * VE;
+            const int col = (j * tpr + t) * VE;
             if (col < a.hidden) {
                 const V vg = src[j * tpr], vh = src[(NV + j) * tpr];
-                float w[VE];
+                float w[VE], d[VE], f[VE];
                 load_weight<VE>(a.weight, a.w_f32, col, w);
+                unpack<VE>(vg, d);
+                unpack<VE>(vh, f);
 #pragma unroll
                 for (int i = 0; i < VE; ++i) {
-                    const float hat = to_f(vh.e[i]) * r, d = to_f(vg.e[i]);
-                    acc[j][i] = fmaf(d, hat, acc[j][i]);
-                    s = fmaf(d * w[i], hat, s);
+                    const float hat = f[i] * r;
+                    acc[j][i] = fmaf(d[i], hat, acc[j][i]);
+                    s = fmaf(d[i] * w[i], hat, s);
                 }
             }
         }
@@ -426,20 +491,23 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_backward_ring(const Norm
         T* dx = static_cast<T*>(a.dx) + row * a.dx_stride;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int64_t col = int64_t(j * tpr + t) * VE;
+            const int col = (j * tpr + t) * VE;
             if (col < a.hidden) {
                 const V vg = src[j * tpr], vh = src[(NV + j) * tpr];
-                float w[VE];
+                float w[VE], d[VE], f[VE];
                 load_weight<VE>(a.weight, a.w_f32, col, w);
-                V o, ve;
-                if (streams == 3) ve = src[(2 * NV + j) * tpr];
+                unpack<VE>(vg, d);
+                unpack<VE>(vh, f);
 #pragma unroll
-                for (int i = 0; i < VE; ++i) {
-                    const float hat = to_f(vh.e[i]) * r;
-                    float d = r * (to_f(vg.e[i]) * w[i] - hat * s);
-                    if (streams == 3) d += to_f(ve.e[i]);
-                    o.e[i] = from_f<T>(d);
+                for (int i = 0; i < VE; ++i) d[i] = r * (d[i] * w[i] - f[i] * r * s);
+                if (streams == 3) {
+                    const V ve = src[(2 * NV + j) * tpr];
+                    unpack<VE>(ve, f);
+#pragma unroll
+                    for (int i = 0; i < VE; ++i) d[i] += f[i];
                 }
+                V o;
+                pack<VE>(d, o);
                 if (VCE_BOUNDS(col >= 0 && col + VE <= a.hidden && row < a.n, a.dev_status))
                     *reinterpret_cast<V*>(dx + col) = o;
             }
@@ -450,7 +518,7 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_backward_ring(const Norm
     float* out = a.part + int64_t(blockIdx.x) * a.hidden;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int64_t col = int64_t(j * tpr + t) * VE;
+        const int col = (j * tpr + t) * VE;
         if (col < a.hidden && VCE_BOUNDS(int(blockIdx.x) < a.parts, a.dev_status))
 #pragma unroll
             for (int i = 0; i < VE; ++i) out[col + i] = acc[j][i];
@@ -496,22 +564,24 @@ __global__ void __launch_bounds__(256) rms_norm_dweight_long(const NormBwdArgs a
     a.part[int64_t(blockIdx.y) * a.hidden + col] = s;
 }
 
-// dw = the sum of the partial rows, in a fixed order: 32 columns per block, 8 threads
-// per column, each over every eighth partial.
-__global__ void __launch_bounds__(256) rms_norm_dweight_sum(const float* __restrict__ part, int parts,
-                                                            int64_t hidden, void* dw, int w_f32) {
-    __shared__ float sm[8][32];
+// dw = the sum of the partial rows, in a fixed order: 32 columns per block, 32 threads
+// per column, each over every 32nd partial (8 threads per column left the loads'
+// latency exposed).
+constexpr int kSumSplit = 32;
+__global__ void __launch_bounds__(32 * kSumSplit) rms_norm_dweight_sum(const float* __restrict__ part, int parts,
+                                                                       int64_t hidden, void* dw, int w_f32) {
+    __shared__ float sm[kSumSplit][32];
     const int lc = threadIdx.x & 31, sp = threadIdx.x >> 5;
     const int64_t col = int64_t(blockIdx.x) * 32 + lc;
     float s = 0.f;
     if (col < hidden) {
 #pragma unroll 8
-        for (int p = sp; p < parts; p += 8) s += part[int64_t(p) * hidden + col];
+        for (int p = sp; p < parts; p += kSumSplit) s += part[int64_t(p) * hidden + col];
     }
     sm[sp][lc] = s;
     __syncthreads();
     if (sp != 0 || col >= hidden) return;
-    for (int k = 1; k < 8; ++k) s += sm[k][lc];
+    for (int k = 1; k < kSumSplit; ++k) s += sm[k][lc];
     if (w_f32) static_cast<float*>(dw)[col] = s;
     else static_cast<__nv_bfloat16*>(dw)[col] = __float2bfloat16_rn(s);
 }
@@ -569,7 +639,8 @@ vce_status norm_forward(NormArgs a, int ve, cudaStream_t s, const DeviceInfo& de
     return cudaGetLastError() == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
 }
 
-constexpr int kRingStages = 3;
+constexpr int kRingStages = 2;
+constexpr int kRingVecs = 2;                // vectors per thread
 constexpr size_t kRingMost = 148 << 10;  // of shared memory per block
 
 template <typename T, int NV>
@@ -597,15 +668,17 @@ vce_status norm_backward(NormBwdArgs a, int ve, int& parts, cudaStream_t s, cons
     const int64_t nvec = (a.hidden + ve - 1) / ve;
     int nv = ve == kFull ? kNv : 16;
     a.parts = parts;
-    // The ring where a row is longer than 128 vectors and three stages of it fit: as many
-    // blocks as shared memory lets an SM hold, so that all run at once.
-    const int threads = nvec > 512 ? 512 : 256;
-    const size_t ring = 64 * sizeof(float) + size_t(kRingStages) * (a.dh ? 3 : 2) * 2 * threads * 16;
-    if (a.n > 0 && ve == kFull && nvec > 128 && nvec <= 2 * threads && ring <= kRingMost) {
+    // The ring where a row is longer than 128 vectors and its stages fit: as many blocks as
+    // shared memory lets an SM hold (at most the four per SM of the workspace), so that all
+    // run at once.  Two stages: more blocks per SM beat more stages (16384 x 4096 BF16, with
+    // the sum of partials: 104 us with two stages, 112 with three, 127 with four).
+    const int threads = pow2_at_least((nvec + kRingVecs - 1) / kRingVecs);
+    const size_t ring = 64 * sizeof(float) + size_t(kRingStages) * (a.dh ? 3 : 2) * kRingVecs * threads * 16;
+    if (a.n > 0 && ve == kFull && nvec > 128 && threads <= kMaxThreads && ring <= kRingMost) {
         const int64_t fit = int64_t(dev.num_sms) * int64_t((228 << 10) / (ring + 1024));
         if (parts > fit) parts = int(fit);
         a.parts = parts;
-        return launch_ring<T, 2>(a, threads, ring, s, dev.ordinal);
+        return launch_ring<T, kRingVecs>(a, threads, ring, s, dev.ordinal);
     }
     if (a.n > 0 && nvec > int64_t(kMaxThreads) * nv) {
         count_launch();  // dw first: dx may be written over dy
@@ -679,7 +752,7 @@ vce_status launch_rms_norm_backward(const void* dy, const void* h, const void* w
                                       : norm_backward<float>(a, ve, parts, s, dev);
     if (st) return st;
     count_launch();
-    rms_norm_dweight_sum<<<unsigned((hidden + 31) / 32), 256, 0, s>>>(a.part, parts, hidden, dweight, a.w_f32);
+    rms_norm_dweight_sum<<<unsigned((hidden + 31) / 32), 32 * kSumSplit, 0, s>>>(a.part, parts, hidden, dweight, a.w_f32);
     return cudaGetLastError() == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
 }
 
