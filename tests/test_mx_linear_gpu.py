@@ -47,6 +47,15 @@ def test_shapes(n, h, v, dtype):
     check(make(n, n, h, "e4m3"), make(v, v, h, "e2m1"), dtype)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,h,v", [(1290, 384, 29002), (1290, 640, 28929), (2100, 128, 32768), (4096, 260, 32001),
+                                   (1537, 1100, 40064)])
+def test_many_tiles(n, h, v, dtype):
+    # enough tiles for the widest ones, with an odd number of column tiles, a last tile of one
+    # row, of one token, and row lengths that are and are not multiples of 16 bytes
+    check(make(n, n, h, "e4m3"), make(v, v, h, "e2m1"), dtype)
+
+
 @pytest.mark.parametrize("n,h,v", [(3, 1024, 300), (300, 2048, 500)])
 def test_scales_of_many_sizes(n, h, v):
     check(make(1, n, h, "e4m3", 20), make(2, v, h, "e2m1", 20), torch.float32)
