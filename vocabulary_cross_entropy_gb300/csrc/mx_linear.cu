@@ -100,21 +100,25 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t addr, uint32_t cols) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
 }
 
-__device__ __forceinline__ void umma_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
+__device__ __forceinline__ void umma_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// Descriptor of a scale tile in shared memory: 32 rows of 16 bytes without swizzle,
-// 8-row groups 128 bytes apart.
-__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
-    return uint64_t((saddr >> 4) & 0x3FFFu) | uint64_t(128 >> 4) << 16 | uint64_t(128 >> 4) << 32 | uint64_t(1) << 46;
-}
+// Matrix descriptors as (low, high) words: everything but the start address (>> 4, in
+// the low word) is the same for all of a kind, so that the issuing thread, whose
+// instructions one by one are what a short stage waits for, only adds to the low word.
+//   operand tiles: 128-byte swizzle, 8-row atoms 1024 bytes apart (see sm100_ptx.cuh)
+//   scale tiles: 32 rows of 16 bytes without swizzle, 8-row groups 128 bytes apart
+constexpr uint32_t kTileHigh = (1024 >> 4) | 1u << 14 | 2u << 29, kTileLow = (16 >> 4) << 16;
+constexpr uint32_t kScaleHigh = (128 >> 4) | 1u << 14, kScaleLow = (128 >> 4) << 16;
 
 // A 512-byte scale tile into four tensor-memory columns (rows 32 j .. 32 j + 31 in
 // column j, a byte per 32 columns of k), repeated in all four lane quadrants.
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t low) {
+    asm volatile(
+        "{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\ttcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr),
+        "r"(low), "n"(kScaleHigh)
+        : "memory");
 }
 
 // Instruction descriptor of kind::mxf8f6f4: A E4M3 (0) at bit 7, B E2M1 (5) at bit 10,
@@ -125,15 +129,33 @@ __device__ constexpr uint32_t idesc_mx(int n, int k_step) {
            (uint32_t(k_step) << 29) | (uint32_t(k_step) << 4);
 }
 
-__device__ __forceinline__ void umma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                        uint32_t accumulate) {
+__device__ __forceinline__ void umma_mx(uint32_t d, uint32_t a_low, uint32_t b_low, uint32_t idesc, uint32_t sfa,
+                                        uint32_t sfb, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %7};\n\tmov.b64 b, {%2, %7};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a, b, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "r"(a_low), "r"(b_low), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "n"(kTileHigh)
+        : "memory");
+}
+
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
-            d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-        : "memory");
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok));
+    return ok != 0;
+}
+
+// A whole warp's wait: every lane polls.  (A branch that only one lane takes costs its
+// warp about as much as the handover itself: a round trip between two warps measured 285
+// clocks with all lanes polling, 472 with one.)
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t timeout_ns) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, timeout_ns));
 }
 
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -225,9 +247,9 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant
     volatile int no_abort = 0;
 
     if (warp == 0) {
-        if (lane == 0) {
+        {
             // ---------------- packed w and its scales ----------------
-            tma_prefetch_desc(&tm_w);
+            if (lane == 0) tma_prefetch_desc(&tm_w);
             uint32_t s = 0, phase = 0, issued = 0, issued_phase = 0;
             bool ok = true;
             for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
@@ -235,14 +257,14 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant
                 const int64_t tile0 = int64_t(tv) * C::kWTiles;
                 const int wt = int(a.w_scale_rows - tile0 < C::kWTiles ? a.w_scale_rows - tile0 : C::kWTiles);
                 for (int k = 0; k < a.k_tiles; k += 2) {
-                    if (!mbar_wait(&p_empty[s], phase ^ 1u, abort_flag, a.timeout_ns)) {
+                    if (!warp_wait(&p_empty[s], phase ^ 1u, abort_flag, a.timeout_ns)) {
                         ok = false;
                         break;
                     }
                     const uint32_t sb = (k + 1 < a.k_tiles ? 2 : 1) * mx::kTileBytes;
-                    mbar_arrive_expect_tx(&p_full[s], C::kPackedBytes + wt * sb);
                     // past the last column and row the copies read zeros
-                    if (VCE_BOUNDS(k * (kK / 2) % 16 == 0 && tv < a.tiles_v && wt >= 1, a.dev_status)) {
+                    if (lane == 0) mbar_arrive_expect_tx(&p_full[s], C::kPackedBytes + wt * sb);
+                    if (lane == 0 && VCE_BOUNDS(k * (kK / 2) % 16 == 0 && tv < a.tiles_v && wt >= 1, a.dev_status)) {
 #pragma unroll
                         for (int j = 0; j < C::kWTiles; ++j)
                             tma_load_2d(smem_u32(packed + size_t(s) * C::kPackedBytes + j * 128 * (kPackedK / 2)), &tm_w,
@@ -261,20 +283,20 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant
                     if ((issued >> i) & 1u) mbar_wait(&p_full[i], (issued_phase >> i) & 1u, &no_abort, kDrainTimeoutNs);
         }
     } else if (warp == 2) {
-        if (lane == 0) {
+        {
             // ---------------- x and its scales ----------------
-            tma_prefetch_desc(&tm_x);
+            if (lane == 0) tma_prefetch_desc(&tm_x);
             uint32_t s = 0, phase = 0, issued = 0, issued_phase = 0;
             bool ok = true;
             for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
                 const int tn = t % a.tiles_n;
                 for (int k = 0; k < a.k_tiles; ++k) {
-                    if (!mbar_wait(&x_empty[s], phase ^ 1u, abort_flag, a.timeout_ns)) {
+                    if (!warp_wait(&x_empty[s], phase ^ 1u, abort_flag, a.timeout_ns)) {
                         ok = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(&x_full[s], a.x_rows * kK + mx::kTileBytes);
-                    if (VCE_BOUNDS(tn < a.tiles_n && a.x_rows <= kTokens, a.dev_status)) {
+                    if (lane == 0) mbar_arrive_expect_tx(&x_full[s], a.x_rows * kK + mx::kTileBytes);
+                    if (lane == 0 && VCE_BOUNDS(tn < a.tiles_n && a.x_rows <= kTokens, a.dev_status)) {
                         tma_load_2d(smem_u32(x_ring + size_t(s) * kXBytes), &tm_x, &x_full[s], k * kK, tn * kTokens);
                         bulk_load(smem_u32(x_scales + size_t(s) * mx::kTileBytes),
                                   a.x_scales + (int64_t(tn) * a.k_tiles + k) * mx::kTileBytes, mx::kTileBytes,
@@ -290,44 +312,53 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant
                     if ((issued >> i) & 1u) mbar_wait(&x_full[i], (issued_phase >> i) & 1u, &no_abort, kDrainTimeoutNs);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        {
             // ---------------- MMA issuer ----------------
             uint32_t sw = 0, w_phase = 0, sx = 0, x_phase = 0, acc = 0, acc_phase = 0;
             const uint32_t sfa = tmem + C::kScaleCol, sfb = sfa + 4;
+            const uint32_t x_lo = (smem_u32(x_ring) >> 4) | kTileLow, w_lo = (smem_u32(w_ring) >> 4) | kTileLow;
+            const uint32_t x_sc = (smem_u32(x_scales) >> 4) | kScaleLow, w_sc = (smem_u32(w_scales) >> 4) | kScaleLow;
+            const uint32_t w_bar = smem_u32(w_empty), x_bar = smem_u32(x_empty);
             bool ok = true;
             for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-                if (!mbar_wait(&t_empty[acc], acc_phase ^ 1u, abort_flag, a.timeout_ns)) break;
+                if (!warp_wait(&t_empty[acc], acc_phase ^ 1u, abort_flag, a.timeout_ns)) break;
                 tc_fence_after();
                 const uint32_t d = tmem + acc * BN;
                 for (int k = 0; k < a.k_tiles; ++k) {
-                    if (!mbar_wait(&x_full[sx], x_phase, abort_flag, a.timeout_ns) ||
-                        !mbar_wait(&w_full[sw], w_phase, abort_flag, a.timeout_ns)) {
+                    if (
+                        !warp_wait(&x_full[sx], x_phase, abort_flag, a.timeout_ns) ||
+                        !warp_wait(&w_full[sw], w_phase, abort_flag, a.timeout_ns)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     // copies to tensor memory and MMAs of one thread run in the order of issue
-                    copy_scales(sfa, scale_desc(smem_u32(x_scales + size_t(sx) * mx::kTileBytes)));
+                    const uint32_t xs = x_sc + sx * (mx::kTileBytes >> 4);
+                    const uint32_t ws = w_sc + sw * (C::kWTiles * mx::kTileBytes >> 4);
+                    const uint32_t ax = x_lo + sx * (kXBytes >> 4), bw = w_lo + sw * (C::kWBytes >> 4);
+                    const uint32_t we = w_bar + sw * 8, xe = x_bar + sx * 8;
+                    if (elect_one()) {
+                        copy_scales(sfa, xs);
 #pragma unroll
-                    for (int j = 0; j < C::kWTiles; ++j)
-                        copy_scales(sfb + 4 * j,
-                                    scale_desc(smem_u32(w_scales + (size_t(sw) * C::kWTiles + j) * mx::kTileBytes)));
-                    const uint32_t ax = smem_u32(x_ring + size_t(sx) * kXBytes);
-                    const uint32_t bw = smem_u32(w_ring + size_t(sw) * C::kWBytes);
+                        for (int j = 0; j < C::kWTiles; ++j) copy_scales(sfb + 4 * j, ws + j * (mx::kTileBytes >> 4));
+                        umma_mx(d, ax, bw, idesc_mx(BN, 0), sfa, sfb, k);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        umma_mx(d, smem_desc_sw128(ax + kk * 32, 16, 1024), smem_desc_sw128(bw + kk * 32, 16, 1024),
-                                idesc_mx(BN, kk), sfa, sfb, (k > 0 || kk > 0) ? 1u : 0u);
-                    umma_commit(&w_empty[sw]);
-                    umma_commit(&x_empty[sx]);
+                        for (int kk = 1; kk < 4; ++kk)
+                            umma_mx(d, ax + kk * 2, bw + kk * 2, idesc_mx(BN, kk), sfa, sfb, 1u);
+                        umma_commit(we);
+                        umma_commit(xe);
+                    }
+                    __syncwarp();
                     if (++sw == uint32_t(C::kW)) sw = 0, w_phase ^= 1u;
                     if (++sx == uint32_t(C::kX)) sx = 0, x_phase ^= 1u;
                 }
                 if (!ok) break;
-                umma_commit(&t_full[acc]);
+                if (elect_one()) umma_commit(smem_u32(&t_full[acc]));
+                __syncwarp();
                 if (++acc == uint32_t(C::kAccs)) acc = 0, acc_phase ^= 1u;
             }
-            umma_commit(drain);  // every MMA completes before tensor memory is released
+            if (elect_one()) umma_commit(smem_u32(drain));
+            __syncwarp();  // every MMA completes before tensor memory is released
             mbar_wait(drain, 0, &no_abort, kDrainTimeoutNs);
         }
     } else if (warp >= C::kFirstConverter) {
@@ -338,37 +369,34 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant
         // one row and lanes 4-7 those of the row four further, which the swizzle puts in
         // the other half of the banks.
         const int cw = warp - C::kFirstConverter;
-        const int sub = lane & 3, row0 = cw * 32 + ((lane >> 2) & 1) * 4 + (lane >> 3);
+        const int sub = lane & 3, row0 = cw * 32 + ((lane >> 2) & 1) * 4 + (lane >> 3), x = row0 & 7;
+        // byte offsets in a tile of this lane's piece of its first row (the others are 1024
+        // further each): packed, for either half of the stage, and the two converted pieces
+        const uint32_t from[2] = {uint32_t(row0 * 128 + ((sub ^ x) << 4)), uint32_t(row0 * 128 + (((4 + sub) ^ x) << 4))};
+        const uint32_t to0 = row0 * 128 + (((2 * sub) ^ x) << 4), to1 = row0 * 128 + (((2 * sub + 1) ^ x) << 4);
         uint32_t ps = 0, p_phase = 0, s = 0, phase = 0;
         bool ok = true;
         for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
             for (int k = 0; k < a.k_tiles && ok; k += 2) {
-                ok = mbar_wait(&p_full[ps], p_phase, abort_flag, a.timeout_ns);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = warp_wait(&p_full[ps], p_phase, abort_flag, a.timeout_ns);
                 if (!ok) break;
                 const uint8_t* src = packed + size_t(ps) * C::kPackedBytes;
                 const int halves = k + 1 < a.k_tiles ? 2 : 1;
                 for (int h = 0; h < halves; ++h) {
                     uint4 q[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int row = row0 + i * 8, x = row & 7;
-                        q[i] = *reinterpret_cast<const uint4*>(src + row * 128 + (((4 * h + sub) ^ x) << 4));
-                    }
+                    for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const uint4*>(src + (h ? from[1] : from[0]) + i * 1024);
                     // a quarter of a scale tile: tile cw / 4, its words 32 (cw % 4) ...
                     const uint32_t sc = reinterpret_cast<const uint32_t*>(
                         packed_scales + size_t(ps) * C::kPackedScales +
                         ((cw >> 2) * 2 + h) * mx::kTileBytes)[(cw & 3) * 32 + lane];
-                    ok = mbar_wait(&w_empty[s], phase ^ 1u, abort_flag, a.timeout_ns);
-                    ok = __all_sync(0xffffffffu, ok);
+                    ok = warp_wait(&w_empty[s], phase ^ 1u, abort_flag, a.timeout_ns);
                     if (!ok) break;
                     uint8_t* dst = w_ring + size_t(s) * C::kWBytes;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int row = row0 + i * 8, x = row & 7;
-                        *reinterpret_cast<uint2*>(dst + row * 128 + (((2 * sub) ^ x) << 4)) = make_uint2(q[i].x, q[i].y);
-                        *reinterpret_cast<uint2*>(dst + row * 128 + (((2 * sub + 1) ^ x) << 4)) =
-                            make_uint2(q[i].z, q[i].w);
+                        *reinterpret_cast<uint2*>(dst + to0 + i * 1024) = make_uint2(q[i].x, q[i].y);
+                        *reinterpret_cast<uint2*>(dst + to1 + i * 1024) = make_uint2(q[i].z, q[i].w);
                     }
                     reinterpret_cast<uint32_t*>(w_scales + size_t(s) * C::kWTiles * mx::kTileBytes)[cw * 32 + lane] = sc;
                     fence_async_shared();  // the tensor core reads these through the async proxy
@@ -390,8 +418,7 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant
         float* mine = reinterpret_cast<float*>(turn + ew * kTurnBytes);
         uint32_t acc = 0, acc_phase = 0;
         for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-            const bool ok = mbar_wait(&t_full[acc], acc_phase, abort_flag, a.timeout_ns);
-            if (!__all_sync(0xffffffffu, ok)) break;
+            if (!warp_wait(&t_full[acc], acc_phase, abort_flag, a.timeout_ns)) break;
             tc_fence_after();
             const int64_t n0 = int64_t(t % a.tiles_n) * kTokens + q * 32;
             const int64_t v0 = int64_t(t / a.tiles_n) * BN + col0;
