@@ -477,6 +477,7 @@ vce_status mx_dequantize(const void* codes, const void* scales, int fmt, int64_t
  * stored here, for sampling (ce_sample) or scoring (ce_forward).
  *
  *   x  E4M3 [n, h] (mx_quantize or rms_norm_mx); w  E2M1 [v, h].
+ *   All four buffers 16-byte aligned, w_codes 32-byte.
  *   out  BF16 or F32 [n, v], rows out_stride elements apart (>= v), aligned to its type.
  * A NaN scale makes the outputs of its row of x (of w) NaN.
  */

@@ -9,14 +9,15 @@
 // with N = 128, and the classifier is what has to be fed through (8 tokens x 4096 x
 // 128256: 120 us that way round).
 //
-// 4-bit values travel packed (two per byte) from HBM to shared memory.  The tensor
-// core wants them there as 16-byte pieces of 16 values, 8 bytes of codes and 8 of
-// padding; converter warps spread the codes from the packed ring into the operand ring.
+// 4-bit values travel packed (two per byte) from HBM.  The tensor core wants them in
+// shared memory as 16-byte pieces of 16 values, 8 bytes of codes and 8 of padding, and
+// a tensor map of type 16U4_ALIGN16B makes the copy engine spread them so (counting the
+// packed bytes on the barrier).  Converter warps in its place took as many cycles of
+// shared memory as feeding the tensor core (1005 us at 2048 tokens x 4096 x 128256).
 //
-// Roles: warp 0 copies packed w and its scales (TMA), warp 1 issues the MMAs, warp 2
-// copies x and its scales, then epilogue warps and converters.  Three rings: ``packed``
-// (256 columns of w per stage, the bytes that come from HBM, kept deep), ``w`` (128
-// columns, converted) and ``x`` (128 columns).  Every wait is bounded, as in lce_tc.cu.
+// Roles: warp 0 copies both operands and their scales (TMA), warp 1 issues the MMAs, warps
+// 4 to 11 drain accumulators.  One ring of 128 columns per stage.  Every wait is
+// bounded, as in lce_tc.cu.
 
 #include "vce_internal.cuh"
 #include "mx_format.cuh"
@@ -31,42 +32,37 @@ namespace {
 using namespace sm100;
 
 constexpr int kTokens = 128;                    // tokens per tile
-constexpr int kK = 128;                         // columns per operand stage: one 128-byte swizzle row
-constexpr int kPackedK = 256;                   // columns per packed stage: 128-byte rows, too
-constexpr uint32_t kXBytes = kTokens * kK;
+constexpr int kK = 128;                         // columns per stage: one 128-byte swizzle row
+constexpr int kRows = 256;                      // classifier rows per tile; the last tiles may have half
+constexpr uint32_t kWBytes = kRows * kK;        // as the tensor core reads them: half is padding
 constexpr int kFirstEpilogue = 4;               // warp; a multiple of 4, as lane quadrants go by warp % 4
-constexpr int kStageCols = 16;                  // columns an epilogue warp turns at a time
-constexpr uint32_t kTurnBytes = 32 * (kStageCols + 1) * 4;  // and its scratch
+constexpr int kEpilogueWarps = 8;               // four per 128 columns
+constexpr int kThreads = (kFirstEpilogue + kEpilogueWarps) * 32;
+constexpr int kTurnCols = 16;                   // columns an epilogue warp turns at a time
+constexpr uint32_t kTurnBytes = 32 * (kTurnCols + 1) * 4;  // and its scratch
+// Tensor memory: two accumulators of 256 columns that share 16 (0-255 and 240-495), x's
+// scales (4 columns) and w's (8) behind them.  A tile's shared columns are drained first,
+// then the next tile's MMAs may start.
+constexpr uint32_t kAccStep = 240, kScaleCol = 496, kTmemCols = 512;
 
-// BN: classifier rows per tile
-template <int BN>
+// XR: rows of x a stage has room for.  Fewer than a tile's 128 serve fewer tokens: the
+// tensor core then reads its other rows from w's tile behind them, whatever that means as
+// E4M3, into accumulator rows that nobody stores.
+template <int XR>
 struct Cfg {
-    static constexpr int kWTiles = BN / 128;                 // scale tiles of w
-    static constexpr uint32_t kWBytes = BN * kK;             // converted
-    static constexpr uint32_t kPackedBytes = BN * kPackedK / 2;
-    static constexpr uint32_t kPackedScales = 2 * kWTiles * mx::kTileBytes;
-    static constexpr int kW = BN == 128 ? 3 : 2;             // stages
-    static constexpr int kX = 3;
-    static constexpr int kPacked = BN == 128 ? 5 : 2;
-    static constexpr int kAccs = BN == 128 ? 2 : 1;
-    static constexpr int kEpilogueWarps = BN / 32;           // four per 128 columns
-    static constexpr int kConverterWarps = BN / 32;          // 32 rows each
-    static constexpr int kFirstConverter = kFirstEpilogue + kEpilogueWarps;
-    static constexpr int kThreads = (kFirstConverter + kConverterWarps) * 32;
-    static constexpr uint32_t kScaleCol = kAccs * BN;        // tensor-memory column of x's scales, w's behind
-    static constexpr uint32_t kTmemCols = 512;
-    static constexpr size_t kSmem = size_t(kW) * (kWBytes + kWTiles * mx::kTileBytes) +
-                                    size_t(kX) * (kXBytes + mx::kTileBytes) +
-                                    size_t(kPacked) * (kPackedBytes + kPackedScales) + kEpilogueWarps * kTurnBytes +
-                                    1024 + 512;
-    static_assert(kScaleCol + 4 + 4 * kWTiles <= kTmemCols && kSmem <= 232448, "tensor and shared memory");
+    static constexpr uint32_t kXBytes = XR * kK;
+    static constexpr uint32_t kStage = kXBytes + kWBytes;
+    static constexpr uint32_t kScales = 3 * mx::kTileBytes;  // x, w, w
+    static constexpr int kStages = XR == 128 ? 4 : 5;
+    static constexpr size_t kSmem = size_t(kStages) * (kStage + kScales) + kEpilogueWarps * kTurnBytes + 1024 + 512;
+    static_assert((kTokens - XR) * kK <= int(kWBytes) / 2 && kSmem <= 232448, "shared memory");
 };
 
 struct LinearArgs {
     int64_t n, v;
     int k_tiles;           // 128-column tiles
-    int tiles_v, tiles_n;
-    int x_rows;            // tokens per copy of x: 16, 32, 64 or 128
+    int tiles_v, tiles_n;  // tiles of classifier rows and of tokens
+    int whole_v;           // the first so many tiles have 256 rows, the others 128
     int64_t w_scale_rows;  // 128-row tiles of w's scales
     const uint8_t *w_scales, *x_scales;
     void* out;
@@ -124,6 +120,7 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t low) {
 // Instruction descriptor of kind::mxf8f6f4: A E4M3 (0) at bit 7, B E2M1 (5) at bit 10,
 // N >> 3 at bit 17, E8M0 scales (bit 23), M >> 4 at bit 24; the byte of the scale
 // columns that holds this k step at bits 29 (A) and 4 (B).
+constexpr uint32_t kScaleIdStep = 1u << 29 | 1u << 4;  // the next k step's scales
 __device__ constexpr uint32_t idesc_mx(int n, int k_step) {
     return (5u << 10) | (uint32_t(n >> 3) << 17) | (1u << 23) | (uint32_t(kTokens >> 4) << 24) |
            (uint32_t(k_step) << 29) | (uint32_t(k_step) << 4);
@@ -183,63 +180,54 @@ __device__ __forceinline__ void store_row32(__nv_bfloat16* p, const uint32_t (&r
     }
 }
 
-template <int BN, typename Out>
-__global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
+// Tile t of the launch: its classifier rows (first, width 256 or 128) and its tokens.
+struct Tile {
+    int64_t v0, n0;
+    int width;
+};
+__device__ __forceinline__ Tile tile_at(const LinearArgs& a, int t) {
+    const int tv = t / a.tiles_n, tn = t - tv * a.tiles_n;
+    const bool whole = tv < a.whole_v;
+    return {int64_t(whole ? tv : a.whole_v) * kRows + (whole ? 0 : int64_t(tv - a.whole_v) * 128), int64_t(tn) * kTokens,
+            whole ? kRows : 128};
+}
+
+template <int XR, typename Out>
+__global__ void __launch_bounds__(kThreads, 1)
 mx_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                  const LinearArgs a) {
-    using C = Cfg<BN>;
+    using C = Cfg<XR>;
+    constexpr int S = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* w_ring = smem;                                           // operand tiles and packed ones: 1024-aligned
-    uint8_t* packed = w_ring + size_t(C::kW) * C::kWBytes;
-    uint8_t* x_ring = packed + size_t(C::kPacked) * C::kPackedBytes;
-    uint8_t* packed_scales = x_ring + size_t(C::kX) * kXBytes;
-    uint8_t* w_scales = packed_scales + size_t(C::kPacked) * C::kPackedScales;
-    uint8_t* x_scales = w_scales + size_t(C::kW) * C::kWTiles * mx::kTileBytes;
-    uint8_t* turn = x_scales + size_t(C::kX) * mx::kTileBytes;
-    uint64_t* p_full = reinterpret_cast<uint64_t*>(turn + C::kEpilogueWarps * kTurnBytes);
-    uint64_t* p_empty = p_full + C::kPacked;  // read by the converter warps
-    uint64_t* w_full = p_empty + C::kPacked;  // converted by them
-    uint64_t* w_empty = w_full + C::kW;       // MMAs done with the stage
-    uint64_t* x_full = w_empty + C::kW;
-    uint64_t* x_empty = x_full + C::kX;
-    uint64_t* t_full = x_empty + C::kX;
-    uint64_t* t_empty = t_full + 2;
-    uint64_t* drain = t_empty + 2;
+    uint8_t* scales = smem + size_t(S) * C::kStage;  // stages of x, then w: multiples of 1024 bytes
+    uint8_t* turn = scales + size_t(S) * C::kScales;
+    uint64_t* full = reinterpret_cast<uint64_t*>(turn + kEpilogueWarps * kTurnBytes);
+    uint64_t* empty = full + S;
+    uint64_t* t_full = empty + S;    // a tile's MMAs are done
+    uint64_t* t_empty = t_full + 2;  // its accumulator is drained
+    uint64_t* shared_empty = t_empty + 2;  // the columns it shares with the other are
+    uint64_t* drain = shared_empty + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tiles = a.tiles_v * a.tiles_n;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::kPacked; ++i) {
-            mbar_init(&p_full[i], 1);
-            mbar_init(&p_empty[i], C::kConverterWarps);
-        }
-        for (int i = 0; i < C::kW; ++i) {
-            mbar_init(&w_full[i], C::kConverterWarps);
-            mbar_init(&w_empty[i], 1);
-        }
-        for (int i = 0; i < C::kX; ++i) {
-            mbar_init(&x_full[i], 1);
-            mbar_init(&x_empty[i], 1);
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&t_full[i], 1);
-            mbar_init(&t_empty[i], C::kEpilogueWarps);
+            mbar_init(&t_empty[i], kEpilogueWarps);
         }
+        mbar_init(shared_empty, 4);
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
-    // Rows of x that no copy writes (fewer tokens than a tile): zeros for the whole launch
-    if (a.x_rows < kTokens) {
-        for (int s = 0; s < C::kX; ++s)
-            for (int i = a.x_rows * 8 + threadIdx.x; i < int(kXBytes / 16); i += C::kThreads)
-                reinterpret_cast<uint4*>(x_ring + size_t(s) * kXBytes)[i] = make_uint4(0, 0, 0, 0);
-        fence_async_shared();
-    }
-    if (warp == 1) tmem_alloc(tmem_slot, C::kTmemCols);
+    if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -247,224 +235,157 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant
     volatile int no_abort = 0;
 
     if (warp == 0) {
-        {
-            // ---------------- packed w and its scales ----------------
-            if (lane == 0) tma_prefetch_desc(&tm_w);
-            uint32_t s = 0, phase = 0, issued = 0, issued_phase = 0;
-            bool ok = true;
-            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-                const int tv = t / a.tiles_n;
-                const int64_t tile0 = int64_t(tv) * C::kWTiles;
-                const int wt = int(a.w_scale_rows - tile0 < C::kWTiles ? a.w_scale_rows - tile0 : C::kWTiles);
-                for (int k = 0; k < a.k_tiles; k += 2) {
-                    if (!warp_wait(&p_empty[s], phase ^ 1u, abort_flag, a.timeout_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t sb = (k + 1 < a.k_tiles ? 2 : 1) * mx::kTileBytes;
-                    // past the last column and row the copies read zeros
-                    if (lane == 0) mbar_arrive_expect_tx(&p_full[s], C::kPackedBytes + wt * sb);
-                    if (lane == 0 && VCE_BOUNDS(k * (kK / 2) % 16 == 0 && tv < a.tiles_v && wt >= 1, a.dev_status)) {
-#pragma unroll
-                        for (int j = 0; j < C::kWTiles; ++j)
-                            tma_load_2d(smem_u32(packed + size_t(s) * C::kPackedBytes + j * 128 * (kPackedK / 2)), &tm_w,
-                                        &p_full[s], k * (kK / 2), tv * BN + j * 128);
-                        for (int j = 0; j < wt; ++j)
-                            bulk_load(smem_u32(packed_scales + size_t(s) * C::kPackedScales + j * 2 * mx::kTileBytes),
-                                      a.w_scales + ((tile0 + j) * a.k_tiles + k) * mx::kTileBytes, sb, &p_full[s]);
-                    }
-                    issued |= 1u << s;
-                    issued_phase = (issued_phase & ~(1u << s)) | (phase << s);
-                    if (++s == uint32_t(C::kPacked)) s = 0, phase ^= 1u;
-                }
-            }
-            if (!ok)  // copies in flight land before shared memory is released
-                for (int i = 0; i < C::kPacked; ++i)
-                    if ((issued >> i) & 1u) mbar_wait(&p_full[i], (issued_phase >> i) & 1u, &no_abort, kDrainTimeoutNs);
+        // ---------------- copies ----------------
+        if (lane == 0) {
+            tma_prefetch_desc(&tm_w);
+            tma_prefetch_desc(&tm_x);
         }
-    } else if (warp == 2) {
-        {
-            // ---------------- x and its scales ----------------
-            if (lane == 0) tma_prefetch_desc(&tm_x);
-            uint32_t s = 0, phase = 0, issued = 0, issued_phase = 0;
-            bool ok = true;
-            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-                const int tn = t % a.tiles_n;
-                for (int k = 0; k < a.k_tiles; ++k) {
-                    if (!warp_wait(&x_empty[s], phase ^ 1u, abort_flag, a.timeout_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    if (lane == 0) mbar_arrive_expect_tx(&x_full[s], a.x_rows * kK + mx::kTileBytes);
-                    if (lane == 0 && VCE_BOUNDS(tn < a.tiles_n && a.x_rows <= kTokens, a.dev_status)) {
-                        tma_load_2d(smem_u32(x_ring + size_t(s) * kXBytes), &tm_x, &x_full[s], k * kK, tn * kTokens);
-                        bulk_load(smem_u32(x_scales + size_t(s) * mx::kTileBytes),
-                                  a.x_scales + (int64_t(tn) * a.k_tiles + k) * mx::kTileBytes, mx::kTileBytes,
-                                  &x_full[s]);
-                    }
-                    issued |= 1u << s;
-                    issued_phase = (issued_phase & ~(1u << s)) | (phase << s);
-                    if (++s == uint32_t(C::kX)) s = 0, phase ^= 1u;
-                }
-            }
-            if (!ok)
-                for (int i = 0; i < C::kX; ++i)
-                    if ((issued >> i) & 1u) mbar_wait(&x_full[i], (issued_phase >> i) & 1u, &no_abort, kDrainTimeoutNs);
-        }
-    } else if (warp == 1) {
-        {
-            // ---------------- MMA issuer ----------------
-            uint32_t sw = 0, w_phase = 0, sx = 0, x_phase = 0, acc = 0, acc_phase = 0;
-            const uint32_t sfa = tmem + C::kScaleCol, sfb = sfa + 4;
-            const uint32_t x_lo = (smem_u32(x_ring) >> 4) | kTileLow, w_lo = (smem_u32(w_ring) >> 4) | kTileLow;
-            const uint32_t x_sc = (smem_u32(x_scales) >> 4) | kScaleLow, w_sc = (smem_u32(w_scales) >> 4) | kScaleLow;
-            const uint32_t w_bar = smem_u32(w_empty), x_bar = smem_u32(x_empty);
-            bool ok = true;
-            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-                if (!warp_wait(&t_empty[acc], acc_phase ^ 1u, abort_flag, a.timeout_ns)) break;
-                tc_fence_after();
-                const uint32_t d = tmem + acc * BN;
-                for (int k = 0; k < a.k_tiles; ++k) {
-                    if (
-                        !warp_wait(&x_full[sx], x_phase, abort_flag, a.timeout_ns) ||
-                        !warp_wait(&w_full[sw], w_phase, abort_flag, a.timeout_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    // copies to tensor memory and MMAs of one thread run in the order of issue
-                    const uint32_t xs = x_sc + sx * (mx::kTileBytes >> 4);
-                    const uint32_t ws = w_sc + sw * (C::kWTiles * mx::kTileBytes >> 4);
-                    const uint32_t ax = x_lo + sx * (kXBytes >> 4), bw = w_lo + sw * (C::kWBytes >> 4);
-                    const uint32_t we = w_bar + sw * 8, xe = x_bar + sx * 8;
-                    if (elect_one()) {
-                        copy_scales(sfa, xs);
-#pragma unroll
-                        for (int j = 0; j < C::kWTiles; ++j) copy_scales(sfb + 4 * j, ws + j * (mx::kTileBytes >> 4));
-                        umma_mx(d, ax, bw, idesc_mx(BN, 0), sfa, sfb, k);
-#pragma unroll
-                        for (int kk = 1; kk < 4; ++kk)
-                            umma_mx(d, ax + kk * 2, bw + kk * 2, idesc_mx(BN, kk), sfa, sfb, 1u);
-                        umma_commit(we);
-                        umma_commit(xe);
-                    }
-                    __syncwarp();
-                    if (++sw == uint32_t(C::kW)) sw = 0, w_phase ^= 1u;
-                    if (++sx == uint32_t(C::kX)) sx = 0, x_phase ^= 1u;
-                }
-                if (!ok) break;
-                if (elect_one()) umma_commit(smem_u32(&t_full[acc]));
-                __syncwarp();
-                if (++acc == uint32_t(C::kAccs)) acc = 0, acc_phase ^= 1u;
-            }
-            if (elect_one()) umma_commit(smem_u32(drain));
-            __syncwarp();  // every MMA completes before tensor memory is released
-            mbar_wait(drain, 0, &no_abort, kDrainTimeoutNs);
-        }
-    } else if (warp >= C::kFirstConverter) {
-        // ---------------- converters: 32 classifier rows per warp ----------------
-        // A lane takes 16 packed bytes (32 values) of a row and stores them as two
-        // 16-byte pieces with 8 bytes of codes each.  Both rings use the 128-byte swizzle
-        // (piece p of row r at p ^ (r & 7)).  Lanes 0-3 read four neighbouring pieces of
-        // one row and lanes 4-7 those of the row four further, which the swizzle puts in
-        // the other half of the banks.
-        const int cw = warp - C::kFirstConverter;
-        const int sub = lane & 3, row0 = cw * 32 + ((lane >> 2) & 1) * 4 + (lane >> 3), x = row0 & 7;
-        // byte offsets in a tile of this lane's piece of its first row (the others are 1024
-        // further each): packed, for either half of the stage, and the two converted pieces
-        const uint32_t from[2] = {uint32_t(row0 * 128 + ((sub ^ x) << 4)), uint32_t(row0 * 128 + (((4 + sub) ^ x) << 4))};
-        const uint32_t to0 = row0 * 128 + (((2 * sub) ^ x) << 4), to1 = row0 * 128 + (((2 * sub + 1) ^ x) << 4);
-        uint32_t ps = 0, p_phase = 0, s = 0, phase = 0;
+        uint32_t s = 0, phase = 0, issued = 0, issued_phase = 0;
         bool ok = true;
         for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-            for (int k = 0; k < a.k_tiles && ok; k += 2) {
-                ok = warp_wait(&p_full[ps], p_phase, abort_flag, a.timeout_ns);
+            const Tile tile = tile_at(a, t);
+            const int64_t st = tile.v0 / 128;  // first scale tile of w
+            const int wt = tile.width == kRows && st + 1 < a.w_scale_rows ? 2 : 1;
+            const uint8_t* ws = a.w_scales + st * a.k_tiles * mx::kTileBytes;
+            const uint8_t* xs = a.x_scales + tile.n0 / 128 * a.k_tiles * mx::kTileBytes;
+            for (int k = 0; k < a.k_tiles; ++k) {
+                ok = warp_wait(&empty[s], phase ^ 1u, abort_flag, a.timeout_ns);
                 if (!ok) break;
-                const uint8_t* src = packed + size_t(ps) * C::kPackedBytes;
-                const int halves = k + 1 < a.k_tiles ? 2 : 1;
-                for (int h = 0; h < halves; ++h) {
-                    uint4 q[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const uint4*>(src + (h ? from[1] : from[0]) + i * 1024);
-                    // a quarter of a scale tile: tile cw / 4, its words 32 (cw % 4) ...
-                    const uint32_t sc = reinterpret_cast<const uint32_t*>(
-                        packed_scales + size_t(ps) * C::kPackedScales +
-                        ((cw >> 2) * 2 + h) * mx::kTileBytes)[(cw & 3) * 32 + lane];
-                    ok = warp_wait(&w_empty[s], phase ^ 1u, abort_flag, a.timeout_ns);
-                    if (!ok) break;
-                    uint8_t* dst = w_ring + size_t(s) * C::kWBytes;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        *reinterpret_cast<uint2*>(dst + to0 + i * 1024) = make_uint2(q[i].x, q[i].y);
-                        *reinterpret_cast<uint2*>(dst + to1 + i * 1024) = make_uint2(q[i].z, q[i].w);
+                // past the last column and row the copies write zeros, which count as bytes; a
+                // copy of w counts its packed bytes
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&full[s], C::kXBytes + tile.width * (kK / 2) + (1 + wt) * mx::kTileBytes);
+                    const uint32_t sx = smem_u32(smem + size_t(s) * C::kStage);
+                    const uint32_t sc = smem_u32(scales + size_t(s) * C::kScales);
+                    if (VCE_BOUNDS(tile.v0 < a.v && tile.n0 < a.n && st + wt <= a.w_scale_rows, a.dev_status)) {
+                        tma_load_2d(sx + C::kXBytes, &tm_w, &full[s], k * kK, int(tile.v0));
+                        if (tile.width == kRows)
+                            tma_load_2d(sx + C::kXBytes + kWBytes / 2, &tm_w, &full[s], k * kK, int(tile.v0) + 128);
+                        for (int j = 0; j < wt; ++j)
+                            bulk_load(sc + (1 + j) * mx::kTileBytes, ws + (int64_t(j) * a.k_tiles + k) * mx::kTileBytes,
+                                      mx::kTileBytes, &full[s]);
+                        tma_load_2d(sx, &tm_x, &full[s], k * kK, int(tile.n0));
+                        bulk_load(sc, xs + int64_t(k) * mx::kTileBytes, mx::kTileBytes, &full[s]);
                     }
-                    reinterpret_cast<uint32_t*>(w_scales + size_t(s) * C::kWTiles * mx::kTileBytes)[cw * 32 + lane] = sc;
-                    fence_async_shared();  // the tensor core reads these through the async proxy
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&w_full[s]);
-                        // only now: loads whose values have been stored are certainly over, and the
-                        // next copy into the packed stage cannot overtake them
-                        if (h + 1 == halves) mbar_arrive(&p_empty[ps]);
-                    }
-                    if (++s == uint32_t(C::kW)) s = 0, phase ^= 1u;
                 }
-                if (++ps == uint32_t(C::kPacked)) ps = 0, p_phase ^= 1u;
+                __syncwarp();
+                issued |= 1u << s;
+                issued_phase = (issued_phase & ~(1u << s)) | (phase << s);
+                if (++s == uint32_t(S)) s = 0, phase ^= 1u;
             }
         }
+        if (!ok)  // copies in flight land before shared memory is released
+            for (int i = 0; i < S; ++i)
+                if ((issued >> i) & 1u) mbar_wait(&full[i], (issued_phase >> i) & 1u, &no_abort, kDrainTimeoutNs);
+    } else if (warp == 1) {
+        // ---------------- MMA issuer ----------------
+        // What the instructions take is computed by the whole warp, outside the one lane's
+        // branch, so that it sits in uniform registers: moved there one by one, the operands
+        // of the seven instructions of a stage cost 660 clocks, now 410.
+        uint32_t s = 0, phase = 0, acc = 0, acc_phase = 0, shared_phase = 0;
+        const uint32_t sfa = tmem + kScaleCol, sfb = sfa + 4;
+        const uint32_t x_lo = (smem_u32(smem) >> 4) | kTileLow, sc_lo = (smem_u32(scales) >> 4) | kScaleLow;
+        const uint32_t empty_at = smem_u32(empty);
+        bool ok = true;
+        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            const int width = tile_at(a, t).width;
+            if (!warp_wait(&t_empty[acc], acc_phase ^ 1u, abort_flag, a.timeout_ns)) break;
+            if (!warp_wait(shared_empty, shared_phase ^ 1u, abort_flag, a.timeout_ns)) break;
+            shared_phase ^= 1u;
+            tc_fence_after();
+            const uint32_t d = tmem + acc * kAccStep;
+            const uint32_t idesc = width == kRows ? idesc_mx(kRows, 0) : idesc_mx(128, 0);
+            for (int k = 0; k < a.k_tiles; ++k) {
+                ok = warp_wait(&full[s], phase, abort_flag, a.timeout_ns);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t sc = sc_lo + s * (C::kScales >> 4);
+                const uint32_t ax = x_lo + s * (C::kStage >> 4), bw = ax + (C::kXBytes >> 4);
+                const uint32_t done = empty_at + s * 8;
+                if (elect_one()) {
+                    // copies to tensor memory and MMAs of one thread run in the order of issue
+                    copy_scales(sfa, sc);
+                    copy_scales(sfb, sc + (mx::kTileBytes >> 4));
+                    if (width == kRows) copy_scales(sfb + 4, sc + 2 * (mx::kTileBytes >> 4));
+                    umma_mx(d, ax, bw, idesc, sfa, sfb, k);
+#pragma unroll
+                    for (int kk = 1; kk < 4; ++kk)
+                        umma_mx(d, ax + kk * 2, bw + kk * 2, idesc + kk * kScaleIdStep, sfa, sfb, 1u);
+                    umma_commit(done);
+                }
+                __syncwarp();
+                if (++s == uint32_t(S)) s = 0, phase ^= 1u;
+            }
+            if (!ok) break;
+            if (elect_one()) umma_commit(smem_u32(&t_full[acc]));
+            __syncwarp();
+            acc ^= 1u;
+            acc_phase ^= acc ^ 1u;
+        }
+        if (elect_one()) umma_commit(smem_u32(drain));  // every MMA completes before tensor memory is released
+        __syncwarp();
+        mbar_wait(drain, 0, &no_abort, kDrainTimeoutNs);
     } else if (warp >= kFirstEpilogue) {
         // ---------------- epilogue: one token per lane, 128 logits per warp ----------------
-        const int ew = warp - kFirstEpilogue, q = warp & 3, col0 = (ew >> 2) * 128;
+        const int ew = warp - kFirstEpilogue, q = warp & 3, half = ew >> 2;
         float* mine = reinterpret_cast<float*>(turn + ew * kTurnBytes);
         uint32_t acc = 0, acc_phase = 0;
         for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
             if (!warp_wait(&t_full[acc], acc_phase, abort_flag, a.timeout_ns)) break;
             tc_fence_after();
-            const int64_t n0 = int64_t(t % a.tiles_n) * kTokens + q * 32;
-            const int64_t v0 = int64_t(t / a.tiles_n) * BN + col0;
+            const Tile tile = tile_at(a, t);
+            const int64_t n0 = tile.n0 + q * 32, v0 = tile.v0 + half * 128;
             const int live = int(a.n - n0 < 32 ? a.n - n0 : 32);  // tokens of this warp
-            const int cols = int(a.v - v0 < 128 ? a.v - v0 : 128);
-            const uint32_t taddr = tmem + (uint32_t(q * 32) << 16) + acc * BN + col0;
+            const int64_t right = a.v < tile.v0 + tile.width ? a.v : tile.v0 + tile.width;
+            const int cols = int(right - v0 < 128 ? right - v0 : 128);
+            const uint32_t taddr = tmem + (uint32_t(q * 32) << 16) + acc * kAccStep + half * 128;
             Out* out = static_cast<Out*>(a.out) + n0 * a.out_stride + v0;
-            if (live > 0 && cols > 0 && VCE_BOUNDS(n0 >= 0 && v0 >= 0, a.dev_status)) {
-                if (a.wide) {
-                    Out* row = out + int64_t(lane) * a.out_stride;
+            // the columns both accumulators have are the last of the first one's second half and
+            // the first of the second one's first half
+            const bool shares = half != int(acc);
+            const bool work = live > 0 && cols > 0 && VCE_BOUNDS(n0 >= 0 && v0 >= 0, a.dev_status);
+            if (shares && !work && lane == 0) mbar_arrive(shared_empty);
+            if (work) {
+                const int chunks = (cols + 31) / 32;
 #pragma unroll 1
-                    for (int c = 0; c < cols; c += 32) {
-                        uint32_t r[32];
-                        tmem_ld32(taddr + c, r);
-                        tmem_ld_wait();
+                for (int i = 0; i < chunks; ++i) {
+                    const int c = (acc == 0 ? chunks - 1 - i : i) * 32;
+                    uint32_t r[32];
+                    tmem_ld32(taddr + c, r);
+                    tmem_ld_wait();
+                    if (shares && i == 0) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(shared_empty);
+                    }
+                    if (a.wide) {
+                        Out* row = out + int64_t(lane) * a.out_stride + c;
                         if (lane < live) {
                             if (cols - c >= 32) {
-                                store_row32(row + c, r);
+                                store_row32(row, r);
                             } else {
 #pragma unroll
                                 for (int j = 0; j < 32; ++j)
-                                    if (j < cols - c) store_logit(row + c + j, __uint_as_float(r[j]));
+                                    if (j < cols - c) store_logit(row + j, __uint_as_float(r[j]));
                             }
                         }
-                    }
-                } else {
-                    // rows at any offset: turned through shared memory, so that half a warp
-                    // stores 16 neighbouring logits of one token
-                    const int hl = lane & 15, hr = lane >> 4;
-#pragma unroll 1
-                    for (int c = 0; c < cols; c += 32) {
-                        uint32_t r[32];
-                        tmem_ld32(taddr + c, r);
-                        tmem_ld_wait();
+                    } else {
+                        // rows at any offset: turned through shared memory, so that half a warp
+                        // stores 16 neighbouring logits of one token
+                        const int hl = lane & 15, hr = lane >> 4;
 #pragma unroll
                         for (int part = 0; part < 2; ++part) {
                             __syncwarp();
 #pragma unroll
-                            for (int j = 0; j < kStageCols; ++j)
-                                mine[lane * (kStageCols + 1) + j] = __uint_as_float(r[part * kStageCols + j]);
+                            for (int j = 0; j < kTurnCols; ++j)
+                                mine[lane * (kTurnCols + 1) + j] = __uint_as_float(r[part * kTurnCols + j]);
                             __syncwarp();
-                            const int cc = c + part * kStageCols + hl;
+                            const int cc = c + part * kTurnCols + hl;
                             if (cc < cols) {
                                 Out* p = out + int64_t(hr) * a.out_stride + cc;
-                                for (int i = hr; i < live; i += 2, p += 2 * a.out_stride)
-                                    store_logit(p, mine[i * (kStageCols + 1) + hl]);
+#pragma unroll 4
+                                for (int i2 = hr; i2 < live; i2 += 2, p += 2 * a.out_stride)
+                                    store_logit(p, mine[i2 * (kTurnCols + 1) + hl]);
                             }
                         }
                     }
@@ -473,7 +394,8 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&t_empty[acc]);
-            if (++acc == uint32_t(C::kAccs)) acc = 0, acc_phase ^= 1u;
+            acc ^= 1u;
+            acc_phase ^= acc ^ 1u;
         }
     }
 
@@ -481,7 +403,7 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant
     if (threadIdx.x == 0 && *abort_flag) report(a.dev_status, VCE_DEVSTATUS_TIMEOUT);
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, C::kTmemCols);
+        tmem_dealloc(tmem, kTmemCols);
     }
 }
 
@@ -503,56 +425,61 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-// Bytes [rows][row_bytes], box of 128 bytes x ``box_rows``, 128-byte swizzle, zeros out of range.
-bool byte_map(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_rows) {
+// Codes [rows][cols], box of 128 columns x ``box_rows``, 128-byte swizzle, zeros out of
+// range.  E2M1 codes are spread to one byte per value's place (see above); that type
+// wants columns and x coordinates in multiples of 128 and the base at 32 bytes.
+bool code_map(CUtensorMap* map, const void* base, bool packed, uint64_t cols, uint64_t rows, uint32_t box_rows) {
     auto fn = encode_fn();
     if (!fn) return false;
-    cuuint64_t dims[2] = {row_bytes, rows};
-    cuuint64_t strides[1] = {row_bytes};
+    cuuint64_t dims[2] = {cols, rows};
+    cuuint64_t strides[1] = {packed ? cols / 2 : cols};
     cuuint32_t box[2] = {128, box_rows};
     cuuint32_t es[2] = {1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    return fn(map, packed ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+              const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN, typename Out>
+template <int XR, typename Out>
 vce_status launch(const void* xc, const void* wc, LinearArgs a, cudaStream_t s, const DeviceInfo& dev) {
     static std::mutex mu;
     static bool ready[64];
     {
         std::lock_guard<std::mutex> lock(mu);
         if (!ready[dev.ordinal]) {
-            if (cudaFuncSetAttribute(mx_linear_kernel<BN, Out>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     int(Cfg<BN>::kSmem)) != cudaSuccess)
+            if (cudaFuncSetAttribute(mx_linear_kernel<XR, Out>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     int(Cfg<XR>::kSmem)) != cudaSuccess)
                 return VCE_ERR_CUDA;
             ready[dev.ordinal] = true;
         }
     }
     CUtensorMap tm_w, tm_x;
     const uint64_t cols = uint64_t(a.k_tiles) * kK;
-    if (!byte_map(&tm_w, wc, cols / 2, uint64_t(a.v), 128) || !byte_map(&tm_x, xc, cols, uint64_t(a.n), a.x_rows))
+    if (!code_map(&tm_w, wc, true, cols, uint64_t(a.v), 128) || !code_map(&tm_x, xc, false, cols, uint64_t(a.n), XR))
         return VCE_ERR_CUDA;
-    a.tiles_v = int((a.v + BN - 1) / BN);
     const int64_t tiles = int64_t(a.tiles_v) * a.tiles_n;
     if (tiles > 0x7fffffff) return VCE_ERR_INVALID_ARG;
     count_launch();
-    mx_linear_kernel<BN, Out>
-        <<<unsigned(tiles < dev.num_sms ? tiles : dev.num_sms), Cfg<BN>::kThreads, Cfg<BN>::kSmem, s>>>(tm_w, tm_x, a);
+    mx_linear_kernel<XR, Out><<<unsigned(tiles < dev.num_sms ? tiles : dev.num_sms), kThreads, Cfg<XR>::kSmem, s>>>(
+        tm_w, tm_x, a);
     return cudaGetLastError() == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
 }
 
 template <typename Out>
 vce_status dispatch(const void* xc, const void* wc, LinearArgs a, cudaStream_t s, const DeviceInfo& dev) {
     a.tiles_n = int((a.n + kTokens - 1) / kTokens);
-    a.x_rows = a.n <= 16 ? 16 : a.n <= 32 ? 32 : a.n <= 64 ? 64 : kTokens;
     a.wide = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.out_stride * int64_t(sizeof(Out)) % 16 == 0;
-#ifdef X_BN
-    return launch<X_BN, Out>(xc, wc, a, s, dev);
-#endif
-    // 256 classifier rows per tile where that many tiles keep every SM busy
-    const int64_t tiles = (a.v + 255) / 256 * a.tiles_n;
-    if (tiles >= 8 * dev.num_sms) return launch<256, Out>(xc, wc, a, s, dev);
+    // Tiles go to the SMs in rounds.  What the last, partial round would hold is cut into
+    // tiles of half the rows where those still fit one round: half a round instead of one.
+    const int64_t all = (a.v + kRows - 1) / kRows, sms = dev.num_sms;
+    const int64_t whole = all * a.tiles_n / sms * sms / a.tiles_n;  // tiles of rows in full rounds
+    const int64_t halves = (a.v - whole * kRows + 127) / 128;
+    const bool cut = whole < all && halves * a.tiles_n <= sms;
+    a.whole_v = int(cut ? whole : all);
+    a.tiles_v = int(cut ? whole + halves : all);
+    if (a.n <= 16) return launch<16, Out>(xc, wc, a, s, dev);
+    if (a.n <= 64) return launch<64, Out>(xc, wc, a, s, dev);
     return launch<128, Out>(xc, wc, a, s, dev);
 }
 

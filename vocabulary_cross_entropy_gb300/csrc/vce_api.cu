@@ -354,7 +354,7 @@ vce_status mx_linear(const void* x_codes, const void* x_scales, const void* w_co
     if (n < 0 || n > kMaxRows || v < 1 || v > kMaxRows || h < 1 || h > kMaxCols || out_stride < v)
         return VCE_ERR_INVALID_ARG;
     if (n > 0 && (!x_codes || !x_scales || !w_codes || !w_scales || !out)) return VCE_ERR_INVALID_ARG;
-    if (!aligned(x_codes, 16) || !aligned(x_scales, 16) || !aligned(w_codes, 16) || !aligned(w_scales, 16) ||
+    if (!aligned(x_codes, 16) || !aligned(x_scales, 16) || !aligned(w_codes, 32) || !aligned(w_scales, 16) ||
         !aligned(out, elem_size(out_dtype)))
         return VCE_ERR_ALIGN;
     DeviceInfo dev;
