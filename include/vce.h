@@ -251,9 +251,9 @@ vce_status ce_forward_noalloc(const void* logits, int dtype, int64_t n_rows, int
  *             likeliest token's probability).
  * The token is the first one at which the cumulated weight exceeds uniform times the
  * weight of all kept ones.  A temperature of 0 or less takes the first token.  The
- * choice is made in whole-number weights of 43 to 46 fractional bits, summed exactly:
- * it does not depend on how a row is split, and a token whose weight is below
- * 2^-(bits + 1) is never drawn.
+ * choice is made in whole-number weights of 43 or 44 fractional bits (relative to the
+ * largest; each within 2^-36 of its own value), whose sums are exact: no order of
+ * additions changes a token.  A token whose weight is below 2^-45 is never drawn.
  *
  *   logits       as in ce_forward, with 1 <= vocab <= VCE_SAMPLE_MAX_VOCAB; -inf marks a
  *                token that is not allowed.

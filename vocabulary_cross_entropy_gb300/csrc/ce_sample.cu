@@ -7,21 +7,22 @@
 //
 // Weights are whole numbers.  The choice compares sums of up to 2^20 weights with a
 // border that lies between two of them; FP32 sums would move it by whole tokens, and a
-// result would depend on how the row is split.  Weight i is
-//     round(2^Q exp2((z_i - m) c)),  c = log2(e) / T,  Q + log2(vocab) <= 63,
-// to about 2^-40 of the largest before rounding (weight_of below), and 64-bit integer sums
-// are exact in any order: the row is split over threads and blocks freely, atomics
-// change nothing, equal inputs give equal tokens.
+// result would depend on the order of additions.  Weight i is
+//     2^(Q + n / 64) s / 2^36,  n / 64 + log2(s / 2^36) = (z_i - m) c,  c = log2(e) / T,
+// with n and s whole and s within 2^-36 of its exact value (relative) (step_of below).  Q is at most
+// 44 and leaves room for the sum of a row.  Integer sums are exact in any order: the
+// row is split over threads and blocks freely, and atomics change nothing.
 //
 // A row never gets sorted as a whole:
 //   heads  (top-k up to kMaxHeads, or min-p without top-p): a bound is found below
 //          which nothing survives - the k-th largest of the maxima of disjoint groups
 //          of elements, or min-p's own - and what lies above it, a little more than the
 //          head, is collected and sorted in shared memory.
-//   masses (otherwise): weights are summed into bins of equal width in the exponent,
-//          which are ordered by construction; a border is located among the bins'
-//          prefix sums, and only the elements of that one bin are collected and sorted.
-//          A bin with too many elements is divided again by the bits of (logit, index).
+//   masses (otherwise): for every n the number of elements and the sum of their s are
+//          collected, three 32-bit atomics each; n is ordered by construction and the
+//          scaling by 2^(n / 64) happens once per n.  A border is located among the
+//          prefix sums of the masses, and only the elements of that one n are collected
+//          and sorted.  Too many of them are divided again by the bits of (logit, index).
 // The logits are read once from HBM; the later passes find them in L2.
 //
 // A row is shared by a cluster of blocks (one when there are rows enough).  Block 0 joins
@@ -41,16 +42,20 @@ using namespace sm100;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 1536;         // 48 octaves, 32 bins each
-constexpr int kBinShift = 3;        // a bin is 8 steps of 2^-8 in the exponent
-constexpr float kLeastLog2 = -47.9f;  // below it a weight is 0 (Q <= 46)
+constexpr int kSteps = 64;            // values of n per octave
+constexpr int kBins = 46 * kSteps;    // 46 octaves of n, from 0 down
+constexpr float kLeastLog2 = -45.9f;  // below it a weight is 0 (Q <= 44)
+constexpr int kFracBits = 36;         // of s
+constexpr int kBiasBits = 29;         // s - 2^36 is above -2^29 and below 2^29
+constexpr int kHalfBits = 15;         // it is summed in two halves, which 2^17 elements cannot overflow
+constexpr int kMaxPart = 1 << 17;     // elements per block
 constexpr int kCap = 2048;          // collected elements; also sub-bins of a divided bin
 constexpr int kCapBits = 11;
-constexpr int kMaxHeads = 256;      // top-k of the collecting path, per block of the cluster
+constexpr int kMaxHeads = 256;      // top-k of the collecting path
 constexpr int kIndexBits = 20;      // vocabulary of at most 2^20
 constexpr int kMaxCluster = 8;
 
-__device__ const uint64_t kExp2Table[256] = {
+__device__ const uint64_t kExp2Table[kSteps] = {
 #include "exp2_table.inc"
 };
 
@@ -74,11 +79,11 @@ struct Command {
 };
 
 struct Shared {
-    uint64_t mass[kBins];     // block 0: inclusive prefix sums once joined
+    uint64_t mass[kBins];  // two 32-bit sums, then the sum of s, then (block 0) inclusive prefix sums of masses
     uint32_t count[kBins];
-    uint64_t list[kCap];      // collected keys; masses of sub-bins
-    uint64_t sums[kCap];      // inclusive prefix sums of the sorted list; counts of sub-bins
-    uint64_t table[256];
+    uint64_t list[kCap];   // collected keys; masses of sub-bins
+    uint64_t sums[kCap];   // inclusive prefix sums of the sorted list; counts of sub-bins
+    uint64_t table[kSteps];
     uint64_t warp_sum[kWarps], warp_sum2[kWarps];
     float group[kThreads];
     float row_max[kMaxCluster], bound[kMaxCluster];  // a block writes its own slot, once
@@ -87,6 +92,12 @@ struct Shared {
     uint64_t min_key, max_key, kept_minp;
     uint32_t n_list, found, argmax;
 };
+
+__device__ __forceinline__ float max_nan(float a, float b) {  // a NaN stays
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 
 __device__ __forceinline__ uint32_t order_bits(float z) {  // monotone in z
     const uint32_t b = __float_as_uint(z);
@@ -118,17 +129,18 @@ __device__ __forceinline__ Scale make_scale(float m, float t) {
 // The leading term of (z - m) c, monotone in z.
 __device__ __forceinline__ float log2_weight(const Scale& s, float z) { return __fmul_rn(z - s.m, s.ch); }
 
-// round(256 p) by adding 1.5 x 2^23 (|256 p| < 2^22)
-__device__ __forceinline__ int steps_of(float p) { return __float_as_int(fmaf(p, 256.f, 12582912.f)) - 0x4b400000; }
-
-__device__ __forceinline__ int bin_of(float p) { return -steps_of(p) >> kBinShift; }
-
-// round(2^Q 2^((z - m) c)) for a log2_weight above kLeastLog2.
+// The element's n (as the bin -n) and s of a log2_weight above kLeastLog2.
 //   (z - m) and its product with c are carried as sums of two floats (TwoSum, FMA), about
-//   2^-47 relative.  The exponent is n / 256 + f with |f| <= 2^-9; 2^(n / 256) comes
-//   from the table, 2^f - 1 = g from its series to the fourth power, split into a
-//   multiple of 2^-31 and a rest so that g is a whole number of 2^-40.
-__device__ __forceinline__ uint64_t weight_of(const Scale& s, float z, const uint64_t* table, int q_bits) {
+//   2^-47 relative.  The exponent is n / 64 + f with |f| <= 2^-7; 2^f - 1 from its series
+//   to the fifth power, its linear term split into a multiple of 2^-29 and a rest.
+//   round(64 p) is taken by adding 1.5 x 2^23.
+__device__ __forceinline__ int bin_of(float p) { return 0x4b400000 - __float_as_int(fmaf(p, float(kSteps), 12582912.f)); }
+
+struct Step {
+    int bin;
+    int g;  // s - 2^kFracBits
+};
+__device__ __forceinline__ Step step_of(const Scale& s, float z) {
     const float d = z - s.m;
     const float b = d - z;
     const float dl = (z - (d - b)) - (s.m + b);
@@ -136,29 +148,41 @@ __device__ __forceinline__ uint64_t weight_of(const Scale& s, float z, const uin
     float e = fmaf(d, s.ch, -p);
     e = fmaf(d, s.cl, e);
     e = fmaf(dl, s.ch, e);
-    const float t = fmaf(p, 256.f, 12582912.f);
-    const int n = __float_as_int(t) - 0x4b400000;
-    const float f = fmaf(t - 12582912.f, -1.f / 256.f, p);
+    const float t = fmaf(p, float(kSteps), 12582912.f);
+    const float f = fmaf(t - 12582912.f, -1.f / kSteps, p);
     const float lh = 0.693147182464599609375f, ll = -1.904654323148236e-9f;  // ln 2 = lh + ll
     const float a = f * lh;
     float r = fmaf(f, lh, -a);
     r = fmaf(f, ll, r);
     r = fmaf(e, lh, r);
-    // ln2^2 / 2, ln2^3 / 6, ln2^4 / 24
-    const float c2 = 0.24022650695910072f, c3 = 0.05550410866482158f, c4 = 0.009618129107628477f;
+    // ln2^k / k! for k = 2 .. 5
+    const float c2 = 0.24022650695910072f, c3 = 0.05550410866482158f, c4 = 0.009618129107628477f,
+                c5 = 0.0013333558146428443f;
     const float fe = f + e;
-    r = fmaf(fe * fe, fmaf(fmaf(c4, f, c3), f, c2), r);
-    const float big = 1.5f * 0x1p-8f;  // |a| < 2^-9: the sum stays in big's binade, whose last bit is 2^-31
+    r = fmaf(fe * fe, fmaf(fmaf(fmaf(c5, f, c4), f, c3), f, c2), r);
+    const float big = 1.5f * 0x1p-6f;  // |a| < 2^-7: the sum stays in big's binade, whose last bit is 2^-29
     const float u = a + big;
     const int hi = __float_as_int(u) - __float_as_int(big);
     r += a - (u - big);
-    const int lo = __float_as_int(fmaf(r, 0x1p40f, 12582912.f)) - 0x4b400000;
-    const int g = hi * 512 + lo;  // 2^f - 1 in units of 2^-40
-    const uint64_t w = table[n & 255];
-    const int64_t more = (int64_t(uint32_t(w >> 32)) * int64_t(g)) >> 8;  // 63 fractional bits
-    const int shift = 63 - q_bits - (n >> 8);                             // at least 17
-    if (shift > 64) return 0;
-    return (((w + uint64_t(more)) >> (shift - 1)) + 1) >> 1;
+    const int lo = __float_as_int(fmaf(r, 0x1p36f, 12582912.f)) - 0x4b400000;
+    return {0x4b400000 - __float_as_int(t), hi * 128 + lo};
+}
+
+// round(2^Q 2^(-bin / 64) sum / 2^36) for a sum of s below 2^57
+__device__ __forceinline__ uint64_t scale_up(uint64_t sum, int bin, const uint64_t* table, int q_bits) {
+    const int n = -bin;
+    const uint64_t t = table[n & (kSteps - 1)];                       // 63 fractional bits
+    const int shift = 63 + kFracBits - q_bits - (n >> 6);             // 55 .. 102
+    const uint64_t hi = __umul64hi(sum, t), lo = sum * t;
+    uint64_t q;  // twice the value, rounded down
+    if (shift - 1 < 64) q = hi << (65 - shift) | lo >> (shift - 1);
+    else q = hi >> (shift - 65);
+    return (q + 1) >> 1;
+}
+
+__device__ __forceinline__ uint64_t weight_of(const Scale& s, float z, const uint64_t* table, int q_bits) {
+    const Step st = step_of(s, z);
+    return scale_up((uint64_t(1) << kFracBits) + int64_t(st.g), st.bin, table, q_bits);
 }
 
 // floor(x y) for a float 0 <= x < 1 and y < 2^63; ``*exact`` tells whether nothing was cut off
@@ -254,16 +278,15 @@ __device__ __forceinline__ void row_barrier(int cluster) {
     else cluster_sync();
 }
 
-// Inclusive prefix sums of a[0 .. n) in place (n at most 4 x kThreads); every thread calls.
-__device__ __forceinline__ void prefix_sums(uint64_t* a, int n, uint64_t* warp_sum) {
+// Inclusive prefix sums of a[0 .. n) in place (n at most 6 x kThreads); every thread calls.
+template <typename T>
+__device__ __forceinline__ void prefix_sums(T* a, int n, uint64_t* warp_sum) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint64_t v[4], s = 0;
-    const int i0 = int(threadIdx.x) * 4;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        s += i0 + k < n ? a[i0 + k] : 0;
-        v[k] = s;
-    }
+    const int per = (n + kThreads - 1) / kThreads;
+    const int i0 = int(threadIdx.x) * per;
+    uint64_t s = 0;
+    for (int k = 0; k < per; ++k)
+        if (i0 + k < n) s += a[i0 + k];
     uint64_t t = s;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -274,9 +297,11 @@ __device__ __forceinline__ void prefix_sums(uint64_t* a, int n, uint64_t* warp_s
     __syncthreads();
     uint64_t before = t - s;
     for (int w = 0; w < warp; ++w) before += warp_sum[w];
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        if (i0 + k < n) a[i0 + k] = before + v[k];
+    for (int k = 0; k < per; ++k)
+        if (i0 + k < n) {
+            before += a[i0 + k];
+            a[i0 + k] = T(before);
+        }
     __syncthreads();
 }
 
@@ -424,12 +449,17 @@ struct Sampler {
         }
         cmd = tell(cmd);
         const Scale s = sc;
+        // the bin's logits lie in here (the bounds are generous, the bin itself decides)
+        const float far = (float(cmd.bin) + 0.75f) / (kSteps * s.ch), near = (float(cmd.bin) - 0.75f) / (kSteps * s.ch);
+        const float slack = fabsf(s.m) * 0x1p-21f;
+        const float z_lo = s.m - far - slack, z_hi = s.m - near + slack;
         // Keys have 52 bits and differ, and a division leaves at most 2^-11 of their range
         // (one key at last): five levels at most.
         for (int level = 0; level < 8; ++level) {
             const int bin = cmd.bin;
             const uint64_t lo = cmd.lo, hi = cmd.hi;
             auto mine = [=](float z, int i) {
+                if (!(z >= z_lo && z <= z_hi)) return false;
                 const float p = log2_weight(s, z);
                 if (!(p > kLeastLog2) || bin_of(p) != bin) return false;
                 const uint64_t k = key_of(z, i);
@@ -528,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
     const int tid = threadIdx.x;
     const int rank = a.cluster == 1 ? 0 : int(cluster_ctarank());
     const int64_t row = int64_t(blockIdx.x) / a.cluster;
-    if (tid < 256) sh.table[tid] = kExp2Table[tid];
+    if (tid < kSteps) sh.table[tid] = kExp2Table[tid];
 
     constexpr int VE = 16 / sizeof(T);
     const T* base = static_cast<const T*>(a.logits) + row * a.stride;
@@ -549,11 +579,8 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
 
     // ---- the largest logit, and the largest of every thread's elements ----
     float m = -INFINITY;
-    bool bad = false;
-    for_each(s.part, a.dev_status, [&](float z, int) {
-        m = fmaxf(m, z);
-        bad |= !(z < INFINITY);
-    });
+    for_each(s.part, a.dev_status, [&](float z, int) { m = max_nan(m, z); });
+    const bool bad = !(m < INFINITY);  // a NaN or +inf among them
     sh.group[tid] = m;
     float wm = m;
 #pragma unroll
@@ -563,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
     // top-k: each block's j-th largest group maximum, j = ceil(k / blocks); at least k
     // elements of the row are as large as the smallest of these
     const int j = (top_k + a.cluster - 1) / a.cluster;
-    const bool heads_k = by_k && j <= kMaxHeads;
+    const bool heads_k = by_k && top_k <= kMaxHeads;
     if (heads_k) {
         int groups = 64;  // of neighbouring threads: larger groups bound less tightly but rank faster
         while (groups < 4 * j && groups < kThreads) groups *= 2;
@@ -674,45 +701,54 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
         }
     }
 
-    // ---- weights of the whole row, summed into bins ----
+    // ---- weights of the whole row, summed by n ----
     for (int i = tid; i < kBins; i += kThreads) sh.mass[i] = 0, sh.count[i] = 0;
     __syncthreads();
+    // min-p (with top-p): whole bins above the border, and single weights next to it
+    const int edge = by_min ? max(0, bin_of(fmaxf(kLeastLog2, log2f(min_p))) - 2) : kBins;
     uint64_t above = 0;
     for_each(s.part, a.dev_status, [&](float z, int) {
-        const float p = log2_weight(sc, z);
-        if (!(p > kLeastLog2)) return;
-        const uint64_t w = weight_of(sc, z, sh.table, a.q_bits);
-        const int b = bin_of(p);
-        if (!VCE_BOUNDS(b >= 0 && b < kBins, a.dev_status)) return;
-        s.add_mass(&sh.mass[b], w);
-        if (by_k) atomicAdd(&sh.count[b], 1u);
-        if (by_min && w >= least) above += w;
+        if (!(log2_weight(sc, z) > kLeastLog2)) return;
+        const Step st = step_of(sc, z);
+        if (!VCE_BOUNDS(st.bin >= 0 && st.bin < kBins, a.dev_status)) return;
+        const uint32_t x = uint32_t(st.g + (1 << kBiasBits));
+        uint32_t* at = reinterpret_cast<uint32_t*>(&sh.mass[st.bin]);
+        atomicAdd(at, x & ((1u << kHalfBits) - 1));
+        atomicAdd(at + 1, x >> kHalfBits);
+        atomicAdd(&sh.count[st.bin], 1u);
+        if (st.bin >= edge && st.bin < edge + 5) {
+            const uint64_t w = weight_of(sc, z, sh.table, a.q_bits);
+            if (w >= least) above += w;
+        }
     });
     if (by_min) {
         above = s.block_sum(above);
         if (tid == 0) sh.kept_minp = above;
     }
+    __syncthreads();
+    for (int i = tid; i < kBins; i += kThreads) {
+        const uint64_t m2 = sh.mass[i], c = sh.count[i];
+        sh.mass[i] = (c << kFracBits) - (c << kBiasBits) + (m2 & 0xffffffffu) + ((m2 >> 32) << kHalfBits);
+    }
     s.barrier();
     uint64_t total = 0;
     if (s.lead()) {
-        for (int i = tid; i < kBins; i += kThreads)
-            for (int c = 1; c < a.cluster; ++c) {
-                sh.mass[i] += remote(&sh.mass[i], c);
-                if (by_k) sh.count[i] += remote(&sh.count[i], c);
-            }
+        for (int i = tid; i < kBins; i += kThreads) {
+            uint64_t sum = sh.mass[i];
+            uint32_t c = sh.count[i];
+            for (int r = 1; r < a.cluster; ++r) sum += remote(&sh.mass[i], r), c += remote(&sh.count[i], r);
+            sh.mass[i] = c ? scale_up(sum, i, sh.table, a.q_bits) : 0;
+            sh.count[i] = c;
+        }
         __syncthreads();
         prefix_sums(sh.mass, kBins, sh.warp_sum);
-        if (by_k) {  // counts through the 64-bit scratch
-            for (int i = tid; i < kBins; i += kThreads) sh.sums[i] = sh.count[i];
-            __syncthreads();
-            prefix_sums(sh.sums, kBins, sh.warp_sum);
-            for (int i = tid; i < kBins; i += kThreads) sh.count[i] = uint32_t(sh.sums[i]);
-            __syncthreads();
+        if (by_k) {
+            prefix_sums(sh.count, kBins, sh.warp_sum);
+            cmd.flag = sh.count[kBins - 1] > uint32_t(top_k);  // the k-th has a weight
         }
         total = sh.mass[kBins - 1];
-        cmd.flag = by_k && sh.count[kBins - 1] > uint32_t(top_k);  // the k-th has a weight
         if (by_min) {
-            above = 0;
+            above = edge ? sh.mass[edge - 1] : 0;
             for (int c = 0; c < a.cluster; ++c) above += remote(&sh.kept_minp, c);
         }
     }
@@ -745,9 +781,11 @@ vce_status launch_ce_sample(const void* logits, int dtype, int64_t n, int64_t vo
                  dev_status};
     int bits = 0;
     while ((int64_t(1) << bits) < vocab) ++bits;
-    a.q_bits = 63 - bits < 46 ? 63 - bits : 46;
+    a.q_bits = 63 - bits < 44 ? 63 - bits : 44;
     // As many blocks per row as fill the SMs twice, each with a part worth a block
-    while (a.cluster < kMaxCluster && n * a.cluster * 2 <= 2 * dev.num_sms && vocab / (a.cluster * 2) >= 4 * kThreads)
+    while (a.cluster < kMaxCluster &&
+           (vocab > int64_t(a.cluster) * (kMaxPart - 64) ||
+            (n * a.cluster * 2 <= 2 * dev.num_sms && vocab / (a.cluster * 2) >= 4 * kThreads)))
         a.cluster *= 2;
     if (n * a.cluster > 0x7fffffff) return VCE_ERR_INVALID_ARG;
     auto kernel = dtype == VCE_BF16 ? ce_sample_kernel<__nv_bfloat16> : ce_sample_kernel<float>;
