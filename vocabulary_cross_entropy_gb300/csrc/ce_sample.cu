@@ -42,6 +42,12 @@ using namespace sm100;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+#ifndef X_U
+#define X_U 1
+#endif
+#ifndef X_FILL
+#define X_FILL 2
+#endif
 constexpr int kSteps = 64;            // values of n per octave
 constexpr int kBins = 46 * kSteps;    // 46 octaves of n, from 0 down
 constexpr float kLeastLog2 = -45.9f;  // below it a weight is 0 (Q <= 44)
@@ -230,31 +236,37 @@ __device__ __forceinline__ float element<__nv_bfloat16>(uint4 v, int e) {
 __device__ __forceinline__ float one(const float* p) { return *p; }
 __device__ __forceinline__ float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
-// fn(logit, index) for every element of the block's part
-template <typename T, typename F>
+// fn(logit, index) for every element of the block's part, U vectors in flight per thread.
+// The vectors that lie in the row as a whole come first, then the elements of the two
+// that may not.
+template <int U, typename T, typename F>
 __device__ __forceinline__ void for_each(const Part<T>& p, int* dev_status, F fn) {
-    constexpr int VE = 16 / sizeof(T), U = 4;
-    for (int q = p.q0 + int(threadIdx.x); q < p.q1; q += U * kThreads) {
+    constexpr int VE = 16 / sizeof(T);
+    const int tid = threadIdx.x;
+    const int head = p.off > 0 ? 1 : 0, whole = (p.off + p.vocab) / VE;  // whole vectors: [head, whole)
+    const int end = min(p.q1, whole);
+    for (int q = max(p.q0, head) + tid; q < end; q += U * kThreads) {
+        const T* at = p.row + (q * VE - p.off);
         uint4 v[U];
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int qk = q + k * kThreads, i = qk * VE - p.off;
-            if (qk < p.q1 && i >= 0 && i + VE <= p.vocab &&
-                VCE_BOUNDS(aligned16(p.row + i), dev_status))
-                v[k] = __ldg(reinterpret_cast<const uint4*>(p.row + i));
-        }
+        for (int k = 0; k < U; ++k)
+            if (q + k * kThreads < end && VCE_BOUNDS(aligned16(at), dev_status))
+                v[k] = __ldg(reinterpret_cast<const uint4*>(at + k * kThreads * VE));
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-            const int qk = q + k * kThreads, i = qk * VE - p.off;
-            if (qk >= p.q1) break;
-            if (i >= 0 && i + VE <= p.vocab) {
+            if (q + k * kThreads >= end) break;
+            const int i = (q + k * kThreads) * VE - p.off;
 #pragma unroll
-                for (int e = 0; e < VE; ++e) fn(element<T>(v[k], e), i + e);
-            } else {
-                for (int e = 0; e < VE; ++e)
-                    if (i + e >= 0 && i + e < p.vocab) fn(one(p.row + i + e), i + e);
-            }
+            for (int e = 0; e < VE; ++e) fn(element<T>(v[k], e), i + e);
         }
+    }
+    // the first vector's elements, then those behind the whole vectors
+    const int first = head && p.q0 == 0 && p.q1 > 0 ? min(VE - p.off, p.vocab) : 0;
+    const int tail0 = max(whole * VE - p.off, head ? VE - p.off : 0);
+    const int last = p.q1 > p.q0 && p.q1 * VE - p.off >= p.vocab ? max(p.vocab - tail0, 0) : 0;
+    if (tid < first + last) {
+        const int i = tid < first ? tid : tail0 + tid - first;
+        fn(one(p.row + i), i);
     }
 }
 
@@ -364,7 +376,7 @@ struct Sampler {
     __device__ __forceinline__ void collect(F take) {
         if (threadIdx.x == 0) sh.n_list = 0;
         __syncthreads();
-        for_each(part, a.dev_status, [&](float z, int i) {
+        for_each<4>(part, a.dev_status, [&](float z, int i) {
             if (!take(z, i)) return;
             const uint32_t at = atomicAdd(&sh.n_list, 1u);
             if (at < kCap) sh.list[at] = key_of(z, i);
@@ -398,7 +410,8 @@ struct Sampler {
     }
 
     // Block 0: the first i < n with s[i] >= target (n when there is none).
-    __device__ __forceinline__ int first_at_least(const uint64_t* s, int n, uint64_t target) {
+    template <typename V>
+    __device__ __forceinline__ int first_at_least(const V* s, int n, V target) {
         __syncthreads();
         if (threadIdx.x == 0) sh.found = uint32_t(n);
         __syncthreads();
@@ -425,47 +438,105 @@ struct Sampler {
         return t;
     }
 
+    // The elements of ``cmd``'s bin and key range, whose logits lie between z_lo and z_hi.
+    struct InBin {
+        Scale s;
+        float z_lo, z_hi;
+        int bin;
+        uint64_t lo, hi;
+        __device__ __forceinline__ bool operator()(float z, int i) const {
+            if (!(z >= z_lo && z <= z_hi)) return false;
+            const float p = log2_weight(s, z);
+            if (!(p > kLeastLog2) || bin_of(p) != bin) return false;
+            const uint64_t k = key_of(z, i);
+            return k >= lo && k <= hi;
+        }
+    };
+    __device__ __forceinline__ InBin in_bin(const Command& cmd) const {
+        // the bounds are generous; the bin itself decides
+        const float far = (float(cmd.bin) + 0.75f) / (kSteps * sc.ch), near = (float(cmd.bin) - 0.75f) / (kSteps * sc.ch);
+        const float slack = fabsf(sc.m) * 0x1p-21f;
+        return {sc, sc.m - far - slack, sc.m - near + slack, cmd.bin, cmd.lo, cmd.hi};
+    }
+
+    // A range that holds more elements than a list: its keys divided into kCap ranges of
+    // equal width, of which the one with the target is the new range.  ``base`` and
+    // ``base_count`` become what lies before it.  Rare, and kept out of the common code.
+    __device__ __noinline__ void divide(Command& cmd, bool by_count, uint64_t target, uint64_t& base,
+                                        uint32_t& base_count) {
+        const InBin mine = in_bin(cmd);
+        uint64_t kmin = ~0ull, kmax = 0;
+        for_each<1>(part, a.dev_status, [&](float z, int i) {
+            if (!mine(z, i)) return;
+            const uint64_t k = key_of(z, i);
+            kmin = k < kmin ? k : kmin;
+            kmax = k > kmax ? k : kmax;
+        });
+        if (threadIdx.x == 0) sh.min_key = ~0ull, sh.max_key = 0;
+        for (int i = threadIdx.x; i < kCap; i += kThreads) sh.list[i] = 0, sh.sums[i] = 0;
+        __syncthreads();
+        atomicMin(reinterpret_cast<unsigned long long*>(&sh.min_key), static_cast<unsigned long long>(kmin));
+        atomicMax(reinterpret_cast<unsigned long long*>(&sh.max_key), static_cast<unsigned long long>(kmax));
+        barrier();
+        if (lead()) {
+            cmd.lo = ~0ull, cmd.hi = 0;
+            for (int c = 0; c < a.cluster; ++c) {
+                const uint64_t x = remote(&sh.min_key, c), y = remote(&sh.max_key, c);
+                cmd.lo = x < cmd.lo ? x : cmd.lo;
+                cmd.hi = y > cmd.hi ? y : cmd.hi;
+            }
+        }
+        cmd = tell(cmd);
+        const uint64_t l = cmd.lo, h = cmd.hi;
+        const int bits = 64 - __clzll(int64_t(h - l));
+        const int shift = bits > kCapBits ? bits - kCapBits : 0;
+        for_each<1>(part, a.dev_status, [&](float z, int i) {
+            if (!mine(z, i)) return;
+            const uint64_t b = (h - key_of(z, i)) >> shift;
+            if (!VCE_BOUNDS(b < uint64_t(kCap), a.dev_status)) return;
+            add_mass(&sh.list[b], weight_of(sc, z, sh.table, a.q_bits));
+            add_mass(&sh.sums[b], 1);
+        });
+        barrier();
+        if (lead()) {
+            for (int i = threadIdx.x; i < kCap; i += kThreads)
+                for (int c = 1; c < a.cluster; ++c) {
+                    sh.list[i] += remote(&sh.list[i], c);
+                    sh.sums[i] += remote(&sh.sums[i], c);
+                }
+            __syncthreads();
+            prefix_sums(sh.list, kCap, sh.warp_sum);
+            prefix_sums(sh.sums, kCap, sh.warp_sum);
+            const int b = min(by_count ? first_at_least(sh.sums, kCap, target - base_count)
+                                       : first_at_least(sh.list, kCap, target > base ? target - base : 1),
+                              kCap - 1);
+            if (b > 0) base += sh.list[b - 1], base_count += uint32_t(sh.sums[b - 1]);
+            const uint64_t width = (uint64_t(1) << shift) - 1;
+            cmd.hi = h - (uint64_t(b) << shift);
+            cmd.lo = cmd.hi - l > width ? cmd.hi - width : l;
+        }
+        cmd = tell(cmd);
+    }
+
     // Finds the first element, in order, at which the cumulated weight (or, by_count, the
     // number of elements) reaches ``target``.  All blocks call; the results are valid in
     // block 0: the element's key and the cumulated weight up to and with it.  ``target`` is
     // within the total.
-    __device__ void locate(bool by_count, uint64_t target, uint64_t& key, uint64_t& upto) {
+    __device__ __forceinline__ void locate(bool by_count, uint64_t target, uint64_t& key, uint64_t& upto) {
         uint64_t base = 0;
         uint32_t base_count = 0;
         Command cmd{0, ~0ull, 0, 0};
         if (lead()) {
-            if (by_count) {
-                __syncthreads();
-                if (threadIdx.x == 0) sh.found = kBins - 1;
-                __syncthreads();
-                for (int i = threadIdx.x; i < kBins; i += kThreads)
-                    if (sh.count[i] >= target && (i == 0 || sh.count[i - 1] < target)) sh.found = uint32_t(i);
-                __syncthreads();
-                cmd.bin = int(sh.found);
-            } else {
-                cmd.bin = min(first_at_least(sh.mass, kBins, target), kBins - 1);
-            }
+            cmd.bin = min(by_count ? first_at_least(sh.count, kBins, uint32_t(target))
+                                   : first_at_least(sh.mass, kBins, target),
+                          kBins - 1);
             if (cmd.bin > 0) base = sh.mass[cmd.bin - 1], base_count = sh.count[cmd.bin - 1];
         }
         cmd = tell(cmd);
-        const Scale s = sc;
-        // the bin's logits lie in here (the bounds are generous, the bin itself decides)
-        const float far = (float(cmd.bin) + 0.75f) / (kSteps * s.ch), near = (float(cmd.bin) - 0.75f) / (kSteps * s.ch);
-        const float slack = fabsf(s.m) * 0x1p-21f;
-        const float z_lo = s.m - far - slack, z_hi = s.m - near + slack;
         // Keys have 52 bits and differ, and a division leaves at most 2^-11 of their range
         // (one key at last): five levels at most.
         for (int level = 0; level < 8; ++level) {
-            const int bin = cmd.bin;
-            const uint64_t lo = cmd.lo, hi = cmd.hi;
-            auto mine = [=](float z, int i) {
-                if (!(z >= z_lo && z <= z_hi)) return false;
-                const float p = log2_weight(s, z);
-                if (!(p > kLeastLog2) || bin_of(p) != bin) return false;
-                const uint64_t k = key_of(z, i);
-                return k >= lo && k <= hi;
-            };
-            collect(mine);
+            collect(in_bin(cmd));
             barrier();
             if (lead()) {
                 int n;
@@ -480,58 +551,9 @@ struct Sampler {
             }
             cmd = tell(cmd);
             if (cmd.flag) return;
-            // Too many: the range of their keys, then masses and counts of its sub-bins.
-            uint64_t kmin = ~0ull, kmax = 0;
-            for_each(part, a.dev_status, [&](float z, int i) {
-                if (!mine(z, i)) return;
-                const uint64_t k = key_of(z, i);
-                kmin = k < kmin ? k : kmin;
-                kmax = k > kmax ? k : kmax;
-            });
-            if (threadIdx.x == 0) sh.min_key = ~0ull, sh.max_key = 0;
-            for (int i = threadIdx.x; i < kCap; i += kThreads) sh.list[i] = 0, sh.sums[i] = 0;
-            __syncthreads();
-            atomicMin(reinterpret_cast<unsigned long long*>(&sh.min_key), static_cast<unsigned long long>(kmin));
-            atomicMax(reinterpret_cast<unsigned long long*>(&sh.max_key), static_cast<unsigned long long>(kmax));
-            barrier();
-            if (lead()) {
-                cmd.lo = ~0ull, cmd.hi = 0;
-                for (int c = 0; c < a.cluster; ++c) {
-                    const uint64_t x = remote(&sh.min_key, c), y = remote(&sh.max_key, c);
-                    cmd.lo = x < cmd.lo ? x : cmd.lo;
-                    cmd.hi = y > cmd.hi ? y : cmd.hi;
-                }
-            }
-            cmd = tell(cmd);
-            const uint64_t l = cmd.lo, h = cmd.hi;
-            const int bits = 64 - __clzll(int64_t(h - l));
-            const int shift = bits > kCapBits ? bits - kCapBits : 0;
-            for_each(part, a.dev_status, [&](float z, int i) {
-                if (!mine(z, i)) return;
-                const uint64_t b = (h - key_of(z, i)) >> shift;
-                if (!VCE_BOUNDS(b < uint64_t(kCap), a.dev_status)) return;
-                add_mass(&sh.list[b], weight_of(s, z, sh.table, a.q_bits));
-                add_mass(&sh.sums[b], 1);
-            });
-            barrier();
-            if (lead()) {
-                for (int i = threadIdx.x; i < kCap; i += kThreads)
-                    for (int c = 1; c < a.cluster; ++c) {
-                        sh.list[i] += remote(&sh.list[i], c);
-                        sh.sums[i] += remote(&sh.sums[i], c);
-                    }
-                __syncthreads();
-                prefix_sums(sh.list, kCap, sh.warp_sum);
-                prefix_sums(sh.sums, kCap, sh.warp_sum);
-                const int b = min(by_count ? first_at_least(sh.sums, kCap, target - base_count)
-                                           : first_at_least(sh.list, kCap, target - base),
-                                  kCap - 1);
-                if (b > 0) base += sh.list[b - 1], base_count += uint32_t(sh.sums[b - 1]);
-                const uint64_t width = (uint64_t(1) << shift) - 1;
-                cmd.hi = h - (uint64_t(b) << shift);
-                cmd.lo = cmd.hi - l > width ? cmd.hi - width : l;
-            }
-            cmd = tell(cmd);
+            Sampler copy = *this;  // its address is taken there, not here
+            copy.divide(cmd, by_count, target, base, base_count);
+            turn = copy.turn;
         }
     }
 
@@ -579,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
 
     // ---- the largest logit, and the largest of every thread's elements ----
     float m = -INFINITY;
-    for_each(s.part, a.dev_status, [&](float z, int) { m = max_nan(m, z); });
+    for_each<4>(s.part, a.dev_status, [&](float z, int) { m = max_nan(m, z); });
     const bool bad = !(m < INFINITY);  // a NaN or +inf among them
     sh.group[tid] = m;
     float wm = m;
@@ -642,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
         if (tid == 0) sh.argmax = 0xffffffffu;
         __syncthreads();
         uint32_t first = 0xffffffffu;
-        for_each(s.part, a.dev_status, [&](float z, int i) {
+        for_each<4>(s.part, a.dev_status, [&](float z, int i) {
             if (z == row_max && uint32_t(i) < first) first = uint32_t(i);
         });
         if (first != 0xffffffffu) atomicMin(&sh.argmax, first);
@@ -707,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
     // min-p (with top-p): whole bins above the border, and single weights next to it
     const int edge = by_min ? max(0, bin_of(fmaxf(kLeastLog2, log2f(min_p))) - 2) : kBins;
     uint64_t above = 0;
-    for_each(s.part, a.dev_status, [&](float z, int) {
+    for_each<X_U>(s.part, a.dev_status, [&](float z, int) {
         if (!(log2_weight(sc, z) > kLeastLog2)) return;
         const Step st = step_of(sc, z);
         if (!VCE_BOUNDS(st.bin >= 0 && st.bin < kBins, a.dev_status)) return;
@@ -752,20 +774,27 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
             for (int c = 0; c < a.cluster; ++c) above += remote(&sh.kept_minp, c);
         }
     }
+    // the border of top-k, then of top-p, then the draw: one after the other, each of
+    // them within the mass that the one before left
+    const bool cut = by_k && s.tell(cmd).flag;
     uint64_t key = 0, mass = total, upto = 0;
-    if (by_k && s.tell(cmd).flag) {
-        s.locate(true, uint64_t(top_k), key, upto);
-        mass = upto;
+#pragma unroll 1
+    for (int step = cut ? 0 : by_p ? 1 : 2; step < 3; ++step) {
+        uint64_t target;
+        if (step == 0) {
+            target = uint64_t(top_k);
+        } else if (step == 1) {
+            if (!by_p) continue;
+            target = floor_product(fmaxf(top_p, 0.f), mass, &exact);
+            target += exact ? 0 : 1;
+            if (target == 0) target = 1;
+        } else {
+            if (by_min && above < mass) mass = above;
+            target = u >= 1.f ? mass : floor_product(fmaxf(u, 0.f), mass, &exact) + 1;
+        }
+        s.locate(step == 0, target, key, upto);
+        if (step < 2) mass = upto;
     }
-    if (by_p) {
-        uint64_t target = floor_product(fmaxf(top_p, 0.f), mass, &exact);
-        target += exact ? 0 : 1;
-        s.locate(false, target ? target : 1, key, upto);
-        mass = upto;
-    }
-    if (by_min && above < mass) mass = above;
-    const uint64_t target = u >= 1.f ? mass - 1 : floor_product(fmaxf(u, 0.f), mass, &exact);
-    s.locate(false, target + 1, key, upto);
     if (s.lead() && tid == 0) s.finish(row, key, mass, temp);
     s.barrier();
 }
@@ -785,7 +814,7 @@ vce_status launch_ce_sample(const void* logits, int dtype, int64_t n, int64_t vo
     // As many blocks per row as fill the SMs twice, each with a part worth a block
     while (a.cluster < kMaxCluster &&
            (vocab > int64_t(a.cluster) * (kMaxPart - 64) ||
-            (n * a.cluster * 2 <= 2 * dev.num_sms && vocab / (a.cluster * 2) >= 4 * kThreads)))
+            (n * a.cluster * 2 <= X_FILL * dev.num_sms && vocab / (a.cluster * 2) >= 4 * kThreads)))
         a.cluster *= 2;
     if (n * a.cluster > 0x7fffffff) return VCE_ERR_INVALID_ARG;
     auto kernel = dtype == VCE_BF16 ? ce_sample_kernel<__nv_bfloat16> : ce_sample_kernel<float>;
