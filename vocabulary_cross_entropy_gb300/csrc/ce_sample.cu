@@ -42,12 +42,6 @@ using namespace sm100;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-#ifndef X_U
-#define X_U 1
-#endif
-#ifndef X_FILL
-#define X_FILL 2
-#endif
 constexpr int kSteps = 64;            // values of n per octave
 constexpr int kBins = 46 * kSteps;    // 46 octaves of n, from 0 down
 constexpr float kLeastLog2 = -45.9f;  // below it a weight is 0 (Q <= 44)
@@ -84,18 +78,28 @@ struct Command {
     int bin, flag;
 };
 
+// Which elements to collect: logits in [z_lo, z_hi] with a log2_weight above p_least, in
+// ``cmd``'s range of keys and, unless its bin is negative, in its bin.
+struct Wanted {
+    float z_lo, z_hi, p_least;
+    Command cmd;
+};
+
 struct Shared {
     uint64_t mass[kBins];  // two 32-bit sums, then the sum of s, then (block 0) inclusive prefix sums of masses
     uint32_t count[kBins];
     uint64_t list[kCap];   // collected keys; masses of sub-bins
     uint64_t sums[kCap];   // inclusive prefix sums of the sorted list; counts of sub-bins
     uint64_t table[kSteps];
-    uint64_t warp_sum[kWarps], warp_sum2[kWarps];
+    uint64_t warp_sum[kWarps];
     float group[kThreads];
-    float row_max[kMaxCluster], bound[kMaxCluster];  // a block writes its own slot, once
-    int bad[kMaxCluster];
-    Command cmd[2];  // consecutive commands take turns: a late reader finds its own intact
+    float warp_max[kWarps];
+    // written by every block into every block's memory, each into the slot of its rank, once
+    float row_max[kMaxCluster], bound[kMaxCluster];
+    Command cmd[2];  // by block 0; consecutive commands take turns: a late reader finds its own intact
+    uint32_t part_n[kMaxCluster];  // block 0's: what the others have collected
     uint64_t min_key, max_key, kept_minp;
+    float my_bound;
     uint32_t n_list, found, argmax;
 };
 
@@ -174,6 +178,48 @@ __device__ __forceinline__ Step step_of(const Scale& s, float z) {
     return {0x4b400000 - __float_as_int(t), hi * 128 + lo};
 }
 
+// step_of for two logits at once, two lanes to an instruction, and with the signs turned:
+// x = (m - z) c = P + E is not negative, F = P - bin / 64, and 2^-(F + E) - 1 is wanted.
+// ``s`` is s + 2^29 - 2^36, not negative.
+struct Step2 {
+    float2 p;
+    int bin[2];
+    uint32_t s[2];
+};
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ Step2 step_of2(const Scale& sc, float2 z) {
+    const float2 minus = both(-1.f), m = both(sc.m);
+    const float2 d = __fadd2_rn(z, both(-sc.m));
+    const float2 b = __ffma2_rn(z, minus, d);
+    const float2 dl = __ffma2_rn(__fadd2_rn(m, b), minus, __ffma2_rn(__ffma2_rn(b, minus, d), minus, z));
+    const float2 nch = both(-sc.ch);
+    const float2 p = __fmul2_rn(d, nch);
+    float2 e = __ffma2_rn(d, nch, __fmul2_rn(d, both(sc.ch)));
+    e = __ffma2_rn(d, both(-sc.cl), e);
+    e = __ffma2_rn(dl, nch, e);
+    const float2 t = __ffma2_rn(p, both(float(kSteps)), both(12582912.f));
+    const float2 f = __ffma2_rn(__fadd2_rn(t, both(-12582912.f)), both(-1.f / kSteps), p);
+    const float lh = 0.693147182464599609375f, ll = -1.904654323148236e-9f;
+    const float2 a = __fmul2_rn(f, both(-lh));
+    float2 r = __ffma2_rn(f, both(-lh), __fmul2_rn(f, both(lh)));
+    r = __ffma2_rn(f, both(-ll), r);
+    r = __ffma2_rn(e, both(-lh), r);
+    const float2 fe = __fadd2_rn(f, e);
+    float2 q = __ffma2_rn(f, both(-0.0013333558146428443f), both(0.009618129107628477f));
+    q = __ffma2_rn(q, f, both(-0.05550410866482158f));
+    q = __ffma2_rn(q, f, both(0.24022650695910072f));
+    r = __ffma2_rn(__fmul2_rn(fe, fe), q, r);
+    const float big = 1.5f * 0x1p-6f;
+    const float2 u = __fadd2_rn(a, both(big));
+    r = __fadd2_rn(r, __ffma2_rn(__fadd2_rn(u, both(-big)), minus, a));
+    const float2 lo = __ffma2_rn(r, both(0x1p36f), both(12582912.f));
+    const uint32_t off = (1u << kBiasBits) - 0x4b400000u - uint32_t(__float_as_int(big)) * 128u;
+    return {p,
+            {__float_as_int(t.x) - 0x4b400000, __float_as_int(t.y) - 0x4b400000},
+            {uint32_t(__float_as_int(u.x)) * 128u + uint32_t(__float_as_int(lo.x)) + off,
+             uint32_t(__float_as_int(u.y)) * 128u + uint32_t(__float_as_int(lo.y)) + off}};
+}
+
 // round(2^Q 2^(-bin / 64) sum / 2^36) for a sum of s below 2^57
 __device__ __forceinline__ uint64_t scale_up(uint64_t sum, int bin, const uint64_t* table, int q_bits) {
     const int n = -bin;
@@ -236,11 +282,11 @@ __device__ __forceinline__ float element<__nv_bfloat16>(uint4 v, int e) {
 __device__ __forceinline__ float one(const float* p) { return *p; }
 __device__ __forceinline__ float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
-// fn(logit, index) for every element of the block's part, U vectors in flight per thread.
-// The vectors that lie in the row as a whole come first, then the elements of the two
-// that may not.
+// fn(logit, logit, index) for every two neighbouring elements of the block's part (index is
+// the first one's), U vectors in flight per thread.  The vectors that lie in the row as a
+// whole come first, then the elements of the two that may not, each with -inf beside it.
 template <int U, typename T, typename F>
-__device__ __forceinline__ void for_each(const Part<T>& p, int* dev_status, F fn) {
+__device__ __forceinline__ void for_pairs(const Part<T>& p, int* dev_status, F fn) {
     constexpr int VE = 16 / sizeof(T);
     const int tid = threadIdx.x;
     const int head = p.off > 0 ? 1 : 0, whole = (p.off + p.vocab) / VE;  // whole vectors: [head, whole)
@@ -257,7 +303,7 @@ __device__ __forceinline__ void for_each(const Part<T>& p, int* dev_status, F fn
             if (q + k * kThreads >= end) break;
             const int i = (q + k * kThreads) * VE - p.off;
 #pragma unroll
-            for (int e = 0; e < VE; ++e) fn(element<T>(v[k], e), i + e);
+            for (int e = 0; e < VE; e += 2) fn(element<T>(v[k], e), element<T>(v[k], e + 1), i + e);
         }
     }
     // the first vector's elements, then those behind the whole vectors
@@ -266,7 +312,59 @@ __device__ __forceinline__ void for_each(const Part<T>& p, int* dev_status, F fn
     const int last = p.q1 > p.q0 && p.q1 * VE - p.off >= p.vocab ? max(p.vocab - tail0, 0) : 0;
     if (tid < first + last) {
         const int i = tid < first ? tid : tail0 + tid - first;
-        fn(one(p.row + i), i);
+        fn(one(p.row + i), -INFINITY, i);
+    }
+}
+
+// fn(logit, index) for every element; also for a -inf with the index after a single one's
+template <int U, typename T, typename F>
+__device__ __forceinline__ void for_each(const Part<T>& p, int* dev_status, F fn) {
+    for_pairs<U>(p, dev_status, [&](float z0, float z1, int i) {
+        fn(z0, i);
+        fn(z1, i + 1);
+    });
+}
+
+// fn(logit, index) for the elements with z_lo <= logit <= z_hi, which are few: a bit per
+// element of U vectors first, then the bits' elements again, from the cache.
+template <int U, typename T, typename F>
+__device__ __forceinline__ void for_hits(const Part<T>& p, int* dev_status, float z_lo, float z_hi, F fn) {
+    constexpr int VE = 16 / sizeof(T);
+    static_assert(U * VE <= 32, "a bit each");
+    const int tid = threadIdx.x;
+    const int head = p.off > 0 ? 1 : 0, whole = (p.off + p.vocab) / VE;  // whole vectors: [head, whole)
+    const int end = min(p.q1, whole);
+    for (int q = max(p.q0, head) + tid; q < end; q += U * kThreads) {
+        const T* at = p.row + (q * VE - p.off);
+        uint4 v[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            if (q + k * kThreads < end && VCE_BOUNDS(aligned16(at), dev_status))
+                v[k] = __ldg(reinterpret_cast<const uint4*>(at + k * kThreads * VE));
+        uint32_t hits = 0;
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            if (q + k * kThreads >= end) break;
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                const float z = element<T>(v[k], e);
+                if (z >= z_lo && z <= z_hi) hits |= 1u << (k * VE + e);
+            }
+        }
+        while (hits) {
+            const int b = __ffs(hits) - 1;
+            hits &= hits - 1;
+            const int j = (b / VE) * kThreads * VE + b % VE;
+            fn(one(at + j), int(at - p.row) + j);
+        }
+    }
+    const int first = head && p.q0 == 0 && p.q1 > 0 ? min(VE - p.off, p.vocab) : 0;
+    const int tail0 = max(whole * VE - p.off, head ? VE - p.off : 0);
+    const int last = p.q1 > p.q0 && p.q1 * VE - p.off >= p.vocab ? max(p.vocab - tail0, 0) : 0;
+    if (tid < first + last) {
+        const int i = tid < first ? tid : tail0 + tid - first;
+        const float z = one(p.row + i);
+        if (z >= z_lo && z <= z_hi) fn(z, i);
     }
 }
 
@@ -285,35 +383,47 @@ __device__ __forceinline__ T remote(const T* p, int rank) {
     }
 }
 
+__device__ __forceinline__ void put(uint64_t* p, int rank, uint64_t v) {
+    asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(mapa_shared(smem_u32(p), uint32_t(rank))), "l"(v) : "memory");
+}
+__device__ __forceinline__ void put(uint32_t* p, int rank, uint32_t v) {
+    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(mapa_shared(smem_u32(p), uint32_t(rank))), "r"(v) : "memory");
+}
+
 __device__ __forceinline__ void row_barrier(int cluster) {
     if (cluster == 1) __syncthreads();
     else cluster_sync();
 }
 
-// Inclusive prefix sums of a[0 .. n) in place (n at most 6 x kThreads); every thread calls.
-template <typename T>
-__device__ __forceinline__ void prefix_sums(T* a, int n, uint64_t* warp_sum) {
+// a[i] = the sum of load(0) ... load(i), i < n (at most 6 x kThreads); load(i) may read a[i].
+// Every thread calls.  Warps take neighbouring ranges and walk them 32 at a time.
+template <typename T, typename F>
+__device__ __forceinline__ void prefix_sums(T* a, int n, uint64_t* warp_sum, F load) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = (n + kThreads - 1) / kThreads;
-    const int i0 = int(threadIdx.x) * per;
-    uint64_t s = 0;
-    for (int k = 0; k < per; ++k)
-        if (i0 + k < n) s += a[i0 + k];
-    uint64_t t = s;
+    const int i0 = warp * per * 32 + lane;
+    uint64_t carry = 0;
+#pragma unroll 1
+    for (int k = 0; k < per; ++k) {
+        const int i = i0 + k * 32;
+        uint64_t t = i < n ? uint64_t(load(i)) : 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t x = __shfl_up_sync(0xffffffffu, t, o);
-        if (lane >= o) t += x;
-    }
-    if (lane == 31) warp_sum[warp] = t;
-    __syncthreads();
-    uint64_t before = t - s;
-    for (int w = 0; w < warp; ++w) before += warp_sum[w];
-    for (int k = 0; k < per; ++k)
-        if (i0 + k < n) {
-            before += a[i0 + k];
-            a[i0 + k] = T(before);
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint64_t x = __shfl_up_sync(0xffffffffu, t, o);
+            if (lane >= o) t += x;
         }
+        t += carry;
+        if (i < n) a[i] = T(t);
+        carry = __shfl_sync(0xffffffffu, t, 31);
+    }
+    if (lane == 0) warp_sum[warp] = carry;
+    __syncthreads();
+    uint64_t before = lane < warp ? warp_sum[lane] : 0;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+    before = __shfl_sync(0xffffffffu, before, 0);  // lanes 0 .. 15 hold the sum of the warps'
+    for (int k = 0; k < per; ++k)
+        if (i0 + k * 32 < n) a[i0 + k * 32] += T(before);
     __syncthreads();
 }
 
@@ -336,7 +446,32 @@ __device__ __forceinline__ void sort_list(uint64_t* list, int n, uint64_t* tmp) 
     while (size < n) size *= 2;
     for (int i = n + t; i < size; i += kThreads) list[i] = 0;  // after every key
     __syncthreads();
+    if (size <= kThreads) {  // one key per thread: partners within a warp need no barrier
+        uint64_t key = t < size ? list[t] : 0;
+#pragma unroll 1
+        for (int len = 2; len <= size; len *= 2)
+#pragma unroll 1
+            for (int step = len / 2; step > 0; step /= 2) {
+                uint64_t other;
+                if (step >= 32) {
+                    __syncthreads();
+                    if (t < size) list[t] = key;
+                    __syncthreads();
+                    other = t < size ? list[t ^ step] : 0;
+                } else {
+                    other = __shfl_xor_sync(0xffffffffu, key, step);
+                }
+                const bool larger = ((t & len) == 0) == ((t & step) == 0);  // this place keeps the larger
+                key = (other > key) == larger ? other : key;
+            }
+        __syncthreads();
+        if (t < size) list[t] = key;
+        __syncthreads();
+        return;
+    }
+#pragma unroll 1
     for (int len = 2; len <= size; len *= 2)
+#pragma unroll 1
         for (int step = len / 2; step > 0; step /= 2) {
             for (int i = t; i < size / 2; i += kThreads) {
                 const int lo = (i / step) * step * 2 + i % step, hi = lo + step;
@@ -357,56 +492,65 @@ struct Sampler {
     Scale sc;
     uint32_t turn;  // commands so far
 
-    // Block 0's command, the same in every block: a barrier, after which all read it.  A slot
-    // is written again two commands later, behind a barrier that its readers have passed.
-    __device__ __forceinline__ Command tell(const Command& c) {
-        Command* slot = &sh.cmd[turn & 1];
-        ++turn;
-        if (lead() && threadIdx.x == 0) *slot = c;
-        barrier();
-        if (a.cluster == 1) return *slot;
-        return {remote(&slot->lo, 0), remote(&slot->hi, 0), remote(&slot->bin, 0), remote(&slot->flag, 0)};
-    }
-
     __device__ __forceinline__ bool lead() const { return rank == 0; }
     __device__ __forceinline__ void barrier() const { row_barrier(a.cluster); }
 
-    // Collects the keys of the elements that ``take`` accepts (its own part); all threads.
-    template <typename F>
-    __device__ __forceinline__ void collect(F take) {
-        if (threadIdx.x == 0) sh.n_list = 0;
-        __syncthreads();
-        for_each<4>(part, a.dev_status, [&](float z, int i) {
-            if (!take(z, i)) return;
-            const uint32_t at = atomicAdd(&sh.n_list, 1u);
-            if (at < kCap) sh.list[at] = key_of(z, i);
-        });
+    // Block 0's command (the same in all its threads), in every block: it is put into their
+    // shared memory before a barrier.  A slot is written again two commands later, behind
+    // a barrier that its readers have passed.
+    __device__ __forceinline__ Command tell(const Command& c) {
+        Command* slot = &sh.cmd[turn & 1];
+        ++turn;
+        if (lead() && int(threadIdx.x) < a.cluster) {
+            if (a.cluster == 1) {
+                *slot = c;
+            } else {
+                put(&slot->lo, threadIdx.x, c.lo);
+                put(&slot->hi, threadIdx.x, c.hi);
+                put(reinterpret_cast<uint32_t*>(&slot->bin), threadIdx.x, uint32_t(c.bin));
+                put(reinterpret_cast<uint32_t*>(&slot->flag), threadIdx.x, uint32_t(c.flag));
+            }
+        }
+        barrier();
+        return *slot;
     }
 
-    // Block 0, after a barrier: the others' lists behind its own.  False when they
-    // are too many.
+    // Collects the keys of the elements that are wanted; behind the barrier block 0 has
+    // every block's number of them.
+    __device__ __forceinline__ void collect(const Wanted& w) {
+        if (threadIdx.x == 0) sh.n_list = 0;
+        __syncthreads();
+        const Scale s = sc;
+        for_hits<16 / sizeof(T) == 8 ? 4 : 8>(part, a.dev_status, w.z_lo, w.z_hi, [&](float z, int i) {
+            const float p = log2_weight(s, z);
+            const uint64_t k = key_of(z, i);
+            if (p > w.p_least && (w.cmd.bin < 0 || bin_of(p) == w.cmd.bin) && k >= w.cmd.lo && k <= w.cmd.hi) {
+                const uint32_t at = atomicAdd(&sh.n_list, 1u);
+                if (at < kCap) sh.list[at] = k;
+            }
+        });
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            if (lead()) sh.part_n[0] = sh.n_list;
+            else put(&sh.part_n[rank], 0, sh.n_list);
+        }
+        barrier();
+    }
+
+    // Block 0: the others' lists behind its own.  False when they are too many.
     __device__ __forceinline__ bool join_lists(int& n) {
         uint32_t total = 0;
-        for (int c = 0; c < a.cluster; ++c) total += c == 0 ? sh.n_list : remote(&sh.n_list, c);
+        for (int c = 0; c < a.cluster; ++c) total += sh.part_n[c];
         if (total > kCap) return false;
-        uint32_t at = sh.n_list;
+        uint32_t at = sh.part_n[0];
         for (int c = 1; c < a.cluster; ++c) {
-            const uint32_t m = remote(&sh.n_list, c);
+            const uint32_t m = sh.part_n[c];
             for (uint32_t i = threadIdx.x; i < m; i += kThreads) sh.list[at + i] = remote(&sh.list[i], c);
             at += m;
         }
         n = int(total);
         __syncthreads();
         return true;
-    }
-
-    // Block 0: sorts the list and makes sh.sums its inclusive prefix sums from ``base``.
-    __device__ __forceinline__ void sort_and_sum(int n, uint64_t base) {
-        sort_list(sh.list, n, sh.sums);
-        for (int i = threadIdx.x; i < n; i += kThreads)
-            sh.sums[i] = weight_of(sc, key_logit(sh.list[i]), sh.table, a.q_bits) + (i == 0 ? base : 0);
-        __syncthreads();
-        prefix_sums(sh.sums, n, sh.warp_sum);
     }
 
     // Block 0: the first i < n with s[i] >= target (n when there is none).
@@ -425,38 +569,11 @@ struct Sampler {
         atomicAdd(reinterpret_cast<unsigned long long*>(at), static_cast<unsigned long long>(w));
     }
 
-    // Sum over the block of one value per thread; valid in thread 0.
-    __device__ __forceinline__ uint64_t block_sum(uint64_t v) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if ((threadIdx.x & 31) == 0) sh.warp_sum2[threadIdx.x >> 5] = v;
-        __syncthreads();
-        uint64_t t = 0;
-        if (threadIdx.x == 0)
-            for (int w = 0; w < kWarps; ++w) t += sh.warp_sum2[w];
-        __syncthreads();
-        return t;
-    }
-
-    // The elements of ``cmd``'s bin and key range, whose logits lie between z_lo and z_hi.
-    struct InBin {
-        Scale s;
-        float z_lo, z_hi;
-        int bin;
-        uint64_t lo, hi;
-        __device__ __forceinline__ bool operator()(float z, int i) const {
-            if (!(z >= z_lo && z <= z_hi)) return false;
-            const float p = log2_weight(s, z);
-            if (!(p > kLeastLog2) || bin_of(p) != bin) return false;
-            const uint64_t k = key_of(z, i);
-            return k >= lo && k <= hi;
-        }
-    };
-    __device__ __forceinline__ InBin in_bin(const Command& cmd) const {
-        // the bounds are generous; the bin itself decides
+    // The elements of one bin.  The logits' bounds are generous; the bin itself decides.
+    __device__ __forceinline__ Wanted in_bin(const Command& cmd) const {
         const float far = (float(cmd.bin) + 0.75f) / (kSteps * sc.ch), near = (float(cmd.bin) - 0.75f) / (kSteps * sc.ch);
         const float slack = fabsf(sc.m) * 0x1p-21f;
-        return {sc, sc.m - far - slack, sc.m - near + slack, cmd.bin, cmd.lo, cmd.hi};
+        return {sc.m - far - slack, sc.m - near + slack, kLeastLog2, cmd};
     }
 
     // A range that holds more elements than a list: its keys divided into kCap ranges of
@@ -464,7 +581,13 @@ struct Sampler {
     // ``base_count`` become what lies before it.  Rare, and kept out of the common code.
     __device__ __noinline__ void divide(Command& cmd, bool by_count, uint64_t target, uint64_t& base,
                                         uint32_t& base_count) {
-        const InBin mine = in_bin(cmd);
+        const Wanted w = in_bin(cmd);
+        auto mine = [&](float z, int i) {
+            if (!(z >= w.z_lo && z <= w.z_hi)) return false;
+            const float p = log2_weight(sc, z);
+            const uint64_t k = key_of(z, i);
+            return p > kLeastLog2 && bin_of(p) == w.cmd.bin && k >= w.cmd.lo && k <= w.cmd.hi;
+        };
         uint64_t kmin = ~0ull, kmax = 0;
         for_each<1>(part, a.dev_status, [&](float z, int i) {
             if (!mine(z, i)) return;
@@ -505,8 +628,8 @@ struct Sampler {
                     sh.sums[i] += remote(&sh.sums[i], c);
                 }
             __syncthreads();
-            prefix_sums(sh.list, kCap, sh.warp_sum);
-            prefix_sums(sh.sums, kCap, sh.warp_sum);
+            prefix_sums(sh.list, kCap, sh.warp_sum, [&](int i) { return sh.list[i]; });
+            prefix_sums(sh.sums, kCap, sh.warp_sum, [&](int i) { return sh.sums[i]; });
             const int b = min(by_count ? first_at_least(sh.sums, kCap, target - base_count)
                                        : first_at_least(sh.list, kCap, target > base ? target - base : 1),
                               kCap - 1);
@@ -518,60 +641,27 @@ struct Sampler {
         cmd = tell(cmd);
     }
 
-    // Finds the first element, in order, at which the cumulated weight (or, by_count, the
-    // number of elements) reaches ``target``.  All blocks call; the results are valid in
-    // block 0: the element's key and the cumulated weight up to and with it.  ``target`` is
-    // within the total.
-    __device__ __forceinline__ void locate(bool by_count, uint64_t target, uint64_t& key, uint64_t& upto) {
-        uint64_t base = 0;
-        uint32_t base_count = 0;
-        Command cmd{0, ~0ull, 0, 0};
-        if (lead()) {
-            cmd.bin = min(by_count ? first_at_least(sh.count, kBins, uint32_t(target))
-                                   : first_at_least(sh.mass, kBins, target),
-                          kBins - 1);
-            if (cmd.bin > 0) base = sh.mass[cmd.bin - 1], base_count = sh.count[cmd.bin - 1];
-        }
-        cmd = tell(cmd);
-        // Keys have 52 bits and differ, and a division leaves at most 2^-11 of their range
-        // (one key at last): five levels at most.
-        for (int level = 0; level < 8; ++level) {
-            collect(in_bin(cmd));
-            barrier();
-            if (lead()) {
-                int n;
-                cmd.flag = join_lists(n);
-                if (cmd.flag) {
-                    sort_and_sum(n, base);
-                    int at = by_count ? int(target - base_count) - 1 : first_at_least(sh.sums, n, target);
-                    at = max(0, min(at, n - 1));
-                    key = sh.list[at];
-                    upto = sh.sums[at];
-                }
-            }
-            cmd = tell(cmd);
-            if (cmd.flag) return;
-            Sampler copy = *this;  // its address is taken there, not here
-            copy.divide(cmd, by_count, target, base, base_count);
-            turn = copy.turn;
-        }
-    }
-
-    __device__ void write(int64_t row, int64_t token, float logprob) {
+    __device__ __forceinline__ void write(int64_t row, int64_t token, float logprob) {
         a.token[row] = token;
         if (a.logprob) a.logprob[row] = logprob;
     }
 
     // Block 0, thread 0: the drawn token and the logarithm of its share of the mass.
-    __device__ void finish(int64_t row, uint64_t key, uint64_t mass, float t) {
+    __device__ __forceinline__ void finish(int64_t row, uint64_t key, uint64_t mass, float t) {
+        write(row, key_index(key), 0.f);
+        if (!a.logprob) return;
         const float z = key_logit(key);
         const uint64_t w = weight_of(sc, z, sh.table, a.q_bits);
         float lp;
         if (w > mass / 2) lp = log1pf(-__ull2float_rn(mass - w) / __ull2float_rn(mass));
         else lp = (z - sc.m) / fminf(fmaxf(t, 1e-30f), 1e30f) - logf(ldexpf(__ull2float_rn(mass), -a.q_bits));
-        write(row, key_index(key), lp);
+        a.logprob[row] = lp;
     }
 };
+
+// What the collected lists are for, in this order: all survivors at once, or the border
+// of top-k, that of top-p, the draw.
+enum { kHeads, kTopK, kTopP, kDraw };
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs a) {
@@ -583,15 +673,16 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
     if (tid < kSteps) sh.table[tid] = kExp2Table[tid];
 
     constexpr int VE = 16 / sizeof(T);
-    const T* base = static_cast<const T*>(a.logits) + row * a.stride;
-    const int off = int(reinterpret_cast<uintptr_t>(base) / sizeof(T) % VE);
+    const T* base_ptr = static_cast<const T*>(a.logits) + row * a.stride;
+    const int off = int(reinterpret_cast<uintptr_t>(base_ptr) / sizeof(T) % VE);
     const int vectors = (off + a.vocab + VE - 1) / VE;
     const int per = (vectors + a.cluster - 1) / a.cluster;
-    Sampler<T> s{a, sh, {base, off, a.vocab, rank * per, min(vectors, (rank + 1) * per)}, rank, {}, 0};
+    Sampler<T> s{a, sh, {base_ptr, off, a.vocab, rank * per, min(vectors, (rank + 1) * per)}, rank, {}, 0};
 
     const float temp = a.temperature ? a.temperature[row] : 1.f;
     const float top_p = a.top_p ? a.top_p[row] : 1.f;
-    const float min_p = a.min_p ? fminf(a.min_p[row], 1.f) : 0.f;
+    const float raw_min_p = a.min_p ? a.min_p[row] : 0.f;
+    const float min_p = fminf(raw_min_p, 1.f);
     const float u = a.uniform[row];
     const int top_k = a.top_k ? a.top_k[row] : 0;
     const bool greedy = temp <= 0.f;
@@ -600,20 +691,21 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
     const bool by_min = min_p > 0.f;
 
     // ---- the largest logit, and the largest of every thread's elements ----
+    // A NaN stays the largest, so one look at the end finds it (and a +inf).
     float m = -INFINITY;
     for_each<4>(s.part, a.dev_status, [&](float z, int) { m = max_nan(m, z); });
-    const bool bad = !(m < INFINITY);  // a NaN or +inf among them
     sh.group[tid] = m;
     float wm = m;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, o));
-    if ((tid & 31) == 0) sh.warp_sum[tid >> 5] = __float_as_uint(wm);
-    const bool any_bad = __syncthreads_or(bad);
+    for (int o = 16; o > 0; o >>= 1) wm = max_nan(wm, __shfl_xor_sync(0xffffffffu, wm, o));
+    if ((tid & 31) == 0) sh.warp_max[tid >> 5] = wm;
+    if (tid == 0) sh.my_bound = -INFINITY;
+    __syncthreads();
     // top-k: each block's j-th largest group maximum, j = ceil(k / blocks); at least k
     // elements of the row are as large as the smallest of these
-    const int j = (top_k + a.cluster - 1) / a.cluster;
-    const bool heads_k = by_k && top_k <= kMaxHeads;
+    const bool heads_k = by_k && top_k <= kMaxHeads && !greedy;
     if (heads_k) {
+        const int j = (top_k + a.cluster - 1) / a.cluster;
         int groups = 64;  // of neighbouring threads: larger groups bound less tightly but rank faster
         while (groups < 4 * j && groups < kThreads) groups *= 2;
         const int width = kThreads / groups;
@@ -625,46 +717,46 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
         __syncthreads();
         if (tid < groups) {
             int before = 0;
+#pragma unroll 8
             for (int i = 0; i < groups; ++i) before += sh.group[i] > g || (sh.group[i] == g && i < tid);
-            if (before == j - 1) sh.bound[rank] = g;
+            if (before == j - 1) sh.my_bound = g;
         }
+        __syncthreads();
     }
-    if (tid == 0) {
-        float r = -INFINITY;
-        for (int w = 0; w < kWarps; ++w) r = fmaxf(r, __uint_as_float(uint32_t(sh.warp_sum[w])));
-        sh.row_max[rank] = r;
-        sh.bad[rank] = any_bad;
+    if (tid < a.cluster) {
+        float r = sh.warp_max[0];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) r = max_nan(r, sh.warp_max[w]);
+        if (a.cluster == 1) {
+            sh.row_max[0] = r, sh.bound[0] = sh.my_bound;
+        } else {
+            put(reinterpret_cast<uint32_t*>(&sh.row_max[rank]), tid, __float_as_uint(r));
+            put(reinterpret_cast<uint32_t*>(&sh.bound[rank]), tid, __float_as_uint(sh.my_bound));
+        }
     }
     s.barrier();
     float row_max = -INFINITY, bound = INFINITY;
-    bool row_bad = !(temp == temp) || !(top_p == top_p) || !(u == u) || (a.min_p && !(a.min_p[row] == a.min_p[row]));
     for (int c = 0; c < a.cluster; ++c) {
-        row_max = fmaxf(row_max, remote(&sh.row_max[c], c));
-        row_bad |= remote(&sh.bad[c], c) != 0;
-        if (heads_k) bound = fminf(bound, remote(&sh.bound[c], c));
+        row_max = max_nan(row_max, sh.row_max[c]);
+        bound = fminf(bound, sh.bound[c]);
     }
-    if (row_bad || row_max == -INFINITY) {  // the same in every block
+    const bool bad_row = !(row_max < INFINITY) || row_max == -INFINITY || !(temp == temp) || !(top_p == top_p) ||
+                         !(u == u) || !(raw_min_p == raw_min_p);
+    if (bad_row) {  // the same in every block; nobody has to read another's memory any more
         if (rank == 0 && tid == 0) {
             s.write(row, -1, __uint_as_float(0x7fc00000u));
             report(a.dev_status, VCE_DEVSTATUS_BAD_ROW);
         }
-        s.barrier();  // nobody leaves while its shared memory is read
         return;
     }
     s.sc = make_scale(row_max, temp);
     const Scale sc = s.sc;
-    const uint64_t least = by_min ? [&] {
-        bool exact;
-        if (min_p >= 1.f) return uint64_t(1) << a.q_bits;
-        const uint64_t f = floor_product(min_p, uint64_t(1) << a.q_bits, &exact);
-        return exact ? f : f + 1;
-    }() : 0;
 
     if (greedy) {
         if (tid == 0) sh.argmax = 0xffffffffu;
         __syncthreads();
         uint32_t first = 0xffffffffu;
-        for_each<4>(s.part, a.dev_status, [&](float z, int i) {
+        for_each<2>(s.part, a.dev_status, [&](float z, int i) {
             if (z == row_max && uint32_t(i) < first) first = uint32_t(i);
         });
         if (first != 0xffffffffu) atomicMin(&sh.argmax, first);
@@ -674,129 +766,173 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
             for (int c = 0; c < a.cluster; ++c) best = min(best, remote(&sh.argmax, c));
             s.write(row, best, 0.f);
         }
-        s.barrier();
+        s.barrier();  // nobody leaves while its shared memory is read
         return;
     }
 
-    bool exact;
-    Command cmd{0, 0, 0, 0};
-    // ---- few survivors: collect them all ----
+    bool exact = true;
+    uint64_t least = 0;  // min-p's least weight
+    if (by_min) {
+        least = uint64_t(1) << a.q_bits;
+        if (min_p < 1.f) {
+            const uint64_t f = floor_product(min_p, least, &exact);
+            least = exact ? f : f + 1;
+        }
+    }
     const bool heads_min = by_min && !by_p;
-    if (heads_k || heads_min) {
-        const float p_least = heads_min ? fmaxf(kLeastLog2, log2f(min_p) - 0.01f) : kLeastLog2;
-        const float z_least = heads_k ? bound : -INFINITY;
-        s.collect([=](float z, int) { return z >= z_least && log2_weight(sc, z) > p_least; });
-        s.barrier();
-        if (s.lead()) {
-            int n;
-            const bool fits = s.join_lists(n);
-            if (fits) {
-                s.sort_and_sum(n, 0);
-                if (by_k && top_k < n) n = top_k;
-                int kept = n;
-                if (by_p) {
-                    uint64_t target = floor_product(fmaxf(top_p, 0.f), sh.sums[n - 1], &exact);
-                    target += exact ? 0 : 1;
-                    kept = s.first_at_least(sh.sums, n, target ? target : 1) + 1;
+    uint64_t key = 0, mass = 0, above = 0;
+    int step = heads_k || heads_min ? kHeads : kTopK;
+#pragma unroll 1
+    for (;; ++step) {
+        uint64_t target = 0, base = 0;
+        uint32_t base_count = 0;
+        Command cmd{0, ~0ull, -1, 0};
+        if (step == kTopK) {
+            // ---- weights of the whole row, summed by n ----
+            for (int i = tid; i < kBins; i += kThreads) sh.mass[i] = 0, sh.count[i] = 0;
+            __syncthreads();
+            // min-p (with top-p): whole bins above the border, and single weights next to it
+            const int edge = by_min ? max(0, bin_of(fmaxf(kLeastLog2, log2f(min_p))) - 2) : kBins;
+            if (tid == 0) sh.kept_minp = 0;
+            for_pairs<1>(s.part, a.dev_status, [&](float z0, float z1, int) {
+                const Step2 st = step_of2(sc, make_float2(z0, z1));
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    if (!((k ? st.p.y : st.p.x) < -kLeastLog2)) continue;
+                    const int bin = st.bin[k];
+                    if (!VCE_BOUNDS(bin >= 0 && bin < kBins, a.dev_status)) continue;
+                    uint32_t* at = reinterpret_cast<uint32_t*>(&sh.mass[bin]);
+                    atomicAdd(at, st.s[k] & ((1u << kHalfBits) - 1));
+                    atomicAdd(at + 1, st.s[k] >> kHalfBits);
+                    atomicAdd(&sh.count[bin], 1u);
                 }
-                if (by_min) {  // weights descend: the first that is too small ends the head
-                    __syncthreads();
-                    if (tid == 0) sh.found = uint32_t(n);
-                    __syncthreads();
-                    for (int i = tid; i < n; i += kThreads) {
-                        const uint64_t w = sh.sums[i] - (i ? sh.sums[i - 1] : 0);
-                        if (w < least) atomicMin(&sh.found, uint32_t(i));
+            });
+            __syncthreads();
+            for (int i = tid; i < kBins; i += kThreads) {
+                const uint64_t m2 = sh.mass[i], c = sh.count[i];
+                sh.mass[i] = (c << kFracBits) - (c << kBiasBits) + (m2 & 0xffffffffu) + ((m2 >> 32) << kHalfBits);
+            }
+            if (by_min) {  // the few elements of five bins
+                const Wanted w = s.in_bin({0, ~0ull, edge + 2, 0});
+                const float wide = 2.f / (kSteps * sc.ch);
+                for_hits<2>(s.part, a.dev_status, w.z_lo - wide, w.z_hi + wide, [&](float z, int) {
+                    const float p = log2_weight(sc, z);
+                    if (!(p > kLeastLog2) || bin_of(p) < edge || bin_of(p) >= edge + 5) return;
+                    const uint64_t x = weight_of(sc, z, sh.table, a.q_bits);
+                    if (x >= least) s.add_mass(&sh.kept_minp, x);
+                });
+            }
+            s.barrier();
+            if (s.lead()) {
+                if (a.cluster > 1) {
+                    for (int i = tid; i < kBins; i += kThreads) {
+                        uint64_t v[kMaxCluster];
+                        uint32_t c[kMaxCluster];
+#pragma unroll
+                        for (int r = 1; r < kMaxCluster; ++r)  // all loads before the sums
+                            if (r < a.cluster) v[r] = remote(&sh.mass[i], r), c[r] = remote(&sh.count[i], r);
+                        uint64_t sum = sh.mass[i];
+                        uint32_t n = sh.count[i];
+#pragma unroll
+                        for (int r = 1; r < kMaxCluster; ++r)
+                            if (r < a.cluster) sum += v[r], n += c[r];
+                        sh.mass[i] = sum;
+                        sh.count[i] = n;
                     }
                     __syncthreads();
-                    kept = min(kept, max(1, int(sh.found)));
                 }
-                const uint64_t mass = sh.sums[kept - 1];
-                uint64_t target = u >= 1.f ? mass - 1 : floor_product(fmaxf(u, 0.f), mass, &exact);
-                const int at = s.first_at_least(sh.sums, kept, target + 1);
-                if (tid == 0) s.finish(row, sh.list[min(at, kept - 1)], mass, temp);
+                prefix_sums(sh.mass, kBins, sh.warp_sum, [&](int i) {
+                    return sh.count[i] ? scale_up(sh.mass[i], i, sh.table, a.q_bits) : uint64_t(0);
+                });
+                if (by_k) prefix_sums(sh.count, kBins, sh.warp_sum, [&](int i) { return sh.count[i]; });
+                mass = sh.mass[kBins - 1];
+                cmd.flag = by_k && sh.count[kBins - 1] > uint32_t(top_k);  // the k-th has a weight
+                if (by_min) {
+                    above = edge ? sh.mass[edge - 1] : 0;
+                    for (int c = 0; c < a.cluster; ++c) above += remote(&sh.kept_minp, c);
+                }
             }
-            cmd.flag = fits;
-        }
-        if (s.tell(cmd).flag) {
-            s.barrier();  // block 0's shared memory is still read
-            return;
-        }
-    }
-
-    // ---- weights of the whole row, summed by n ----
-    for (int i = tid; i < kBins; i += kThreads) sh.mass[i] = 0, sh.count[i] = 0;
-    __syncthreads();
-    // min-p (with top-p): whole bins above the border, and single weights next to it
-    const int edge = by_min ? max(0, bin_of(fmaxf(kLeastLog2, log2f(min_p))) - 2) : kBins;
-    uint64_t above = 0;
-    for_each<X_U>(s.part, a.dev_status, [&](float z, int) {
-        if (!(log2_weight(sc, z) > kLeastLog2)) return;
-        const Step st = step_of(sc, z);
-        if (!VCE_BOUNDS(st.bin >= 0 && st.bin < kBins, a.dev_status)) return;
-        const uint32_t x = uint32_t(st.g + (1 << kBiasBits));
-        uint32_t* at = reinterpret_cast<uint32_t*>(&sh.mass[st.bin]);
-        atomicAdd(at, x & ((1u << kHalfBits) - 1));
-        atomicAdd(at + 1, x >> kHalfBits);
-        atomicAdd(&sh.count[st.bin], 1u);
-        if (st.bin >= edge && st.bin < edge + 5) {
-            const uint64_t w = weight_of(sc, z, sh.table, a.q_bits);
-            if (w >= least) above += w;
-        }
-    });
-    if (by_min) {
-        above = s.block_sum(above);
-        if (tid == 0) sh.kept_minp = above;
-    }
-    __syncthreads();
-    for (int i = tid; i < kBins; i += kThreads) {
-        const uint64_t m2 = sh.mass[i], c = sh.count[i];
-        sh.mass[i] = (c << kFracBits) - (c << kBiasBits) + (m2 & 0xffffffffu) + ((m2 >> 32) << kHalfBits);
-    }
-    s.barrier();
-    uint64_t total = 0;
-    if (s.lead()) {
-        for (int i = tid; i < kBins; i += kThreads) {
-            uint64_t sum = sh.mass[i];
-            uint32_t c = sh.count[i];
-            for (int r = 1; r < a.cluster; ++r) sum += remote(&sh.mass[i], r), c += remote(&sh.count[i], r);
-            sh.mass[i] = c ? scale_up(sum, i, sh.table, a.q_bits) : 0;
-            sh.count[i] = c;
-        }
-        __syncthreads();
-        prefix_sums(sh.mass, kBins, sh.warp_sum);
-        if (by_k) {
-            prefix_sums(sh.count, kBins, sh.warp_sum);
-            cmd.flag = sh.count[kBins - 1] > uint32_t(top_k);  // the k-th has a weight
-        }
-        total = sh.mass[kBins - 1];
-        if (by_min) {
-            above = edge ? sh.mass[edge - 1] : 0;
-            for (int c = 0; c < a.cluster; ++c) above += remote(&sh.kept_minp, c);
-        }
-    }
-    // the border of top-k, then of top-p, then the draw: one after the other, each of
-    // them within the mass that the one before left
-    const bool cut = by_k && s.tell(cmd).flag;
-    uint64_t key = 0, mass = total, upto = 0;
-#pragma unroll 1
-    for (int step = cut ? 0 : by_p ? 1 : 2; step < 3; ++step) {
-        uint64_t target;
-        if (step == 0) {
+            if (by_k && !s.tell(cmd).flag) continue;
+            if (!by_k) continue;
             target = uint64_t(top_k);
-        } else if (step == 1) {
+        } else if (step == kTopP) {
             if (!by_p) continue;
             target = floor_product(fmaxf(top_p, 0.f), mass, &exact);
             target += exact ? 0 : 1;
             if (target == 0) target = 1;
-        } else {
+        } else if (step == kDraw) {
             if (by_min && above < mass) mass = above;
             target = u >= 1.f ? mass : floor_product(fmaxf(u, 0.f), mass, &exact) + 1;
         }
-        s.locate(step == 0, target, key, upto);
-        if (step < 2) mass = upto;
+        // ---- the border's bin, told to all ----
+        Wanted w{heads_k ? bound : -INFINITY, INFINITY,
+                 heads_min ? fmaxf(kLeastLog2, log2f(min_p) - 0.01f) : kLeastLog2, cmd};
+        if (step != kHeads) {
+            if (s.lead()) {
+                cmd.bin = min(step == kTopK ? s.first_at_least(sh.count, kBins, uint32_t(target))
+                                            : s.first_at_least(sh.mass, kBins, target),
+                              kBins - 1);
+                if (cmd.bin > 0) base = sh.mass[cmd.bin - 1], base_count = sh.count[cmd.bin - 1];
+            }
+            w = s.in_bin(s.tell(cmd));
+        }
+        // ---- its elements, collected and sorted ----
+        // Keys have 52 bits and differ, and a division leaves at most 2^-11 of their range
+        // (one key at last): five levels at most.
+#pragma unroll 1
+        for (int level = 0; level < 8; ++level) {
+            s.collect(w);
+            cmd = w.cmd;
+            if (s.lead()) {
+                int n;
+                cmd.flag = s.join_lists(n);
+                if (cmd.flag) {
+                    sort_list(sh.list, n, sh.sums);
+                    prefix_sums(sh.sums, n, sh.warp_sum, [&](int i) {
+                        return weight_of(sc, key_logit(sh.list[i]), sh.table, a.q_bits) + (i == 0 ? base : 0);
+                    });
+                    int at;
+                    if (step == kTopK) {
+                        at = int(target - base_count) - 1;
+                    } else {
+                        if (step == kHeads) {
+                            if (by_k && top_k < n) n = top_k;
+                            mass = sh.sums[n - 1];
+                            if (by_p) {
+                                target = floor_product(fmaxf(top_p, 0.f), mass, &exact);
+                                target += exact ? 0 : 1;
+                                n = s.first_at_least(sh.sums, n, target ? target : uint64_t(1)) + 1;
+                            }
+                            if (by_min) {  // weights descend: the first that is too small ends the head
+                                __syncthreads();
+                                if (tid == 0) sh.found = uint32_t(n);
+                                __syncthreads();
+                                for (int i = tid; i < n; i += kThreads)
+                                    if (sh.sums[i] - (i ? sh.sums[i - 1] : 0) < least) atomicMin(&sh.found, uint32_t(i));
+                                __syncthreads();
+                                n = max(1, int(sh.found));
+                            }
+                            mass = sh.sums[n - 1];
+                            target = u >= 1.f ? mass : floor_product(fmaxf(u, 0.f), mass, &exact) + 1;
+                        }
+                        at = s.first_at_least(sh.sums, n, target);
+                    }
+                    at = max(0, min(at, n - 1));
+                    key = sh.list[at];
+                    if (step == kTopK || step == kTopP) mass = sh.sums[at];
+                }
+            }
+            cmd = s.tell(cmd);
+            if (cmd.flag || step == kHeads) break;
+            Sampler<T> copy = s;  // its address is taken there, not here
+            copy.divide(cmd, step == kTopK, target, base, base_count);
+            s.turn = copy.turn;
+            w = s.in_bin(cmd);
+        }
+        if (step == kDraw || (step == kHeads && cmd.flag)) break;  // heads that are too many: by masses
     }
     if (s.lead() && tid == 0) s.finish(row, key, mass, temp);
-    s.barrier();
+    s.barrier();  // nobody leaves while its shared memory is read
 }
 
 }  // namespace
@@ -814,7 +950,7 @@ vce_status launch_ce_sample(const void* logits, int dtype, int64_t n, int64_t vo
     // As many blocks per row as fill the SMs twice, each with a part worth a block
     while (a.cluster < kMaxCluster &&
            (vocab > int64_t(a.cluster) * (kMaxPart - 64) ||
-            (n * a.cluster * 2 <= X_FILL * dev.num_sms && vocab / (a.cluster * 2) >= 4 * kThreads)))
+            (n * a.cluster * 2 <= 2 * dev.num_sms && vocab / (a.cluster * 2) >= 4 * kThreads)))
         a.cluster *= 2;
     if (n * a.cluster > 0x7fffffff) return VCE_ERR_INVALID_ARG;
     auto kernel = dtype == VCE_BF16 ? ce_sample_kernel<__nv_bfloat16> : ce_sample_kernel<float>;
