@@ -18,9 +18,9 @@
 //          which nothing survives - the k-th largest of the maxima of disjoint groups
 //          of elements, or min-p's own - and what lies above it, a little more than the
 //          head, is collected and sorted in shared memory.
-//   masses (otherwise): for every n the number of elements and the sum of their s are
-//          collected, three 32-bit atomics each; n is ordered by construction and the
-//          scaling by 2^(n / 64) happens once per n.  A border is located among the
+//   masses (otherwise): for every n the sum of its elements' s is collected by 32-bit
+//          atomics; n is ordered by construction and the scaling by 2^(n / 64) happens
+//          once per n.  A border is located among the
 //          prefix sums of the masses, and only the elements of that one n are collected
 //          and sorted.  Too many of them are divided again by the bits of (logit, index).
 // The logits are read once from HBM; the later passes find them in L2.
@@ -47,8 +47,15 @@ constexpr int kBins = 46 * kSteps;    // 46 octaves of n, from 0 down
 constexpr float kLeastLog2 = -45.9f;  // below it a weight is 0 (Q <= 44)
 constexpr int kFracBits = 36;         // of s
 constexpr int kBiasBits = 29;         // s - 2^36 is above -2^29 and below 2^29
-constexpr int kHalfBits = 15;         // it is summed in two halves, which 2^17 elements cannot overflow
+// Sums of s are kept in 32-bit words of 15 bits of every s, which 2^17 elements cannot
+// overflow.  The 8 octaves below the largest logit get s - 2^36 + 2^29 in two words and
+// a count; further down 30 bits of s itself are enough (2^-30 of a weight that is at most
+// 2^-8), two words and no count.
+constexpr int kHalfBits = 15;
 constexpr int kMaxPart = 1 << 17;     // elements per block
+constexpr int kFineBins = 8 * kSteps;
+constexpr int kCoarseBits = 7;        // of s, rounded away further down
+constexpr uint32_t kCoarseOffset = (1u << (kFracBits - kCoarseBits)) - (1u << (kBiasBits - kCoarseBits));  // 2^36 - 2^29 there
 constexpr int kCap = 2048;          // collected elements; also sub-bins of a divided bin
 constexpr int kCapBits = 11;
 constexpr int kMaxHeads = 256;      // top-k of the collecting path
@@ -86,8 +93,8 @@ struct Wanted {
 };
 
 struct Shared {
-    uint64_t mass[kBins];  // two 32-bit sums, then the sum of s, then (block 0) inclusive prefix sums of masses
-    uint32_t count[kBins];
+    uint64_t mass[kBins];  // words of low and then of high halves, then the sum of s, then (block 0) prefix sums of masses
+    uint32_t count[kBins];  // for top-k; the first kFineBins always
     uint64_t list[kCap];   // collected keys; masses of sub-bins
     uint64_t sums[kCap];   // inclusive prefix sums of the sorted list; counts of sub-bins
     uint64_t table[kSteps];
@@ -395,59 +402,72 @@ __device__ __forceinline__ void row_barrier(int cluster) {
     else cluster_sync();
 }
 
-// a[i] = the sum of load(0) ... load(i), i < n (at most 6 x kThreads); load(i) may read a[i].
-// Every thread calls.  Warps take neighbouring ranges and walk them 32 at a time.
-template <typename T, typename F>
+// a[i] = the sum of load(0) ... load(i), i < n <= PER x kThreads; load(i) may read a[i].
+// Every thread calls; each takes PER neighbours.
+template <int PER, typename T, typename F>
 __device__ __forceinline__ void prefix_sums(T* a, int n, uint64_t* warp_sum, F load) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int per = (n + kThreads - 1) / kThreads;
-    const int i0 = warp * per * 32 + lane;
-    uint64_t carry = 0;
-#pragma unroll 1
-    for (int k = 0; k < per; ++k) {
-        const int i = i0 + k * 32;
-        uint64_t t = i < n ? uint64_t(load(i)) : 0;
+    const int i0 = int(threadIdx.x) * PER;
+    uint64_t v[PER], s = 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint64_t x = __shfl_up_sync(0xffffffffu, t, o);
-            if (lane >= o) t += x;
-        }
-        t += carry;
-        if (i < n) a[i] = T(t);
-        carry = __shfl_sync(0xffffffffu, t, 31);
+    for (int k = 0; k < PER; ++k) {
+        s += i0 + k < n ? uint64_t(load(i0 + k)) : 0;
+        v[k] = s;
     }
-    if (lane == 0) warp_sum[warp] = carry;
+    uint64_t t = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t x = __shfl_up_sync(0xffffffffu, t, o);
+        if (lane >= o) t += x;
+    }
+    if (lane == 31) warp_sum[warp] = t;
     __syncthreads();
     uint64_t before = lane < warp ? warp_sum[lane] : 0;
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-    before = __shfl_sync(0xffffffffu, before, 0);  // lanes 0 .. 15 hold the sum of the warps'
-    for (int k = 0; k < per; ++k)
-        if (i0 + k * 32 < n) a[i0 + k * 32] += T(before);
+    before = __shfl_sync(0xffffffffu, before, 0) + t - s;  // lanes 0 .. 15 hold the sum of the warps'
+#pragma unroll
+    for (int k = 0; k < PER; ++k)
+        if (i0 + k < n) a[i0 + k] = T(before + v[k]);
     __syncthreads();
+}
+
+// The first i < n with s[i] >= target in an ascending s (n when there is none); every
+// thread finds it by itself.
+template <typename V>
+__device__ __forceinline__ int first_at_least(const V* s, int n, V target) {
+    int lo = 0, hi = n;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (s[mid] >= target) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo;
 }
 
 // Sorts list[0 .. n), n <= kCap, descending (all keys differ); ``tmp`` is scratch.
 __device__ __forceinline__ void sort_list(uint64_t* list, int n, uint64_t* tmp) {
     const int t = threadIdx.x;
-    if (n <= 128) {  // each key counts those before it
-        if (t < n) {
-            const uint64_t k = list[t];
-            int r = 0;
-            for (int j = 0; j < n; ++j) r += list[j] > k;
-            tmp[r] = k;
-        }
+    if (n <= kThreads / 2) {  // each key counts those before it, two threads to a key
+        const int i = t >> 1, half = (n + 1) >> 1;
+        const uint64_t k = i < n ? list[i] : 0;
+        int r = 0;
+        const int end = t & 1 ? n : half;
+#pragma unroll 4
+        for (int j = t & 1 ? half : 0; j < end; ++j) r += list[j] > k;
+        r += __shfl_xor_sync(0xffffffffu, r, 1);
+        if (i < n && !(t & 1)) tmp[r] = k;
         __syncthreads();
         if (t < n) list[t] = tmp[t];
         __syncthreads();
         return;
     }
-    int size = 256;
+    int size = kThreads;
     while (size < n) size *= 2;
     for (int i = n + t; i < size; i += kThreads) list[i] = 0;  // after every key
     __syncthreads();
-    if (size <= kThreads) {  // one key per thread: partners within a warp need no barrier
-        uint64_t key = t < size ? list[t] : 0;
+    if (size == kThreads) {  // one key per thread: partners within a warp need no barrier
+        uint64_t key = list[t];
 #pragma unroll 1
         for (int len = 2; len <= size; len *= 2)
 #pragma unroll 1
@@ -455,9 +475,9 @@ __device__ __forceinline__ void sort_list(uint64_t* list, int n, uint64_t* tmp) 
                 uint64_t other;
                 if (step >= 32) {
                     __syncthreads();
-                    if (t < size) list[t] = key;
+                    list[t] = key;
                     __syncthreads();
-                    other = t < size ? list[t ^ step] : 0;
+                    other = list[t ^ step];
                 } else {
                     other = __shfl_xor_sync(0xffffffffu, key, step);
                 }
@@ -465,7 +485,7 @@ __device__ __forceinline__ void sort_list(uint64_t* list, int n, uint64_t* tmp) 
                 key = (other > key) == larger ? other : key;
             }
         __syncthreads();
-        if (t < size) list[t] = key;
+        list[t] = key;
         __syncthreads();
         return;
     }
@@ -542,27 +562,15 @@ struct Sampler {
         uint32_t total = 0;
         for (int c = 0; c < a.cluster; ++c) total += sh.part_n[c];
         if (total > kCap) return false;
-        uint32_t at = sh.part_n[0];
-        for (int c = 1; c < a.cluster; ++c) {
-            const uint32_t m = sh.part_n[c];
-            for (uint32_t i = threadIdx.x; i < m; i += kThreads) sh.list[at + i] = remote(&sh.list[i], c);
-            at += m;
-        }
         n = int(total);
+        if (a.cluster == 1) return true;
+        for (uint32_t i = sh.part_n[0] + threadIdx.x; i < total; i += kThreads) {
+            uint32_t c = 0, j = i;
+            while (j >= sh.part_n[c]) j -= sh.part_n[c++];
+            sh.list[i] = remote(&sh.list[j], int(c));
+        }
         __syncthreads();
         return true;
-    }
-
-    // Block 0: the first i < n with s[i] >= target (n when there is none).
-    template <typename V>
-    __device__ __forceinline__ int first_at_least(const V* s, int n, V target) {
-        __syncthreads();
-        if (threadIdx.x == 0) sh.found = uint32_t(n);
-        __syncthreads();
-        for (int i = threadIdx.x; i < n; i += kThreads)
-            if (s[i] >= target && (i == 0 || s[i - 1] < target)) sh.found = uint32_t(i);
-        __syncthreads();
-        return int(sh.found);
     }
 
     __device__ __forceinline__ void add_mass(uint64_t* at, uint64_t w) {
@@ -628,8 +636,8 @@ struct Sampler {
                     sh.sums[i] += remote(&sh.sums[i], c);
                 }
             __syncthreads();
-            prefix_sums(sh.list, kCap, sh.warp_sum, [&](int i) { return sh.list[i]; });
-            prefix_sums(sh.sums, kCap, sh.warp_sum, [&](int i) { return sh.sums[i]; });
+            prefix_sums<kCap / kThreads>(sh.list, kCap, sh.warp_sum, [&](int i) { return sh.list[i]; });
+            prefix_sums<kCap / kThreads>(sh.sums, kCap, sh.warp_sum, [&](int i) { return sh.sums[i]; });
             const int b = min(by_count ? first_at_least(sh.sums, kCap, target - base_count)
                                        : first_at_least(sh.list, kCap, target > base ? target - base : 1),
                               kCap - 1);
@@ -646,12 +654,11 @@ struct Sampler {
         if (a.logprob) a.logprob[row] = logprob;
     }
 
-    // Block 0, thread 0: the drawn token and the logarithm of its share of the mass.
-    __device__ __forceinline__ void finish(int64_t row, uint64_t key, uint64_t mass, float t) {
+    // Block 0, thread 0: the drawn token, of weight w, and the logarithm of its share of the mass.
+    __device__ __forceinline__ void finish(int64_t row, uint64_t key, uint64_t w, uint64_t mass, float t) {
         write(row, key_index(key), 0.f);
         if (!a.logprob) return;
         const float z = key_logit(key);
-        const uint64_t w = weight_of(sc, z, sh.table, a.q_bits);
         float lp;
         if (w > mass / 2) lp = log1pf(-__ull2float_rn(mass - w) / __ull2float_rn(mass));
         else lp = (z - sc.m) / fminf(fmaxf(t, 1e-30f), 1e30f) - logf(ldexpf(__ull2float_rn(mass), -a.q_bits));
@@ -707,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
     if (heads_k) {
         const int j = (top_k + a.cluster - 1) / a.cluster;
         int groups = 64;  // of neighbouring threads: larger groups bound less tightly but rank faster
-        while (groups < 4 * j && groups < kThreads) groups *= 2;
+        while (groups < 2 * j && groups < kThreads) groups *= 2;
         const int width = kThreads / groups;
         float g = -INFINITY;
         if (tid < groups)
@@ -780,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
         }
     }
     const bool heads_min = by_min && !by_p;
-    uint64_t key = 0, mass = 0, above = 0;
+    uint64_t key = 0, weight_drawn = 0, mass = 0, above = 0;
     int step = heads_k || heads_min ? kHeads : kTopK;
 #pragma unroll 1
     for (;; ++step) {
@@ -790,10 +797,11 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
         if (step == kTopK) {
             // ---- weights of the whole row, summed by n ----
             for (int i = tid; i < kBins; i += kThreads) sh.mass[i] = 0, sh.count[i] = 0;
-            __syncthreads();
             // min-p (with top-p): whole bins above the border, and single weights next to it
             const int edge = by_min ? max(0, bin_of(fmaxf(kLeastLog2, log2f(min_p))) - 2) : kBins;
             if (tid == 0) sh.kept_minp = 0;
+            __syncthreads();
+            uint32_t* const words = reinterpret_cast<uint32_t*>(sh.mass);  // low halves, then high ones
             for_pairs<1>(s.part, a.dev_status, [&](float z0, float z1, int) {
                 const Step2 st = step_of2(sc, make_float2(z0, z1));
 #pragma unroll
@@ -801,16 +809,29 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
                     if (!((k ? st.p.y : st.p.x) < -kLeastLog2)) continue;
                     const int bin = st.bin[k];
                     if (!VCE_BOUNDS(bin >= 0 && bin < kBins, a.dev_status)) continue;
-                    uint32_t* at = reinterpret_cast<uint32_t*>(&sh.mass[bin]);
-                    atomicAdd(at, st.s[k] & ((1u << kHalfBits) - 1));
-                    atomicAdd(at + 1, st.s[k] >> kHalfBits);
-                    atomicAdd(&sh.count[bin], 1u);
+                    const bool fine = bin < kFineBins;
+                    const uint32_t coarse = (st.s[k] + (1u << (kCoarseBits - 1)) >> kCoarseBits) + kCoarseOffset;
+                    const uint32_t x = fine ? st.s[k] : coarse;
+                    atomicAdd(words + bin, x & ((1u << kHalfBits) - 1));
+                    atomicAdd(words + kBins + bin, x >> kHalfBits);
+                    if (fine || by_k) atomicAdd(&sh.count[bin], 1u);
                 }
             });
             __syncthreads();
-            for (int i = tid; i < kBins; i += kThreads) {
-                const uint64_t m2 = sh.mass[i], c = sh.count[i];
-                sh.mass[i] = (c << kFracBits) - (c << kBiasBits) + (m2 & 0xffffffffu) + ((m2 >> 32) << kHalfBits);
+            {
+                constexpr int kPer = (kBins + kThreads - 1) / kThreads;
+                uint64_t v[kPer];
+#pragma unroll
+                for (int k = 0; k < kPer; ++k) {
+                    const int i = tid + k * kThreads;
+                    if (i >= kBins) break;
+                    const uint64_t x = words[i] + (uint64_t(words[kBins + i]) << kHalfBits), c = sh.count[i];
+                    v[k] = i < kFineBins ? x + (c << kFracBits) - (c << kBiasBits) : x << kCoarseBits;
+                }
+                __syncthreads();
+#pragma unroll
+                for (int k = 0; k < kPer; ++k)
+                    if (tid + k * kThreads < kBins) sh.mass[tid + k * kThreads] = v[k];
             }
             if (by_min) {  // the few elements of five bins
                 const Wanted w = s.in_bin({0, ~0ull, edge + 2, 0});
@@ -823,28 +844,33 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
                 });
             }
             s.barrier();
-            if (s.lead()) {
-                if (a.cluster > 1) {
-                    for (int i = tid; i < kBins; i += kThreads) {
-                        uint64_t v[kMaxCluster];
-                        uint32_t c[kMaxCluster];
+            if (a.cluster > 1) {
+                // Each block adds up all blocks' sums of its share of the bins and puts the
+                // results into block 0 (whose sums of these bins nobody else reads).
+                const int share = (kBins + a.cluster - 1) / a.cluster, end = min(kBins, (rank + 1) * share);
+                for (int i = rank * share + tid; i < end; i += kThreads) {
+                    uint64_t v[kMaxCluster];
+                    uint32_t c[kMaxCluster];
 #pragma unroll
-                        for (int r = 1; r < kMaxCluster; ++r)  // all loads before the sums
-                            if (r < a.cluster) v[r] = remote(&sh.mass[i], r), c[r] = remote(&sh.count[i], r);
-                        uint64_t sum = sh.mass[i];
-                        uint32_t n = sh.count[i];
+                    for (int r = 0; r < kMaxCluster; ++r)  // all loads before the sums
+                        if (r < a.cluster) v[r] = remote(&sh.mass[i], r), c[r] = remote(&sh.count[i], r);
+                    uint64_t sum = 0;
+                    uint32_t n = 0;
 #pragma unroll
-                        for (int r = 1; r < kMaxCluster; ++r)
-                            if (r < a.cluster) sum += v[r], n += c[r];
-                        sh.mass[i] = sum;
-                        sh.count[i] = n;
-                    }
-                    __syncthreads();
+                    for (int r = 0; r < kMaxCluster; ++r)
+                        if (r < a.cluster) sum += v[r], n += c[r];
+                    put(&sh.mass[i], 0, sum);
+                    put(&sh.count[i], 0, n);
                 }
-                prefix_sums(sh.mass, kBins, sh.warp_sum, [&](int i) {
-                    return sh.count[i] ? scale_up(sh.mass[i], i, sh.table, a.q_bits) : uint64_t(0);
+                s.barrier();
+            }
+            if (s.lead()) {
+                constexpr int kPer = (kBins + kThreads - 1) / kThreads;
+                prefix_sums<kPer>(sh.mass, kBins, sh.warp_sum, [&](int i) {
+                    const uint64_t sum = sh.mass[i];
+                    return sum ? scale_up(sum, i, sh.table, a.q_bits) : uint64_t(0);
                 });
-                if (by_k) prefix_sums(sh.count, kBins, sh.warp_sum, [&](int i) { return sh.count[i]; });
+                if (by_k) prefix_sums<kPer>(sh.count, kBins, sh.warp_sum, [&](int i) { return sh.count[i]; });
                 mass = sh.mass[kBins - 1];
                 cmd.flag = by_k && sh.count[kBins - 1] > uint32_t(top_k);  // the k-th has a weight
                 if (by_min) {
@@ -869,8 +895,8 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
                  heads_min ? fmaxf(kLeastLog2, log2f(min_p) - 0.01f) : kLeastLog2, cmd};
         if (step != kHeads) {
             if (s.lead()) {
-                cmd.bin = min(step == kTopK ? s.first_at_least(sh.count, kBins, uint32_t(target))
-                                            : s.first_at_least(sh.mass, kBins, target),
+                cmd.bin = min(step == kTopK ? first_at_least(sh.count, kBins, uint32_t(target))
+                                            : first_at_least(sh.mass, kBins, target),
                               kBins - 1);
                 if (cmd.bin > 0) base = sh.mass[cmd.bin - 1], base_count = sh.count[cmd.bin - 1];
             }
@@ -888,9 +914,11 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
                 cmd.flag = s.join_lists(n);
                 if (cmd.flag) {
                     sort_list(sh.list, n, sh.sums);
-                    prefix_sums(sh.sums, n, sh.warp_sum, [&](int i) {
+                    auto weight = [&](int i) {
                         return weight_of(sc, key_logit(sh.list[i]), sh.table, a.q_bits) + (i == 0 ? base : 0);
-                    });
+                    };
+                    if (n <= kThreads) prefix_sums<1>(sh.sums, n, sh.warp_sum, weight);
+                    else prefix_sums<kCap / kThreads>(sh.sums, n, sh.warp_sum, weight);
                     int at;
                     if (step == kTopK) {
                         at = int(target - base_count) - 1;
@@ -901,7 +929,7 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
                             if (by_p) {
                                 target = floor_product(fmaxf(top_p, 0.f), mass, &exact);
                                 target += exact ? 0 : 1;
-                                n = s.first_at_least(sh.sums, n, target ? target : uint64_t(1)) + 1;
+                                n = first_at_least(sh.sums, n, target ? target : uint64_t(1)) + 1;
                             }
                             if (by_min) {  // weights descend: the first that is too small ends the head
                                 __syncthreads();
@@ -915,10 +943,11 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
                             mass = sh.sums[n - 1];
                             target = u >= 1.f ? mass : floor_product(fmaxf(u, 0.f), mass, &exact) + 1;
                         }
-                        at = s.first_at_least(sh.sums, n, target);
+                        at = first_at_least(sh.sums, n, target);
                     }
                     at = max(0, min(at, n - 1));
                     key = sh.list[at];
+                    weight_drawn = sh.sums[at] - (at ? sh.sums[at - 1] : base);
                     if (step == kTopK || step == kTopP) mass = sh.sums[at];
                 }
             }
@@ -931,7 +960,7 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
         }
         if (step == kDraw || (step == kHeads && cmd.flag)) break;  // heads that are too many: by masses
     }
-    if (s.lead() && tid == 0) s.finish(row, key, mass, temp);
+    if (s.lead() && tid == 0) s.finish(row, key, weight_drawn, mass, temp);
     s.barrier();  // nobody leaves while its shared memory is read
 }
 
