@@ -1,13 +1,14 @@
 """ctypes marshalling for the operators around the vocabulary cross entropy: the norm
-before the classifier, microscaled tensors and their product, and sampling (see include/vce.h for what each
-computes).  As in ``_binding``, torch tensors supply memory and the current stream.
+before the classifier, microscaled tensors and their product, and sampling (see
+include/vce.h for what each computes).  As in ``_binding``, torch tensors supply memory
+and the current stream.
 
-A call given ``stream`` allocates what it was not given (outputs and workspace) from
-that stream, so memory it drops on return is reused only behind its kernels.
+A call given ``stream`` runs as if that stream were current: what it was not given
+(outputs and workspace) is allocated from it too, so memory it drops on return is reused
+only behind its kernels.
 """
 from __future__ import annotations
 
-import contextlib
 from collections import namedtuple
 
 import torch
@@ -23,13 +24,12 @@ RMSNormMX = namedtuple("RMSNormMX", "y h rstd")
 RMSNormBackward = namedtuple("RMSNormBackward", "dx dweight")
 CESample = namedtuple("CESample", "token logprob dev_status")
 
-
 _CODES = {torch.bfloat16: b.BF16, torch.float32: b.F32}
-_no_stream = contextlib.nullcontext()
 
 
-def _on_stream(stream):
-    return _no_stream if stream is None else torch.cuda.stream(stream)
+def _under(stream, fn, *args, **kwargs):
+    with torch.cuda.stream(stream):
+        return fn(*args, **kwargs)
 
 
 def _float_code(dtype, name):
@@ -41,9 +41,10 @@ def _float_code(dtype, name):
 
 def _rows_of(t, name):
     """(rows, cols, row stride) of a 2-D tensor with contiguous rows."""
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{name} must be a 2-D tensor with contiguous rows")
-    n, c = t.shape
+    n, c = shape
     rs, cs = t.stride()
     if cs != 1 and c > 1:
         raise ValueError(f"{name} must be a 2-D tensor with contiguous rows")
@@ -81,11 +82,14 @@ def _weight(t, hidden, index):
 
 
 def _launch(name, device, fn, *args):
-    """fn(*args, stream) of the library, once everything about the arguments has been checked."""
-    if device.type != "cuda":
+    """fn(*args, current stream) of the library, once everything about the arguments has been checked."""
+    index = device.index
+    if index is None:
         raise ValueError(f"{name}: tensors must be on a CUDA device, got {device}")
-    *args, stream = args
-    st = b._on(device, fn, *args, b._stream(device, stream))
+    if b._raw_stream is not None and b._raw_device() == index:  # the common case, without detours
+        st = fn(*args, b._raw_stream(index))
+    else:
+        st = b._on(device, fn, *args, b._stream(device, None))
     if st:
         b._check(name, st)
 
@@ -110,9 +114,9 @@ class MXTensor(namedtuple("MXTensor", "codes scales rows cols fmt")):
 
     @staticmethod
     def empty(rows, cols, fmt, device):
-        padded = -(-cols // 128) * 128
-        codes = torch.empty(rows, padded // (2 if fmt == "e2m1" else 1), dtype=torch.uint8, device=device)
-        scales = torch.empty(-(-rows // 128), padded // 128, 32, 4, 4, dtype=torch.uint8, device=device)
+        tiles = -(-cols // 128)
+        codes = torch.empty((rows, tiles * (64 if fmt == "e2m1" else 128)), dtype=torch.uint8, device=device)
+        scales = torch.empty((-(-rows // 128), tiles, 32, 4, 4), dtype=torch.uint8, device=device)
         return MXTensor(codes, scales, rows, cols, fmt)
 
     @staticmethod
@@ -169,40 +173,44 @@ def mx_scales_size(rows: int, cols: int) -> int:
 
 def mx_quantize(x, fmt="e2m1", *, out=None, dev_status=None, stream=None) -> MXTensor:
     """``x`` [rows, cols] (bfloat16 or float32) as a microscaled tensor."""
+    if stream is not None:
+        return _under(stream, mx_quantize, x, fmt, out=out, dev_status=dev_status)
     code, fcode = _float_code(x.dtype, "x"), _fmt(fmt)
     rows, cols, stride = _rows_of(x, "x")
     dev, index = x.device, x.get_device()
     if out is None:
-        with _on_stream(stream):
-            out = MXTensor.empty(rows, cols, fmt, dev)
+        out = MXTensor.empty(rows, cols, fmt, dev)
     else:
         _check_mx(out, "out")
         if out[2:] != (rows, cols, fmt) or out.codes.get_device() != index:
             raise ValueError("out must have x's shape and device, and the format asked for")
     _launch("mx_quantize", dev, b.library().mx_quantize, x.data_ptr(), code, rows, cols, stride, fcode,
-            out.codes.data_ptr(), out.scales.data_ptr(), _status(dev_status, index), stream)
+            out.codes.data_ptr(), out.scales.data_ptr(), _status(dev_status, index))
     return out
 
 
 def mx_dequantize(t: MXTensor, dtype=torch.bfloat16, *, out=None, dev_status=None, stream=None):
     """The values of a microscaled tensor, [rows, cols] in bfloat16 or float32."""
+    if stream is not None:
+        return _under(stream, mx_dequantize, t, dtype, out=out, dev_status=dev_status)
     fcode, code = _check_mx(t, "t"), _float_code(dtype, "dtype")
     codes, scales, rows, cols, _ = t
     dev, index = codes.device, codes.get_device()
     stride = cols
     if out is None:
-        with _on_stream(stream):
-            out = torch.empty(rows, cols, dtype=dtype, device=dev)
+        out = torch.empty(rows, cols, dtype=dtype, device=dev)
     else:
         stride = _written_rows(out, "out", (rows, cols), dtype, index)
-    _launch("mx_dequantize", dev, b.library().mx_dequantize, codes.data_ptr(), scales.data_ptr(), fcode, rows, cols,
-            out.data_ptr(), code, stride, _status(dev_status, index), stream)
+    _launch("mx_dequantize", dev, b.library().mx_dequantize, codes.data_ptr(), scales.data_ptr(), fcode,
+            rows, cols, out.data_ptr(), code, stride, _status(dev_status, index))
     return out
 
 
 def mx_linear(x: MXTensor, w: MXTensor, out_dtype=torch.bfloat16, *, out=None, dev_status=None, stream=None):
     """``x @ w.T`` of the values of x (e4m3, [n, h]) and the classifier w (e2m1, [v, h]):
     logits [n, v] in bfloat16 or float32.  dev_status is None or an int32 [1] tensor."""
+    if stream is not None:
+        return _under(stream, mx_linear, x, w, out_dtype, out=out, dev_status=dev_status)
     if (_check_mx(x, "x"), _check_mx(w, "w")) != (MX_E4M3, MX_E2M1):
         raise ValueError(f"x must be e4m3 and w e2m1, got {x.fmt} and {w.fmt}")
     xc, xs, n, h, _ = x
@@ -214,12 +222,11 @@ def mx_linear(x: MXTensor, w: MXTensor, out_dtype=torch.bfloat16, *, out=None, d
         raise ValueError("x and w are on different devices")
     code, stride = _float_code(out_dtype, "out_dtype"), v
     if out is None:
-        with _on_stream(stream):
-            out = torch.empty(n, v, dtype=out_dtype, device=dev)
+        out = torch.empty(n, v, dtype=out_dtype, device=dev)
     else:
         stride = _written_rows(out, "out", (n, v), out_dtype, index)
-    _launch("mx_linear", dev, b.library().mx_linear, xc.data_ptr(), xs.data_ptr(), wc.data_ptr(), ws.data_ptr(), n, h,
-            v, out.data_ptr(), code, stride, _status(dev_status, index), stream)
+    _launch("mx_linear", dev, b.library().mx_linear, xc.data_ptr(), xs.data_ptr(), wc.data_ptr(),
+            ws.data_ptr(), n, h, v, out.data_ptr(), code, stride, _status(dev_status, index))
     return out
 
 
@@ -227,9 +234,9 @@ def mx_linear(x: MXTensor, w: MXTensor, out_dtype=torch.bfloat16, *, out=None, d
 # the norm before the classifier
 # ---------------------------------------------------------------------------
 
-def _norm_inputs(x, weight, residual, h, stream):
-    """What both norms hand to the library, and h: (code, n, hidden, x stride, residual, its stride,
-    weight code, h's pointer, its stride), device index, h."""
+def _norm_inputs(x, weight, residual, h):
+    """What both norms hand to the library: (x's type, n, hidden, x's stride, residual, its stride,
+    weight, its type), then h's pointer and stride, the device's index, and h itself."""
     code = _float_code(x.dtype, "x")
     n, hidden, xs = _rows_of(x, "x")
     index = x.get_device()
@@ -240,8 +247,7 @@ def _norm_inputs(x, weight, residual, h, stream):
         return (code, n, hidden, xs, None, hidden, weight.data_ptr(), wcode), None, hidden, index, x
     rs, hs = _same_rows(residual, "residual", x), hidden
     if h is None:
-        with _on_stream(stream):
-            h = torch.empty(n, hidden, dtype=x.dtype, device=x.device)
+        h = torch.empty(n, hidden, dtype=x.dtype, device=x.device)
     else:
         hs = _written_rows(h, "h", (n, hidden), x.dtype, index)
     return (code, n, hidden, xs, residual.data_ptr(), rs, weight.data_ptr(), wcode), h.data_ptr(), hs, index, h
@@ -251,39 +257,41 @@ def rms_norm_forward(x, weight, eps=1e-6, residual=None, *, h=None, y=None, rstd
                      stream=None):
     """Norm of x + residual over the last dimension of ``x`` [n, hidden].  Returns (y, h, rstd):
     h is the rounded sum (``x`` itself without a residual), rstd FP32 [n]."""
-    args, hp, hs, index, h = _norm_inputs(x, weight, residual, h, stream)
+    if stream is not None:
+        return _under(stream, rms_norm_forward, x, weight, eps, residual, h=h, y=y, rstd=rstd, dev_status=dev_status)
+    args, hp, hs, index, h = _norm_inputs(x, weight, residual, h)
     n, hidden = args[1], args[2]
     dev, ys = x.device, hidden
-    with _on_stream(stream):
-        if y is None:
-            y = torch.empty(n, hidden, dtype=x.dtype, device=dev)
-        else:
-            ys = _written_rows(y, "y", (n, hidden), x.dtype, index)
-        if rstd is None:
-            rstd = torch.empty(n, dtype=torch.float32, device=dev)
-        else:
-            _vector(rstd, "rstd", n, torch.float32, index)
-    _launch("rms_norm_forward", dev, b.library().rms_norm_forward, x.data_ptr(), *args, eps, hp, hs, y.data_ptr(), ys,
-            rstd.data_ptr(), _status(dev_status, index), stream)
+    if y is None:
+        y = torch.empty(n, hidden, dtype=x.dtype, device=dev)
+    else:
+        ys = _written_rows(y, "y", (n, hidden), x.dtype, index)
+    if rstd is None:
+        rstd = torch.empty(n, dtype=torch.float32, device=dev)
+    else:
+        _vector(rstd, "rstd", n, torch.float32, index)
+    _launch("rms_norm_forward", dev, b.library().rms_norm_forward, x.data_ptr(), *args, eps, hp, hs,
+            y.data_ptr(), ys, rstd.data_ptr(), _status(dev_status, index))
     return RMSNormForward(y, h, rstd)
 
 
 def rms_norm_mx(x, weight, eps=1e-6, residual=None, *, h=None, out=None, rstd=None, dev_status=None, stream=None):
     """rms_norm_forward with y as an E4M3 microscaled tensor, mx_linear's input.  Returns
     (y: MXTensor, h, rstd); rstd only when a tensor is passed for it."""
-    args, hp, hs, index, h = _norm_inputs(x, weight, residual, h, stream)
+    if stream is not None:
+        return _under(stream, rms_norm_mx, x, weight, eps, residual, h=h, out=out, rstd=rstd, dev_status=dev_status)
+    args, hp, hs, index, h = _norm_inputs(x, weight, residual, h)
     n, hidden = args[1], args[2]
     if out is None:
-        with _on_stream(stream):
-            out = MXTensor.empty(n, hidden, "e4m3", x.device)
+        out = MXTensor.empty(n, hidden, "e4m3", x.device)
     else:
         _check_mx(out, "out")
         if out[2:] != (n, hidden, "e4m3") or out.codes.get_device() != index:
             raise ValueError("out must be an e4m3 tensor of x's shape and device")
     if rstd is not None:
         _vector(rstd, "rstd", n, torch.float32, index)
-    _launch("rms_norm_mx", x.device, b.library().rms_norm_mx, x.data_ptr(), *args, eps, hp, hs, out.codes.data_ptr(),
-            out.scales.data_ptr(), b._ptr(rstd), _status(dev_status, index), stream)
+    _launch("rms_norm_mx", x.device, b.library().rms_norm_mx, x.data_ptr(), *args, eps, hp, hs,
+            out.codes.data_ptr(), out.scales.data_ptr(), b._ptr(rstd), _status(dev_status, index))
     return RMSNormMX(out, h, rstd)
 
 
@@ -295,6 +303,9 @@ def rms_norm_backward(dy, h, weight, rstd, dh=None, *, dx=None, dweight=None, wo
                       stream=None):
     """Backward of rms_norm_forward.  Returns (dx, dweight): dx is the gradient of x and of the
     residual; ``dh`` is the gradient that reaches h by another way."""
+    if stream is not None:
+        return _under(stream, rms_norm_backward, dy, h, weight, rstd, dh, dx=dx, dweight=dweight, workspace=workspace,
+                      dev_status=dev_status)
     lib = b.library()
     dev, index = dy.device, dy.get_device()
     code = _float_code(dy.dtype, "dy")
@@ -304,23 +315,23 @@ def rms_norm_backward(dy, h, weight, rstd, dh=None, *, dx=None, dweight=None, wo
     wcode = _weight(weight, hidden, index)
     _vector(rstd, "rstd", n, torch.float32, index)
     xs = hidden
-    with _on_stream(stream):
-        if dx is None:
-            dx = torch.empty(n, hidden, dtype=dy.dtype, device=dev)
-        else:
-            xs = _written_rows(dx, "dx", (n, hidden), dy.dtype, index)
-        if dweight is None:
-            dweight = torch.empty(hidden, dtype=weight.dtype, device=dev)
-        else:
-            _vector(dweight, "dweight", hidden, weight.dtype, index)
-        if workspace is None:
-            size = b._on(dev, lib.rms_norm_workspace_size, n, hidden)
-            workspace = torch.empty(size or 1, dtype=torch.uint8, device=dev)
-        elif workspace.get_device() != index or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on the inputs' device")
-    _launch("rms_norm_backward", dev, lib.rms_norm_backward, dy.data_ptr(), code, n, hidden, gs, h.data_ptr(), hs,
-            weight.data_ptr(), wcode, rstd.data_ptr(), b._ptr(dh), ds, dx.data_ptr(), xs, dweight.data_ptr(),
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), _status(dev_status, index), stream)
+    if dx is None:
+        dx = torch.empty(n, hidden, dtype=dy.dtype, device=dev)
+    else:
+        xs = _written_rows(dx, "dx", (n, hidden), dy.dtype, index)
+    if dweight is None:
+        dweight = torch.empty(hidden, dtype=weight.dtype, device=dev)
+    else:
+        _vector(dweight, "dweight", hidden, weight.dtype, index)
+    if workspace is None:
+        size = b._on(dev, lib.rms_norm_workspace_size, n, hidden)
+        workspace = torch.empty(size or 1, dtype=torch.uint8, device=dev)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+    _launch("rms_norm_backward", dev, lib.rms_norm_backward, dy.data_ptr(), code, n, hidden, gs,
+            h.data_ptr(), hs, weight.data_ptr(), wcode, rstd.data_ptr(), b._ptr(dh), ds, dx.data_ptr(), xs,
+            dweight.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+            _status(dev_status, index))
     return RMSNormBackward(dx, dweight)
 
 
@@ -345,28 +356,30 @@ def ce_sample(logits, uniform, temperature=None, top_k=None, top_p=None, min_p=N
     first two shaped like the leading dimensions; logprob is the logarithm of the probability
     the token was drawn with.  A row from which nothing can be drawn gives -1 and NaN, and sets
     a bit of ``dev_status`` (int32 [1]) where one is passed."""
+    if stream is not None:
+        return _under(stream, ce_sample, logits, uniform, temperature, top_k, top_p, min_p, token=token,
+                      logprob=logprob, dev_status=dev_status)
     dev, index = logits.device, logits.get_device()
     code = _float_code(logits.dtype, "logits")
     n, vocab, stride = b._rows_view(logits)
     lead = logits.shape[:-1]
     _vector(uniform, "uniform", n, torch.float32, index)
-    with _on_stream(stream):
-        temperature = _per_row(temperature, "temperature", n, torch.float32, index, dev)
-        top_k = _per_row(top_k, "top_k", n, torch.int32, index, dev)
-        top_p = _per_row(top_p, "top_p", n, torch.float32, index, dev)
-        min_p = _per_row(min_p, "min_p", n, torch.float32, index, dev)
-        if token is None:
-            token = torch.empty(lead, dtype=torch.int64, device=dev)
-        else:
-            _vector(token, "token", n, torch.int64, index)
-        if logprob is None:
-            logprob = torch.empty(lead, dtype=torch.float32, device=dev)
-        else:
-            _vector(logprob, "logprob", n, torch.float32, index)
+    temperature = _per_row(temperature, "temperature", n, torch.float32, index, dev)
+    top_k = _per_row(top_k, "top_k", n, torch.int32, index, dev)
+    top_p = _per_row(top_p, "top_p", n, torch.float32, index, dev)
+    min_p = _per_row(min_p, "min_p", n, torch.float32, index, dev)
+    if token is None:
+        token = torch.empty(lead, dtype=torch.int64, device=dev)
+    else:
+        _vector(token, "token", n, torch.int64, index)
+    if logprob is None:
+        logprob = torch.empty(lead, dtype=torch.float32, device=dev)
+    else:
+        _vector(logprob, "logprob", n, torch.float32, index)
     ptr = b._ptr
-    _launch("ce_sample", dev, b.library().ce_sample, logits.data_ptr(), code, n, vocab, stride, uniform.data_ptr(),
-            ptr(temperature), ptr(top_k), ptr(top_p), ptr(min_p), token.data_ptr(), logprob.data_ptr(),
-            _status(dev_status, index), stream)
+    _launch("ce_sample", dev, b.library().ce_sample, logits.data_ptr(), code, n, vocab, stride,
+            uniform.data_ptr(), ptr(temperature), ptr(top_k), ptr(top_p), ptr(min_p), token.data_ptr(),
+            logprob.data_ptr(), _status(dev_status, index))
     return CESample(token, logprob, dev_status)
 
 
@@ -375,15 +388,18 @@ def linear_sample(embeddings, classifier: MXTensor, uniform, temperature=None, t
     """The next token after ``embeddings`` [..., H], the counterpart of linear_cross_entropy when a
     model answers: the norm (with ``norm_weight`` [H]; plus ``residual``) in 8 bits, the product
     with the 4-bit ``classifier``, and ce_sample of the logits.  Returns ce_sample's results."""
+    if stream is not None:
+        return _under(stream, linear_sample, embeddings, classifier, uniform, temperature, top_k, top_p, min_p,
+                      norm_weight=norm_weight, norm_eps=norm_eps, residual=residual, dev_status=dev_status)
     lead, h = embeddings.shape[:-1], embeddings.shape[-1]
     x = embeddings.reshape(-1, h)
     if norm_weight is not None:
         res = None if residual is None else residual.reshape(-1, h)
-        q = rms_norm_mx(x, norm_weight, norm_eps, res, stream=stream).y
+        q = rms_norm_mx(x, norm_weight, norm_eps, res).y
     elif residual is not None:
         raise ValueError("residual is added by the norm: it needs norm_weight")
     else:
-        q = mx_quantize(x, "e4m3", stream=stream)
-    logits = mx_linear(q, classifier, torch.float32, dev_status=dev_status, stream=stream)
-    r = ce_sample(logits, uniform, temperature, top_k, top_p, min_p, dev_status=dev_status, stream=stream)
+        q = mx_quantize(x, "e4m3")
+    logits = mx_linear(q, classifier, torch.float32, dev_status=dev_status)
+    r = ce_sample(logits, uniform, temperature, top_k, top_p, min_p, dev_status=dev_status)
     return CESample(r.token.view(lead), r.logprob.view(lead), dev_status)
