@@ -290,27 +290,51 @@ __device__ __forceinline__ float one(const float* p) { return *p; }
 __device__ __forceinline__ float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
 // fn(logit, logit, index) for every two neighbouring elements of the block's part (index is
-// the first one's), U vectors in flight per thread.  The vectors that lie in the row as a
-// whole come first, then the elements of the two that may not, each with -inf beside it.
-template <int U, typename T, typename F>
+// the first one's).  The vectors that lie in the row as a whole come first, then the
+// elements of the two that may not, each with -inf beside it.  Short bodies take U vectors
+// at a time, all of them loaded first; long ones (kAhead > 0) one, with the next kAhead on
+// their way: their code, laid out several times, cost more in instruction fetches than
+// the loads in flight gained.
+template <int U, int kAhead = 0, typename T, typename F>
 __device__ __forceinline__ void for_pairs(const Part<T>& p, int* dev_status, F fn) {
     constexpr int VE = 16 / sizeof(T);
     const int tid = threadIdx.x;
     const int head = p.off > 0 ? 1 : 0, whole = (p.off + p.vocab) / VE;  // whole vectors: [head, whole)
     const int end = min(p.q1, whole);
-    for (int q = max(p.q0, head) + tid; q < end; q += U * kThreads) {
-        const T* at = p.row + (q * VE - p.off);
-        uint4 v[U];
+    int q = max(p.q0, head) + tid;
+    const T* at = p.row + (q * VE - p.off);
+    auto fetch = [&](int k) {  // vector q + k kThreads
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (q + k * kThreads < end && VCE_BOUNDS(aligned16(at), dev_status))
+            v = __ldg(reinterpret_cast<const uint4*>(at + k * kThreads * VE));
+        return v;
+    };
+    if constexpr (kAhead > 0) {  // long bodies, one vector at a time: the next ones are on their way
+        uint4 ring[kAhead];
 #pragma unroll
-        for (int k = 0; k < U; ++k)
-            if (q + k * kThreads < end && VCE_BOUNDS(aligned16(at), dev_status))
-                v[k] = __ldg(reinterpret_cast<const uint4*>(at + k * kThreads * VE));
+        for (int k = 0; k < kAhead; ++k) ring[k] = fetch(k);
+#pragma unroll 1
+        for (; q < end; q += kThreads, at += kThreads * VE) {
+            const uint4 v = ring[0];
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            if (q + k * kThreads >= end) break;
-            const int i = (q + k * kThreads) * VE - p.off;
+            for (int k = 0; k + 1 < kAhead; ++k) ring[k] = ring[k + 1];
+            ring[kAhead - 1] = fetch(kAhead);
+            const int i = q * VE - p.off;
 #pragma unroll
-            for (int e = 0; e < VE; e += 2) fn(element<T>(v[k], e), element<T>(v[k], e + 1), i + e);
+            for (int e = 0; e < VE; e += 2) fn(element<T>(v, e), element<T>(v, e + 1), i + e);
+        }
+    } else {
+        for (; q < end; q += U * kThreads, at += U * kThreads * VE) {
+            uint4 v[U];
+#pragma unroll
+            for (int k = 0; k < U; ++k) v[k] = fetch(k);
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                if (q + k * kThreads >= end) break;
+                const int i = (q + k * kThreads) * VE - p.off;
+#pragma unroll
+                for (int e = 0; e < VE; e += 2) fn(element<T>(v[k], e), element<T>(v[k], e + 1), i + e);
+            }
         }
     }
     // the first vector's elements, then those behind the whole vectors
@@ -324,55 +348,12 @@ __device__ __forceinline__ void for_pairs(const Part<T>& p, int* dev_status, F f
 }
 
 // fn(logit, index) for every element; also for a -inf with the index after a single one's
-template <int U, typename T, typename F>
+template <int U, int kAhead = 0, typename T, typename F>
 __device__ __forceinline__ void for_each(const Part<T>& p, int* dev_status, F fn) {
-    for_pairs<U>(p, dev_status, [&](float z0, float z1, int i) {
+    for_pairs<U, kAhead>(p, dev_status, [&](float z0, float z1, int i) {
         fn(z0, i);
         fn(z1, i + 1);
     });
-}
-
-// fn(logit, index) for the elements with z_lo <= logit <= z_hi, which are few: a bit per
-// element of U vectors first, then the bits' elements again, from the cache.
-template <int U, typename T, typename F>
-__device__ __forceinline__ void for_hits(const Part<T>& p, int* dev_status, float z_lo, float z_hi, F fn) {
-    constexpr int VE = 16 / sizeof(T);
-    static_assert(U * VE <= 32, "a bit each");
-    const int tid = threadIdx.x;
-    const int head = p.off > 0 ? 1 : 0, whole = (p.off + p.vocab) / VE;  // whole vectors: [head, whole)
-    const int end = min(p.q1, whole);
-    for (int q = max(p.q0, head) + tid; q < end; q += U * kThreads) {
-        const T* at = p.row + (q * VE - p.off);
-        uint4 v[U];
-#pragma unroll
-        for (int k = 0; k < U; ++k)
-            if (q + k * kThreads < end && VCE_BOUNDS(aligned16(at), dev_status))
-                v[k] = __ldg(reinterpret_cast<const uint4*>(at + k * kThreads * VE));
-        uint32_t hits = 0;
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            if (q + k * kThreads >= end) break;
-#pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                const float z = element<T>(v[k], e);
-                if (z >= z_lo && z <= z_hi) hits |= 1u << (k * VE + e);
-            }
-        }
-        while (hits) {
-            const int b = __ffs(hits) - 1;
-            hits &= hits - 1;
-            const int j = (b / VE) * kThreads * VE + b % VE;
-            fn(one(at + j), int(at - p.row) + j);
-        }
-    }
-    const int first = head && p.q0 == 0 && p.q1 > 0 ? min(VE - p.off, p.vocab) : 0;
-    const int tail0 = max(whole * VE - p.off, head ? VE - p.off : 0);
-    const int last = p.q1 > p.q0 && p.q1 * VE - p.off >= p.vocab ? max(p.vocab - tail0, 0) : 0;
-    if (tid < first + last) {
-        const int i = tid < first ? tid : tail0 + tid - first;
-        const float z = one(p.row + i);
-        if (z >= z_lo && z <= z_hi) fn(z, i);
-    }
 }
 
 // the address of ``p`` (in shared memory) in block ``rank`` of the cluster
@@ -535,19 +516,23 @@ struct Sampler {
         return *slot;
     }
 
+    __device__ __forceinline__ void take(const Wanted& w, float z, int i) {
+        const float p = log2_weight(sc, z);
+        const uint64_t k = key_of(z, i);
+        if (p > w.p_least && (w.cmd.bin < 0 || bin_of(p) == w.cmd.bin) && k >= w.cmd.lo && k <= w.cmd.hi) {
+            const uint32_t at = atomicAdd(&sh.n_list, 1u);
+            if (at < kCap) sh.list[at] = k;
+        }
+    }
+
     // Collects the keys of the elements that are wanted; behind the barrier block 0 has
     // every block's number of them.
     __device__ __forceinline__ void collect(const Wanted& w) {
         if (threadIdx.x == 0) sh.n_list = 0;
         __syncthreads();
-        const Scale s = sc;
-        for_hits<16 / sizeof(T) == 8 ? 4 : 8>(part, a.dev_status, w.z_lo, w.z_hi, [&](float z, int i) {
-            const float p = log2_weight(s, z);
-            const uint64_t k = key_of(z, i);
-            if (p > w.p_least && (w.cmd.bin < 0 || bin_of(p) == w.cmd.bin) && k >= w.cmd.lo && k <= w.cmd.hi) {
-                const uint32_t at = atomicAdd(&sh.n_list, 1u);
-                if (at < kCap) sh.list[at] = k;
-            }
+        const float z_lo = w.z_lo, z_hi = w.z_hi;
+        for_each<1, 2>(part, a.dev_status, [&](float z, int i) {
+            if (z >= z_lo && z <= z_hi) take(w, z, i);
         });
         __syncthreads();
         if (threadIdx.x == 0) {
@@ -802,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
             if (tid == 0) sh.kept_minp = 0;
             __syncthreads();
             uint32_t* const words = reinterpret_cast<uint32_t*>(sh.mass);  // low halves, then high ones
-            for_pairs<1>(s.part, a.dev_status, [&](float z0, float z1, int) {
+            for_pairs<1, 1>(s.part, a.dev_status, [&](float z0, float z1, int) {
                 const Step2 st = step_of2(sc, make_float2(z0, z1));
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
@@ -836,7 +821,8 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
             if (by_min) {  // the few elements of five bins
                 const Wanted w = s.in_bin({0, ~0ull, edge + 2, 0});
                 const float wide = 2.f / (kSteps * sc.ch);
-                for_hits<2>(s.part, a.dev_status, w.z_lo - wide, w.z_hi + wide, [&](float z, int) {
+                for_each<1>(s.part, a.dev_status, [&](float z, int) {
+                    if (!(z >= w.z_lo - wide && z <= w.z_hi + wide)) return;
                     const float p = log2_weight(sc, z);
                     if (!(p > kLeastLog2) || bin_of(p) < edge || bin_of(p) >= edge + 5) return;
                     const uint64_t x = weight_of(sc, z, sh.table, a.q_bits);
@@ -891,8 +877,8 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
             target = u >= 1.f ? mass : floor_product(fmaxf(u, 0.f), mass, &exact) + 1;
         }
         // ---- the border's bin, told to all ----
-        Wanted w{heads_k ? bound : -INFINITY, INFINITY,
-                 heads_min ? fmaxf(kLeastLog2, log2f(min_p) - 0.01f) : kLeastLog2, cmd};
+        Wanted w{0.f, row_max, heads_min ? fmaxf(kLeastLog2, log2f(min_p) - 0.01f) : kLeastLog2, cmd};
+        w.z_lo = heads_k ? bound : sc.m + (w.p_least - 0.1f) / sc.ch - fabsf(sc.m) * 0x1p-21f;
         if (step != kHeads) {
             if (s.lead()) {
                 cmd.bin = min(step == kTopK ? first_at_least(sh.count, kBins, uint32_t(target))
