@@ -414,7 +414,7 @@ vce_status rms_norm_mx(const void* x, int dtype, int64_t n, int64_t hidden, int6
                        void* scales, float* rstd, int* dev_status, void* stream);
 
 /* Bytes of workspace rms_norm_backward needs (FP32 partial sums of the weight's
- * gradient: at most four rows of ``hidden`` per SM), on the current device. */
+ * gradient: at most sixteen rows of ``hidden`` per SM), on the current device. */
 size_t rms_norm_workspace_size(int64_t n, int64_t hidden);
 
 /*

@@ -141,8 +141,12 @@ __device__ __forceinline__ void store_mx(const NormArgs& a, uint8_t* codes, uint
 #pragma unroll
     for (int i = 0; i < VE; ++i) top = mx::max_abs(top, y[i]);
     uint32_t m = __float_as_uint(top);
+    if constexpr (kLanes == 32) {
+        m = __reduce_max_sync(0xffffffffu, m);
+    } else {
 #pragma unroll
-    for (int o = 1; o < kLanes; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        for (int o = 1; o < kLanes; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    }
     const uint32_t sb = mx::scale_byte<VCE_MX_E4M3>(m);
     const bool bad = sb == mx::kNanScale;
     const float inv = mx::inverse_scale(bad ? 0u : sb);
@@ -666,7 +670,7 @@ vce_status norm_backward(NormBwdArgs a, int ve, int& parts, cudaStream_t s, cons
     constexpr int kFull = 16 / sizeof(T);
     constexpr int kNv = 32 / kFull;  // 32 sums of dw per thread
     const int64_t nvec = (a.hidden + ve - 1) / ve;
-    int nv = ve == kFull ? kNv : 16;
+    int nv = ve == kFull ? kNv : 8;
     a.parts = parts;
     // The ring where a row is longer than 128 vectors and its stages fit: as many blocks as
     // shared memory lets an SM hold (at most the four per SM of the workspace), so that all
@@ -696,9 +700,9 @@ vce_status norm_backward(NormBwdArgs a, int ve, int& parts, cudaStream_t s, cons
             else if (nv == kNv / 2) rms_norm_backward_rows<T, kFull, kNv / 2><<<parts, block, smem, s>>>(a);
             else rms_norm_backward_rows<T, kFull, kNv / 4><<<parts, block, smem, s>>>(a);
         } else if (ve == 2) {
-            rms_norm_backward_rows<T, 2, 16><<<parts, block, smem, s>>>(a);
+            rms_norm_backward_rows<T, 2, 8><<<parts, block, smem, s>>>(a);
         } else {
-            rms_norm_backward_rows<T, 1, 16><<<parts, block, smem, s>>>(a);
+            rms_norm_backward_rows<T, 1, 8><<<parts, block, smem, s>>>(a);
         }
     }
     return cudaGetLastError() == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
@@ -706,9 +710,11 @@ vce_status norm_backward(NormBwdArgs a, int ve, int& parts, cudaStream_t s, cons
 
 }  // namespace
 
-// Partial rows of dw: four blocks per SM, or one per row.
-int rms_norm_parts(int64_t n, int num_sms) {
-    const int64_t most = int64_t(num_sms) * 4;
+// Partial rows of dw, one per block: four blocks per SM, up to sixteen where rows are
+// short and blocks small (four of 64 threads left most of an SM idle), but at most one
+// per row.
+int rms_norm_parts(int64_t n, int64_t hidden, int num_sms) {
+    const int64_t most = int64_t(num_sms) * (hidden <= 1024 ? 16 : hidden <= 2048 ? 8 : 4);
     return int(n < most ? n : most);
 }
 
@@ -744,7 +750,7 @@ vce_status launch_rms_norm_backward(const void* dy, const void* h, const void* w
     a.n = n; a.hidden = hidden; a.dy_stride = dy_stride; a.h_stride = h_stride; a.dh_stride = dh_stride;
     a.dx_stride = dx_stride; a.dx = dx; a.part = static_cast<float*>(ws); a.dev_status = dev_status;
     const size_t es = dtype == VCE_BF16 ? 2 : 4;
-    int parts = rms_norm_parts(n, dev.num_sms);
+    int parts = rms_norm_parts(n, hidden, dev.num_sms);
     const int ve = n == 0 ? 1
                           : pick_ve(int(16 / es), hidden, es, {dy, h, dh ? dh : h, dx},
                                     {dy_stride, h_stride, dh ? dh_stride : 0, dx_stride}, weight, a.w_f32);

@@ -286,7 +286,7 @@ vce_status rms_norm_mx(const void* x, int dtype, int64_t n, int64_t hidden, int6
 size_t rms_norm_workspace_size(int64_t n, int64_t hidden) {
     DeviceInfo dev;
     if (n <= 0 || hidden <= 0 || current_device(dev) != VCE_OK) return 0;
-    return align256(size_t(rms_norm_parts(n, dev.num_sms)) * size_t(hidden) * sizeof(float));
+    return align256(size_t(rms_norm_parts(n, hidden, dev.num_sms)) * size_t(hidden) * sizeof(float));
 }
 
 vce_status rms_norm_backward(const void* dy, int dtype, int64_t n, int64_t hidden, int64_t dy_stride,

@@ -150,7 +150,7 @@ vce_status launch_ce_sample(const void* logits, int dtype, int64_t n, int64_t vo
                             const DeviceInfo& dev);
 
 // ---- the norm before the classifier (rms_norm.cu) ----
-int rms_norm_parts(int64_t n, int num_sms);
+int rms_norm_parts(int64_t n, int64_t hidden, int num_sms);
 vce_status launch_rms_norm(const void* x, const void* residual, const void* weight, int dtype, int w_dtype,
                            int64_t n, int64_t hidden, int64_t x_stride, int64_t r_stride, int64_t h_stride,
                            int64_t y_stride, float eps, void* h, void* y, float* rstd, uint8_t* codes,
