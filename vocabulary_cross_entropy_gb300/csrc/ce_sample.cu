@@ -52,7 +52,7 @@ constexpr int kBiasBits = 29;         // s - 2^36 is above -2^29 and below 2^29
 // a count; further down 30 bits of s itself are enough (2^-30 of a weight that is at most
 // 2^-8), two words and no count.
 constexpr int kHalfBits = 15;
-constexpr int kMaxPart = 1 << 17;     // elements per block
+constexpr int kMaxPart = 1 << 17;     // elements per block, at most
 constexpr int kFineBins = 8 * kSteps;
 constexpr int kCoarseBits = 7;        // of s, rounded away further down
 constexpr uint32_t kCoarseOffset = (1u << (kFracBits - kCoarseBits)) - (1u << (kBiasBits - kCoarseBits));  // 2^36 - 2^29 there
@@ -267,12 +267,15 @@ __device__ __forceinline__ uint64_t floor_product(float x, uint64_t y, bool* exa
 }
 
 // This block's part of a row.  Vectors are 16 bytes at 16-byte aligned addresses; vector
-// q holds elements q VE - off ...; the first and the last may reach past the row.
+// q holds elements q VE - off ....  The vectors that lie in the row as a whole are divided
+// among the blocks, [q0, q1) to this one; the elements before and behind them are the last
+// block's, which has fewest vectors: no block has more than kMaxPart elements.
 template <typename T>
 struct Part {
     const T* row;
     int off, vocab;
     int q0, q1;
+    bool last;
 };
 
 template <typename T>
@@ -290,8 +293,7 @@ __device__ __forceinline__ float one(const float* p) { return *p; }
 __device__ __forceinline__ float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
 // fn(logit, logit, index) for every two neighbouring elements of the block's part (index is
-// the first one's).  The vectors that lie in the row as a whole come first, then the
-// elements of the two that may not, each with -inf beside it.  Short bodies take U vectors
+// the first one's).  The vectors come first, then single elements, each with -inf beside it.  Short bodies take U vectors
 // at a time, all of them loaded first; long ones (kAhead > 0) one, with the next kAhead on
 // their way: their code, laid out several times, cost more in instruction fetches than
 // the loads in flight gained.
@@ -299,9 +301,8 @@ template <int U, int kAhead = 0, typename T, typename F>
 __device__ __forceinline__ void for_pairs(const Part<T>& p, int* dev_status, F fn) {
     constexpr int VE = 16 / sizeof(T);
     const int tid = threadIdx.x;
-    const int head = p.off > 0 ? 1 : 0, whole = (p.off + p.vocab) / VE;  // whole vectors: [head, whole)
-    const int end = min(p.q1, whole);
-    int q = max(p.q0, head) + tid;
+    const int end = p.q1;
+    int q = p.q0 + tid;
     const T* at = p.row + (q * VE - p.off);
     auto fetch = [&](int k) {  // vector q + k kThreads
         uint4 v = make_uint4(0, 0, 0, 0);
@@ -338,10 +339,10 @@ __device__ __forceinline__ void for_pairs(const Part<T>& p, int* dev_status, F f
         }
     }
     // the first vector's elements, then those behind the whole vectors
-    const int first = head && p.q0 == 0 && p.q1 > 0 ? min(VE - p.off, p.vocab) : 0;
-    const int tail0 = max(whole * VE - p.off, head ? VE - p.off : 0);
-    const int last = p.q1 > p.q0 && p.q1 * VE - p.off >= p.vocab ? max(p.vocab - tail0, 0) : 0;
-    if (tid < first + last) {
+    if (!p.last) return;
+    const int whole = (p.off + p.vocab) / VE, first = p.off > 0 ? min(VE - p.off, p.vocab) : 0;
+    const int tail0 = max(whole * VE - p.off, first);
+    if (tid < first + max(p.vocab - tail0, 0)) {
         const int i = tid < first ? tid : tail0 + tid - first;
         fn(one(p.row + i), -INFINITY, i);
     }
@@ -377,6 +378,10 @@ __device__ __forceinline__ void put(uint64_t* p, int rank, uint64_t v) {
 __device__ __forceinline__ void put(uint32_t* p, int rank, uint32_t v) {
     asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(mapa_shared(smem_u32(p), uint32_t(rank))), "r"(v) : "memory");
 }
+
+// The two halves of a cluster barrier.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ void row_barrier(int cluster) {
     if (cluster == 1) __syncthreads();
@@ -667,9 +672,11 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
     constexpr int VE = 16 / sizeof(T);
     const T* base_ptr = static_cast<const T*>(a.logits) + row * a.stride;
     const int off = int(reinterpret_cast<uintptr_t>(base_ptr) / sizeof(T) % VE);
-    const int vectors = (off + a.vocab + VE - 1) / VE;
-    const int per = (vectors + a.cluster - 1) / a.cluster;
-    Sampler<T> s{a, sh, {base_ptr, off, a.vocab, rank * per, min(vectors, (rank + 1) * per)}, rank, {}, 0};
+    const int q0 = off > 0 ? 1 : 0, whole = (off + a.vocab) / VE;
+    const int per = (max(whole - q0, 0) + a.cluster - 1) / a.cluster;
+    Sampler<T> s{a, sh, {base_ptr, off, a.vocab, q0 + rank * per, min(whole, q0 + (rank + 1) * per),
+                         rank == a.cluster - 1}, rank, {}, 0};
+    if (a.cluster > 1) cluster_arrive();  // waited for below, before the first store to another block
 
     const float temp = a.temperature ? a.temperature[row] : 1.f;
     const float top_p = a.top_p ? a.top_p[row] : 1.f;
@@ -715,6 +722,7 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
         }
         __syncthreads();
     }
+    if (a.cluster > 1) cluster_wait();  // every block of the cluster runs: its shared memory may be written
     if (tid < a.cluster) {
         float r = sh.warp_max[0];
 #pragma unroll
