@@ -274,6 +274,46 @@ def test_linear_cross_entropy_with_norm(residual):
             assert float((s.grad.double() - t.grad).norm()) <= 0.02 * float(t.grad.norm())
 
 
+def test_training_step_captured():
+    # forward and backward of norm and loss in one graph; refused while an eager graph of the same
+    # leaves is alive, and fine once it is gone
+    n, h, v = 40, 256, 1000
+    leaves = [rand(1, n, h, dtype=torch.bfloat16).contiguous(), (1 + 0.1 * rand(2, h, dtype=torch.float32)).bfloat16(),
+              rand(3, v, h, dtype=torch.bfloat16, std=h ** -0.5).contiguous()]
+    x, nw, w = [t.requires_grad_() for t in leaves]
+    y = torch.randint(0, v, (n,), device=DEV, generator=torch.Generator(DEV).manual_seed(1))
+
+    def step():
+        loss = vce.linear_cross_entropy(x, w, y, norm_weight=nw)
+        loss.backward()
+        return loss
+
+    def grads():
+        torch.cuda.synchronize()
+        return [t.grad.clone() for t in (x, nw, w)]
+
+    loss = step()
+    want, value = grads(), loss.detach().clone()
+    x.grad = nw.grad = w.grad = None
+    out = vce.rms_norm(x, nw)
+    graph = torch.cuda.CUDAGraph()
+    with pytest.raises(RuntimeError, match="still alive"):
+        with torch.cuda.graph(graph):
+            vce.rms_norm(x, nw)
+    del out, loss
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        loss = step()
+    for t in (x, nw, w):
+        t.grad.zero_()
+    for k in range(1, 3):  # a replay writes the gradients anew
+        graph.replay()
+        for a, c in zip(grads(), want):
+            assert torch.equal(a, c)
+        assert torch.equal(loss.detach(), value)
+
+
 # ---------------------------------------------------------------------------
 # quantisation
 # ---------------------------------------------------------------------------

@@ -217,6 +217,21 @@ def test_largest_vocabulary(dtype):
         check(z, u, **f)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("offset", [0, 1, 7])
+def test_largest_vocabulary_of_equal_logits(offset, dtype):
+    # every token but one in a single step of the exponent, at rows that start off a 16-byte
+    # boundary: sums of the largest parts of a row stay within their words
+    v, n = vce.SAMPLE_MAX_VOCAB, 6
+    z = torch.empty(n, v + 8, device=DEV, dtype=DT[dtype])
+    z[:] = -torch.tensor([0.25, 0.00546875, 0.0027, 1.7, 4.03125, 7.9], device=DEV).to(DT[dtype])[:, None]
+    z = z[:, offset:offset + v]
+    z[:, 0] = 0
+    u = torch.rand(n, device=DEV, generator=torch.Generator(DEV).manual_seed(5 + offset))
+    check(z, u)
+    check(z, u, top_p=0.6)
+
+
 def test_distribution():
     # uniform numbers on a fine grid draw every token in proportion to its probability
     z, _ = make(10, 1, 12, "f32", peaks=False)
@@ -285,6 +300,16 @@ def test_linear_sample(n):
     plain = vce.linear_sample(x[0], w, u[:n], 0.0)
     zq = vce.mx_linear(vce.mx_quantize(x[0], "e4m3"), w, torch.float32)
     assert torch.equal(plain.token, zq.argmax(1))
+    # embeddings of any strides: one row for all (expanded), transposed
+    same = vce.linear_sample(x[0, :1].expand(5, h), w, u[:1].expand(5).contiguous(), 0.8, norm_weight=nw)
+    one = vce.linear_sample(x[0, :1], w, u[:1], 0.8, norm_weight=nw)
+    assert torch.equal(same.token, one.token.expand(5))
+    turned = vce.linear_sample(x.transpose(0, 1), w, u, 0.8, norm_weight=nw, residual=res.transpose(0, 1))
+    assert turned.token.shape == (n, 2)
+    assert torch.equal(turned.token, vce.linear_sample(x.transpose(0, 1).contiguous(), w, u, 0.8, norm_weight=nw,
+                                                       residual=res.transpose(0, 1).contiguous()).token)
+    none = vce.linear_sample(x[:, :0], w, u[:0], 0.8, norm_weight=nw)
+    assert none.token.shape == (2, 0)
 
 
 def test_rows_past_32_bits():

@@ -51,6 +51,13 @@ def _rows_of(t, name):
     return n, c, rs if n > 1 else c
 
 
+def flat_rows(t):
+    """``t`` [..., H] as [rows, H] with contiguous rows that do not overlap (a gradient may be
+    expanded, an input transposed)."""
+    flat = t.reshape(-1, t.shape[-1])
+    return flat if flat.stride(-1) == 1 and flat.stride(0) >= flat.shape[1] else flat.contiguous()
+
+
 def _same_rows(t, name, like):
     """Row stride of a tensor that has to match ``like`` in shape, type and device."""
     if t.shape != like.shape or t.dtype is not like.dtype or t.get_device() != like.get_device():
@@ -391,10 +398,11 @@ def linear_sample(embeddings, classifier: MXTensor, uniform, temperature=None, t
     if stream is not None:
         return _under(stream, linear_sample, embeddings, classifier, uniform, temperature, top_k, top_p, min_p,
                       norm_weight=norm_weight, norm_eps=norm_eps, residual=residual, dev_status=dev_status)
-    lead, h = embeddings.shape[:-1], embeddings.shape[-1]
-    x = embeddings.reshape(-1, h)
+    lead, x = embeddings.shape[:-1], flat_rows(embeddings)
     if norm_weight is not None:
-        res = None if residual is None else residual.reshape(-1, h)
+        if residual is not None and residual.shape != embeddings.shape:
+            raise ValueError("residual must have the shape of embeddings")
+        res = None if residual is None else flat_rows(residual)
         q = rms_norm_mx(x, norm_weight, norm_eps, res).y
     elif residual is not None:
         raise ValueError("residual is added by the norm: it needs norm_weight")

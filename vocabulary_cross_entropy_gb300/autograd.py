@@ -20,6 +20,7 @@ from torch.autograd.function import once_differentiable
 
 from . import _binding as b
 from . import _head
+from ._head import flat_rows
 
 
 def _grad_tensor(grad, reduce_code, n, device):
@@ -84,11 +85,24 @@ class _LinearCE(torch.autograd.Function):
         return r.dX, r.dW, None, None, None, None, None
 
 
-def _rows(t):
-    """``t`` [..., H] as [rows, H] with contiguous rows that do not overlap (a gradient may be
-    expanded, an input transposed)."""
-    flat = t.reshape(-1, t.shape[-1])
-    return flat if flat.stride(-1) == 1 and flat.stride(0) >= flat.shape[1] else flat.contiguous()
+def _accumulators(*tensors):
+    """What adds to the .grad of those ``tensors`` that are leaves, each with a note of the
+    stream it was first seen on; the caller keeps them until the graph does.
+
+    torch makes one such node per leaf, which lives as long as any graph of the leaf and works
+    on the stream that it was made on.  A graph that is captured while an eager one of the same
+    leaves is alive would draw that stream into the capture: refused here, where nothing has
+    been launched yet, as torch's own failure in the backward pass can end the process."""
+    nodes = []
+    for t in tensors:
+        if t is not None and t.is_leaf and t.requires_grad and t.is_cuda:
+            node = torch.autograd.graph.get_gradient_edge(t).node
+            stream = torch.cuda.current_stream(t.device).cuda_stream
+            if node.metadata.setdefault("vce_stream", stream) != stream and torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("an earlier result computed from the same parameters is still alive: drop it "
+                                   "(or detach it) before the forward and backward pass are captured into a graph")
+            nodes.append(node)
+    return nodes
 
 
 class _RMSNorm(torch.autograd.Function):
@@ -97,7 +111,7 @@ class _RMSNorm(torch.autograd.Function):
     # made outside would each look like the only owner)
     @staticmethod
     def forward(ctx, x, weight, residual, eps):
-        f = _head.rms_norm_forward(_rows(x), weight, eps, None if residual is None else _rows(residual))
+        f = _head.rms_norm_forward(flat_rows(x), weight, eps, None if residual is None else flat_rows(residual))
         ctx.save_for_backward(f.h, weight, f.rstd)
         ctx.set_materialize_grads(False)
         ctx.with_residual = residual is not None
@@ -111,7 +125,7 @@ class _RMSNorm(torch.autograd.Function):
         if dy is None:  # only the residual stream was used, or nothing
             dx, dweight = dh, None
         else:
-            dx, dweight = _head.rms_norm_backward(_rows(dy), h, weight, rstd, None if dh is None else _rows(dh))
+            dx, dweight = _head.rms_norm_backward(flat_rows(dy), h, weight, rstd, None if dh is None else flat_rows(dh))
             dx = dx.view(dy.shape)
         return dx, dweight, dx if ctx.with_residual else None, None
 
@@ -125,7 +139,10 @@ def rms_norm(x, weight, eps: float = 1e-6, residual=None):
     """
     if residual is not None and residual.shape != x.shape:
         raise ValueError("residual must have the shape of x")
-    return _RMSNorm.apply(x, weight, residual, float(eps))
+    nodes = _accumulators(x, weight, residual) if torch.is_grad_enabled() else None
+    out = _RMSNorm.apply(x, weight, residual, float(eps))
+    del nodes  # the graph holds them now
+    return out
 
 
 def linear_cross_entropy(embeddings, classifier, labels, ignore_index: int = -100, reduction: str = "mean",
