@@ -23,6 +23,11 @@
  *       "Implementation": forward GEMM fused with NLL/LSE, backward = logits
  *       recomputation, dX and dW).
  *
+ *   output head  rms_norm_*, mx_*, ce_sample
+ *       What surrounds the loss in a model: the norm before the classifier (forward,
+ *       8-bit, backward), microscaled tensors and the product that gives a quantised
+ *       classifier's logits, and the draw of a token from logits.
+ *
  * Common conventions
  *   - Every pointer argument is a DEVICE pointer unless said otherwise; the
  *     caller owns every buffer and the stream.  The library never allocates,
@@ -51,7 +56,8 @@
  *     may be NULL): VCE_DEVSTATUS_BAD_TARGET for a target outside [0, V) that
  *     is not ignore_idx (that row's loss is NaN and its gradient row 0),
  *     VCE_DEVSTATUS_TIMEOUT when a wait of a tensor-core or copy pipeline gave
- *     up (the outputs are then incomplete).
+ *     up (the outputs are then incomplete), VCE_DEVSTATUS_BAD_ROW for a row from
+ *     which ce_sample can draw nothing.
  *   - The library runs on compute capability 10.3 (GB300) only; on any other
  *     device every compute call returns VCE_ERR_ARCH.
  */

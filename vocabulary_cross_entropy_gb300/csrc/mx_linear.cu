@@ -7,13 +7,18 @@
 // tensor-memory lane) and the classifier's rows the N operand, for few tokens too: an
 // instruction with N = 16 tokens over 128 classifier rows costs nearly as much as one
 // with N = 128, and the classifier is what has to be fed through (8 tokens x 4096 x
-// 128256: 120 us that way round).
+// 128256: 105 us that way round).
 //
 // 4-bit values travel packed (two per byte) from HBM.  The tensor core wants them in
 // shared memory as 16-byte pieces of 16 values, 8 bytes of codes and 8 of padding, and
 // a tensor map of type 16U4_ALIGN16B makes the copy engine spread them so (counting the
 // packed bytes on the barrier).  Converter warps in its place took as many cycles of
-// shared memory as feeding the tensor core (1005 us at 2048 tokens x 4096 x 128256).
+// shared memory as feeding the tensor core (83 us at 8 tokens, 1005 us at 2048).
+//
+// Times at 4096 x 128256 with BF16 logits: 8 tokens 53 us, bound by memory (281 MB, 0.79 of
+// the copy rate; the rest is the start of the pipeline and a last round that is half full);
+// 2048 tokens 648 us, 3.3 PFLOP/s, bound by the tensor core and its reads of shared memory,
+// and by the power limit where calls follow one another for long (718 us).
 //
 // Roles: warp 0 copies both operands and their scales (TMA), warp 1 issues the MMAs, warps
 // 4 to 11 drain accumulators.  One ring of 128 columns per stage.  Every wait is
@@ -154,8 +159,6 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t timeout_ns) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, timeout_ns));
 }
-
-__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 __device__ __forceinline__ void store_logit(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_logit(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }

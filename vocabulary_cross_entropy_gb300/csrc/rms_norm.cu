@@ -15,7 +15,9 @@
 // besides h is the store of y (dx, dw).
 //
 // All three are bound by memory: a row is read once into registers, reduced over
-// its threads and written from registers.
+// its threads and written from registers.  16384 x 4096 BF16 with a residual (537 MB, 80 us
+// at the copy rate): forward 82 us, backward 101 us.  The 8-bit form is bound by
+// instructions (54 us without a residual, 202 MB).
 
 #include "vce_internal.cuh"
 #include "mx_format.cuh"
