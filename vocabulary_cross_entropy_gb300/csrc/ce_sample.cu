@@ -34,7 +34,7 @@
 // the others' results, which it reads from their shared memory, and decides; the others
 // read its decision.
 
-#include "vce_internal.cuh"
+#include "head_internal.cuh"
 #include "sm100_ptx.cuh"
 
 #include <math.h>

@@ -24,7 +24,7 @@
 // 4 to 11 drain accumulators.  One ring of 128 columns per stage.  Every wait is
 // bounded, as in lce_tc.cu.
 
-#include "vce_internal.cuh"
+#include "head_internal.cuh"
 #include "mx_format.cuh"
 #include "sm100_ptx.cuh"
 

@@ -4,7 +4,7 @@
 // find its largest magnitude with two shuffles.  65536 x 4096 BF16 to E2M1 125 us, back
 // 109 us (680 MB each, 0.81 and 0.93 of the copy rate); instructions are the rest.
 
-#include "vce_internal.cuh"
+#include "head_internal.cuh"
 #include "mx_format.cuh"
 
 namespace vce {

@@ -19,7 +19,7 @@
 // at the copy rate): forward 82 us, backward 101 us.  The 8-bit form is bound by
 // instructions (54 us without a residual, 202 MB).
 
-#include "vce_internal.cuh"
+#include "head_internal.cuh"
 #include "mx_format.cuh"
 
 #include <math.h>

@@ -2,7 +2,7 @@
 // Every host-detectable error returns before any launch; nothing here
 // allocates, frees or synchronises.
 
-#include "vce_internal.cuh"
+#include "head_internal.cuh"
 #include "mx_format.cuh"
 
 #include <atomic>
