@@ -156,8 +156,9 @@ __device__ __forceinline__ bool elect_one() {
 // A whole warp's wait: every lane polls.  (A branch that only one lane takes costs its
 // warp about as much as the handover itself: a round trip between two warps measured 285
 // clocks with all lanes polling, 472 with one.)
+template <bool kCluster = false>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t timeout_ns) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, timeout_ns));
+    return __all_sync(0xffffffffu, mbar_wait<kCluster>(bar, parity, abort, timeout_ns));
 }
 
 __device__ __forceinline__ void store_logit(float* p, float v) { *p = v; }
@@ -193,6 +194,71 @@ __device__ __forceinline__ Tile tile_at(const LinearArgs& a, int t) {
     const bool whole = tv < a.whole_v;
     return {int64_t(whole ? tv : a.whole_v) * kRows + (whole ? 0 : int64_t(tv - a.whole_v) * 128), int64_t(tn) * kTokens,
             whole ? kRows : 128};
+}
+
+// An epilogue warp's part of a finished tile: one token per lane, from n0 on, and 128 logits
+// from v0 on, below ``end``.  ``shared_drained`` is called (by one lane) when the columns
+// that both accumulators have are out of tensor memory, if this warp has them.
+template <typename Out, typename F>
+__device__ __forceinline__ void store_tile(const LinearArgs& a, int64_t n0, int64_t v0, int64_t end, uint32_t accum,
+                                           uint32_t acc, int q, int half, float* mine, F shared_drained) {
+    const int lane = threadIdx.x & 31;
+    const int live = int(a.n - n0 < 32 ? a.n - n0 : 32);  // tokens of this warp
+    const int64_t right = a.v < end ? a.v : end;
+    const int cols = int(right - v0 < 128 ? right - v0 : 128);
+    const uint32_t taddr = accum + (uint32_t(q * 32) << 16) + half * 128;
+    Out* out = static_cast<Out*>(a.out) + n0 * a.out_stride + v0;
+    // the columns both accumulators have are the last of the first one's second half and
+    // the first of the second one's first half
+    const bool shares = half != int(acc);
+    const bool work = live > 0 && cols > 0 && VCE_BOUNDS(n0 >= 0 && v0 >= 0, a.dev_status);
+    if (shares && !work && lane == 0) shared_drained();
+    if (work) {
+        const int chunks = (cols + 31) / 32;
+#pragma unroll 1
+        for (int i = 0; i < chunks; ++i) {
+            const int c = (acc == 0 ? chunks - 1 - i : i) * 32;
+            uint32_t r[32];
+            tmem_ld32(taddr + c, r);
+            tmem_ld_wait();
+            if (shares && i == 0) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) shared_drained();
+            }
+            if (a.wide) {
+                Out* row = out + int64_t(lane) * a.out_stride + c;
+                if (lane < live) {
+                    if (cols - c >= 32) {
+                        store_row32(row, r);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (j < cols - c) store_logit(row + j, __uint_as_float(r[j]));
+                    }
+                }
+            } else {
+                // rows at any offset: turned through shared memory, so that half a warp
+                // stores 16 neighbouring logits of one token
+                const int hl = lane & 15, hr = lane >> 4;
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < kTurnCols; ++j)
+                        mine[lane * (kTurnCols + 1) + j] = __uint_as_float(r[part * kTurnCols + j]);
+                    __syncwarp();
+                    const int cc = c + part * kTurnCols + hl;
+                    if (cc < cols) {
+                        Out* p = out + int64_t(hr) * a.out_stride + cc;
+#pragma unroll 4
+                        for (int i2 = hr; i2 < live; i2 += 2, p += 2 * a.out_stride)
+                            store_logit(p, mine[i2 * (kTurnCols + 1) + hl]);
+                    }
+                }
+            }
+        }
+    }
 }
 
 template <int XR, typename Out>
@@ -338,62 +404,8 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant
             tc_fence_after();
             const Tile tile = tile_at(a, t);
             const int64_t n0 = tile.n0 + q * 32, v0 = tile.v0 + half * 128;
-            const int live = int(a.n - n0 < 32 ? a.n - n0 : 32);  // tokens of this warp
-            const int64_t right = a.v < tile.v0 + tile.width ? a.v : tile.v0 + tile.width;
-            const int cols = int(right - v0 < 128 ? right - v0 : 128);
-            const uint32_t taddr = tmem + (uint32_t(q * 32) << 16) + acc * kAccStep + half * 128;
-            Out* out = static_cast<Out*>(a.out) + n0 * a.out_stride + v0;
-            // the columns both accumulators have are the last of the first one's second half and
-            // the first of the second one's first half
-            const bool shares = half != int(acc);
-            const bool work = live > 0 && cols > 0 && VCE_BOUNDS(n0 >= 0 && v0 >= 0, a.dev_status);
-            if (shares && !work && lane == 0) mbar_arrive(shared_empty);
-            if (work) {
-                const int chunks = (cols + 31) / 32;
-#pragma unroll 1
-                for (int i = 0; i < chunks; ++i) {
-                    const int c = (acc == 0 ? chunks - 1 - i : i) * 32;
-                    uint32_t r[32];
-                    tmem_ld32(taddr + c, r);
-                    tmem_ld_wait();
-                    if (shares && i == 0) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(shared_empty);
-                    }
-                    if (a.wide) {
-                        Out* row = out + int64_t(lane) * a.out_stride + c;
-                        if (lane < live) {
-                            if (cols - c >= 32) {
-                                store_row32(row, r);
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < 32; ++j)
-                                    if (j < cols - c) store_logit(row + j, __uint_as_float(r[j]));
-                            }
-                        }
-                    } else {
-                        // rows at any offset: turned through shared memory, so that half a warp
-                        // stores 16 neighbouring logits of one token
-                        const int hl = lane & 15, hr = lane >> 4;
-#pragma unroll
-                        for (int part = 0; part < 2; ++part) {
-                            __syncwarp();
-#pragma unroll
-                            for (int j = 0; j < kTurnCols; ++j)
-                                mine[lane * (kTurnCols + 1) + j] = __uint_as_float(r[part * kTurnCols + j]);
-                            __syncwarp();
-                            const int cc = c + part * kTurnCols + hl;
-                            if (cc < cols) {
-                                Out* p = out + int64_t(hr) * a.out_stride + cc;
-#pragma unroll 4
-                                for (int i2 = hr; i2 < live; i2 += 2, p += 2 * a.out_stride)
-                                    store_logit(p, mine[i2 * (kTurnCols + 1) + hl]);
-                            }
-                        }
-                    }
-                }
-            }
+            store_tile<Out>(a, n0, v0, tile.v0 + tile.width, tmem + acc * kAccStep, acc, q, half, mine,
+                            [&] { mbar_arrive(shared_empty); });
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&t_empty[acc]);
@@ -407,6 +419,206 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// CTA pairs
+// ---------------------------------------------------------------------------
+
+// The same for more than 128 tokens: two CTAs of a cluster take 256 tokens, 128 each, by 256
+// classifier rows, of which each holds half in its shared memory; the even one issues the
+// MMAs (cta_group::2) for both.  What a CTA writes and reads of shared memory per stage of
+// 128 columns falls from 96 KB (768 clocks at 128 bytes per clock, which is what bound the
+// kernel above) to 64 KB, below the tensor core's own time.
+struct PairCfg {
+    static constexpr uint32_t kXBytes = 128 * kK, kWHalf = 128 * kK;  // as the tensor core reads them
+    static constexpr uint32_t kStage = kXBytes + kWHalf;
+    static constexpr uint32_t kScales = 3 * mx::kTileBytes;  // the CTA's tokens', all 256 rows'
+    static constexpr uint32_t kTx = 2 * (kXBytes + 128 * (kK / 2) + kScales);  // bytes a stage's copies count
+    static constexpr int kStages = 6;
+    static constexpr size_t kSmem = size_t(kStages) * (kStage + kScales) + kEpilogueWarps * kTurnBytes + 1024 + 512;
+    static_assert(kSmem <= 232448, "shared memory");
+};
+
+__device__ __forceinline__ void copy_scales_pair(uint32_t taddr, uint32_t low) {  // in both CTAs, from their own memory
+    asm volatile(
+        "{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\ttcgen05.cp.cta_group::2.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr),
+        "r"(low), "n"(kScaleHigh)
+        : "memory");
+}
+
+__device__ __forceinline__ void umma_mx_pair(uint32_t d, uint32_t a_low, uint32_t b_low, uint32_t idesc, uint32_t sfa,
+                                             uint32_t sfb, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %7};\n\tmov.b64 b, {%2, %7};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a, b, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "r"(a_low), "r"(b_low), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "n"(kTileHigh)
+        : "memory");
+}
+
+template <typename Out>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+mx_linear_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                      const __grid_constant__ CUtensorMap tm_ws, const __grid_constant__ CUtensorMap tm_xs,
+                      const LinearArgs a) {
+    using C = PairCfg;
+    constexpr int S = C::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* scales = smem + size_t(S) * C::kStage;
+    uint8_t* turn = scales + size_t(S) * C::kScales;
+    uint64_t* full = reinterpret_cast<uint64_t*>(turn + kEpilogueWarps * kTurnBytes);  // the even CTA's is used
+    uint64_t* empty = full + S;
+    uint64_t* t_full = empty + S;
+    uint64_t* t_empty = t_full + 2;        // the even CTA's
+    uint64_t* shared_empty = t_empty + 2;  // the even CTA's
+    uint64_t* drain = shared_empty + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int tiles = a.tiles_v * a.tiles_n, pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&t_full[i], 1);
+            mbar_init(&t_empty[i], 2 * kEpilogueWarps);
+        }
+        mbar_init(shared_empty, 2 * 4);
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, kTmemCols);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync();  // both CTAs' barriers exist before the first signal from one to the other
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    volatile int no_abort = 0;
+
+    if (warp == 0) {
+        // ---------------- copies, each CTA its own; all count on the even CTA's barriers ----------------
+        if (lane == 0) {
+            tma_prefetch_desc(&tm_w);
+            tma_prefetch_desc(&tm_x);
+            tma_prefetch_desc(&tm_ws);
+            tma_prefetch_desc(&tm_xs);
+        }
+        uint32_t s = 0, phase = 0, issued = 0, issued_phase = 0;
+        const uint32_t full_at = mapa_shared(smem_u32(full), 0);
+        bool ok = true;
+        for (int t = pair; t < tiles && ok; t += pairs) {
+            const int tv = t / a.tiles_n, tn = t - tv * a.tiles_n;
+            const int64_t v0 = int64_t(tv) * kRows, n0 = (int64_t(tn) * 2 + rank) * kTokens;
+            // rows past the last come as zeros, for scales too; all of them count as bytes
+            const int w_row = int(v0) + int(rank) * 128;
+            const int ws = int(v0 / 128 * a.k_tiles * 2), xs = int(n0 / 128 * a.k_tiles * 2);
+            for (int k = 0; k < a.k_tiles; ++k) {
+                ok = warp_wait(&empty[s], phase ^ 1u, abort_flag, a.timeout_ns);
+                if (!ok) break;
+                if (elect_one()) {
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], C::kTx);
+                    const uint32_t sx = smem_u32(smem + size_t(s) * C::kStage);
+                    const uint32_t sc = smem_u32(scales + size_t(s) * C::kScales);
+                    const uint32_t bar = full_at + s * 8;
+                    if (VCE_BOUNDS(v0 < a.v && tn * 2 * int64_t(kTokens) < a.n && ws >= 0 && xs >= 0, a.dev_status)) {
+                        tma_load_2d_pair(sx + C::kXBytes, &tm_w, bar, k * kK, w_row);
+                        tma_load_2d_pair(sc + mx::kTileBytes, &tm_ws, bar, 0, ws + k * 2);
+                        tma_load_2d_pair(sc + 2 * mx::kTileBytes, &tm_ws, bar, 0, ws + (a.k_tiles + k) * 2);
+                        tma_load_2d_pair(sx, &tm_x, bar, k * kK, int(n0));
+                        tma_load_2d_pair(sc, &tm_xs, bar, 0, xs + k * 2);
+                    }
+                }
+                __syncwarp();
+                issued |= 1u << s;
+                issued_phase = (issued_phase & ~(1u << s)) | (phase << s);
+                if (++s == uint32_t(S)) s = 0, phase ^= 1u;
+            }
+        }
+        if (!ok && rank == 0)  // copies in flight land before shared memory is released
+            for (int i = 0; i < S; ++i)
+                if ((issued >> i) & 1u) mbar_wait(&full[i], (issued_phase >> i) & 1u, &no_abort, kDrainTimeoutNs);
+    } else if (warp == 1 && rank == 0) {
+        // ---------------- MMA issuer ----------------
+        uint32_t s = 0, phase = 0, acc = 0, acc_phase = 0, shared_phase = 0;
+        const uint32_t sfa = tmem + kScaleCol, sfb = sfa + 4;
+        const uint32_t x_lo = (smem_u32(smem) >> 4) | kTileLow, sc_lo = (smem_u32(scales) >> 4) | kScaleLow;
+        constexpr uint32_t idesc = idesc_mx(kRows, 0) + (uint32_t(kTokens >> 4) << 24);  // M = 256
+        bool ok = true;
+        for (int t = pair; t < tiles && ok; t += pairs) {
+            if (!warp_wait<true>(&t_empty[acc], acc_phase ^ 1u, abort_flag, a.timeout_ns)) break;
+            if (!warp_wait<true>(shared_empty, shared_phase ^ 1u, abort_flag, a.timeout_ns)) break;
+            shared_phase ^= 1u;
+            tc_fence_after();
+            const uint32_t d = tmem + acc * kAccStep;
+            for (int k = 0; k < a.k_tiles; ++k) {
+                ok = warp_wait(&full[s], phase, abort_flag, a.timeout_ns);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t sc = sc_lo + s * (C::kScales >> 4);
+                const uint32_t ax = x_lo + s * (C::kStage >> 4), bw = ax + (C::kXBytes >> 4);
+                if (elect_one()) {
+                    copy_scales_pair(sfa, sc);
+                    copy_scales_pair(sfb, sc + (mx::kTileBytes >> 4));
+                    copy_scales_pair(sfb + 4, sc + 2 * (mx::kTileBytes >> 4));
+                    umma_mx_pair(d, ax, bw, idesc, sfa, sfb, k);
+#pragma unroll
+                    for (int kk = 1; kk < 4; ++kk)
+                        umma_mx_pair(d, ax + kk * 2, bw + kk * 2, idesc + kk * kScaleIdStep, sfa, sfb, 1u);
+                    umma_commit_pair(&empty[s], 0x3);
+                }
+                __syncwarp();
+                if (++s == uint32_t(S)) s = 0, phase ^= 1u;
+            }
+            if (!ok) break;
+            if (elect_one()) umma_commit_pair(&t_full[acc], 0x3);
+            __syncwarp();
+            acc ^= 1u;
+            acc_phase ^= acc ^ 1u;
+        }
+        if (elect_one()) umma_commit_pair(drain, 0x1);  // every MMA completes before tensor memory is released
+        __syncwarp();
+        mbar_wait(drain, 0, &no_abort, kDrainTimeoutNs);
+    } else if (warp >= kFirstEpilogue) {
+        const int ew = warp - kFirstEpilogue, q = warp & 3, half = ew >> 2;
+        float* mine = reinterpret_cast<float*>(turn + ew * kTurnBytes);
+        const uint32_t t_empty_at = mapa_shared(smem_u32(t_empty), 0);
+        const uint32_t shared_at = mapa_shared(smem_u32(shared_empty), 0);
+        uint32_t acc = 0, acc_phase = 0;
+        for (int t = pair; t < tiles; t += pairs) {
+            if (!warp_wait(&t_full[acc], acc_phase, abort_flag, a.timeout_ns)) break;
+            tc_fence_after();
+            const int tv = t / a.tiles_n, tn = t - tv * a.tiles_n;
+            const int64_t v0 = int64_t(tv) * kRows, n0 = (int64_t(tn) * 2 + rank) * kTokens + q * 32;
+            store_tile<Out>(a, n0, v0 + half * 128, v0 + kRows, tmem + acc * kAccStep, acc, q, half, mine,
+                            [&] { mbar_arrive_cluster(shared_at); });
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(t_empty_at + acc * 8);
+            acc ^= 1u;
+            acc_phase ^= acc ^ 1u;
+        }
+    }
+
+    __syncthreads();
+    if (threadIdx.x == 0 && *abort_flag) report(a.dev_status, VCE_DEVSTATUS_TIMEOUT);
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync();  // no more MMAs, copies or signals from the other CTA
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, kTmemCols);
     }
 }
 
@@ -442,6 +654,45 @@ bool code_map(CUtensorMap* map, const void* base, bool packed, uint64_t cols, ui
               const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Scale tiles as rows of 256 bytes, two to a tile.
+bool scale_map(CUtensorMap* map, const void* base, uint64_t tiles) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {256, tiles * 2};
+    cuuint64_t strides[1] = {256};
+    cuuint32_t box[2] = {256, 2};
+    cuuint32_t es[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename Out>
+vce_status launch_pair(const void* xc, const void* wc, LinearArgs a, cudaStream_t s, const DeviceInfo& dev) {
+    static std::mutex mu;
+    static bool ready[64];
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!ready[dev.ordinal]) {
+            if (cudaFuncSetAttribute(mx_linear_pair_kernel<Out>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     int(PairCfg::kSmem)) != cudaSuccess)
+                return VCE_ERR_CUDA;
+            ready[dev.ordinal] = true;
+        }
+    }
+    CUtensorMap tm_w, tm_x, tm_ws, tm_xs;
+    const uint64_t cols = uint64_t(a.k_tiles) * kK;
+    if (!code_map(&tm_w, wc, true, cols, uint64_t(a.v), 128) || !code_map(&tm_x, xc, false, cols, uint64_t(a.n), 128) ||
+        !scale_map(&tm_ws, a.w_scales, uint64_t(a.w_scale_rows) * a.k_tiles) ||
+        !scale_map(&tm_xs, a.x_scales, uint64_t((a.n + 127) / 128) * a.k_tiles))
+        return VCE_ERR_CUDA;
+    const int64_t tiles = int64_t(a.tiles_v) * a.tiles_n;
+    count_launch();
+    mx_linear_pair_kernel<Out><<<2 * unsigned(tiles < dev.num_sms / 2 ? tiles : dev.num_sms / 2), kThreads,
+                                 PairCfg::kSmem, s>>>(tm_w, tm_x, tm_ws, tm_xs, a);
+    return cudaGetLastError() == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
 }
 
 template <int XR, typename Out>
@@ -481,6 +732,21 @@ vce_status dispatch(const void* xc, const void* wc, LinearArgs a, cudaStream_t s
     const bool cut = whole < all && halves * a.tiles_n <= sms;
     a.whole_v = int(cut ? whole : all);
     a.tiles_v = int(cut ? whole + halves : all);
+    // Pairs of CTAs where they need less time: a round of theirs takes 0.93 of a round of single
+    // CTAs, their start as long as five stages more; but they have tiles of 256 tokens and no
+    // half tiles.  At 4096 x 128256, single / pairs: 256 tokens 103 / 95 us, 384 tokens 139 / 169,
+    // 512 185 / 176, 640 234 / 255, 1024 369 / 341, 2048 712 / 654.  (They address scale tiles
+    // by 32-bit rows.)
+    const int64_t pair_n = (a.n + 2 * kTokens - 1) / (2 * kTokens), pair_tiles = pair_n * all, pairs = sms / 2;
+    const double single = cut ? double(whole * a.tiles_n / sms) + 0.5
+                              : double((all * a.tiles_n + sms - 1) / sms);
+    const double paired = 0.93 * double((pair_tiles + pairs - 1) / pairs) + 5.0 / a.k_tiles;
+    const int64_t scale_rows = 2 * int64_t(a.k_tiles) * ((a.n > a.v ? a.n : a.v) / 128 + 4);
+    if (a.n > kTokens && paired < single && pair_tiles < 0x7fffffff && scale_rows < 0x7fffffff) {
+        a.tiles_n = int(pair_n);
+        a.tiles_v = a.whole_v = int(all);
+        return launch_pair<Out>(xc, wc, a, s, dev);
+    }
     if (a.n <= 16) return launch<16, Out>(xc, wc, a, s, dev);
     if (a.n <= 64) return launch<64, Out>(xc, wc, a, s, dev);
     return launch<128, Out>(xc, wc, a, s, dev);
