@@ -61,7 +61,7 @@ def main():
                 for out in (torch.bfloat16, torch.float32):
                     d = status_of(lambda st: vce.mx_dequantize(q, out, dev_status=st))
                     assert torch.allclose(d.float(), x.float(), rtol=tol, atol=0.3 if fmt == "e2m1" else 1e-2)
-    for n, h, v in ((1, 128, 1), (5, 96, 300), (33, 1000, 257), (100, 256, 32001), (257, 640, 3001), (1290, 384, 29002)):
+    for n, h, v in ((1, 128, 1), (5, 96, 300), (33, 1000, 257), (100, 256, 32001), (257, 640, 3001), (1290, 384, 29002), (1921, 1300, 24100)):
         x, w = vce.mx_quantize(rand(n, h, torch.float32), "e4m3"), vce.mx_quantize(rand(v, h, torch.float32), "e2m1")
         ref = vce.mx_dequantize(x, torch.float32) @ vce.mx_dequantize(w, torch.float32).t()
         for dtype in (torch.float32, torch.bfloat16):

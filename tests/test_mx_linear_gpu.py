@@ -84,6 +84,32 @@ def test_strided_and_unaligned_output():
     assert (full[:, :3] == 7).all() and (full[:, 304:] == 7).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,v", [(37, 301), (200, 1), (300, 290), (300, 129)])
+def test_output_rows_at_every_offset(n, v, dtype):
+    # rows that start at any element, in steps of any parity: the same bits as in a plain output,
+    # and nothing beside them
+    x, w = make(3, n, 384, "e4m3"), make(4, v, 384, "e2m1")
+    want = vce.mx_linear(x, w, dtype)
+    for offset in (0, 1, 2, 7, 8, 16):
+        for pad in (17, 18, 24, 32 - v % 16):
+            full = torch.full((n, v + pad), 7.0, dtype=dtype, device=DEV)
+            vce.mx_linear(x, w, dtype, out=full[:, offset:offset + v])
+            assert torch.equal(full[:, offset:offset + v], want), (offset, pad)
+            assert (full[:, :offset] == 7).all() and (full[:, offset + v:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,h,v", [(250, 4700, 38900), (1000, 2100, 43600), (1921, 1300, 24100), (2000, 1300, 24200),
+                                   (2048, 1400, 24320)])
+def test_pairs_of_tiles(n, h, v, dtype):
+    # whole rounds of tiles of 256 tokens x 256 rows on 76 pairs of SMs, long enough to be taken by
+    # CTA pairs: last tiles of one token, of few rows (with and without a second tile of scales)
+    rounds, k_tiles = -(-n // 256) * -(-v // 256) / 76, -(-h // 128)
+    assert rounds == int(rounds) and 0.07 * rounds * k_tiles > 5
+    check(make(5, n, h, "e4m3"), make(6, v, h, "e2m1"), dtype)
+
+
 @pytest.mark.parametrize("n", [4, 200])
 def test_nan_scales_stay_in_their_row(n):
     x = torch.randn(n, 256, device=DEV)

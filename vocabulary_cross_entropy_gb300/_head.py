@@ -408,6 +408,9 @@ def linear_sample(embeddings, classifier: MXTensor, uniform, temperature=None, t
         raise ValueError("residual is added by the norm: it needs norm_weight")
     else:
         q = mx_quantize(x, "e4m3")
-    logits = mx_linear(q, classifier, torch.float32, dev_status=dev_status)
+    # rows a multiple of 32 bytes apart: mx_linear stores, and ce_sample loads, whole sectors
+    n, v = q.rows, classifier.rows
+    logits = torch.empty(n, -(-v // 8) * 8, dtype=torch.float32, device=x.device)[:, :v]
+    mx_linear(q, classifier, torch.float32, out=logits, dev_status=dev_status)
     r = ce_sample(logits, uniform, temperature, top_k, top_p, min_p, dev_status=dev_status)
     return CESample(r.token.view(lead), r.logprob.view(lead), dev_status)

@@ -17,8 +17,8 @@
 //
 // Times at 4096 x 128256 with BF16 logits: 8 tokens 53 us, bound by memory (281 MB, 0.79 of
 // the copy rate; the rest is the start of the pipeline and a last round that is half full);
-// 2048 tokens 648 us, 3.3 PFLOP/s, bound by the tensor core and its reads of shared memory,
-// and by the power limit where calls follow one another for long (718 us).
+// 2048 tokens (in CTA pairs) 580 us, 3.7 PFLOP/s, bound by the tensor core, and by the power
+// limit where calls follow one another for long.
 //
 // Roles: warp 0 copies both operands and their scales (TMA), warp 1 issues the MMAs, warps
 // 4 to 11 drain accumulators.  One ring of 128 columns per stage.  Every wait is
@@ -72,7 +72,7 @@ struct LinearArgs {
     const uint8_t *w_scales, *x_scales;
     void* out;
     int64_t out_stride;
-    int wide;              // every 32 columns of a row start 16-byte aligned
+    int wide;              // every 32 columns of a row start 16-byte (1) or 32-byte (2) aligned
     int* dev_status;
     uint64_t timeout_ns;
 };
@@ -164,23 +164,58 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 __device__ __forceinline__ void store_logit(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_logit(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// 32 consecutive logits of one token, 16-byte aligned
-__device__ __forceinline__ void store_row32(float* p, const uint32_t (&r)[32]) {
+// 32 consecutive logits of one token as words.  Rows that start 32-byte aligned are stored by
+// 32 bytes, whole sectors of L2: the stores of 16 bytes, two requests per sector, bound the
+// kernel where tiles are short (2048 x 1024 x 128256 BF16: 315 us by 16 bytes, 219 by 32).
+__device__ __forceinline__ void store_words(void* p, const uint32_t* u, int words, bool sectors) {
+    if (sectors) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        reinterpret_cast<uint4*>(p)[i] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+        for (int i = 0; i < words; i += 8)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(static_cast<uint32_t*>(p) + i),
+                         "r"(u[i]), "r"(u[i + 1]), "r"(u[i + 2]), "r"(u[i + 3]), "r"(u[i + 4]), "r"(u[i + 5]),
+                         "r"(u[i + 6]), "r"(u[i + 7])
+                         : "memory");
+    } else {
+#pragma unroll
+        for (int i = 0; i < words; i += 4)
+            *reinterpret_cast<uint4*>(static_cast<uint32_t*>(p) + i) = make_uint4(u[i], u[i + 1], u[i + 2], u[i + 3]);
+    }
 }
-__device__ __forceinline__ void store_row32(__nv_bfloat16* p, const uint32_t (&r)[32]) {
+__device__ __forceinline__ uint32_t logit_pair(uint32_t lo, uint32_t hi) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(lo), __uint_as_float(hi));
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+__device__ __forceinline__ void store_row32(float* p, const uint32_t (&r)[32], bool sectors) {
+    store_words(p, r, 32, sectors);
+}
+__device__ __forceinline__ void store_row32(__nv_bfloat16* p, const uint32_t (&r)[32], bool sectors) {
+    uint32_t u[16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t u[4];
+    for (int i = 0; i < 16; ++i) u[i] = logit_pair(r[2 * i], r[2 * i + 1]);
+    store_words(p, u, 16, sectors);
+}
+
+// The first ``left`` of 32 consecutive logits of ``live`` tokens (one per lane) in rows at any
+// offset from ``out`` on: turned through shared memory, so that half a warp stores 16
+// neighbouring logits of one token.  (BF16 logits two to a word, with the odd rows' words put
+// together from neighbours, took 64 us where this takes 45: 1024 x 512 x 32001.)
+template <typename Out>
+__device__ __forceinline__ void store_turned(Out* out, int64_t stride, const uint32_t (&r)[32], int live, int left,
+                                             float* mine) {
+    const int lane = threadIdx.x & 31, hl = lane & 15, hr = lane >> 4;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(r[8 * i + 2 * k]),
-                                                           __uint_as_float(r[8 * i + 2 * k + 1]));
-            u[k] = *reinterpret_cast<const uint32_t*>(&b);
+    for (int part = 0; part < 2; ++part) {
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < kTurnCols; ++j)
+            mine[lane * (kTurnCols + 1) + j] = __uint_as_float(r[part * kTurnCols + j]);
+        __syncwarp();
+        const int c = part * kTurnCols + hl;
+        if (c < left) {
+            Out* p = out + int64_t(hr) * stride + c;
+#pragma unroll 4
+            for (int i = hr; i < live; i += 2, p += 2 * stride) store_logit(p, mine[i * (kTurnCols + 1) + hl]);
         }
-        reinterpret_cast<uint4*>(p)[i] = make_uint4(u[0], u[1], u[2], u[3]);
     }
 }
 
@@ -230,7 +265,7 @@ __device__ __forceinline__ void store_tile(const LinearArgs& a, int64_t n0, int6
                 Out* row = out + int64_t(lane) * a.out_stride + c;
                 if (lane < live) {
                     if (cols - c >= 32) {
-                        store_row32(row, r);
+                        store_row32(row, r, a.wide == 2);
                     } else {
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
@@ -238,24 +273,7 @@ __device__ __forceinline__ void store_tile(const LinearArgs& a, int64_t n0, int6
                     }
                 }
             } else {
-                // rows at any offset: turned through shared memory, so that half a warp
-                // stores 16 neighbouring logits of one token
-                const int hl = lane & 15, hr = lane >> 4;
-#pragma unroll
-                for (int part = 0; part < 2; ++part) {
-                    __syncwarp();
-#pragma unroll
-                    for (int j = 0; j < kTurnCols; ++j)
-                        mine[lane * (kTurnCols + 1) + j] = __uint_as_float(r[part * kTurnCols + j]);
-                    __syncwarp();
-                    const int cc = c + part * kTurnCols + hl;
-                    if (cc < cols) {
-                        Out* p = out + int64_t(hr) * a.out_stride + cc;
-#pragma unroll 4
-                        for (int i2 = hr; i2 < live; i2 += 2, p += 2 * a.out_stride)
-                            store_logit(p, mine[i2 * (kTurnCols + 1) + hl]);
-                    }
-                }
+                store_turned(out + c, a.out_stride, r, live, min(32, cols - c), mine);
             }
         }
     }
@@ -723,7 +741,8 @@ vce_status launch(const void* xc, const void* wc, LinearArgs a, cudaStream_t s, 
 template <typename Out>
 vce_status dispatch(const void* xc, const void* wc, LinearArgs a, cudaStream_t s, const DeviceInfo& dev) {
     a.tiles_n = int((a.n + kTokens - 1) / kTokens);
-    a.wide = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.out_stride * int64_t(sizeof(Out)) % 16 == 0;
+    const int64_t at = int64_t(reinterpret_cast<uintptr_t>(a.out)) | a.out_stride * int64_t(sizeof(Out));
+    a.wide = at % 32 == 0 ? 2 : at % 16 == 0 ? 1 : 0;
     // Tiles go to the SMs in rounds.  What the last, partial round would hold is cut into
     // tiles of half the rows where those still fit one round: half a round instead of one.
     const int64_t all = (a.v + kRows - 1) / kRows, sms = dev.num_sms;
@@ -734,9 +753,9 @@ vce_status dispatch(const void* xc, const void* wc, LinearArgs a, cudaStream_t s
     a.tiles_v = int(cut ? whole + halves : all);
     // Pairs of CTAs where they need less time: a round of theirs takes 0.93 of a round of single
     // CTAs, their start as long as five stages more; but they have tiles of 256 tokens and no
-    // half tiles.  At 4096 x 128256, single / pairs: 256 tokens 103 / 95 us, 384 tokens 139 / 169,
-    // 512 185 / 176, 640 234 / 255, 1024 369 / 341, 2048 712 / 654.  (They address scale tiles
-    // by 32-bit rows.)
+    // half tiles.  At 4096 x 128256, single / pairs (before the stores of 32 bytes): 256 tokens 103 /
+    // 95 us, 384 139 / 169, 512 185 / 176, 640 234 / 255, 1024 369 / 341, 2048 712 / 654.
+    // (They address scale tiles by 32-bit rows.)
     const int64_t pair_n = (a.n + 2 * kTokens - 1) / (2 * kTokens), pair_tiles = pair_n * all, pairs = sms / 2;
     const double single = cut ? double(whole * a.tiles_n / sms) + 0.5
                               : double((all * a.tiles_n + sms - 1) / sms);
