@@ -301,6 +301,16 @@ def test_training_step_captured():
         with torch.cuda.graph(graph):
             vce.rms_norm(x, nw)
     del out, loss
+    # nodes that something else holds (a data-parallel wrapper, say) and made on a side stream: fine
+    with torch.cuda.stream(torch.cuda.Stream()):
+        held = [torch.autograd.graph.get_gradient_edge(t).node for t in (x, nw)]
+    out = vce.rms_norm(x, nw)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = vce.rms_norm(x, nw)
+    graph.replay()
+    assert torch.equal(got, out)
+    del held, out, got, graph
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):

@@ -85,23 +85,34 @@ class _LinearCE(torch.autograd.Function):
         return r.dX, r.dW, None, None, None, None, None
 
 
+_NOTE = "vce_stream"
+
+
 def _accumulators(*tensors):
-    """What adds to the .grad of those ``tensors`` that are leaves, each with a note of the
-    stream it was first seen on; the caller keeps them until the graph does.
+    """What adds to the .grad of those ``tensors`` that are leaves; the caller keeps them until
+    the graph does.
 
     torch makes one such node per leaf, which lives as long as any graph of the leaf and works
     on the stream that it was made on.  A graph that is captured while an eager one of the same
-    leaves is alive would draw that stream into the capture: refused here, where nothing has
-    been launched yet, as torch's own failure in the backward pass can end the process."""
+    leaves is alive, made on the default stream, would draw that stream into the capture:
+    refused here, where nothing has been launched yet, as torch's own failure in the backward
+    pass can end the process."""
     nodes = []
     for t in tensors:
-        if t is not None and t.is_leaf and t.requires_grad and t.is_cuda:
+        if t is None or not (t.is_leaf and t.requires_grad and t.is_cuda):
+            continue
+        node = torch.autograd.graph.get_gradient_edge(t).node
+        if _NOTE not in node.metadata:
+            # the note outlives the node's name here only if something else holds the node,
+            # which was then made at an unknown time; otherwise the next one is made now
+            node.metadata[_NOTE] = None
+            del node
             node = torch.autograd.graph.get_gradient_edge(t).node
-            stream = torch.cuda.current_stream(t.device).cuda_stream
-            if node.metadata.setdefault("vce_stream", stream) != stream and torch.cuda.is_current_stream_capturing():
-                raise RuntimeError("an earlier result computed from the same parameters is still alive: drop it "
-                                   "(or detach it) before the forward and backward pass are captured into a graph")
-            nodes.append(node)
+            node.metadata.setdefault(_NOTE, torch.cuda.current_stream(t.device).cuda_stream)
+        if node.metadata[_NOTE] == 0 and torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("an earlier result computed from the same parameters is still alive: drop it "
+                               "(or detach it) before the forward and backward pass are captured into a graph")
+        nodes.append(node)
     return nodes
 
 
