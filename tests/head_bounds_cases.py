@@ -52,7 +52,7 @@ def main():
     assert vce.vce_bounds_check_build(), "VCE_LIBRARY does not point at the bounds-checking build"
     for dtype in (torch.bfloat16, torch.float32):
         for n, h, pad, offset in ((3, 7, 2, 1), (130, 256, 0, 0), (33, 1030, 0, 0), (40, 2048, 8, 8), (300, 4096, 0, 0),
-                                  (9, 8192, 0, 0), (5, 9001, 2, 1), (2, 40000, 0, 0)):
+                                  (9, 8192, 0, 0), (5, 9001, 2, 1), (2, 40000, 0, 0), (1300, 1031, 0, 0), (3, 515, 0, 0)):
             norms(n, h, dtype, pad, offset)
         for n, c, pad, offset in ((1, 1, 0, 0), (130, 100, 3, 1), (257, 2056, 0, 0)):
             for fmt, tol in (("e2m1", 0.34), ("e4m3", 0.07)):

@@ -128,6 +128,21 @@ def test_zero_row_and_non_finite_rows():
     assert vce.rms_norm_forward(x[:1], w, 0.0).y.isnan().all()
 
 
+def compare_backward(got, dy, hs, w, r, dh):
+    n, dtype, wdtype = dy.shape[0], dy.dtype, w.dtype
+    dx, dw = head.rms_norm_backward(f64(dy), f64(hs), f64(w), f64(r), None if dh is None else f64(dh))
+    rr, g = f64(r)[:, None], f64(dy) * f64(w)
+    hat = f64(hs) * rr
+    c, cabs = (g * hat).mean(1, keepdims=True), np.abs(g * hat).mean(1, keepdims=True)
+    terms = np.abs(rr * g) + np.abs(rr * hat * c) + (0 if dh is None else np.abs(f64(dh)))
+    lim = half_step(dtype) * np.abs(dx) * (1 + 1e-5) + 84 * U * np.abs(rr * hat) * cabs + 6 * U * terms
+    assert np.all(np.abs(f64(got.dx) - dx) <= lim + 1e-45)
+    parts = min(n, 608)
+    mag = np.abs(f64(dy) * hat).sum(0)
+    lim = half_step(wdtype) * np.abs(dw) * (1 + 1e-5) + (n / max(parts, 1) + 120) * U * mag
+    assert np.all(np.abs(f64(got.dweight) - dw) <= lim + 1e-45)
+
+
 def check_backward(n, h, dtype, wdtype, with_dh, pad=0, offset=0):
     hs = rand(1, n, h, dtype=dtype, std=2.0, pad=pad, offset=offset)
     w = (1 + 0.3 * rand(2, h, dtype=torch.float32)).to(wdtype).contiguous()
@@ -140,17 +155,7 @@ def check_backward(n, h, dtype, wdtype, with_dh, pad=0, offset=0):
     torch.cuda.synchronize()
     assert int(status) == 0
     assert torch.equal(got.dx, again.dx) and torch.equal(got.dweight, again.dweight)
-    dx, dw = head.rms_norm_backward(f64(dy), f64(hs), f64(w), f64(r), None if dh is None else f64(dh))
-    rr, g = f64(r)[:, None], f64(dy) * f64(w)
-    hat = f64(hs) * rr
-    c, cabs = (g * hat).mean(1, keepdims=True), np.abs(g * hat).mean(1, keepdims=True)
-    terms = np.abs(rr * g) + np.abs(rr * hat * c) + (0 if dh is None else np.abs(f64(dh)))
-    lim = half_step(dtype) * np.abs(dx) * (1 + 1e-5) + 84 * U * np.abs(rr * hat) * cabs + 6 * U * terms
-    assert np.all(np.abs(f64(got.dx) - dx) <= lim + 1e-45)
-    parts = min(n, 608)
-    mag = np.abs(f64(dy) * hat).sum(0)
-    lim = half_step(wdtype) * np.abs(dw) * (1 + 1e-5) + (n / max(parts, 1) + 120) * U * mag
-    assert np.all(np.abs(f64(got.dweight) - dw) <= lim + 1e-45)
+    compare_backward(got, dy, hs, w, r, dh)
 
 
 @pytest.mark.parametrize("dtype,wdtype", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
@@ -166,6 +171,33 @@ def test_backward(n, h, dtype, wdtype, with_dh):
                                             (3, 40000, 0, 0)])
 def test_backward_strided_and_long(n, h, pad, offset, dtype):
     check_backward(n, h, DT[dtype], DT[dtype], True, pad, offset)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,h", [(3000, 1031), (1500, 2049), (1400, 4097), (2500, 301), (9, 301), (2, 2317)])
+@pytest.mark.parametrize("with_dh", [False, True])
+def test_backward_rows_off_16_bytes(n, h, dtype, with_dh):
+    # many rows to a block, every offset of a row from a 16-byte boundary
+    check_backward(n, h, DT[dtype], DT[dtype], with_dh)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("alias", [None, "dy", "dh"])
+@pytest.mark.parametrize("n,h,pad,offset", [(1300, 1031, 2, 1), (1300, 1024, 5, 3), (3, 2000, 6, 1)])
+def test_backward_of_views_at_one_offset(n, h, pad, offset, alias, dtype):
+    # views with one offset and stride, the output among them; nothing beside them is written
+    def view(seed):
+        return rand(seed, n, h + pad, dtype=DT[dtype]).contiguous()
+    base = [view(k) for k in (1, 2, 3, 4)]
+    hs, dy, dh, dx = (t[:, offset:offset + h] for t in base)
+    w = rand(5, h, dtype=DT[dtype]).contiguous()
+    r = vce.rms_norm_forward(hs, w).rstd
+    out, full = {None: (dx, base[3]), "dy": (dy, base[1]), "dh": (dh, base[2])}[alias]
+    before, given = full.clone(), [t.clone() for t in (dy, hs, dh)]
+    got = vce.rms_norm_backward(dy, hs, w, r, dh, dx=out)
+    compare_backward(got, given[0], given[1], w, r, given[2])
+    before[:, offset:offset + h] = got.dx
+    assert torch.equal(full, before)
 
 
 @pytest.mark.parametrize("h", [1024, 333, 40000])

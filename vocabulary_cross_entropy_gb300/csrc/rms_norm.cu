@@ -23,6 +23,7 @@
 #include "mx_format.cuh"
 
 #include <math.h>
+#include <algorithm>
 #include <initializer_list>
 #include <mutex>
 
@@ -30,6 +31,7 @@ namespace vce {
 namespace {
 
 constexpr int kMaxThreads = 512;
+constexpr int kRingThreads = 1024;  // (64 registers)
 
 template <typename T, int VE>
 struct alignas(sizeof(T) * VE) Vec {
@@ -429,40 +431,87 @@ __device__ __forceinline__ void copy16_async(void* dst, const void* src) {
                  : "memory");
 }
 
-// The same for 16-byte aligned rows of one block each, with the loads of the next kStages
-// - 1 rows in flight: a thread copies its own vectors to its own slots of shared memory
-// and reads them back itself, so the ring needs no barrier.
-template <typename T, int NV, int kStages>
-__global__ void __launch_bounds__(kMaxThreads) rms_norm_backward_ring(const NormBwdArgs a) {
+// The same with rows of one block each read by 16 bytes, the loads of the next kStages - 1
+// rows in flight: a thread copies its own vectors to its own slots of shared memory and
+// reads them back itself, so the ring needs no barrier.
+//   kShift: rows that start anywhere, at the same offset from a 16-byte boundary in all
+// operands.  A block's rows are a multiple of VE rows apart, so that they share one offset
+// ``off`` and a thread keeps its columns; vector v holds columns v VE - off ....  The first and
+// the last vector of a row hold elements of its neighbours too, which are masked; where there
+// is no neighbour (the tensor's own first and last bytes) the elements are loaded one by one.
+// The weight is laid out by the same offset in shared memory.
+template <typename T, int NV, int kStages, bool kShift>
+__global__ void __launch_bounds__(kRingThreads) rms_norm_backward_ring(const NormBwdArgs a) {
     constexpr int VE = 16 / sizeof(T);
     using V = Vec<T, VE>;
     extern __shared__ __align__(16) uint8_t ring_raw[];
-    float* slots = reinterpret_cast<float*>(ring_raw);        // [2][32]
-    V* ring = reinterpret_cast<V*>(ring_raw + 64 * sizeof(float));  // [kStages][streams][NV][threads]
-    const int t = threadIdx.x, tpr = blockDim.x, streams = a.dh ? 3 : 2;
+    float* slots = reinterpret_cast<float*>(ring_raw);  // [2][32]
+    float* sw = slots + 64;                             // kShift: [vectors][VE]
+    const int t = threadIdx.x, tpr = blockDim.x, streams = a.dh ? 3 : 2, hidden = int(a.hidden);
+    const int off = kShift ? int(reinterpret_cast<uintptr_t>(static_cast<const T*>(a.dy) + blockIdx.x * a.dy_stride) /
+                                 sizeof(T) % VE)
+                           : 0;
+    V* ring = reinterpret_cast<V*>(kShift ? sw + (hidden + 2 * VE - 1) / VE * VE : sw);  // [kStages][streams][NV][threads]
     const int stage_vecs = streams * NV * tpr;
+    if constexpr (kShift) {
+        for (int i = t; i < (hidden + off + VE - 1) / VE * VE; i += tpr) {
+            float w[1] = {0.f};
+            if (i >= off && i - off < hidden) load_weight<1>(a.weight, a.w_f32, i - off, w);
+            sw[i] = w[0];
+        }
+        __syncthreads();
+    }
     float acc[NV][VE];
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int i = 0; i < VE; ++i) acc[j][i] = 0.f;
+    auto whole = [&](int col) { return !kShift || (col >= 0 && col + VE <= hidden); };
+    // one vector of an operand to its slot
+    auto copy = [&](V* dst, const void* base, int64_t stride, int64_t row, int col) {
+        const T* src = static_cast<const T*>(base) + row * stride + col;
+        if (kShift && ((row == 0 && col < 0) || (row == a.n - 1 && col + VE > hidden))) {
+            V v;
+#pragma unroll
+            for (int i = 0; i < VE; ++i) v.e[i] = from_f<T>(0.f);
+#pragma unroll
+            for (int i = 0; i < VE; ++i)
+                if (uint32_t(col + i) < uint32_t(hidden)) v.e[i] = src[i];
+            *dst = v;
+        } else if (VCE_BOUNDS(aligned16(src), a.dev_status)) {
+            copy16_async(dst, src);
+        }
+    };
     auto prefetch = [&](int64_t row, int stage) {
         if (row < a.n) {
-            const T* dy = static_cast<const T*>(a.dy) + row * a.dy_stride;
-            const T* h = static_cast<const T*>(a.h) + row * a.h_stride;
-            const T* dh = static_cast<const T*>(a.dh) + row * a.dh_stride;
             V* dst = ring + stage * stage_vecs + t;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                const int col = (j * tpr + t) * VE;
-                if (col < a.hidden && VCE_BOUNDS(aligned16(dy + col) && aligned16(h + col), a.dev_status)) {
-                    copy16_async(dst + j * tpr, dy + col);
-                    copy16_async(dst + (NV + j) * tpr, h + col);
-                    if (streams == 3) copy16_async(dst + (2 * NV + j) * tpr, dh + col);
+                const int col = (j * tpr + t) * VE - off;
+                if (col < hidden) {
+                    copy(dst + j * tpr, a.dy, a.dy_stride, row, col);
+                    copy(dst + (NV + j) * tpr, a.h, a.h_stride, row, col);
+                    if (streams == 3) copy(dst + (2 * NV + j) * tpr, a.dh, a.dh_stride, row, col);
                 }
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");  // one group per row, empty past the end
+    };
+    // a vector's dy, h and weight, zeros outside the row
+    auto load = [&](const V* src, int j, int col, float (&d)[VE], float (&f)[VE], float (&w)[VE]) {
+        if constexpr (kShift) {
+#pragma unroll
+            for (int i = 0; i < VE; ++i) w[i] = sw[(j * tpr + t) * VE + i];
+        } else {
+            load_weight<VE>(a.weight, a.w_f32, col, w);
+        }
+        unpack<VE>(src[j * tpr], d);
+        unpack<VE>(src[(NV + j) * tpr], f);
+        if (!whole(col)) {
+#pragma unroll
+            for (int i = 0; i < VE; ++i)
+                if (uint32_t(col + i) >= uint32_t(hidden)) d[i] = f[i] = 0.f;
+        }
     };
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) prefetch(int64_t(blockIdx.x) + int64_t(s) * gridDim.x, s);
@@ -477,13 +526,10 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_backward_ring(const Norm
         float s = 0.f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int col = (j * tpr + t) * VE;
-            if (col < a.hidden) {
-                const V vg = src[j * tpr], vh = src[(NV + j) * tpr];
+            const int col = (j * tpr + t) * VE - off;
+            if (col < hidden) {
                 float w[VE], d[VE], f[VE];
-                load_weight<VE>(a.weight, a.w_f32, col, w);
-                unpack<VE>(vg, d);
-                unpack<VE>(vh, f);
+                load(src, j, col, d, f, w);
 #pragma unroll
                 for (int i = 0; i < VE; ++i) {
                     const float hat = f[i] * r;
@@ -497,13 +543,10 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_backward_ring(const Norm
         T* dx = static_cast<T*>(a.dx) + row * a.dx_stride;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int col = (j * tpr + t) * VE;
-            if (col < a.hidden) {
-                const V vg = src[j * tpr], vh = src[(NV + j) * tpr];
+            const int col = (j * tpr + t) * VE - off;
+            if (col < hidden) {
                 float w[VE], d[VE], f[VE];
-                load_weight<VE>(a.weight, a.w_f32, col, w);
-                unpack<VE>(vg, d);
-                unpack<VE>(vh, f);
+                load(src, j, col, d, f, w);
 #pragma unroll
                 for (int i = 0; i < VE; ++i) d[i] = r * (d[i] * w[i] - f[i] * r * s);
                 if (streams == 3) {
@@ -514,8 +557,14 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_backward_ring(const Norm
                 }
                 V o;
                 pack<VE>(d, o);
-                if (VCE_BOUNDS(col >= 0 && col + VE <= a.hidden && row < a.n, a.dev_status))
-                    *reinterpret_cast<V*>(dx + col) = o;
+                if (whole(col)) {
+                    if (VCE_BOUNDS(col >= 0 && col + VE <= hidden && row < a.n && aligned16(dx + col), a.dev_status))
+                        *reinterpret_cast<V*>(dx + col) = o;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < VE; ++i)
+                        if (uint32_t(col + i) < uint32_t(hidden)) dx[col + i] = o.e[i];
+                }
             }
         }
         if (++stage == kStages) stage = 0;
@@ -524,10 +573,11 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_backward_ring(const Norm
     float* out = a.part + int64_t(blockIdx.x) * a.hidden;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int col = (j * tpr + t) * VE;
-        if (col < a.hidden && VCE_BOUNDS(int(blockIdx.x) < a.parts, a.dev_status))
+        const int col = (j * tpr + t) * VE - off;
+        if (col < hidden && VCE_BOUNDS(int(blockIdx.x) < a.parts, a.dev_status))
 #pragma unroll
-            for (int i = 0; i < VE; ++i) out[col + i] = acc[j][i];
+            for (int i = 0; i < VE; ++i)
+                if (!kShift || uint32_t(col + i) < uint32_t(hidden)) out[col + i] = acc[j][i];
     }
 }
 
@@ -607,11 +657,8 @@ int pick_ve(int full, int64_t hidden, size_t es, std::initializer_list<const voi
     return 1;
 }
 
-int pow2_at_least(int64_t x) {
-    int p = 32;
-    while (p < x) p *= 2;
-    return p;
-}
+// threads in whole warps
+int warps_for(int64_t x) { return x <= 32 ? 32 : int((x + 31) / 32 * 32); }
 
 template <typename T, bool kMx>
 vce_status norm_forward(NormArgs a, int ve, cudaStream_t s, const DeviceInfo& dev) {
@@ -629,7 +676,7 @@ vce_status norm_forward(NormArgs a, int ve, cudaStream_t s, const DeviceInfo& de
         rms_norm_long<T, kMx><<<unsigned(rows), kMaxThreads, 0, s>>>(a);
         return cudaGetLastError() == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
     }
-    a.tpr = pow2_at_least((nvec + nv - 1) / nv);
+    a.tpr = warps_for((nvec + nv - 1) / nv);
     const int block = a.tpr == 32 ? 128 : a.tpr;  // four rows of one warp each, or one row
     const unsigned grid = unsigned((rows + block / a.tpr - 1) / (block / a.tpr));
     if (ve == kFull) {
@@ -649,42 +696,51 @@ constexpr int kRingStages = 2;
 constexpr int kRingVecs = 2;                // vectors per thread
 constexpr size_t kRingMost = 148 << 10;  // of shared memory per block
 
-template <typename T, int NV>
+template <typename T, int NV, bool kShift>
 vce_status launch_ring(const NormBwdArgs& a, int threads, size_t smem, cudaStream_t s, int device) {
     static std::mutex mu;
     static bool ready[64];
     {
         std::lock_guard<std::mutex> lock(mu);
         if (!ready[device]) {
-            if (cudaFuncSetAttribute(rms_norm_backward_ring<T, NV, kRingStages>,
+            if (cudaFuncSetAttribute(rms_norm_backward_ring<T, NV, kRingStages, kShift>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, int(kRingMost)) != cudaSuccess)
                 return VCE_ERR_CUDA;
             ready[device] = true;
         }
     }
     count_launch();
-    rms_norm_backward_ring<T, NV, kRingStages><<<a.parts, threads, smem, s>>>(a);
+    rms_norm_backward_ring<T, NV, kRingStages, kShift><<<a.parts, threads, smem, s>>>(a);
     return cudaGetLastError() == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
 }
 
 template <typename T>
-vce_status norm_backward(NormBwdArgs a, int ve, int& parts, cudaStream_t s, const DeviceInfo& dev) {
+vce_status norm_backward(NormBwdArgs a, int ve, bool same_offset, int& parts, cudaStream_t s, const DeviceInfo& dev) {
     constexpr int kFull = 16 / sizeof(T);
     constexpr int kNv = 32 / kFull;  // 32 sums of dw per thread
     const int64_t nvec = (a.hidden + ve - 1) / ve;
     int nv = ve == kFull ? kNv : 8;
     a.parts = parts;
-    // The ring where a row is longer than 128 vectors and its stages fit: as many blocks as
-    // shared memory lets an SM hold (at most the four per SM of the workspace), so that all
-    // run at once.  Two stages: more blocks per SM beat more stages (16384 x 4096 BF16, with
-    // the sum of partials: 104 us with two stages, 112 with three, 127 with four).
-    const int threads = pow2_at_least((nvec + kRingVecs - 1) / kRingVecs);
-    const size_t ring = 64 * sizeof(float) + size_t(kRingStages) * (a.dh ? 3 : 2) * kRingVecs * threads * 16;
-    if (a.n > 0 && ve == kFull && nvec > 128 && threads <= kMaxThreads && ring <= kRingMost) {
-        const int64_t fit = int64_t(dev.num_sms) * int64_t((228 << 10) / (ring + 1024));
+    // The ring where a row is longer than 128 vectors and its stages fit: as many blocks as an
+    // SM holds (and the workspace has partial rows for), so that all run at once.  Rows that
+    // start off 16-byte boundaries, with narrow accesses / in the ring: 16000 x 4097 BF16 285 /
+    // 121 us, 3035 x 2317 44 / 26, 16000 x 300 31 / 27.  Two stages: more blocks per SM beat
+    // more stages (16384 x 4096 BF16, with the sum of partials: 104 us with two stages, 112 with
+    // three, 127 with four).
+    const bool shift = ve != kFull && same_offset;
+    const int64_t wide = shift ? (a.hidden + 2 * kFull - 2) / kFull : nvec;  // vectors of a row, at most
+    const int threads = warps_for((wide + kRingVecs - 1) / kRingVecs);
+    const size_t ring = 64 * sizeof(float) + (shift ? size_t((a.hidden + 2 * kFull - 1) / kFull * kFull) * sizeof(float) : 0) +
+                        size_t(kRingStages) * (a.dh ? 3 : 2) * kRingVecs * threads * 16;
+    if (a.n > 0 && (ve == kFull || shift) && wide > (shift ? 32 : 128) && threads <= kRingThreads && ring <= kRingMost) {
+        // resident at once: by shared memory, and by registers (64 for each of 1024 threads)
+        const int64_t fit = int64_t(dev.num_sms) *
+                            std::min(int64_t((228 << 10) / (ring + 1024)), int64_t(kRingThreads / threads));
         if (parts > fit) parts = int(fit);
+        if (shift && parts < a.n) parts -= parts % kFull;  // a block's rows share their offset
         a.parts = parts;
-        return launch_ring<T, kRingVecs>(a, threads, ring, s, dev.ordinal);
+        return shift ? launch_ring<T, kRingVecs, true>(a, threads, ring, s, dev.ordinal)
+                     : launch_ring<T, kRingVecs, false>(a, threads, ring, s, dev.ordinal);
     }
     if (a.n > 0 && nvec > int64_t(kMaxThreads) * nv) {
         count_launch();  // dw first: dx may be written over dy
@@ -693,7 +749,7 @@ vce_status norm_backward(NormBwdArgs a, int ve, int& parts, cudaStream_t s, cons
         rms_norm_backward_long<T><<<unsigned(a.n), kMaxThreads, 0, s>>>(a);
     } else if (a.n > 0) {
         while (nv > 1 && nvec <= 32 * (nv / 2) && ve == kFull) nv /= 2;
-        a.tpr = pow2_at_least((nvec + nv - 1) / nv);
+        a.tpr = warps_for((nvec + nv - 1) / nv);
         const int block = a.tpr == 32 ? 128 : a.tpr;
         const size_t smem = 64 * sizeof(float) + (block == a.tpr ? 0 : size_t(a.hidden) * sizeof(float));
         count_launch();
@@ -756,8 +812,15 @@ vce_status launch_rms_norm_backward(const void* dy, const void* h, const void* w
     const int ve = n == 0 ? 1
                           : pick_ve(int(16 / es), hidden, es, {dy, h, dh ? dh : h, dx},
                                     {dy_stride, h_stride, dh ? dh_stride : 0, dx_stride}, weight, a.w_f32);
-    vce_status st = dtype == VCE_BF16 ? norm_backward<__nv_bfloat16>(a, ve, parts, s, dev)
-                                      : norm_backward<float>(a, ve, parts, s, dev);
+    // whether a row starts at the same offset from a 16-byte boundary in all operands
+    bool same = true;
+    const void* dh_at = dh ? dh : dy;
+    for (const void* p : {h, dh_at, static_cast<const void*>(dx)})
+        same = same && (reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(dy)) % 16 == 0;
+    for (int64_t d : {h_stride - dy_stride, (dh ? dh_stride : dy_stride) - dy_stride, dx_stride - dy_stride})
+        same = same && d * int64_t(es) % 16 == 0;
+    vce_status st = dtype == VCE_BF16 ? norm_backward<__nv_bfloat16>(a, ve, same, parts, s, dev)
+                                      : norm_backward<float>(a, ve, same, parts, s, dev);
     if (st) return st;
     count_launch();
     rms_norm_dweight_sum<<<unsigned((hidden + 31) / 32), 32 * kSumSplit, 0, s>>>(a.part, parts, hidden, dweight, a.w_f32);
