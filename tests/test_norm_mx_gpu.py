@@ -98,6 +98,37 @@ def test_scale_rows_past_the_end_are_zero(n):
         assert (t.codes[:, 160:] == 0).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,h", [(3000, 1031), (1400, 4097), (2000, 2317), (2500, 301), (1200, 2050), (9, 301)])
+@pytest.mark.parametrize("residual", [False, True])
+def test_forward_rows_off_16_bytes(n, h, dtype, residual):
+    # many rows to a block, every offset of a row from a 16-byte boundary
+    check_forward(n, h, DT[dtype], DT[dtype], residual)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("alias", [None, "x", "residual"])
+@pytest.mark.parametrize("n,h,pad,offset", [(2600, 1031, 2, 1), (1300, 1024, 5, 3), (3, 2000, 7, 1), (700, 2048, 3, 1)])
+def test_forward_of_views_at_one_offset(n, h, pad, offset, alias, dtype):
+    # views with one offset and stride, the outputs among them: the same h as plainly added, y
+    # within its bound, and nothing beside the views is written
+    base = [rand(k, n, h + pad, dtype=DT[dtype]).contiguous() for k in (1, 2, 3, 4)]
+    x, res, hh, y = (t[:, offset:offset + h] for t in base)
+    w = rand(5, h, dtype=DT[dtype]).contiguous()
+    want_h = (x.float() + res.float()).to(DT[dtype])
+    want_y, _ = head.rms_norm(f64(want_h), f64(w), 1e-6)
+    i = {None: 2, "x": 0, "residual": 1}[alias]
+    before = [base[i].clone(), base[3].clone()]
+    got = vce.rms_norm_forward(x, w, 1e-6, res, h=(x, res, hh)[i], y=y)
+    assert torch.equal(got.h, want_h)
+    assert np.all(np.abs(f64(got.y) - want_y) <= (half_step(DT[dtype]) * (1 + 1e-5) + 47 * U) * np.abs(want_y) + 1e-45)
+    for full, was, part in ((base[i], before[0], got.h), (base[3], before[1], got.y)):
+        was[:, offset:offset + h] = part
+        assert torch.equal(full, was)
+    plain = vce.rms_norm_forward(want_h[:, :], w, 1e-6, y=y)
+    assert np.all(np.abs(f64(plain.y) - want_y) <= (half_step(DT[dtype]) * (1 + 1e-5) + 47 * U) * np.abs(want_y) + 1e-45)
+
+
 @pytest.mark.parametrize("alias", ["h_is_residual", "h_is_x", "y_is_x", "y_is_residual"])
 @pytest.mark.parametrize("h", [4096, 1031, 70001])
 def test_forward_in_place(alias, h):
