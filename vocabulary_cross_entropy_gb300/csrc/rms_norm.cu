@@ -16,7 +16,7 @@
 //
 // All three are bound by memory: a row is read once into registers, reduced over
 // its threads and written from registers.  16384 x 4096 BF16 with a residual (537 MB, 80 us
-// at the copy rate): forward 82 us, backward 101 us.  The 8-bit form is bound by
+// at the copy rate): forward 82 us, backward 99 us.  The 8-bit form is bound by
 // instructions (54 us without a residual, 202 MB).
 
 #include "head_internal.cuh"
@@ -727,26 +727,41 @@ __global__ void __launch_bounds__(256) rms_norm_dweight_long(const NormBwdArgs a
     a.part[int64_t(blockIdx.y) * a.hidden + col] = s;
 }
 
-// dw = the sum of the partial rows, in a fixed order: 32 columns per block, 32 threads
-// per column, each over every 32nd partial (8 threads per column left the loads'
-// latency exposed).
-constexpr int kSumSplit = 32;
-__global__ void __launch_bounds__(32 * kSumSplit) rms_norm_dweight_sum(const float* __restrict__ part, int parts,
-                                                                       int64_t hidden, void* dw, int w_f32) {
-    __shared__ float sm[kSumSplit][32];
-    const int lc = threadIdx.x & 31, sp = threadIdx.x >> 5;
-    const int64_t col = int64_t(blockIdx.x) * 32 + lc;
-    float s = 0.f;
+// dw = the sum of the partial rows, in a fixed order: 32 columns per block, VE per thread,
+// the partial rows dealt out to the threads that share columns, whose loads are then all on
+// their way at once.  Launched so that it overlaps the end of the kernel before (16384 x 4096
+// BF16 101 -> 99 us; started earlier than that kernel's last blocks, 2880 FP32 columns lost 6%).
+template <int VE>
+__global__ void __launch_bounds__(1024) rms_norm_dweight_sum(const float* __restrict__ part, int parts, int64_t hidden,
+                                                             void* dw, int w_f32) {
+    constexpr int kLanes = 32 / VE, kSplit = 1024 / kLanes;
+    __shared__ float sm[kSplit][33];
+    const int lc = threadIdx.x % kLanes, sp = threadIdx.x / kLanes;
+    const int64_t col0 = int64_t(blockIdx.x) * 32, col = col0 + lc * VE;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // for the partial rows
+    float s[VE];
+#pragma unroll
+    for (int i = 0; i < VE; ++i) s[i] = 0.f;
     if (col < hidden) {
 #pragma unroll 8
-        for (int p = sp; p < parts; p += kSumSplit) s += part[int64_t(p) * hidden + col];
+        for (int p = sp; p < parts; p += kSplit) {
+            const Vec<float, VE> v = *reinterpret_cast<const Vec<float, VE>*>(part + int64_t(p) * hidden + col);
+#pragma unroll
+            for (int i = 0; i < VE; ++i) s[i] += v.e[i];
+        }
     }
-    sm[sp][lc] = s;
+#pragma unroll
+    for (int i = 0; i < VE; ++i) sm[sp][lc * VE + i] = s[i];
     __syncthreads();
-    if (sp != 0 || col >= hidden) return;
-    for (int k = 1; k < kSumSplit; ++k) s += sm[k][lc];
-    if (w_f32) static_cast<float*>(dw)[col] = s;
-    else static_cast<__nv_bfloat16*>(dw)[col] = __float2bfloat16_rn(s);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;  // a warp per column
+    float t = 0.f;
+#pragma unroll
+    for (int k = lane; k < kSplit; k += 32) t += sm[k][warp];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    if (lane != 0 || col0 + warp >= hidden) return;
+    if (w_f32) static_cast<float*>(dw)[col0 + warp] = t;
+    else static_cast<__nv_bfloat16*>(dw)[col0 + warp] = __float2bfloat16_rn(t);
 }
 
 // Elements per access: the widest of the kernel's choices that divides the row length and
@@ -958,8 +973,18 @@ vce_status launch_rms_norm_backward(const void* dy, const void* h, const void* w
                                       : norm_backward<float>(a, ve, same, parts, s, dev);
     if (st) return st;
     count_launch();
-    rms_norm_dweight_sum<<<unsigned((hidden + 31) / 32), 32 * kSumSplit, 0, s>>>(a.part, parts, hidden, dweight, a.w_f32);
-    return cudaGetLastError() == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
+    cudaLaunchConfig_t cfg{};  // its launch overlaps the end of the kernel before, for which it waits
+    cfg.gridDim = dim3(unsigned((hidden + 31) / 32));
+    cfg.blockDim = dim3(1024);
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const float* part = a.part;
+    const auto sum = hidden % 4 == 0 ? rms_norm_dweight_sum<4> : rms_norm_dweight_sum<1>;
+    return cudaLaunchKernelEx(&cfg, sum, part, parts, hidden, dweight, a.w_f32) == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
 }
 
 }  // namespace vce
