@@ -232,6 +232,21 @@ def test_largest_vocabulary_of_equal_logits(offset, dtype):
     check(z, u, top_p=0.6)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("v", [1 << 18, 1 << 19, 1 << 20])
+def test_rows_of_full_weights(v, dtype):
+    # equal logits, and any logits at the highest temperature: the sum of a row is the largest there is
+    z = torch.full((3, v), -1.5, dtype=DT[dtype], device=DEV)
+    u = torch.tensor([0.0, 0.37, 1.0 - 2.0 ** -24], device=DEV)
+    check(z, u)
+    check(z, u, top_p=0.3)
+    check(z, u, top_k=v - 1)
+    g = torch.Generator(DEV).manual_seed(v)
+    z = torch.randn(2, v, device=DEV, generator=g).to(DT[dtype])
+    check(z, u[:2], temperature=float("inf"))
+    check(z, u[1:], temperature=float("inf"), top_p=0.7)
+
+
 def test_distribution():
     # uniform numbers on a fine grid draw every token in proportion to its probability
     z, _ = make(10, 1, 12, "f32", peaks=False)

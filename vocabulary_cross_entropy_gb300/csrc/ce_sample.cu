@@ -238,10 +238,15 @@ __device__ __forceinline__ uint64_t scale_up(uint64_t sum, int bin, const uint64
     const uint64_t t = table[n & (kSteps - 1)];                       // 63 fractional bits
     const int shift = 63 + kFracBits - q_bits - (n >> 6);             // 55 .. 102
     const uint64_t hi = __umul64hi(sum, t), lo = sum * t;
-    uint64_t q;  // twice the value, rounded down
-    if (shift - 1 < 64) q = hi << (65 - shift) | lo >> (shift - 1);
-    else q = hi >> (shift - 65);
-    return (q + 1) >> 1;
+    uint64_t q, rest;  // the value rounded down (2^63 for a row of full weights), and the bits below it from the top down
+    if (shift < 64) {
+        q = hi << (64 - shift) | lo >> shift;
+        rest = lo << (64 - shift);
+    } else {
+        q = hi >> (shift - 64);
+        rest = shift == 64 ? lo : hi << (128 - shift);
+    }
+    return q + (rest >> 63);
 }
 
 __device__ __forceinline__ uint64_t weight_of(const Scale& s, float z, const uint64_t* table, int q_bits) {
@@ -249,7 +254,7 @@ __device__ __forceinline__ uint64_t weight_of(const Scale& s, float z, const uin
     return scale_up((uint64_t(1) << kFracBits) + int64_t(st.g), st.bin, table, q_bits);
 }
 
-// floor(x y) for a float 0 <= x < 1 and y < 2^63; ``*exact`` tells whether nothing was cut off
+// floor(x y) for a float 0 <= x < 1 and y <= 2^63; ``*exact`` tells whether nothing was cut off
 __device__ __forceinline__ uint64_t floor_product(float x, uint64_t y, bool* exact) {
     const uint32_t b = __float_as_uint(x);
     const int e = int(b >> 23) & 255;
