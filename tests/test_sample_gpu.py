@@ -175,6 +175,42 @@ def test_uniform_at_the_ends():
     assert torch.equal(over.token, last)
 
 
+def last_kept(z, top_k=None, top_p=None, min_p=None):
+    """The last token of each row's kept head, in FP64."""
+    zs, order = torch.sort(z.double(), dim=1, descending=True, stable=True)
+    w = torch.exp(zs - zs[:, :1])
+    rank = torch.arange(z.shape[1], device=z.device)
+    keep = torch.ones_like(w, dtype=torch.bool)
+    if top_k is not None:
+        keep &= rank < top_k[:, None]
+    w = w * keep
+    if top_p is not None:
+        keep &= (torch.cumsum(w, 1) - w < top_p.double()[:, None] * w.sum(1, keepdim=True)) | (rank == 0)
+    if min_p is not None:
+        keep &= w >= min_p.double()[:, None]
+    return order.gather(1, keep.sum(1, keepdim=True) - 1)[:, 0]
+
+
+@pytest.mark.parametrize("filters", ["k", "p", "m", "kp", "km", "pm", "kpm"])
+@pytest.mark.parametrize("n,v,dtype", [(600, 50257, "f32"), (600, 32001, "bf16"), (40, 128256, "f32")])
+def test_uniform_of_one_takes_the_last_kept(n, v, dtype, filters):
+    # heads too long for the collecting path: a border's mass and the masses that the draw is
+    # looked up in are rounded differently, and the draw must not land behind the border
+    z, _ = make(21, n, v, dtype)
+    g = torch.Generator(DEV).manual_seed(22)
+    rnd = lambda: torch.rand(n, device=DEV, generator=g)
+    f = {}
+    if "k" in filters:
+        f["top_k"] = (257 + 4000 * rnd()).int()
+    if "p" in filters:
+        f["top_p"] = 0.3 + 0.699 * rnd()
+    if "m" in filters:
+        f["min_p"] = torch.exp(-12 * rnd())
+    want = last_kept(z, **f)
+    for u in (1.0, 1.5):
+        assert torch.equal(vce.ce_sample(z, torch.full((n,), u, device=DEV), **f).token, want)
+
+
 def test_parameters_that_filter_nothing():
     z, u = make(6, 30, 2000, "bf16")
     want = check(z, u)

@@ -66,6 +66,7 @@ constexpr int kCapBits = 11;
 constexpr int kMaxHeads = 256;      // top-k of the collecting path
 constexpr int kIndexBits = 20;      // vocabulary of at most 2^20
 constexpr int kMaxCluster = 8;
+constexpr int kEdgeBins = 5;       // around min-p's border: weights there are compared one by one
 
 __device__ const uint64_t kExp2Table[kSteps] = {
 #include "exp2_table.inc"
@@ -110,7 +111,8 @@ struct Shared {
     float row_max[kMaxCluster], bound[kMaxCluster];
     Command cmd[2];  // by block 0; consecutive commands take turns: a late reader finds its own intact
     uint32_t part_n[kMaxCluster];  // block 0's: what the others have collected
-    uint64_t min_key, max_key, kept_minp;
+    uint64_t min_key, max_key;
+    uint64_t kept_minp[kEdgeBins];  // sums of the weights that min-p keeps, per bin
     float my_bound;
     uint32_t n_list, found, argmax;
 };
@@ -802,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
             for (int i = tid; i < kBins; i += kThreads) sh.mass[i] = 0, sh.count[i] = 0;
             // min-p (with top-p): whole bins above the border, and single weights next to it
             const int edge = by_min ? max(0, bin_of(fmaxf(kLeastLog2, log2f(min_p))) - 2) : kBins;
-            if (tid == 0) sh.kept_minp = 0;
+            if (tid < kEdgeBins) sh.kept_minp[tid] = 0;
             __syncthreads();
             uint32_t* const words = reinterpret_cast<uint32_t*>(sh.mass);  // low halves, then high ones
             for_pairs<1, 1>(s.part, a.dev_status, [&](float z0, float z1, int) {
@@ -836,15 +838,16 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
                 for (int k = 0; k < kPer; ++k)
                     if (tid + k * kThreads < kBins) sh.mass[tid + k * kThreads] = v[k];
             }
-            if (by_min) {  // the few elements of five bins
-                const Wanted w = s.in_bin({0, ~0ull, edge + 2, 0});
+            if (by_min) {  // the few elements of kEdgeBins bins
+                const Wanted w = s.in_bin({0, ~0ull, edge + kEdgeBins / 2, 0});
                 const float wide = 2.f / (kSteps * sc.ch);
                 for_each<1>(s.part, a.dev_status, [&](float z, int) {
                     if (!(z >= w.z_lo - wide && z <= w.z_hi + wide)) return;
                     const float p = log2_weight(sc, z);
-                    if (!(p > kLeastLog2) || bin_of(p) < edge || bin_of(p) >= edge + 5) return;
+                    const int k = bin_of(p) - edge;
+                    if (!(p > kLeastLog2) || k < 0 || k >= kEdgeBins) return;
                     const uint64_t x = weight_of(sc, z, sh.table, a.q_bits);
-                    if (x >= least) s.add_mass(&sh.kept_minp, x);
+                    if (x >= least) s.add_mass(&sh.kept_minp[k], x);
                 });
             }
             s.barrier();
@@ -879,7 +882,12 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
                 cmd.flag = by_k && sh.count[kBins - 1] > uint32_t(top_k);  // the k-th has a weight
                 if (by_min) {
                     above = edge ? sh.mass[edge - 1] : 0;
-                    for (int c = 0; c < a.cluster; ++c) above += remote(&sh.kept_minp, c);
+                    for (int k = 0; k < kEdgeBins; ++k) {  // the last bin with a kept weight decides
+                        uint64_t kept = 0;
+                        for (int c = 0; c < a.cluster; ++c) kept += remote(&sh.kept_minp[k], c);
+                        const int bin = edge + k;
+                        if (kept) above = min((bin ? sh.mass[bin - 1] : 0) + kept, sh.mass[bin]);
+                    }
                 }
             }
             if (by_k && !s.tell(cmd).flag) continue;
@@ -952,7 +960,9 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
                     at = max(0, min(at, n - 1));
                     key = sh.list[at];
                     weight_drawn = sh.sums[at] - (at ? sh.sums[at - 1] : base);
-                    if (step == kTopK || step == kTopP) mass = sh.sums[at];
+                    // (never past the border's bin: weights rounded one by one can sum to more than
+                    // the bin's, which was rounded once, and the draw would look behind the bin)
+                    if (step == kTopK || step == kTopP) mass = min(sh.sums[at], sh.mass[cmd.bin]);
                 }
             }
             cmd = s.tell(cmd);
