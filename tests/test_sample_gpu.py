@@ -211,6 +211,17 @@ def test_uniform_of_one_takes_the_last_kept(n, v, dtype, filters):
         assert torch.equal(vce.ce_sample(z, torch.full((n,), u, device=DEV), **f).token, want)
 
 
+@pytest.mark.parametrize("n", [1, 200])
+@pytest.mark.parametrize("v", [1500, 5000])
+def test_uniform_of_one_among_least_weights(n, v):
+    # weights of 1.41 units of the least one: rounded one by one they sum to less than together,
+    # and more of them than a list holds
+    z = torch.full((n, v), -43.5 * float(np.log(2)), device=DEV)
+    z[:, 77] = 0.0
+    for u in (1.0, 1.5):
+        assert (vce.ce_sample(z, torch.full((n,), u, device=DEV)).token == v - 1).all()
+
+
 def test_parameters_that_filter_nothing():
     z, u = make(6, 30, 2000, "bf16")
     want = check(z, u)

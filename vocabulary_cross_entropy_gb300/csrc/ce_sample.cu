@@ -640,9 +640,11 @@ struct Sampler {
             __syncthreads();
             prefix_sums<kCap / kThreads>(sh.list, kCap, sh.warp_sum, [&](int i) { return sh.list[i]; });
             prefix_sums<kCap / kThreads>(sh.sums, kCap, sh.warp_sum, [&](int i) { return sh.sums[i]; });
+            // (the bin's mass, rounded once, can be more than the sum of its weights, rounded one
+            // by one: a target between the two takes the last range that holds a key)
             const int b = min(by_count ? first_at_least(sh.sums, kCap, target - base_count)
                                        : first_at_least(sh.list, kCap, target > base ? target - base : 1),
-                              kCap - 1);
+                              int((h - l) >> shift));
             if (b > 0) base += sh.list[b - 1], base_count += uint32_t(sh.sums[b - 1]);
             const uint64_t width = (uint64_t(1) << shift) - 1;
             cmd.hi = h - (uint64_t(b) << shift);
