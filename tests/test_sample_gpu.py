@@ -222,6 +222,20 @@ def test_uniform_of_one_among_least_weights(n, v):
         assert (vce.ce_sample(z, torch.full((n,), u, device=DEV)).token == v - 1).all()
 
 
+@pytest.mark.parametrize("n,v", [(1, 1500), (1, 5000), (200, 1500), (200, 5000), (1, 1 << 20)])
+def test_least_weights_are_never_drawn(n, v):
+    # 0.4 units of the least weight each: below the border, however many there are
+    unit = -44 if v <= 1 << 19 else -43
+    z = torch.full((n, v), (unit - 1.35) * float(np.log(2)), device=DEV)
+    z[:, 77] = 0.0
+    for f in (dict(), dict(top_k=v - 1)):
+        for u in (1.0, 1.5):
+            r = vce.ce_sample(z, torch.full((n,), u, device=DEV), **f)
+            assert (r.token == 77).all() and (r.logprob == 0).all()
+    z[:, v // 2] = (unit - 0.9) * float(np.log(2))  # 0.54 units
+    assert (vce.ce_sample(z, torch.ones(n, device=DEV)).token == v // 2).all()
+
+
 def test_parameters_that_filter_nothing():
     z, u = make(6, 30, 2000, "bf16")
     want = check(z, u)

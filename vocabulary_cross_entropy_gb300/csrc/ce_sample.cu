@@ -49,7 +49,6 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSteps = 64;            // values of n per octave
 constexpr int kBins = 46 * kSteps;    // 46 octaves of n, from 0 down
-constexpr float kLeastLog2 = -45.9f;  // below it a weight is 0 (Q <= 44)
 constexpr int kFracBits = 36;         // of s
 constexpr int kBiasBits = 29;         // s - 2^36 is above -2^29 and below 2^29
 // Sums of s are kept in 32-bit words of 15 bits of every s, which 2^17 elements cannot
@@ -82,6 +81,7 @@ struct SampleArgs {
     float* logprob;
     int cluster;
     int q_bits;  // Q
+    float least_log2;  // weights above it round to one unit 2^-Q at least, others count as 0
     int* dev_status;
 };
 
@@ -153,7 +153,7 @@ __device__ __forceinline__ Scale make_scale(float m, float t) {
 // The leading term of (z - m) c, monotone in z.
 __device__ __forceinline__ float log2_weight(const Scale& s, float z) { return __fmul_rn(z - s.m, s.ch); }
 
-// The element's n (as the bin -n) and s of a log2_weight above kLeastLog2.
+// The element's n (as the bin -n) and s of a log2_weight above least_log2.
 //   (z - m) and its product with c are carried as sums of two floats (TwoSum, FMA), about
 //   2^-47 relative.  The exponent is n / 64 + f with |f| <= 2^-7; 2^f - 1 from its series
 //   to the fifth power, its linear term split into a multiple of 2^-29 and a rest.
@@ -583,7 +583,7 @@ struct Sampler {
     __device__ __forceinline__ Wanted in_bin(const Command& cmd) const {
         const float far = (float(cmd.bin) + 0.75f) / (kSteps * sc.ch), near = (float(cmd.bin) - 0.75f) / (kSteps * sc.ch);
         const float slack = fabsf(sc.m) * 0x1p-21f;
-        return {sc.m - far - slack, sc.m - near + slack, kLeastLog2, cmd};
+        return {sc.m - far - slack, sc.m - near + slack, a.least_log2, cmd};
     }
 
     // A range that holds more elements than a list: its keys divided into kCap ranges of
@@ -596,7 +596,7 @@ struct Sampler {
             if (!(z >= w.z_lo && z <= w.z_hi)) return false;
             const float p = log2_weight(sc, z);
             const uint64_t k = key_of(z, i);
-            return p > kLeastLog2 && bin_of(p) == w.cmd.bin && k >= w.cmd.lo && k <= w.cmd.hi;
+            return p > a.least_log2 && bin_of(p) == w.cmd.bin && k >= w.cmd.lo && k <= w.cmd.hi;
         };
         uint64_t kmin = ~0ull, kmax = 0;
         for_each<1>(part, a.dev_status, [&](float z, int i) {
@@ -805,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
             // ---- weights of the whole row, summed by n ----
             for (int i = tid; i < kBins; i += kThreads) sh.mass[i] = 0, sh.count[i] = 0;
             // min-p (with top-p): whole bins above the border, and single weights next to it
-            const int edge = by_min ? max(0, bin_of(fmaxf(kLeastLog2, log2f(min_p))) - 2) : kBins;
+            const int edge = by_min ? max(0, bin_of(fmaxf(a.least_log2, log2f(min_p))) - 2) : kBins;
             if (tid < kEdgeBins) sh.kept_minp[tid] = 0;
             __syncthreads();
             uint32_t* const words = reinterpret_cast<uint32_t*>(sh.mass);  // low halves, then high ones
@@ -813,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
                 const Step2 st = step_of2(sc, make_float2(z0, z1));
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    if (!((k ? st.p.y : st.p.x) < -kLeastLog2)) continue;
+                    if (!((k ? st.p.y : st.p.x) < -a.least_log2)) continue;
                     const int bin = st.bin[k];
                     if (!VCE_BOUNDS(bin >= 0 && bin < kBins, a.dev_status)) continue;
                     const bool fine = bin < kFineBins;
@@ -847,7 +847,7 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
                     if (!(z >= w.z_lo - wide && z <= w.z_hi + wide)) return;
                     const float p = log2_weight(sc, z);
                     const int k = bin_of(p) - edge;
-                    if (!(p > kLeastLog2) || k < 0 || k >= kEdgeBins) return;
+                    if (!(p > a.least_log2) || k < 0 || k >= kEdgeBins) return;
                     const uint64_t x = weight_of(sc, z, sh.table, a.q_bits);
                     if (x >= least) s.add_mass(&sh.kept_minp[k], x);
                 });
@@ -905,7 +905,7 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
             target = u >= 1.f ? mass : floor_product(fmaxf(u, 0.f), mass, &exact) + 1;
         }
         // ---- the border's bin, told to all ----
-        Wanted w{0.f, row_max, heads_min ? fmaxf(kLeastLog2, log2f(min_p) - 0.01f) : kLeastLog2, cmd};
+        Wanted w{0.f, row_max, heads_min ? fmaxf(a.least_log2, log2f(min_p) - 0.01f) : a.least_log2, cmd};
         w.z_lo = heads_k ? bound : sc.m + (w.p_least - 0.1f) / sc.ch - fabsf(sc.m) * 0x1p-21f;
         if (step != kHeads) {
             if (s.lead()) {
@@ -988,10 +988,13 @@ vce_status launch_ce_sample(const void* logits, int dtype, int64_t n, int64_t vo
                             const DeviceInfo& dev) {
     if (n == 0) return VCE_OK;
     SampleArgs a{logits, n, stride, int(vocab), uniform, temperature, top_p, min_p, top_k, token, logprob, 1, 0,
-                 dev_status};
+                 0.f, dev_status};
     int bits = 0;
     while ((int64_t(1) << bits) < vocab) ++bits;
     a.q_bits = 63 - bits < 44 ? 63 - bits : 44;
+    // half a unit, and 2^-10 for the rounding of a log2_weight (below 2^-16): whatever is counted
+    // has a weight that is not 0 after its rounding either
+    a.least_log2 = -float(a.q_bits + 1) + 0x1p-10f;
     // As many blocks per row as fill the SMs once, each with a part worth a block.  (Filled
     // twice, 256 x 128256 rows took 171 -> 144 us where a few rows need several borders, but
     // 108 -> 135 us where all are alike.)
