@@ -256,14 +256,19 @@ vce_status ce_forward_noalloc(const void* logits, int dtype, int64_t n_rows, int
  *     min_p   the tokens of weight at least min_p (of at least min_p times the
  *             likeliest token's probability).
  * The token is the first one at which the cumulated weight exceeds uniform times the
- * weight of all kept ones.  A temperature of 0 or less takes the first token.  The
- * choice is made in whole-number weights of 43 or 44 fractional bits (relative to the
- * largest; each within 2^-36 of its own value), whose sums are exact: no order of
- * additions changes a token.  A token whose weight is below 2^-45 is never drawn.
+ * weight of all kept ones.  A temperature of 0 or less takes the first token.
+ *
+ * The choice is made in whole numbers, so that no order of additions changes a token.
+ * Their unit is 2^-44 of the largest weight (2^-43 where vocab is above 2^19).  A border
+ * is first located among the sums of the weights in each 1/64 octave: weights down to
+ * 2^-8 of the largest enter those within 2^-36 of their own values, smaller ones within
+ * 2^-29, and each sum is rounded to the unit as a whole.  Inside its 1/64 octave it is
+ * located among weights within 2^-36 of their own values, each rounded to the unit.  A
+ * token whose weight is below half a unit is never drawn.
  *
  *   logits       as in ce_forward, with 1 <= vocab <= VCE_SAMPLE_MAX_VOCAB; -inf marks a
  *                token that is not allowed.
- *   uniform      F32 [n_rows], in [0, 1) (smaller counts as 0, larger takes the last kept).
+ *   uniform      F32 [n_rows], in [0, 1) (smaller counts as 0, 1 and larger take the last kept).
  *   temperature, top_p, min_p  F32 [n_rows], top_k int32 [n_rows]; each may be NULL:
  *                temperature 1, no filter.  top_k <= 0 or >= vocab, top_p >= 1 and
  *                min_p <= 0 leave their filter out; min_p above 1 counts as 1;

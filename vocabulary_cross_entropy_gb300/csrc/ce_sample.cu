@@ -10,8 +10,10 @@
 // result would depend on the order of additions.  Weight i is
 //     2^(Q + n / 64) s / 2^36,  n / 64 + log2(s / 2^36) = (z_i - m) c,  c = log2(e) / T,
 // with n and s whole and s within 2^-36 of its exact value (relative) (step_of below).  Q is at most
-// 44 and leaves room for the sum of a row.  Integer sums are exact in any order: the
-// row is split over threads and blocks freely, and atomics change nothing.
+// 44 and leaves room for the sum of a row (2^63).  Integer sums come out the same in any order: the
+// row is split over threads and blocks freely, and atomics change nothing.  They are rounded,
+// though: a mass (below) as a whole, far down of s in steps of 2^7, a sorted token's weight by
+// itself.  Where both meet, a head's mass is kept from passing that of its last n.
 //
 // A row never gets sorted as a whole:
 //   heads  (top-k up to kMaxHeads, or min-p without top-p): a bound is found below
@@ -53,7 +55,7 @@ constexpr int kFracBits = 36;         // of s
 constexpr int kBiasBits = 29;         // s - 2^36 is above -2^29 and below 2^29
 // Sums of s are kept in 32-bit words of 15 bits of every s, which 2^17 elements cannot
 // overflow.  The 8 octaves below the largest logit get s - 2^36 + 2^29 in two words and
-// a count; further down 30 bits of s itself are enough (2^-30 of a weight that is at most
+// a count; further down 30 bits of s itself are enough (2^-29 of a weight that is at most
 // 2^-8), two words and no count.
 constexpr int kHalfBits = 15;
 constexpr int kMaxPart = 1 << 17;     // elements per block, at most
