@@ -455,7 +455,7 @@ vce_status rms_norm_backward(const void* dy, int dtype, int64_t n, int64_t hidde
 /*
  * A microscaled tensor [rows, cols] is a buffer of codes and a buffer of scales.
  *   codes   rows of padded columns (cols rounded up to 128, the rest 0).  E4M3: one
- *           byte a value.  E2M1: two values a byte, the even column in the low
+ *           byte a value (127 and 255 are NaN; mx_quantize writes neither).  E2M1: two values a byte, the even column in the low
  *           four bits (sign, two exponent bits, one mantissa bit).
  *   scales  E8M0 bytes (2^(byte - 127); 255 is NaN), one per row and 32 columns, in
  *           tiles of 128 rows x 4 blocks: the scale of (row, block) is byte

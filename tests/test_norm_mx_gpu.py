@@ -451,6 +451,23 @@ def test_mx_from_parts():
         assert torch.equal(t.codes, q.codes) and torch.equal(t.scales, q.scales)
 
 
+@pytest.mark.parametrize("cols", [256, 255])
+def test_every_code(cols):
+    # all 256 codes of E4M3, its two NaNs among them, and all 16 of E2M1
+    for fmt, codes in (("e4m3", torch.arange(256)[:cols]), ("e2m1", torch.arange(cols) * 7 % 16)):
+        raw = codes.to(torch.uint8).numpy()[None]
+        want = head.mx_dequantize(np.pad(raw, ((0, 0), (0, 256 - cols))).astype(int), np.full((1, 8), 3), fmt)[:, :cols]
+        if fmt == "e2m1":
+            raw = np.pad(raw, ((0, 0), (0, cols % 2)))
+            raw = raw[:, 0::2] | (raw[:, 1::2] << 4)
+        t = vce.MXTensor.from_parts(torch.from_numpy(raw).to(DEV), torch.full((1, 8), 130, dtype=torch.uint8, device=DEV),
+                                    cols, fmt)
+        for dtype in (torch.float32, torch.bfloat16):
+            got = f64(vce.mx_dequantize(t, dtype))
+            assert np.array_equal(got, want, equal_nan=True), (fmt, dtype)
+            assert np.isnan(got).sum() == (min(2, cols - 254) if fmt == "e4m3" else 0)
+
+
 def test_streams_and_graphs():
     # another stream than the current one, with outputs and workspace allocated by the call;
     # then a captured chain replayed on new inputs

@@ -76,21 +76,25 @@ __device__ __forceinline__ float max_abs(float m, float x) {
     return r;
 }
 
-// Decoding by bits: a code's exponent and mantissa put at the same places of a BF16 are
-// the value times 2^-126 (E2M1, exponent bias 1) or 2^-120 (E4M3, bias 7), subnormals
-// among them.  Two codes (bits 0-3 and 4-7, or 0-7 and 8-15 of ``c``) to a BF16 pair:
+// Two codes (bits 0-3 and 4-7, or 0-7 and 8-15 of ``c``) as FP32 values.
+//   E4M3 by the conversion instruction: every value is one of FP16, and its NaN (which
+// mx_quantize never writes but other sources may) stays one.
+//   E2M1 by bits: a code's exponent and mantissa put at the same places of a BF16 are the
+// value times 2^-126 (exponent bias 1), the subnormal among them; the product is exact.
 template <int kFmt>
-__device__ __forceinline__ uint32_t decode_pair(uint32_t c) {
+__device__ __forceinline__ float2 decode_pair(uint32_t c) {
     if (kFmt == VCE_MX_E2M1) {
         const uint32_t t = (c & 0xfu) | (c & 0xf0u) << 12;
-        return (t & 0x00070007u) << 6 | (t & 0x00080008u) << 12;
+        const uint32_t pair = (t & 0x00070007u) << 6 | (t & 0x00080008u) << 12;
+        return make_float2(__uint_as_float(pair << 16) * 0x1p126f, __uint_as_float(pair & 0xffff0000u) * 0x1p126f);
     }
-    const uint32_t t = (c & 0xffu) | (c & 0xff00u) << 8;
-    return (t & 0x007f007fu) << 4 | (t & 0x00800080u) << 8;
-}
-template <int kFmt>
-__device__ __forceinline__ float decode_factor() {
-    return kFmt == VCE_MX_E2M1 ? 0x1p126f : 0x1p120f;
+    float2 v;
+    asm("{\n\t.reg .b32 h;\n\t.reg .b16 lo, hi;\n\t"
+        "cvt.rn.f16x2.e4m3x2 h, %2;\n\tmov.b32 {lo, hi}, h;\n\t"
+        "cvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
+        : "=f"(v.x), "=f"(v.y)
+        : "h"(uint16_t(c)));
+    return v;
 }
 
 }  // namespace mx

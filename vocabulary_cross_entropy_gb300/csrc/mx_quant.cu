@@ -173,13 +173,12 @@ __global__ void __launch_bounds__(kThreads) mx_dequantize_kernel(const DequantAr
             const float s = mx::scale_value(sb[k]);
             float v[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {  // a BF16 pair of the values times 1 / decode_factor
-                const uint32_t pair =
+            for (int i = 0; i < 4; ++i) {
+                const float2 q =
                     kFmt == VCE_MX_E4M3 ? mx::decode_pair<kFmt>((i < 2 ? c[k].x : c[k].y) >> (16 * (i & 1)) & 0xffffu)
                                         : mx::decode_pair<kFmt>(c[k].x >> (8 * i) & 0xffu);
-                // the first product is exact, the second but for results below 2^-126
-                v[2 * i] = __uint_as_float(pair << 16) * mx::decode_factor<kFmt>() * s;
-                v[2 * i + 1] = __uint_as_float(pair & 0xffff0000u) * mx::decode_factor<kFmt>() * s;
+                v[2 * i] = q.x * s;  // exact but for results below 2^-126
+                v[2 * i + 1] = q.y * s;
             }
             store8(out + col, v);
         }
@@ -210,8 +209,7 @@ __global__ void __launch_bounds__(kThreads) mx_dequantize_odd_kernel(const Dequa
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const int col = (b0 + k) * mx::kBlock + lane;
-            const float q = __uint_as_float(mx::decode_pair<kFmt>(c[k]) << 16) * mx::decode_factor<kFmt>();
-            if (col < cols) store1(out + col, q * mx::scale_value(word >> (8 * k) & 0xffu));
+            if (col < cols) store1(out + col, mx::decode_pair<kFmt>(c[k]).x * mx::scale_value(word >> (8 * k) & 0xffu));
         }
     }
 }
