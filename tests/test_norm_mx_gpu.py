@@ -302,6 +302,34 @@ def test_autograd_uses_of_either_output():
 
 
 @pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("shape", [(64,), (9, 64), (3, 4, 64), (0, 64)])
+def test_rms_norm_outputs_change_in_place(shape, residual):
+    x, w = rand(1, *shape, dtype=torch.float32), rand(2, 64, dtype=torch.float32)
+    res = rand(3, *shape, dtype=torch.float32) if residual else None
+
+    def grads(double):
+        leaves = [None if t is None else t.clone().requires_grad_() for t in (x, w, res)]
+        out = vce.rms_norm(leaves[0], leaves[1], 1e-6, leaves[2])
+        y = out[0] if residual else out
+        double(y).square().sum().backward()
+        return [t.grad for t in leaves if t is not None]
+
+    for a, b in zip(grads(lambda y: y.mul_(2.0)), grads(lambda y: y * 2.0)):
+        assert torch.equal(a, b)
+    if residual:  # h may change too, but not before a backward pass that needs it
+        a, b, c = (t.clone().requires_grad_() for t in (x, w, res))
+        y, h = vce.rms_norm(a, b, 1e-6, c)
+        h.add_(1.0)
+        h.sum().backward()
+        assert torch.equal(a.grad, torch.ones_like(a)) and b.grad is None
+        y, h = vce.rms_norm(a, b, 1e-6, c)
+        h.add_(1.0)
+        if h.numel():
+            with pytest.raises(RuntimeError, match="inplace"):
+                y.sum().backward()
+
+
+@pytest.mark.parametrize("residual", [False, True])
 def test_linear_cross_entropy_with_norm(residual):
     b, sq, h, v = 2, 65, 256, 1000
     x = rand(1, b, sq, h, dtype=torch.bfloat16).contiguous()

@@ -119,24 +119,32 @@ def _accumulators(*tensors):
 class _RMSNorm(torch.autograd.Function):
     # takes and gives back x's own shape: the gradient of x and of the residual is then one
     # tensor with two owners, which autograd copies before it makes it a leaf's .grad (views
-    # made outside would each look like the only owner)
+    # made outside would each look like the only owner).  The outputs are made in that shape
+    # and the library gets views of them: an output that is a view may not be changed in place.
     @staticmethod
     def forward(ctx, x, weight, residual, eps):
-        f = _head.rms_norm_forward(flat_rows(x), weight, eps, None if residual is None else flat_rows(residual))
-        ctx.save_for_backward(f.h, weight, f.rstd)
+        rows = (-1, x.shape[-1])
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        h = None if residual is None else torch.empty_like(y)
+        flat = flat_rows(x)
+        f = _head.rms_norm_forward(flat, weight, eps, None if residual is None else flat_rows(residual),
+                                   h=None if h is None else h.view(rows), y=y.view(rows))
+        # h itself, not a view of it, and x likewise unless its rows had to be copied
+        kept = h if h is not None else x if flat.data_ptr() == x.data_ptr() else flat
+        ctx.save_for_backward(kept, weight, f.rstd)
         ctx.set_materialize_grads(False)
         ctx.with_residual = residual is not None
-        y = f.y.view(x.shape)
-        return (y, f.h.view(x.shape)) if residual is not None else y
+        return y if h is None else (y, h)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy, dh=None):
-        h, weight, rstd = ctx.saved_tensors
         if dy is None:  # only the residual stream was used, or nothing
             dx, dweight = dh, None
         else:
-            dx, dweight = _head.rms_norm_backward(flat_rows(dy), h, weight, rstd, None if dh is None else flat_rows(dh))
+            h, weight, rstd = ctx.saved_tensors
+            dx, dweight = _head.rms_norm_backward(flat_rows(dy), flat_rows(h), weight, rstd,
+                                                  None if dh is None else flat_rows(dh))
             dx = dx.view(dy.shape)
         return dx, dweight, dx if ctx.with_residual else None, None
 
