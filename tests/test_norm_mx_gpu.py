@@ -329,6 +329,14 @@ def test_rms_norm_outputs_change_in_place(shape, residual):
                 y.sum().backward()
 
 
+def test_rms_norm_gradient_has_the_weights_shape():
+    x, w = rand(1, 9, 64, dtype=torch.float32), rand(2, 64, dtype=torch.float32)
+    flat, row = w.clone().requires_grad_(), w[None].clone().requires_grad_()
+    for t in (flat, row):
+        vce.rms_norm(x, t).square().sum().backward()
+    assert row.grad.shape == (1, 64) and torch.equal(row.grad[0], flat.grad)
+
+
 @pytest.mark.parametrize("residual", [False, True])
 def test_linear_cross_entropy_with_norm(residual):
     b, sq, h, v = 2, 65, 256, 1000

@@ -145,7 +145,7 @@ class _RMSNorm(torch.autograd.Function):
             h, weight, rstd = ctx.saved_tensors
             dx, dweight = _head.rms_norm_backward(flat_rows(dy), flat_rows(h), weight, rstd,
                                                   None if dh is None else flat_rows(dh))
-            dx = dx.view(dy.shape)
+            dx, dweight = dx.view(dy.shape), dweight.view(weight.shape)
         return dx, dweight, dx if ctx.with_residual else None, None
 
 
