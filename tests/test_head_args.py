@@ -129,6 +129,33 @@ def test_sample_refusals():
         vce.linear_sample(z, vce.MXTensor.empty(9, 10, "e2m1", "cpu"), u, residual=z)
 
 
+def test_linear_sample_checks_before_it_launches(monkeypatch):
+    from vocabulary_cross_entropy_gb300 import _head
+    x, w = torch.zeros(4, 64), vce.MXTensor.empty(9, 64, "e2m1", "cpu")
+    u = torch.zeros(4)
+
+    class Launched(Exception):
+        pass
+
+    def launched(*args, **kwargs):
+        raise Launched
+
+    for name in ("rms_norm_mx", "mx_quantize"):
+        monkeypatch.setattr(_head, name, launched)
+    for norm in (None, torch.ones(64)):
+        with pytest.raises(Launched):
+            vce.linear_sample(x, w, u, 0.7, 5, torch.ones(4), None, norm_weight=norm)
+        for args, kw in (((x, w, u[:3]), {}), ((x, w, u.double()), {}), ((x, w, u, torch.ones(3)), {}),
+                         ((x, w, u), dict(top_k=torch.ones(4))), ((x, w, u), dict(top_p=torch.ones(4).double())),
+                         ((x, w, u), dict(min_p=torch.ones(4, 2)[:, 0])), ((x, w, u), dict(dev_status=torch.zeros(1))),
+                         ((x[:, :63], w, u), {}), ((x, vce.MXTensor.empty(9, 64, "e4m3", "cpu"), u), {}),
+                         ((x, vce.MXTensor.empty(0, 64, "e2m1", "cpu"), u), {}),
+                         ((x, vce.MXTensor.empty(vce.SAMPLE_MAX_VOCAB + 1, 64, "e2m1", "cpu"), u), {}),
+                         ((x, w._replace(codes=w.codes[:8]), u), {})):
+            with pytest.raises(ValueError):
+                vce.linear_sample(*args, norm_weight=norm, **kw)
+
+
 def test_sampling_definition():
     rng = np.random.default_rng(0)
     z = rng.normal(size=50) * 2

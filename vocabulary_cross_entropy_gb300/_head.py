@@ -346,13 +346,22 @@ def rms_norm_backward(dy, h, weight, rstd, dh=None, *, dx=None, dweight=None, wo
 # sampling
 # ---------------------------------------------------------------------------
 
-def _per_row(value, name, n, dtype, index, device):
-    """A sampling parameter: None, a number for all rows, or a tensor with one entry per row."""
-    if value is None:
-        return None
-    if isinstance(value, torch.Tensor):
-        return _vector(value, name, n, dtype, index)
-    return torch.full((n,), value, dtype=dtype, device=device)
+_PARAMS = (("temperature", torch.float32), ("top_k", torch.int32), ("top_p", torch.float32), ("min_p", torch.float32))
+
+
+def _check_params(uniform, params, n, index):
+    """Checks ``uniform`` and temperature, top_k, top_p, min_p: each None, a number for all rows, or
+    a tensor with one entry per row."""
+    _vector(uniform, "uniform", n, torch.float32, index)
+    for (name, dtype), value in zip(_PARAMS, params):
+        if isinstance(value, torch.Tensor):
+            _vector(value, name, n, dtype, index)
+
+
+def _per_row(params, n, device):
+    """Checked parameters as the library takes them: a number becomes a tensor."""
+    return [value if value is None or isinstance(value, torch.Tensor) else
+            torch.full((n,), value, dtype=dtype, device=device) for (_, dtype), value in zip(_PARAMS, params)]
 
 
 def ce_sample(logits, uniform, temperature=None, top_k=None, top_p=None, min_p=None, *, token=None, logprob=None,
@@ -370,11 +379,8 @@ def ce_sample(logits, uniform, temperature=None, top_k=None, top_p=None, min_p=N
     code = _float_code(logits.dtype, "logits")
     n, vocab, stride = b._rows_view(logits)
     lead = logits.shape[:-1]
-    _vector(uniform, "uniform", n, torch.float32, index)
-    temperature = _per_row(temperature, "temperature", n, torch.float32, index, dev)
-    top_k = _per_row(top_k, "top_k", n, torch.int32, index, dev)
-    top_p = _per_row(top_p, "top_p", n, torch.float32, index, dev)
-    min_p = _per_row(min_p, "min_p", n, torch.float32, index, dev)
+    params = (temperature, top_k, top_p, min_p)
+    _check_params(uniform, params, n, index)
     if token is None:
         token = torch.empty(lead, dtype=torch.int64, device=dev)
     else:
@@ -383,10 +389,10 @@ def ce_sample(logits, uniform, temperature=None, top_k=None, top_p=None, min_p=N
         logprob = torch.empty(lead, dtype=torch.float32, device=dev)
     else:
         _vector(logprob, "logprob", n, torch.float32, index)
-    ptr = b._ptr
+    status = _status(dev_status, index)
+    params = _per_row(params, n, dev)
     _launch("ce_sample", dev, b.library().ce_sample, logits.data_ptr(), code, n, vocab, stride,
-            uniform.data_ptr(), ptr(temperature), ptr(top_k), ptr(top_p), ptr(min_p), token.data_ptr(),
-            logprob.data_ptr(), _status(dev_status, index))
+            uniform.data_ptr(), *map(b._ptr, params), token.data_ptr(), logprob.data_ptr(), status)
     return CESample(token, logprob, dev_status)
 
 
@@ -398,7 +404,18 @@ def linear_sample(embeddings, classifier: MXTensor, uniform, temperature=None, t
     if stream is not None:
         return _under(stream, linear_sample, embeddings, classifier, uniform, temperature, top_k, top_p, min_p,
                       norm_weight=norm_weight, norm_eps=norm_eps, residual=residual, dev_status=dev_status)
-    lead, x = embeddings.shape[:-1], flat_rows(embeddings)
+    lead, h, v, index = embeddings.shape[:-1], embeddings.shape[-1], classifier.rows, embeddings.get_device()
+    n = lead.numel()
+    # what the norm and the quantisation do not check themselves, before either is launched
+    if _check_mx(classifier, "classifier") != MX_E2M1 or classifier.cols != h:
+        raise ValueError(f"classifier must be e2m1 with {h} columns, got {classifier.fmt} with {classifier.cols}")
+    if not 1 <= v <= SAMPLE_MAX_VOCAB:
+        raise ValueError(f"classifier must have 1 to {SAMPLE_MAX_VOCAB} rows, got {v}")
+    if classifier.codes.get_device() != index:
+        raise ValueError("embeddings and classifier are on different devices")
+    _check_params(uniform, (temperature, top_k, top_p, min_p), n, index)
+    _status(dev_status, index)
+    x = flat_rows(embeddings)
     if norm_weight is not None:
         if residual is not None and residual.shape != embeddings.shape:
             raise ValueError("residual must have the shape of embeddings")
@@ -409,7 +426,6 @@ def linear_sample(embeddings, classifier: MXTensor, uniform, temperature=None, t
     else:
         q = mx_quantize(x, "e4m3")
     # rows a multiple of 32 bytes apart: mx_linear stores, and ce_sample loads, whole sectors
-    n, v = q.rows, classifier.rows
     logits = torch.empty(n, -(-v // 8) * 8, dtype=torch.float32, device=x.device)[:, :v]
     mx_linear(q, classifier, torch.float32, out=logits, dev_status=dev_status)
     r = ce_sample(logits, uniform, temperature, top_k, top_p, min_p, dev_status=dev_status)
