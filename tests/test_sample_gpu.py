@@ -248,6 +248,15 @@ def test_parameters_that_filter_nothing():
         assert torch.equal(got.token, first), f
 
 
+def test_numbers_past_their_type():
+    z, u = make(6, 30, 2000, "f32")
+    want = vce.ce_sample(z, u).token
+    for f in (dict(top_k=1 << 40), dict(top_k=float("inf")), dict(top_p=1e39), dict(min_p=-1e39)):
+        assert torch.equal(vce.ce_sample(z, u, **f).token, want), f
+    assert torch.equal(vce.ce_sample(z, u, temperature=1e39).token, vce.ce_sample(z, u, temperature=1e30).token)
+    assert torch.equal(vce.ce_sample(z, u, top_k=50.0).token, vce.ce_sample(z, u, top_k=50).token)
+
+
 @pytest.mark.parametrize("v", [100, 40000])
 @pytest.mark.parametrize("f", [dict(), dict(top_k=10), dict(top_p=0.9), dict(min_p=0.1), dict(temperature=0.0)])
 def test_masks_and_bad_rows(v, f):

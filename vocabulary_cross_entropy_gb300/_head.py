@@ -347,15 +347,27 @@ def rms_norm_backward(dy, h, weight, rstd, dh=None, *, dx=None, dweight=None, wo
 # ---------------------------------------------------------------------------
 
 _PARAMS = (("temperature", torch.float32), ("top_k", torch.int32), ("top_p", torch.float32), ("min_p", torch.float32))
+_I32_MAX, _F32_MAX = 2 ** 31 - 1, torch.finfo(torch.float32).max
 
 
 def _check_params(uniform, params, n, index):
     """Checks ``uniform`` and temperature, top_k, top_p, min_p: each None, a number for all rows, or
-    a tensor with one entry per row."""
+    a tensor with one entry per row.  Returns the four; numbers that their type cannot hold as its
+    largest, which filters as they would."""
     _vector(uniform, "uniform", n, torch.float32, index)
+    checked = []
     for (name, dtype), value in zip(_PARAMS, params):
         if isinstance(value, torch.Tensor):
             _vector(value, name, n, dtype, index)
+        elif value is not None and dtype is torch.int32:
+            value = max(min(value, _I32_MAX), -1)  # (a NaN stays one)
+            if value != value or value != int(value):
+                raise ValueError(f"{name} must be a whole number, got {value}")
+            value = int(value)
+        elif value is not None:
+            value = max(min(value, _F32_MAX), -_F32_MAX)
+        checked.append(value)
+    return checked
 
 
 def _per_row(params, n, device):
@@ -379,8 +391,7 @@ def ce_sample(logits, uniform, temperature=None, top_k=None, top_p=None, min_p=N
     code = _float_code(logits.dtype, "logits")
     n, vocab, stride = b._rows_view(logits)
     lead = logits.shape[:-1]
-    params = (temperature, top_k, top_p, min_p)
-    _check_params(uniform, params, n, index)
+    params = _check_params(uniform, (temperature, top_k, top_p, min_p), n, index)
     if token is None:
         token = torch.empty(lead, dtype=torch.int64, device=dev)
     else:
