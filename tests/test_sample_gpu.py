@@ -397,6 +397,21 @@ def test_linear_sample(n):
     assert none.token.shape == (2, 0)
 
 
+def test_linear_sample_reports_a_status():
+    g = torch.Generator(DEV).manual_seed(2)
+    x = torch.randn(3, 64, device=DEV, generator=g)
+    w = vce.mx_quantize(torch.randn(50, 64, device=DEV, generator=g), "e2m1")
+    u = torch.rand(3, device=DEV, generator=g)
+    r = vce.linear_sample(x, w, u)
+    assert r.dev_status.shape == (1,) and int(r.dev_status) == 0
+    x[1, 3] = float("nan")
+    r = vce.linear_sample(x, w, u, norm_weight=torch.ones(64, device=DEV))
+    assert r.token[1] == -1 and int(r.dev_status) == vce.DEVSTATUS_BAD_ROW
+    mine = torch.full((1,), 64, dtype=torch.int32, device=DEV)
+    r = vce.linear_sample(x, w, u, dev_status=mine)
+    assert r.dev_status is mine and int(mine) == 64 | vce.DEVSTATUS_BAD_ROW
+
+
 def test_rows_past_32_bits():
     n, v = 17000, 128257
     z = torch.zeros(n, v, dtype=torch.bfloat16, device=DEV)

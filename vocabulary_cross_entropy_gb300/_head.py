@@ -215,7 +215,8 @@ def mx_dequantize(t: MXTensor, dtype=torch.bfloat16, *, out=None, dev_status=Non
 
 def mx_linear(x: MXTensor, w: MXTensor, out_dtype=torch.bfloat16, *, out=None, dev_status=None, stream=None):
     """``x @ w.T`` of the values of x (e4m3, [n, h]) and the classifier w (e2m1, [v, h]):
-    logits [n, v] in bfloat16 or float32.  dev_status is None or an int32 [1] tensor."""
+    logits [n, v] in bfloat16 or float32.  Only ``dev_status`` (an int32 [1] tensor, its bits set
+    by the call) tells of a pipeline wait that gave up, after which logits are missing."""
     if stream is not None:
         return _under(stream, mx_linear, x, w, out_dtype, out=out, dev_status=dev_status)
     if (_check_mx(x, "x"), _check_mx(w, "w")) != (MX_E4M3, MX_E2M1):
@@ -411,7 +412,8 @@ def linear_sample(embeddings, classifier: MXTensor, uniform, temperature=None, t
                   norm_weight=None, norm_eps=1e-6, residual=None, dev_status=None, stream=None):
     """The next token after ``embeddings`` [..., H], the counterpart of linear_cross_entropy when a
     model answers: the norm (with ``norm_weight`` [H]; plus ``residual``) in 8 bits, the product
-    with the 4-bit ``classifier``, and ce_sample of the logits.  Returns ce_sample's results."""
+    with the 4-bit ``classifier``, and ce_sample of the logits.  Returns ce_sample's results, with
+    a zeroed ``dev_status`` of its own where none is passed: mx_linear's bits are in it too."""
     if stream is not None:
         return _under(stream, linear_sample, embeddings, classifier, uniform, temperature, top_k, top_p, min_p,
                       norm_weight=norm_weight, norm_eps=norm_eps, residual=residual, dev_status=dev_status)
@@ -425,17 +427,20 @@ def linear_sample(embeddings, classifier: MXTensor, uniform, temperature=None, t
     if classifier.codes.get_device() != index:
         raise ValueError("embeddings and classifier are on different devices")
     _check_params(uniform, (temperature, top_k, top_p, min_p), n, index)
-    _status(dev_status, index)
+    if dev_status is None:
+        dev_status = torch.zeros(1, dtype=torch.int32, device=embeddings.device)
+    else:
+        _status(dev_status, index)
     x = flat_rows(embeddings)
     if norm_weight is not None:
         if residual is not None and residual.shape != embeddings.shape:
             raise ValueError("residual must have the shape of embeddings")
         res = None if residual is None else flat_rows(residual)
-        q = rms_norm_mx(x, norm_weight, norm_eps, res).y
+        q = rms_norm_mx(x, norm_weight, norm_eps, res, dev_status=dev_status).y
     elif residual is not None:
         raise ValueError("residual is added by the norm: it needs norm_weight")
     else:
-        q = mx_quantize(x, "e4m3")
+        q = mx_quantize(x, "e4m3", dev_status=dev_status)
     # rows a multiple of 32 bytes apart: mx_linear stores, and ce_sample loads, whole sectors
     logits = torch.empty(n, -(-v // 8) * 8, dtype=torch.float32, device=x.device)[:, :v]
     mx_linear(q, classifier, torch.float32, out=logits, dev_status=dev_status)
