@@ -140,7 +140,7 @@ def test_linear_sample_checks_before_it_launches(monkeypatch):
     def launched(*args, **kwargs):
         raise Launched
 
-    for name in ("rms_norm_mx", "mx_quantize"):
+    for name in ("rms_norm_mx", "mx_quantize", "flat_rows"):
         monkeypatch.setattr(_head, name, launched)
     for norm in (None, torch.ones(64)):
         with pytest.raises(Launched):
@@ -151,7 +151,7 @@ def test_linear_sample_checks_before_it_launches(monkeypatch):
                          ((x[:, :63], w, u), {}), ((x, vce.MXTensor.empty(9, 64, "e4m3", "cpu"), u), {}),
                          ((x, vce.MXTensor.empty(0, 64, "e2m1", "cpu"), u), {}),
                          ((x, vce.MXTensor.empty(vce.SAMPLE_MAX_VOCAB + 1, 64, "e2m1", "cpu"), u), {}),
-                         ((x, w._replace(codes=w.codes[:8]), u), {})):
+                         ((x, w._replace(codes=w.codes[:8]), u), {}), ((x, w, u), dict(residual=x[:3]))):
             with pytest.raises(ValueError):
                 vce.linear_sample(*args, norm_weight=norm, **kw)
 

@@ -427,18 +427,17 @@ def linear_sample(embeddings, classifier: MXTensor, uniform, temperature=None, t
     if classifier.codes.get_device() != index:
         raise ValueError("embeddings and classifier are on different devices")
     _check_params(uniform, (temperature, top_k, top_p, min_p), n, index)
+    _status(dev_status, index)
+    if residual is not None and norm_weight is None:
+        raise ValueError("residual is added by the norm: it needs norm_weight")
+    if residual is not None and residual.shape != embeddings.shape:
+        raise ValueError("residual must have the shape of embeddings")
     if dev_status is None:
         dev_status = torch.zeros(1, dtype=torch.int32, device=embeddings.device)
-    else:
-        _status(dev_status, index)
     x = flat_rows(embeddings)
     if norm_weight is not None:
-        if residual is not None and residual.shape != embeddings.shape:
-            raise ValueError("residual must have the shape of embeddings")
         res = None if residual is None else flat_rows(residual)
         q = rms_norm_mx(x, norm_weight, norm_eps, res, dev_status=dev_status).y
-    elif residual is not None:
-        raise ValueError("residual is added by the norm: it needs norm_weight")
     else:
         q = mx_quantize(x, "e4m3", dev_status=dev_status)
     # rows a multiple of 32 bytes apart: mx_linear stores, and ce_sample loads, whole sectors
