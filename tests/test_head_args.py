@@ -171,6 +171,21 @@ def test_sampling_numbers():
     assert np.isnan(_check_params(u, (float("nan"), None, None, None), 4, -1)[0])
 
 
+def test_stream_of_another_device():
+    class Stream:
+        device = torch.device("cuda", 1)
+        cuda_stream = 0
+
+    x, w, s = torch.zeros(4, 64), torch.ones(64), Stream()
+    q, c = vce.MXTensor.empty(4, 64, "e4m3", "cpu"), vce.MXTensor.empty(9, 64, "e2m1", "cpu")
+    for fn, args in ((vce.mx_quantize, (x,)), (vce.mx_dequantize, (q,)), (vce.mx_linear, (q, c)),
+                     (vce.rms_norm_forward, (x, w)), (vce.rms_norm_mx, (x, w)),
+                     (vce.rms_norm_backward, (x, x, w, w[:4])), (vce.ce_sample, (x, w[:4])),
+                     (vce.linear_sample, (x, c, w[:4]))):
+        with pytest.raises(ValueError, match="stream is on cuda:1"):
+            fn(*args, stream=s)
+
+
 def test_sampling_definition():
     rng = np.random.default_rng(0)
     z = rng.normal(size=50) * 2

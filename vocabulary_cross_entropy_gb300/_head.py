@@ -27,9 +27,13 @@ CESample = namedtuple("CESample", "token logprob dev_status")
 _CODES = {torch.bfloat16: b.BF16, torch.float32: b.F32}
 
 
-def _under(stream, fn, *args, **kwargs):
+def _under(stream, fn, first, *args, **kwargs):
+    """fn with ``stream``, a stream of its first argument's device, current."""
+    device = first[0].device if isinstance(first, tuple) else first.device
+    if stream.device != device:  # its own current stream would be used instead
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
     with torch.cuda.stream(stream):
-        return fn(*args, **kwargs)
+        return fn(first, *args, **kwargs)
 
 
 def _float_code(dtype, name):
