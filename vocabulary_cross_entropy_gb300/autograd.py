@@ -175,6 +175,12 @@ def linear_cross_entropy(embeddings, classifier, labels, ignore_index: int = -10
     ``return_entropy`` the per-token entropy of the softmax is returned as well.  With
     ``norm_weight`` [H] the classifier takes rms_norm(embeddings, norm_weight, norm_eps,
     residual): the last norm of a model, whose gradients are part of the backward pass.
+
+    To capture forward and backward in a CUDA graph, first drop every earlier result computed
+    from the same parameters on the default stream: torch cannot capture a backward pass beside
+    one, and its failure can end the process.  (rms_norm, the norm here included, refuses such a
+    capture for its own leaves; to look for the classifier's would add half again to the time
+    of a small call.)
     """
     if norm_weight is not None:
         out = rms_norm(embeddings, norm_weight, norm_eps, residual)
