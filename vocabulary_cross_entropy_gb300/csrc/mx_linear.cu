@@ -26,6 +26,7 @@
 
 #include "head_internal.cuh"
 #include "mx_format.cuh"
+#include "mx_plan.h"
 #include "sm100_ptx.cuh"
 
 #include <cudaTypedefs.h>
@@ -36,9 +37,9 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kTokens = 128;                    // tokens per tile
+constexpr int kTokens = mx::kLinearTokens;      // per tile
 constexpr int kK = 128;                         // columns per stage: one 128-byte swizzle row
-constexpr int kRows = 256;                      // classifier rows per tile; the last tiles may have half
+constexpr int kRows = mx::kLinearRows;          // of the classifier per tile; the last tiles may have half
 constexpr uint32_t kWBytes = kRows * kK;        // as the tensor core reads them: half is padding
 constexpr int kFirstEpilogue = 4;               // warp; a multiple of 4, as lane quadrants go by warp % 4
 constexpr int kEpilogueWarps = 8;               // four per 128 columns
@@ -740,32 +741,11 @@ vce_status launch(const void* xc, const void* wc, LinearArgs a, cudaStream_t s, 
 
 template <typename Out>
 vce_status dispatch(const void* xc, const void* wc, LinearArgs a, cudaStream_t s, const DeviceInfo& dev) {
-    a.tiles_n = int((a.n + kTokens - 1) / kTokens);
     const int64_t at = int64_t(reinterpret_cast<uintptr_t>(a.out)) | a.out_stride * int64_t(sizeof(Out));
     a.wide = at % 32 == 0 ? 2 : at % 16 == 0 ? 1 : 0;
-    // Tiles go to the SMs in rounds.  What the last, partial round would hold is cut into
-    // tiles of half the rows where those still fit one round: half a round instead of one.
-    const int64_t all = (a.v + kRows - 1) / kRows, sms = dev.num_sms;
-    const int64_t whole = all * a.tiles_n / sms * sms / a.tiles_n;  // tiles of rows in full rounds
-    const int64_t halves = (a.v - whole * kRows + 127) / 128;
-    const bool cut = whole < all && halves * a.tiles_n <= sms;
-    a.whole_v = int(cut ? whole : all);
-    a.tiles_v = int(cut ? whole + halves : all);
-    // Pairs of CTAs where they need less time: a round of theirs takes 0.93 of a round of single
-    // CTAs, their start as long as five stages more; but they have tiles of 256 tokens and no
-    // half tiles.  At 4096 x 128256, single / pairs (before the stores of 32 bytes): 256 tokens 103 /
-    // 95 us, 384 139 / 169, 512 185 / 176, 640 234 / 255, 1024 369 / 341, 2048 712 / 654.
-    // (They address scale tiles by 32-bit rows.)
-    const int64_t pair_n = (a.n + 2 * kTokens - 1) / (2 * kTokens), pair_tiles = pair_n * all, pairs = sms / 2;
-    const double single = cut ? double(whole * a.tiles_n / sms) + 0.5
-                              : double((all * a.tiles_n + sms - 1) / sms);
-    const double paired = 0.93 * double((pair_tiles + pairs - 1) / pairs) + 5.0 / a.k_tiles;
-    const int64_t scale_rows = 2 * int64_t(a.k_tiles) * ((a.n > a.v ? a.n : a.v) / 128 + 4);
-    if (a.n > kTokens && paired < single && pair_tiles < 0x7fffffff && scale_rows < 0x7fffffff) {
-        a.tiles_n = int(pair_n);
-        a.tiles_v = a.whole_v = int(all);
-        return launch_pair<Out>(xc, wc, a, s, dev);
-    }
+    const mx::LinearPlan p = mx::plan_linear(a.n, a.v, a.k_tiles, dev.num_sms);
+    a.tiles_n = int(p.tiles_n), a.tiles_v = int(p.tiles_v), a.whole_v = int(p.whole_v);
+    if (p.pairs) return launch_pair<Out>(xc, wc, a, s, dev);
     if (a.n <= 16) return launch<16, Out>(xc, wc, a, s, dev);
     if (a.n <= 64) return launch<64, Out>(xc, wc, a, s, dev);
     return launch<128, Out>(xc, wc, a, s, dev);
