@@ -157,18 +157,18 @@ def test_linear_sample_checks_before_it_launches(monkeypatch):
 
 
 def test_sampling_numbers():
-    from vocabulary_cross_entropy_gb300._head import _F32_MAX, _check_params
+    from vocabulary_cross_entropy_gb300._head import _F32_MAX, _params
     u = torch.zeros(4)
     for k in (0.5, 49.9, float("nan")):
         with pytest.raises(ValueError, match="whole"):
             vce.ce_sample(torch.zeros(4, 10), u, top_k=k)
     inf = float("inf")
     for given, taken in ((50, 50), (50.0, 50), (-7, -1), (1 << 40, (1 << 31) - 1), (inf, (1 << 31) - 1)):
-        k = _check_params(u, (None, given, None, None), 4, -1)[1]
+        k = _params(u, None, given, None, None, 4, -1)[1]
         assert k == taken and isinstance(k, int)
     for given, taken in ((0.7, 0.7), (1e39, _F32_MAX), (inf, _F32_MAX), (-inf, -_F32_MAX)):
-        assert _check_params(u, (given, None, given, given), 4, -1) == [taken, None, taken, taken]
-    assert np.isnan(_check_params(u, (float("nan"), None, None, None), 4, -1)[0])
+        assert _params(u, given, None, given, given, 4, -1) == (taken, None, taken, taken)
+    assert np.isnan(_params(u, float("nan"), None, None, None, 4, -1)[0])
 
 
 def test_stream_of_another_device():

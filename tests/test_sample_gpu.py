@@ -254,6 +254,8 @@ def test_numbers_past_their_type():
     for f in (dict(top_k=1 << 40), dict(top_k=float("inf")), dict(top_p=1e39), dict(min_p=-1e39)):
         assert torch.equal(vce.ce_sample(z, u, **f).token, want), f
     assert torch.equal(vce.ce_sample(z, u, temperature=1e39).token, vce.ce_sample(z, u, temperature=1e30).token)
+    ones = torch.ones(30, device=DEV)  # numbers of one value for parameters of two types
+    assert torch.equal(vce.ce_sample(z, u, 1, 1, 1, 1).token, vce.ce_sample(z, u, ones, ones.int(), ones, ones).token)
     assert torch.equal(vce.ce_sample(z, u, top_k=50.0).token, vce.ce_sample(z, u, top_k=50).token)
 
 

@@ -351,34 +351,45 @@ def rms_norm_backward(dy, h, weight, rstd, dh=None, *, dx=None, dweight=None, wo
 # sampling
 # ---------------------------------------------------------------------------
 
-_PARAMS = (("temperature", torch.float32), ("top_k", torch.int32), ("top_p", torch.float32), ("min_p", torch.float32))
 _I32_MAX, _F32_MAX = 2 ** 31 - 1, torch.finfo(torch.float32).max
 
 
-def _check_params(uniform, params, n, index):
-    """Checks ``uniform`` and temperature, top_k, top_p, min_p: each None, a number for all rows, or
-    a tensor with one entry per row.  Returns the four; numbers that their type cannot hold as its
-    largest, which filters as they would."""
+def _param(value, name, n, dtype, index):
+    """A sampling parameter, checked: None, a tensor with one entry per row, or a number for all rows
+    (one that ``dtype`` cannot hold becomes its largest, which filters as it would)."""
+    if value is None:
+        return None
+    if isinstance(value, torch.Tensor):
+        return _vector(value, name, n, dtype, index)
+    if dtype is torch.float32:
+        return max(min(value, _F32_MAX), -_F32_MAX)  # (a NaN stays one)
+    value = max(min(value, _I32_MAX), -1)
+    if value != value or value != int(value):
+        raise ValueError(f"{name} must be a whole number, got {value}")
+    return int(value)
+
+
+def _params(uniform, temperature, top_k, top_p, min_p, n, index):
+    """Checks ``uniform`` and the four parameters; returns the latter."""
     _vector(uniform, "uniform", n, torch.float32, index)
-    checked = []
-    for (name, dtype), value in zip(_PARAMS, params):
-        if isinstance(value, torch.Tensor):
-            _vector(value, name, n, dtype, index)
-        elif value is not None and dtype is torch.int32:
-            value = max(min(value, _I32_MAX), -1)  # (a NaN stays one)
-            if value != value or value != int(value):
-                raise ValueError(f"{name} must be a whole number, got {value}")
-            value = int(value)
-        elif value is not None:
-            value = max(min(value, _F32_MAX), -_F32_MAX)
-        checked.append(value)
-    return checked
+    return (_param(temperature, "temperature", n, torch.float32, index), _param(top_k, "top_k", n, torch.int32, index),
+            _param(top_p, "top_p", n, torch.float32, index), _param(min_p, "min_p", n, torch.float32, index))
 
 
-def _per_row(params, n, device):
-    """Checked parameters as the library takes them: a number becomes a tensor."""
-    return [value if value is None or isinstance(value, torch.Tensor) else
-            torch.full((n,), value, dtype=dtype, device=device) for (_, dtype), value in zip(_PARAMS, params)]
+def _per_row(value, n, dtype, device):
+    return value if value is None or isinstance(value, torch.Tensor) else \
+        torch.full((n,), value, dtype=dtype, device=device)
+
+
+def _sample(logits, code, n, vocab, stride, uniform, params, token, logprob, status):
+    """The library's call, all arguments checked; numbers among ``params`` become tensors."""
+    dev, f32 = logits.device, torch.float32
+    temperature, top_k, top_p, min_p = params
+    t, k = _per_row(temperature, n, f32, dev), _per_row(top_k, n, torch.int32, dev)
+    p, m = _per_row(top_p, n, f32, dev), _per_row(min_p, n, f32, dev)
+    ptr = b._ptr
+    _launch("ce_sample", dev, b.library().ce_sample, logits.data_ptr(), code, n, vocab, stride,
+            uniform.data_ptr(), ptr(t), ptr(k), ptr(p), ptr(m), token.data_ptr(), logprob.data_ptr(), status)
 
 
 def ce_sample(logits, uniform, temperature=None, top_k=None, top_p=None, min_p=None, *, token=None, logprob=None,
@@ -396,7 +407,7 @@ def ce_sample(logits, uniform, temperature=None, top_k=None, top_p=None, min_p=N
     code = _float_code(logits.dtype, "logits")
     n, vocab, stride = b._rows_view(logits)
     lead = logits.shape[:-1]
-    params = _check_params(uniform, (temperature, top_k, top_p, min_p), n, index)
+    params = _params(uniform, temperature, top_k, top_p, min_p, n, index)
     if token is None:
         token = torch.empty(lead, dtype=torch.int64, device=dev)
     else:
@@ -405,10 +416,7 @@ def ce_sample(logits, uniform, temperature=None, top_k=None, top_p=None, min_p=N
         logprob = torch.empty(lead, dtype=torch.float32, device=dev)
     else:
         _vector(logprob, "logprob", n, torch.float32, index)
-    status = _status(dev_status, index)
-    params = _per_row(params, n, dev)
-    _launch("ce_sample", dev, b.library().ce_sample, logits.data_ptr(), code, n, vocab, stride,
-            uniform.data_ptr(), *map(b._ptr, params), token.data_ptr(), logprob.data_ptr(), status)
+    _sample(logits, code, n, vocab, stride, uniform, params, token, logprob, _status(dev_status, index))
     return CESample(token, logprob, dev_status)
 
 
@@ -430,7 +438,7 @@ def linear_sample(embeddings, classifier: MXTensor, uniform, temperature=None, t
         raise ValueError(f"classifier must have 1 to {SAMPLE_MAX_VOCAB} rows, got {v}")
     if classifier.codes.get_device() != index:
         raise ValueError("embeddings and classifier are on different devices")
-    _check_params(uniform, (temperature, top_k, top_p, min_p), n, index)
+    params = _params(uniform, temperature, top_k, top_p, min_p, n, index)
     _status(dev_status, index)
     if residual is not None and norm_weight is None:
         raise ValueError("residual is added by the norm: it needs norm_weight")
@@ -445,7 +453,9 @@ def linear_sample(embeddings, classifier: MXTensor, uniform, temperature=None, t
     else:
         q = mx_quantize(x, "e4m3", dev_status=dev_status)
     # rows a multiple of 32 bytes apart: mx_linear stores, and ce_sample loads, whole sectors
-    logits = torch.empty(n, -(-v // 8) * 8, dtype=torch.float32, device=x.device)[:, :v]
-    mx_linear(q, classifier, torch.float32, out=logits, dev_status=dev_status)
-    r = ce_sample(logits, uniform, temperature, top_k, top_p, min_p, dev_status=dev_status)
-    return CESample(r.token.view(lead), r.logprob.view(lead), dev_status)
+    logits = torch.empty(n, -(-v // 8) * 8, dtype=torch.float32, device=x.device)
+    mx_linear(q, classifier, torch.float32, out=logits[:, :v], dev_status=dev_status)
+    token = torch.empty(lead, dtype=torch.int64, device=x.device)
+    logprob = torch.empty(lead, dtype=torch.float32, device=x.device)
+    _sample(logits, b.F32, n, v, logits.shape[1], uniform, params, token, logprob, dev_status.data_ptr())
+    return CESample(token, logprob, dev_status)
