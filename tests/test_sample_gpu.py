@@ -222,6 +222,27 @@ def test_uniform_of_one_among_least_weights(n, v):
         assert (vce.ce_sample(z, torch.full((n,), u, device=DEV)).token == v - 1).all()
 
 
+@pytest.mark.parametrize("n,v", [(1, 700), (300, 700), (1, 9000), (300, 9000)])
+def test_uniform_of_one_counts_tokens_near_the_least_weight(n, v):
+    # 0.55 to 1.6 units each, many of them equal or nearly so: no sum of theirs, rounded together
+    # or one by one, tells which is the last
+    g = torch.Generator(DEV).manual_seed(v + n)
+    z = (-44.8 + 1.5 * (torch.rand(n, v, device=DEV, generator=g) * 20).floor() / 20) * float(np.log(2))
+    z[:, v // 3] = 0.0
+    k = (2 + (v - 2) * torch.rand(n, device=DEV, generator=g)).int()
+    m = torch.full((n,), 1.5 * 2.0 ** -44, device=DEV)
+    for dtype in (torch.float32, torch.bfloat16):
+        zz = z.to(dtype)
+        for u in (1.0, 1.5):
+            uu = torch.full((n,), u, device=DEV)
+            assert torch.equal(vce.ce_sample(zz, uu).token, last_kept(zz))
+            if v > 700:  # (shorter heads are collected as a whole)
+                k = k.clamp(min=257)
+            assert torch.equal(vce.ce_sample(zz, uu, top_k=k).token, last_kept(zz, top_k=k))
+            # one and a half units: where whole units and weights agree on what is kept
+            assert torch.equal(vce.ce_sample(zz, uu, min_p=m).token, last_kept(zz, min_p=m))
+
+
 @pytest.mark.parametrize("n,v", [(1, 1500), (1, 5000), (200, 1500), (200, 5000), (1, 1 << 20)])
 def test_least_weights_are_never_drawn(n, v):
     # 0.4 units of the least weight each: below the border, however many there are

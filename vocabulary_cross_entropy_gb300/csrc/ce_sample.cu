@@ -102,7 +102,7 @@ struct Wanted {
 
 struct Shared {
     uint64_t mass[kBins];  // words of low and then of high halves, then the sum of s, then (block 0) prefix sums of masses
-    uint32_t count[kBins];  // for top-k; the first kFineBins always
+    uint32_t count[kBins];  // for top-k and the last kept; the first kFineBins always
     uint64_t list[kCap];   // collected keys; masses of sub-bins
     uint64_t sums[kCap];   // inclusive prefix sums of the sorted list; counts of sub-bins
     uint64_t table[kSteps];
@@ -114,9 +114,11 @@ struct Shared {
     Command cmd[2];  // by block 0; consecutive commands take turns: a late reader finds its own intact
     uint32_t part_n[kMaxCluster];  // block 0's: what the others have collected
     uint64_t min_key, max_key;
-    uint64_t kept_minp[kEdgeBins];  // sums of the weights that min-p keeps, per bin
+    uint64_t kept_minp[kEdgeBins];  // sums of the weights that min-p keeps, per bin, and
+    uint32_t kept_n[kEdgeBins];     // how many they are
     float my_bound;
     uint32_t n_list, found, argmax;
+    uint32_t n_kept, n_above;  // block 0's: tokens that top-k and top-p keep, and min-p
 };
 
 __device__ __forceinline__ float max_nan(float a, float b) {  // a NaN stays
@@ -704,6 +706,9 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
     const bool by_k = top_k > 0 && top_k < a.vocab;
     const bool by_p = top_p < 1.f;
     const bool by_min = min_p > 0.f;
+    // the last kept token, whose place is counted: sums of weights near the unit, rounded
+    // together or one by one, do not tell the last of several apart
+    const bool by_last = u >= 1.f;
 
     // ---- the largest logit, and the largest of every thread's elements ----
     // A NaN stays the largest, so one look at the end finds it (and a +inf).
@@ -808,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
             for (int i = tid; i < kBins; i += kThreads) sh.mass[i] = 0, sh.count[i] = 0;
             // min-p (with top-p): whole bins above the border, and single weights next to it
             const int edge = by_min ? max(0, bin_of(fmaxf(a.least_log2, log2f(min_p))) - 2) : kBins;
-            if (tid < kEdgeBins) sh.kept_minp[tid] = 0;
+            if (tid < kEdgeBins) sh.kept_minp[tid] = 0, sh.kept_n[tid] = 0;
             __syncthreads();
             uint32_t* const words = reinterpret_cast<uint32_t*>(sh.mass);  // low halves, then high ones
             for_pairs<1, 1>(s.part, a.dev_status, [&](float z0, float z1, int) {
@@ -823,7 +828,7 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
                     const uint32_t x = fine ? st.s[k] : coarse;
                     atomicAdd(words + bin, x & ((1u << kHalfBits) - 1));
                     atomicAdd(words + kBins + bin, x >> kHalfBits);
-                    if (fine || by_k) atomicAdd(&sh.count[bin], 1u);
+                    if (fine || by_k || by_last) atomicAdd(&sh.count[bin], 1u);
                 }
             });
             __syncthreads();
@@ -851,7 +856,9 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
                     const int k = bin_of(p) - edge;
                     if (!(p > a.least_log2) || k < 0 || k >= kEdgeBins) return;
                     const uint64_t x = weight_of(sc, z, sh.table, a.q_bits);
-                    if (x >= least) s.add_mass(&sh.kept_minp[k], x);
+                    if (x < least) return;
+                    s.add_mass(&sh.kept_minp[k], x);
+                    if (by_last) atomicAdd(&sh.kept_n[k], 1u);
                 });
             }
             s.barrier();
@@ -881,17 +888,23 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
                     const uint64_t sum = sh.mass[i];
                     return sum ? scale_up(sum, i, sh.table, a.q_bits) : uint64_t(0);
                 });
-                if (by_k) prefix_sums<kPer>(sh.count, kBins, sh.warp_sum, [&](int i) { return sh.count[i]; });
+                if (by_k || by_last) prefix_sums<kPer>(sh.count, kBins, sh.warp_sum, [&](int i) { return sh.count[i]; });
                 mass = sh.mass[kBins - 1];
+                if (tid == 0) sh.n_kept = sh.count[kBins - 1];
                 cmd.flag = by_k && sh.count[kBins - 1] > uint32_t(top_k);  // the k-th has a weight
                 if (by_min) {
                     above = edge ? sh.mass[edge - 1] : 0;
+                    uint32_t n_above = edge ? sh.count[edge - 1] : 0;
                     for (int k = 0; k < kEdgeBins; ++k) {  // the last bin with a kept weight decides
                         uint64_t kept = 0;
-                        for (int c = 0; c < a.cluster; ++c) kept += remote(&sh.kept_minp[k], c);
+                        for (int c = 0; c < a.cluster; ++c) {
+                            kept += remote(&sh.kept_minp[k], c);
+                            n_above += remote(&sh.kept_n[k], c);
+                        }
                         const int bin = edge + k;
                         if (kept) above = min((bin ? sh.mass[bin - 1] : 0) + kept, sh.mass[bin]);
                     }
+                    if (tid == 0) sh.n_above = n_above;
                 }
             }
             if (by_k && !s.tell(cmd).flag) continue;
@@ -904,15 +917,21 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
             if (target == 0) target = 1;
         } else if (step == kDraw) {
             if (by_min && above < mass) mass = above;
-            target = u >= 1.f ? mass : floor_product(fmaxf(u, 0.f), mass, &exact) + 1;
+            if (by_last) {
+                __syncthreads();
+                target = by_min ? min(sh.n_kept, sh.n_above) : sh.n_kept;
+            } else {
+                target = floor_product(fmaxf(u, 0.f), mass, &exact) + 1;
+            }
         }
+        const bool by_count = step == kTopK || (step == kDraw && by_last);
         // ---- the border's bin, told to all ----
         Wanted w{0.f, row_max, heads_min ? fmaxf(a.least_log2, log2f(min_p) - 0.01f) : a.least_log2, cmd};
         w.z_lo = heads_k ? bound : sc.m + (w.p_least - 0.1f) / sc.ch - fabsf(sc.m) * 0x1p-21f;
         if (step != kHeads) {
             if (s.lead()) {
-                cmd.bin = min(step == kTopK ? first_at_least(sh.count, kBins, uint32_t(target))
-                                            : first_at_least(sh.mass, kBins, target),
+                cmd.bin = min(by_count ? first_at_least(sh.count, kBins, uint32_t(target))
+                                       : first_at_least(sh.mass, kBins, target),
                               kBins - 1);
                 if (cmd.bin > 0) base = sh.mass[cmd.bin - 1], base_count = sh.count[cmd.bin - 1];
             }
@@ -936,7 +955,7 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
                     if (n <= kThreads) prefix_sums<1>(sh.sums, n, sh.warp_sum, weight);
                     else prefix_sums<kCap / kThreads>(sh.sums, n, sh.warp_sum, weight);
                     int at;
-                    if (step == kTopK) {
+                    if (by_count) {
                         at = int(target - base_count) - 1;
                     } else {
                         if (step == kHeads) {
@@ -957,7 +976,7 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
                                 n = max(1, int(sh.found));
                             }
                             mass = sh.sums[n - 1];
-                            target = u >= 1.f ? mass : floor_product(fmaxf(u, 0.f), mass, &exact) + 1;
+                            target = by_last ? mass : floor_product(fmaxf(u, 0.f), mass, &exact) + 1;
                         }
                         at = first_at_least(sh.sums, n, target);
                     }
@@ -966,13 +985,16 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
                     weight_drawn = sh.sums[at] - (at ? sh.sums[at - 1] : base);
                     // (never past the border's bin: weights rounded one by one can sum to more than
                     // the bin's, which was rounded once, and the draw would look behind the bin)
-                    if (step == kTopK || step == kTopP) mass = min(sh.sums[at], sh.mass[cmd.bin]);
+                    if (step == kTopK || step == kTopP) {
+                        mass = min(sh.sums[at], sh.mass[cmd.bin]);
+                        if (tid == 0) sh.n_kept = base_count + at + 1;
+                    }
                 }
             }
             cmd = s.tell(cmd);
             if (cmd.flag || step == kHeads) break;
             Sampler<T> copy = s;  // its address is taken there, not here
-            copy.divide(cmd, step == kTopK, target, base, base_count);
+            copy.divide(cmd, by_count, target, base, base_count);
             s.turn = copy.turn;
             w = s.in_bin(cmd);
         }
