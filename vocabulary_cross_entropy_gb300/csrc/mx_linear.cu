@@ -17,7 +17,7 @@
 //
 // Times at 4096 x 128256 with BF16 logits: 8 tokens 53 us, bound by memory (281 MB, 0.79 of
 // the copy rate; the rest is the start of the pipeline and a last round that is half full);
-// 2048 tokens (in CTA pairs) 580 us, 3.7 PFLOP/s, bound by the tensor core, and by the power
+// 2048 tokens (in CTA pairs) 588 us, 3.7 PFLOP/s, bound by the tensor core, and by the power
 // limit where calls follow one another for long.
 //
 // Roles: warp 0 copies both operands and their scales (TMA), warp 1 issues the MMAs, warps
