@@ -435,6 +435,33 @@ def test_linear_sample_reports_a_status():
     assert r.dev_status is mine and int(mine) == 64 | vce.DEVSTATUS_BAD_ROW
 
 
+@pytest.mark.parametrize("n", [1, 40])
+def test_linear_sample_captured(n):
+    # numbers as parameters and a status of the call's own, replayed on other inputs
+    h, v = 192, 3001
+    g = torch.Generator(DEV).manual_seed(n)
+    x, res = (torch.randn(n, h, device=DEV, generator=g).bfloat16() for _ in range(2))
+    w = vce.mx_quantize(torch.randn(v, h, device=DEV, generator=g) * h ** -0.5, "e2m1")
+    u, nw = torch.rand(n, device=DEV, generator=g), torch.full((h,), 3.0, device=DEV)
+
+    def call():
+        return vce.linear_sample(x, w, u, 0.8, 50, 0.9, 0.01, norm_weight=nw, residual=res)
+
+    call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r = call()
+    for k in range(3):
+        x.copy_(torch.randn(n, h, device=DEV, generator=g))
+        u.copy_(torch.rand(n, device=DEV, generator=g))
+        if k == 1:
+            x[0, 0] = float("nan")
+        graph.replay()
+        want = call()
+        assert torch.equal(r.token, want.token) and torch.equal(r.logprob.nan_to_num(7.0), want.logprob.nan_to_num(7.0))
+        assert int(r.dev_status) == int(want.dev_status) == (vce.DEVSTATUS_BAD_ROW if k == 1 else 0)
+
+
 def test_rows_past_32_bits():
     n, v = 17000, 128257
     z = torch.zeros(n, v, dtype=torch.bfloat16, device=DEV)
