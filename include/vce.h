@@ -98,6 +98,9 @@ typedef enum vce_dtype {
  * among the logits, or a NaN parameter); its token is -1. */
 #define VCE_DEVSTATUS_BAD_ROW 8
 
+/* beam_reorder, adapter_linear: an index outside its range; what it names counts as absent. */
+#define VCE_DEVSTATUS_BAD_INDEX 16
+
 /* Formats of microscaled tensors: one power-of-two scale per 32 columns. */
 #define VCE_MX_E4M3 0 /* 8-bit values, at most 448 */
 #define VCE_MX_E2M1 1 /* 4-bit values: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives */
@@ -283,6 +286,82 @@ vce_status ce_sample(const void* logits, int dtype, int64_t n_rows, int64_t voca
                      const float* uniform, const float* temperature, const int32_t* top_k,
                      const float* top_p, const float* min_p, int64_t* token, float* logprob,
                      int* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* beam search                                                              */
+/* ------------------------------------------------------------------------ */
+
+#define VCE_BEAM_MAX_BEAMS 32
+#define VCE_BEAM_MAX_COUNT 64
+
+/* Bytes of workspace ce_beam needs. */
+size_t ce_beam_workspace_size(int64_t batch, int beams, int count);
+
+/*
+ * The next hypotheses of a beam search.  Each of ``batch`` requests has ``beams`` beams: a row
+ * of logits z, a score s (the sum of its tokens' log probabilities) and, where given, a
+ * length l and whether it has ended.  With m = max z,
+ *     a beam that goes on offers every token v, at   c = s + (z_v - m) - log sum_v exp(z_v - m)
+ *                                                    and length l + 1;
+ *     one that has ended offers itself: token ``end``, c = s, length l.
+ * The best ``count`` of a request by c / max(length, 1)^length_penalty are taken, in that
+ * order, the lowest (beam, token) first among equal ones.  (Within a beam that is the order of
+ * the logits.)  Sums and comparisons are FP64 but for the sum of the exponentials, whose error
+ * is a few 1e-9; equal rows give equal sums bit for bit.
+ *
+ *   logits   as in ce_forward, rows request by request, 1 <= vocab <= VCE_SAMPLE_MAX_VOCAB;
+ *            -inf marks a token that is not allowed.
+ *   score    F32 [batch, beams]; -inf marks a beam that offers nothing (a request's first
+ *            step has one live beam).  Its logits, and those of an ended beam, are not read.
+ *   ended    uint8 [batch, beams] (0 or not 0) or NULL: none.
+ *   length   int32 [batch, beams] or NULL (then length_penalty must be 0).
+ *   end      the token that ends a hypothesis, or -1 (then ended must be NULL).
+ *   length_penalty  between -16 and 16; 0 compares scores.
+ *   beams    1 to VCE_BEAM_MAX_BEAMS;  count  1 to VCE_BEAM_MAX_COUNT.
+ *   keep_places  0: hypotheses come in their order.  Not 0 (count must equal beams): the first
+ *            child of every beam is put at its parent's place and the others at the free
+ *            places in their order, so that beam_reorder moves no beam that has a child.
+ *   token, parent  int64 [batch, count]; out_score F32; out_ended uint8 (required when ended is
+ *            given or end >= 0, else may be NULL); out_length int32 (required when length is
+ *            given, else NULL).  out_score, out_ended and out_length may be score, ended and
+ *            length themselves.
+ *   ws       ce_beam_workspace_size bytes, 256-byte aligned.
+ * Where a request offers fewer than ``count`` candidates the rest have token -1, score -inf,
+ * ended 0, and the beam at their own place (modulo beams) as parent, with its length.  A beam
+ * that goes on but whose logits are all -inf or hold a NaN or +inf, and one whose score is
+ * NaN or +inf, offers nothing and sets VCE_DEVSTATUS_BAD_ROW.
+ */
+vce_status ce_beam(const void* logits, int dtype, int64_t batch, int beams, int64_t vocab, int64_t row_stride,
+                   const float* score, const uint8_t* ended, const int32_t* length, int64_t end,
+                   float length_penalty, int count, int keep_places, int64_t* token, int64_t* parent,
+                   float* out_score, uint8_t* out_ended, int32_t* out_length, void* ws, size_t ws_bytes,
+                   int* dev_status, void* stream);
+
+/*
+ * A state of the beams: a row of ``parts`` blocks per beam, each of ``positions`` positions of
+ * position_bytes contiguous bytes one after another.  (Keys of a cache [rows, heads, T, D]:
+ * parts = heads, positions = T, position_bytes = D elements; [rows, T, heads, D]: parts = 1.)
+ * Strides are in bytes; src and dst are device pointers.
+ */
+typedef struct vce_state {
+    const void* src;
+    void* dst; /* src itself (with its strides): in place; otherwise no overlap with any src */
+    int64_t src_row_stride, dst_row_stride;
+    int64_t parts, src_part_stride, dst_part_stride;
+    int64_t positions, position_bytes;
+} vce_state;
+
+/*
+ * dst[b, k] = src[b, parent[b, k]] for every state, rows request by request, for the first
+ * lengths[b] positions (all of them where lengths is NULL); the others stay as they are.
+ *
+ *   states   HOST array of ``count`` states (read before the call returns).
+ *   parent   int64 [batch, beams], as ce_beam writes it.  An entry outside [0, beams) counts as
+ *            the beam itself and sets VCE_DEVSTATUS_BAD_INDEX.
+ *   lengths  int32 [batch] or NULL; below 0 counts as 0, above a state's positions as all.
+ */
+vce_status beam_reorder(const vce_state* states, int count, const int64_t* parent, int64_t batch, int beams,
+                        const int32_t* lengths, int* dev_status, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* linear form (X, W and the gradients are BF16; accumulation is FP32)      */

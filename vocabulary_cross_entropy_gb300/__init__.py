@@ -16,6 +16,7 @@ from ._binding import (  # noqa: F401
     DEVSTATUS_TIMEOUT,
     DEVSTATUS_BOUNDS,
     DEVSTATUS_BAD_ROW,
+    DEVSTATUS_BAD_INDEX,
     DEFAULT_SLAB_BYTES,
     SLAB_UNCAPPED,
     REDUCE_NONE,
@@ -55,5 +56,12 @@ from ._head import (  # noqa: F401,E402
     rms_norm_backward,
     ce_sample,
     linear_sample,
+)
+from ._beam import (  # noqa: F401,E402
+    BEAM_MAX_BEAMS,
+    BEAM_MAX_COUNT,
+    ce_beam_workspace_size,
+    ce_beam,
+    beam_reorder,
 )
 from .autograd import parallel_cross_entropy, linear_cross_entropy, rms_norm  # noqa: F401,E402

@@ -18,6 +18,7 @@ DEVSTATUS_BAD_TARGET = 1
 DEVSTATUS_TIMEOUT = 2
 DEVSTATUS_BOUNDS = 4
 DEVSTATUS_BAD_ROW = 8
+DEVSTATUS_BAD_INDEX = 16
 # max_slab_bytes: 0 selects the library's default cap (VCE_DEFAULT_SLAB_BYTES);
 # SLAB_UNCAPPED lets one dZ slab cover the whole vocabulary
 DEFAULT_SLAB_BYTES = 256 << 20
@@ -104,6 +105,13 @@ def library() -> ctypes.CDLL:
     lib.ce_sample.argtypes = [_c_p, _c_int, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p,
                               _c_p]
     lib.ce_sample.restype = _c_int
+    lib.ce_beam_workspace_size.argtypes = [_c_i64, _c_int, _c_int]
+    lib.ce_beam_workspace_size.restype = _c_size
+    lib.ce_beam.argtypes = [_c_p, _c_int, _c_i64, _c_int, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_i64, _c_f32, _c_int,
+                            _c_int, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_size, _c_p, _c_p]
+    lib.ce_beam.restype = _c_int
+    lib.beam_reorder.argtypes = [_c_p, _c_int, _c_p, _c_i64, _c_int, _c_p, _c_p, _c_p]
+    lib.beam_reorder.restype = _c_int
     lib.vce_selftest_wait_timeout.argtypes = [ctypes.c_uint64, _c_p, _c_p, _c_p]
     lib.vce_selftest_wait_timeout.restype = _c_int
     lib.vce_selftest_lce_forward_timeout.argtypes = [_c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_p, ctypes.c_uint64,

@@ -11,6 +11,16 @@ vce_status launch_ce_sample(const void* logits, int dtype, int64_t n, int64_t vo
                             const float* min_p, int64_t* token, float* logprob, int* dev_status, cudaStream_t s,
                             const DeviceInfo& dev);
 
+// ---- beam search (ce_beam.cu, beam_reorder.cu) ----
+size_t ce_beam_ws_bytes(int64_t rows, int count);
+vce_status launch_ce_beam(const void* logits, int dtype, int64_t batch, int beams, int64_t vocab, int64_t stride,
+                          const float* score, const uint8_t* ended, const int* length, int64_t end, float penalty,
+                          int count, int keep, int64_t* token, int64_t* parent, float* out_score,
+                          uint8_t* out_ended, int* out_length, void* ws, int* dev_status, cudaStream_t s,
+                          const DeviceInfo& dev);
+vce_status launch_beam_reorder(const vce_state* states, int count, const int64_t* parent, int64_t batch, int beams,
+                               const int* lengths, int* dev_status, cudaStream_t s, const DeviceInfo& dev);
+
 // ---- the norm before the classifier (rms_norm.cu) ----
 int rms_norm_parts(int64_t n, int64_t hidden, int num_sms);
 vce_status launch_rms_norm(const void* x, const void* residual, const void* weight, int dtype, int w_dtype,

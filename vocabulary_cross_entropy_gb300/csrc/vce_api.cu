@@ -380,4 +380,65 @@ vce_status ce_sample(const void* logits, int dtype, int64_t n_rows, int64_t voca
                             token, logprob, dev_status, static_cast<cudaStream_t>(stream), dev);
 }
 
+size_t ce_beam_workspace_size(int64_t batch, int beams, int count) {
+    if (batch <= 0 || batch > kMaxRows || beams < 1 || beams > VCE_BEAM_MAX_BEAMS || count < 1 ||
+        count > VCE_BEAM_MAX_COUNT)
+        return 0;
+    return ce_beam_ws_bytes(batch * beams, count);
+}
+
+vce_status ce_beam(const void* logits, int dtype, int64_t batch, int beams, int64_t vocab, int64_t row_stride,
+                   const float* score, const uint8_t* ended, const int32_t* length, int64_t end,
+                   float length_penalty, int count, int keep_places, int64_t* token, int64_t* parent,
+                   float* out_score, uint8_t* out_ended, int32_t* out_length, void* ws, size_t ws_bytes,
+                   int* dev_status, void* stream) {
+    if (!dtype_ok(dtype)) return VCE_ERR_DTYPE;
+    if (batch < 0 || batch > kMaxRows || beams < 1 || beams > VCE_BEAM_MAX_BEAMS || batch * beams > kMaxRows ||
+        vocab < 1 || vocab > VCE_SAMPLE_MAX_VOCAB || row_stride < vocab || count < 1 || count > VCE_BEAM_MAX_COUNT ||
+        (keep_places && count != beams) || end < -1 || end >= vocab || (ended && end < 0) ||
+        !(length_penalty >= -16.f && length_penalty <= 16.f) || (length_penalty != 0.f && !length))
+        return VCE_ERR_INVALID_ARG;
+    if (batch > 0 && (!logits || !score || !token || !parent || !out_score || ((ended || end >= 0) && !out_ended) ||
+                      (length && !out_length)))
+        return VCE_ERR_INVALID_ARG;
+    if (!length && out_length) return VCE_ERR_INVALID_ARG;
+    if (!aligned(logits, elem_size(dtype)) || !aligned(score, 4) || !aligned(length, 4) || !aligned(token, 8) ||
+        !aligned(parent, 8) || !aligned(out_score, 4) || !aligned(out_length, 4) || !aligned(ws, 256))
+        return VCE_ERR_ALIGN;
+    if (batch > 0 && (!ws || ws_bytes < ce_beam_workspace_size(batch, beams, count))) return VCE_ERR_WORKSPACE;
+    DeviceInfo dev;
+    if (vce_status st = current_device(dev)) return st;
+    return launch_ce_beam(logits, dtype, batch, beams, vocab, row_stride, score, ended, length, end, length_penalty,
+                          count, keep_places != 0, token, parent, out_score, out_ended, out_length, ws, dev_status,
+                          static_cast<cudaStream_t>(stream), dev);
+}
+
+vce_status beam_reorder(const vce_state* states, int count, const int64_t* parent, int64_t batch, int beams,
+                        const int32_t* lengths, int* dev_status, void* stream) {
+    constexpr int64_t kMost = int64_t(1) << 46;  // bytes; keeps every product below in 63 bits
+    if (count < 0 || (count > 0 && !states) || batch < 0 || batch > kMaxRows || beams < 1 ||
+        beams > VCE_BEAM_MAX_BEAMS || batch * beams > kMaxRows)
+        return VCE_ERR_INVALID_ARG;
+    for (int i = 0; i < count; ++i) {
+        const vce_state& s = states[i];
+        if (s.parts < 0 || s.positions < 0 || s.position_bytes < 0 || s.parts > kMost || s.positions > kMost ||
+            s.position_bytes > kMost)
+            return VCE_ERR_INVALID_ARG;
+        if (s.parts == 0 || s.positions == 0 || s.position_bytes == 0) continue;
+        if (s.positions > kMost / s.position_bytes || s.positions * s.position_bytes > kMost / s.parts)
+            return VCE_ERR_INVALID_ARG;
+        if (batch > 0 && (!s.src || !s.dst)) return VCE_ERR_INVALID_ARG;
+        for (int64_t stride : {s.src_row_stride, s.dst_row_stride, s.src_part_stride, s.dst_part_stride})
+            if (stride < 0 || stride > kMost) return VCE_ERR_INVALID_ARG;
+        if (s.src == s.dst && (s.src_row_stride != s.dst_row_stride || s.src_part_stride != s.dst_part_stride))
+            return VCE_ERR_INVALID_ARG;
+    }
+    if (batch > 0 && count > 0 && !parent) return VCE_ERR_INVALID_ARG;
+    if (!aligned(parent, 8) || !aligned(lengths, 4)) return VCE_ERR_ALIGN;
+    DeviceInfo dev;
+    if (vce_status st = current_device(dev)) return st;
+    return launch_beam_reorder(states, count, parent, batch, beams, lengths, dev_status,
+                               static_cast<cudaStream_t>(stream), dev);
+}
+
 }  // extern "C"
