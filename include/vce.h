@@ -576,6 +576,42 @@ vce_status mx_linear(const void* x_codes, const void* x_scales, const void* w_co
                      int* dev_status, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* adapters beside a shared projection                                      */
+/* ------------------------------------------------------------------------ */
+
+#define VCE_MAX_ADAPTERS 4096
+#define VCE_MAX_ADAPTER_RANK 128
+
+/* Bytes of workspace adapter_linear needs. */
+size_t adapter_workspace_size(int64_t n, int64_t adapters, int rank);
+
+/*
+ * Low-rank adapters of many requests at once, added to the outputs of a projection that all
+ * of them share (mx_linear's logits, for instance):
+ *     out[n, :] = y[n, :] + scale[i] B[i] (A[i] x[n, :]),   i = index[n].
+ * A token's result depends on its own row and adapter alone, not on its neighbours.  A[i] x is
+ * FP32; the product with B takes 24 bits of it for F32 logits and 16 for BF16 ones, sums
+ * are FP32, and y enters before the one rounding to out's type.
+ *
+ *   y       [n, vocab], BF16 or F32, rows y_stride elements apart.
+ *   x       [n, hidden], BF16 or F32, rows x_stride elements apart; 16-byte aligned, hidden a
+ *           multiple of 8, rows a multiple of 16 bytes apart.
+ *   A       BF16 [adapters, rank, hidden], B BF16 [adapters, vocab, rank]; 16-byte aligned.
+ *           rank is a multiple of 8 up to VCE_MAX_ADAPTER_RANK (adapters of smaller rank are
+ *           padded with zeros), adapters 1 to VCE_MAX_ADAPTERS.
+ *   index   int32 [n]; -1: no adapter.  Any other number outside [0, adapters) counts as -1 and
+ *           sets VCE_DEVSTATUS_BAD_INDEX.
+ *   scale   F32 [adapters] or NULL (1).
+ *   out     like y, rows out_stride apart; y itself (same stride) or without overlap.
+ *   ws      adapter_workspace_size bytes, 256-byte aligned.
+ * Rows of y and out that start at 16-byte boundaries are read and written by 16 bytes.
+ */
+vce_status adapter_linear(const void* y, int y_dtype, int64_t n, int64_t vocab, int64_t y_stride, const void* x,
+                          int x_dtype, int64_t hidden, int64_t x_stride, const void* A, const void* B,
+                          int64_t adapters, int rank, const int32_t* index, const float* scale, void* out,
+                          int64_t out_stride, void* ws, size_t ws_bytes, int* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* diagnostics                                                              */
 /* ------------------------------------------------------------------------ */
 

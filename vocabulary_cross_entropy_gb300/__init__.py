@@ -44,6 +44,8 @@ from ._head import (  # noqa: F401,E402
     MX_E4M3,
     MX_E2M1,
     SAMPLE_MAX_VOCAB,
+    MAX_ADAPTERS,
+    MAX_ADAPTER_RANK,
     MXTensor,
     mx_codes_size,
     mx_scales_size,
@@ -54,6 +56,9 @@ from ._head import (  # noqa: F401,E402
     rms_norm_mx,
     rms_norm_workspace_size,
     rms_norm_backward,
+    Adapters,
+    adapter_workspace_size,
+    adapter_linear,
     ce_sample,
     linear_sample,
 )
@@ -62,6 +67,7 @@ from ._beam import (  # noqa: F401,E402
     BEAM_MAX_COUNT,
     ce_beam_workspace_size,
     ce_beam,
+    linear_beam,
     beam_reorder,
 )
 from .autograd import parallel_cross_entropy, linear_cross_entropy, rms_norm  # noqa: F401,E402

@@ -11,7 +11,8 @@ from functools import lru_cache
 import torch
 
 from . import _binding as b
-from ._head import SAMPLE_MAX_VOCAB, _float_code, _launch, _status, _under, _vector
+from ._head import (SAMPLE_MAX_VOCAB, MXTensor, _check_head, _float_code, _head_logits, _launch, _status, _under,
+                    _vector)
 
 BEAM_MAX_BEAMS, BEAM_MAX_COUNT = 32, 64
 
@@ -53,11 +54,10 @@ def _beam_args(score, ended, length, end, length_penalty, count, keep_places, vo
     return rows // beams, beams, int(count), int(end)
 
 
-def _choose(logits, code, vocab, stride, args, score, ended, length, length_penalty, keep_places, out, workspace, status):
-    """The library's call; the logits and what _beam_args takes have been checked."""
-    dev, index = logits.device, logits.get_device()
-    batch, beams, count, end = args
-    shape, n = (*score.shape[:-1], count), batch * count
+def _outputs(dev, index, args, score, ended, length, out):
+    """The outputs, checked where they are given: token, parent, score, ended, length."""
+    _, beams, count, end = args
+    shape, n = (*score.shape[:-1], count), score.numel() // beams * count
     token, parent, out_score, out_ended, out_length = out
 
     def written(t, name, dtype):
@@ -73,16 +73,23 @@ def _choose(logits, code, vocab, stride, args, score, ended, length, length_pena
         out_length = written(out_length, "out_length", torch.int32)
     elif out_length is not None:
         raise ValueError("out_length is written only when length is given")
+    return token, parent, out_score, out_ended, out_length
+
+
+def _choose(logits, code, vocab, stride, args, score, ended, length, length_penalty, keep_places, out, workspace, status):
+    """The library's call, all arguments checked."""
+    dev = logits.device
+    batch, beams, count, end = args
+    token, parent, out_score, out_ended, out_length = out
     lib, ptr = b.library(), b._ptr
     if workspace is None:
         workspace = torch.empty(max(1, lib.ce_beam_workspace_size(batch, beams, count)), dtype=torch.uint8, device=dev)
-    elif workspace.get_device() != index or not workspace.is_contiguous():
+    elif workspace.get_device() != logits.get_device() or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the logits' device")
     _launch("ce_beam", dev, lib.ce_beam, logits.data_ptr(), code, batch, beams, vocab, stride, score.data_ptr(),
             ptr(ended), ptr(length), end, length_penalty, count, int(bool(keep_places)), token.data_ptr(),
             parent.data_ptr(), out_score.data_ptr(), ptr(out_ended), ptr(out_length), workspace.data_ptr(),
             workspace.numel() * workspace.element_size(), status)
-    return token, parent, out_score, out_ended, out_length
 
 
 def ce_beam(logits, score, *, ended=None, length=None, end=-1, length_penalty=0.0, count=None, keep_places=False,
@@ -114,9 +121,35 @@ def ce_beam(logits, score, *, ended=None, length=None, end=-1, length_penalty=0.
     args = _beam_args(score, ended, length, end, length_penalty, count, keep_places, vocab, index)
     if n != score.numel():
         raise ValueError(f"logits have {n} rows, score {score.numel()} beams")
-    res = _choose(logits, code, vocab, stride, args, score, ended, length, length_penalty, keep_places,
-                  (token, parent, out_score, out_ended, out_length), workspace, _status(dev_status, index))
-    return CEBeam(*res, dev_status)
+    out = _outputs(logits.device, index, args, score, ended, length, (token, parent, out_score, out_ended, out_length))
+    _choose(logits, code, vocab, stride, args, score, ended, length, length_penalty, keep_places, out, workspace,
+            _status(dev_status, index))
+    return CEBeam(*out, dev_status)
+
+
+def linear_beam(embeddings, classifier: MXTensor, score, *, ended=None, length=None, end=-1, length_penalty=0.0,
+                count=None, keep_places=False, norm_weight=None, norm_eps=1e-6, residual=None, adapters=None,
+                adapter_index=None, out_score=None, out_ended=None, out_length=None, dev_status=None, stream=None):
+    """The next hypotheses after ``embeddings`` [..., H], a row per beam: linear_sample's norm, product
+    and adapters, and ce_beam of the logits.  Returns ce_beam's results, with a zeroed ``dev_status``
+    of its own where none is passed: mx_linear's bits are in it too."""
+    if stream is not None:
+        return _under(stream, linear_beam, embeddings, classifier, score, ended=ended, length=length, end=end,
+                      length_penalty=length_penalty, count=count, keep_places=keep_places, norm_weight=norm_weight,
+                      norm_eps=norm_eps, residual=residual, adapters=adapters, adapter_index=adapter_index,
+                      out_score=out_score, out_ended=out_ended, out_length=out_length, dev_status=dev_status)
+    n, v, index = _check_head(embeddings, classifier, norm_weight, residual, adapters, adapter_index, dev_status)
+    args = _beam_args(score, ended, length, end, length_penalty, count, keep_places, v, index)
+    if n != score.numel():
+        raise ValueError(f"embeddings have {n} rows, score {score.numel()} beams")
+    out = _outputs(embeddings.device, index, args, score, ended, length, (None, None, out_score, out_ended, out_length))
+    if dev_status is None:
+        dev_status = torch.zeros(1, dtype=torch.int32, device=embeddings.device)
+    logits = _head_logits(embeddings, classifier, n, v, norm_weight, norm_eps, residual, adapters, adapter_index,
+                          dev_status)
+    _choose(logits, b.F32, v, logits.stride(0), args, score, ended, length, length_penalty, keep_places, out, None,
+            dev_status.data_ptr())
+    return CEBeam(*out, dev_status)
 
 
 # ---------------------------------------------------------------------------

@@ -105,6 +105,11 @@ def library() -> ctypes.CDLL:
     lib.ce_sample.argtypes = [_c_p, _c_int, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p,
                               _c_p]
     lib.ce_sample.restype = _c_int
+    lib.adapter_workspace_size.argtypes = [_c_i64, _c_i64, _c_int]
+    lib.adapter_workspace_size.restype = _c_size
+    lib.adapter_linear.argtypes = [_c_p, _c_int, _c_i64, _c_i64, _c_i64, _c_p, _c_int, _c_i64, _c_i64, _c_p, _c_p,
+                                   _c_i64, _c_int, _c_p, _c_p, _c_p, _c_i64, _c_p, _c_size, _c_p, _c_p]
+    lib.adapter_linear.restype = _c_int
     lib.ce_beam_workspace_size.argtypes = [_c_i64, _c_int, _c_int]
     lib.ce_beam_workspace_size.restype = _c_size
     lib.ce_beam.argtypes = [_c_p, _c_int, _c_i64, _c_int, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_i64, _c_f32, _c_int,

@@ -1,6 +1,6 @@
 """ctypes marshalling for the operators around the vocabulary cross entropy: the norm
-before the classifier, microscaled tensors and their product, and sampling (see
-include/vce.h for what each computes).  As in ``_binding``, torch tensors supply memory
+before the classifier, microscaled tensors and their product, adapters beside it, and
+sampling (see include/vce.h for what each computes).  As in ``_binding``, torch tensors supply memory
 and the current stream.
 
 A call given ``stream`` runs as if that stream were current: what it was not given
@@ -17,6 +17,7 @@ from . import _binding as b
 
 MX_E4M3, MX_E2M1 = 0, 1
 SAMPLE_MAX_VOCAB = 1 << 20
+MAX_ADAPTERS, MAX_ADAPTER_RANK = 4096, 128
 _FMT = {"e4m3": MX_E4M3, "e2m1": MX_E2M1}
 
 RMSNormForward = namedtuple("RMSNormForward", "y h rstd")
@@ -420,42 +421,151 @@ def ce_sample(logits, uniform, temperature=None, top_k=None, top_p=None, min_p=N
     return CESample(token, logprob, dev_status)
 
 
-def linear_sample(embeddings, classifier: MXTensor, uniform, temperature=None, top_k=None, top_p=None, min_p=None, *,
-                  norm_weight=None, norm_eps=1e-6, residual=None, dev_status=None, stream=None):
-    """The next token after ``embeddings`` [..., H], the counterpart of linear_cross_entropy when a
-    model answers: the norm (with ``norm_weight`` [H]; plus ``residual``) in 8 bits, the product
-    with the 4-bit ``classifier``, and ce_sample of the logits.  Returns ce_sample's results, with
-    a zeroed ``dev_status`` of its own where none is passed: mx_linear's bits are in it too."""
+# ---------------------------------------------------------------------------
+# adapters beside a shared projection
+# ---------------------------------------------------------------------------
+
+class Adapters(namedtuple("Adapters", "a b scale")):
+    """Low-rank adapters of a projection: ``a`` bfloat16 [adapters, rank, hidden], ``b`` bfloat16
+    [adapters, vocab, rank] and ``scale`` float32 [adapters] or None."""
+    __slots__ = ()
+
+    def __new__(cls, a, b, scale=None):
+        return super().__new__(cls, a, b, scale)
+
+
+def _check_adapters(a, b_, scale, row, n, hidden, vocab, index):
+    """Checks adapters for ``n`` tokens; returns (adapters, rank)."""
+    if a.dim() != 3 or b_.dim() != 3 or a.dtype is not torch.bfloat16 or b_.dtype is not torch.bfloat16 or \
+            not a.is_contiguous() or not b_.is_contiguous() or a.get_device() != index or b_.get_device() != index:
+        raise ValueError("a [adapters, rank, hidden] and b [adapters, vocab, rank] must be contiguous bfloat16 tensors "
+                         "on the inputs' device")
+    count, rank, h = a.shape
+    if h != hidden or b_.shape != (count, vocab, rank):
+        raise ValueError(f"a must be [adapters, rank, {hidden}] and b [adapters, {vocab}, rank], got {tuple(a.shape)} and "
+                         f"{tuple(b_.shape)}")
+    if not 1 <= count <= MAX_ADAPTERS or not 8 <= rank <= MAX_ADAPTER_RANK or rank % 8 or hidden % 8:
+        raise ValueError(f"1 to {MAX_ADAPTERS} adapters of a rank that is a multiple of 8 up to {MAX_ADAPTER_RANK}, and a "
+                         f"hidden dimension that is one, are needed: got {count}, {rank}, {hidden}")
+    if scale is not None:
+        _vector(scale, "scale", count, torch.float32, index)
+    _vector(row, "index", n, torch.int32, index)
+    return count, rank
+
+
+def adapter_workspace_size(n: int, adapters: int, rank: int) -> int:
+    return int(b.library().adapter_workspace_size(n, adapters, rank))
+
+
+def adapter_linear(y, x, a, b_, index, scale=None, *, out=None, workspace=None, dev_status=None, stream=None):
+    """``y`` [..., V] plus each token's adapter: y + scale[i] B[i] (A[i] x), i = ``index`` (int32, one
+    per token; -1: none), for the outputs y of a projection of ``x`` [..., H] that all tokens
+    share.  y and x are bfloat16 or float32; ``a`` [adapters, rank, H] and ``b_`` [adapters, V,
+    rank] bfloat16, the rank a multiple of 8 up to 128; ``scale`` float32 [adapters] or None.
+    Returns ``out`` (y itself may be given), like y.  An index outside the adapters counts as
+    -1 and sets a bit of ``dev_status`` (int32 [1])."""
     if stream is not None:
-        return _under(stream, linear_sample, embeddings, classifier, uniform, temperature, top_k, top_p, min_p,
-                      norm_weight=norm_weight, norm_eps=norm_eps, residual=residual, dev_status=dev_status)
-    lead, h, v, index = embeddings.shape[:-1], embeddings.shape[-1], classifier.rows, embeddings.get_device()
-    n = lead.numel()
-    # what the norm and the quantisation do not check themselves, before either is launched
+        return _under(stream, adapter_linear, y, x, a, b_, index, scale, out=out, workspace=workspace,
+                      dev_status=dev_status)
+    code, xcode = _float_code(y.dtype, "y"), _float_code(x.dtype, "x")
+    n, vocab, stride = b._rows_view(y)
+    xn, hidden, xs = b._rows_view(x)
+    dev, device = y.device, y.get_device()
+    if xn != n or x.get_device() != device:
+        raise ValueError(f"x must have a row for each of y's {n}, on its device")
+    count, rank = _check_adapters(a, b_, scale, index, n, hidden, vocab, device)
+    if out is None:
+        out, to_stride = torch.empty(y.shape, dtype=y.dtype, device=dev), vocab
+    elif out is y:
+        to_stride = stride
+    else:
+        if out.shape != y.shape or out.dtype is not y.dtype or out.get_device() != device:
+            raise ValueError(f"out must be like y: {y.dtype}, {tuple(y.shape)} on {dev}")
+        to_stride = b._rows_view(out)[2]
+    if to_stride < vocab or stride < vocab or xs < hidden:
+        raise ValueError("the rows of a tensor overlap")
+    lib = b.library()
+    if workspace is None:
+        workspace = torch.empty(max(1, lib.adapter_workspace_size(n, count, rank)), dtype=torch.uint8, device=dev)
+    elif workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+    _launch("adapter_linear", dev, lib.adapter_linear, y.data_ptr(), code, n, vocab, stride, x.data_ptr(), xcode, hidden, xs,
+            a.data_ptr(), b_.data_ptr(), count, rank, index.data_ptr(), b._ptr(scale), out.data_ptr(), to_stride,
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), _status(dev_status, device))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# the whole head
+# ---------------------------------------------------------------------------
+
+def _check_head(embeddings, classifier, norm_weight, residual, adapters, adapter_index, dev_status):
+    """What the norm, the quantisation and the adapters do not check themselves, before any of
+    them is launched; returns (tokens, vocab, the device's index)."""
+    h, v, index = embeddings.shape[-1], classifier.rows, embeddings.get_device()
+    n = embeddings.shape[:-1].numel()
     if _check_mx(classifier, "classifier") != MX_E2M1 or classifier.cols != h:
         raise ValueError(f"classifier must be e2m1 with {h} columns, got {classifier.fmt} with {classifier.cols}")
     if not 1 <= v <= SAMPLE_MAX_VOCAB:
         raise ValueError(f"classifier must have 1 to {SAMPLE_MAX_VOCAB} rows, got {v}")
     if classifier.codes.get_device() != index:
         raise ValueError("embeddings and classifier are on different devices")
-    params = _params(uniform, temperature, top_k, top_p, min_p, n, index)
     _status(dev_status, index)
     if residual is not None and norm_weight is None:
         raise ValueError("residual is added by the norm: it needs norm_weight")
     if residual is not None and residual.shape != embeddings.shape:
         raise ValueError("residual must have the shape of embeddings")
-    if dev_status is None:
-        dev_status = torch.zeros(1, dtype=torch.int32, device=embeddings.device)
+    if (adapters is None) != (adapter_index is None):
+        raise ValueError("adapters and adapter_index belong together")
+    if adapters is not None:
+        _check_adapters(*Adapters(*adapters), adapter_index, n, h, v, index)
+    return n, v, index
+
+
+def _head_logits(embeddings, classifier, n, v, norm_weight, norm_eps, residual, adapters, adapter_index, dev_status):
+    """FP32 logits [n, v] of the head, in rows a multiple of 32 bytes apart: mx_linear stores, and what
+    follows loads, whole sectors.  All arguments are checked."""
     x = flat_rows(embeddings)
     if norm_weight is not None:
         res = None if residual is None else flat_rows(residual)
-        q = rms_norm_mx(x, norm_weight, norm_eps, res, dev_status=dev_status).y
+        norm = rms_norm_mx(x, norm_weight, norm_eps, res, dev_status=dev_status)
+        q, x = norm.y, norm.h
     else:
         q = mx_quantize(x, "e4m3", dev_status=dev_status)
-    # rows a multiple of 32 bytes apart: mx_linear stores, and ce_sample loads, whole sectors
-    logits = torch.empty(n, -(-v // 8) * 8, dtype=torch.float32, device=x.device)
-    mx_linear(q, classifier, torch.float32, out=logits[:, :v], dev_status=dev_status)
-    token = torch.empty(lead, dtype=torch.int64, device=x.device)
-    logprob = torch.empty(lead, dtype=torch.float32, device=x.device)
-    _sample(logits, b.F32, n, v, logits.shape[1], uniform, params, token, logprob, dev_status.data_ptr())
+    logits = torch.empty(n, -(-v // 8) * 8, dtype=torch.float32, device=x.device)[:, :v]
+    mx_linear(q, classifier, torch.float32, out=logits, dev_status=dev_status)
+    if adapters is not None:
+        # adapters take the hidden states unquantised
+        if norm_weight is not None:
+            x = rms_norm_forward(x, norm_weight, norm_eps, dev_status=dev_status).y
+        elif x.data_ptr() % 16 or (n > 1 and x.stride(0) * x.element_size() % 16):
+            x = x.clone(memory_format=torch.contiguous_format)
+        a, b_, scale = Adapters(*adapters)
+        adapter_linear(logits, x, a, b_, adapter_index, scale, out=logits, dev_status=dev_status)
+    return logits
+
+
+def linear_sample(embeddings, classifier: MXTensor, uniform, temperature=None, top_k=None, top_p=None, min_p=None, *,
+                  norm_weight=None, norm_eps=1e-6, residual=None, adapters=None, adapter_index=None, dev_status=None,
+                  stream=None):
+    """The next token after ``embeddings`` [..., H], the counterpart of linear_cross_entropy when a
+    model answers: the norm (with ``norm_weight`` [H]; plus ``residual``) in 8 bits, the product
+    with the 4-bit ``classifier``, and ce_sample of the logits.  ``adapters`` (an Adapters of the
+    classifier) and ``adapter_index`` (int32, one per token) add each token's adapter to its logits.
+    Returns ce_sample's results, with a zeroed ``dev_status`` of its own where none is passed:
+    mx_linear's bits are in it too."""
+    if stream is not None:
+        return _under(stream, linear_sample, embeddings, classifier, uniform, temperature, top_k, top_p, min_p,
+                      norm_weight=norm_weight, norm_eps=norm_eps, residual=residual, adapters=adapters,
+                      adapter_index=adapter_index, dev_status=dev_status)
+    n, v, index = _check_head(embeddings, classifier, norm_weight, residual, adapters, adapter_index, dev_status)
+    params = _params(uniform, temperature, top_k, top_p, min_p, n, index)
+    if dev_status is None:
+        dev_status = torch.zeros(1, dtype=torch.int32, device=embeddings.device)
+    logits = _head_logits(embeddings, classifier, n, v, norm_weight, norm_eps, residual, adapters, adapter_index,
+                          dev_status)
+    lead, dev = embeddings.shape[:-1], logits.device
+    token = torch.empty(lead, dtype=torch.int64, device=dev)
+    logprob = torch.empty(lead, dtype=torch.float32, device=dev)
+    _sample(logits, b.F32, n, v, logits.stride(0), uniform, params, token, logprob, dev_status.data_ptr())
     return CESample(token, logprob, dev_status)

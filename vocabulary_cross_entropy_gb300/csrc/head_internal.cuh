@@ -21,6 +21,13 @@ vce_status launch_ce_beam(const void* logits, int dtype, int64_t batch, int beam
 vce_status launch_beam_reorder(const vce_state* states, int count, const int64_t* parent, int64_t batch, int beams,
                                const int* lengths, int* dev_status, cudaStream_t s, const DeviceInfo& dev);
 
+// ---- adapters beside a shared projection (adapter_linear.cu) ----
+size_t adapter_ws_bytes(int64_t n, int64_t adapters, int rank);
+vce_status launch_adapter_linear(const void* y, int y_dtype, int64_t n, int64_t vocab, int64_t y_stride, const void* x,
+                                 int x_dtype, int64_t hidden, int64_t x_stride, const void* a, const void* b,
+                                 int64_t adapters, int rank, const int* index, const float* scale, void* out,
+                                 int64_t out_stride, void* ws, int* dev_status, cudaStream_t s, const DeviceInfo& dev);
+
 // ---- the norm before the classifier (rms_norm.cu) ----
 int rms_norm_parts(int64_t n, int64_t hidden, int num_sms);
 vce_status launch_rms_norm(const void* x, const void* residual, const void* weight, int dtype, int w_dtype,

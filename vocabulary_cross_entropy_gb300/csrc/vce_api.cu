@@ -66,6 +66,7 @@ bool mx_ok(int fmt) { return fmt == VCE_MX_E4M3 || fmt == VCE_MX_E2M1; }
 // the rows that fill a scale tile), 32-bit columns inside a row.
 constexpr int64_t kMaxRows = 0x7fffff00;
 constexpr int64_t kMaxCols = int64_t(1) << 28;
+constexpr int64_t kMaxTokens = int64_t(1) << 27;  // of adapter_linear, whose grid has eight blocks for each
 
 vce_status check_norm(int dtype, int64_t n, int64_t hidden, const void* x, int64_t x_stride, const void* residual,
                       int64_t residual_stride, const void* weight, int weight_dtype, float eps, const void* h,
@@ -439,6 +440,35 @@ vce_status beam_reorder(const vce_state* states, int count, const int64_t* paren
     if (vce_status st = current_device(dev)) return st;
     return launch_beam_reorder(states, count, parent, batch, beams, lengths, dev_status,
                                static_cast<cudaStream_t>(stream), dev);
+}
+
+size_t adapter_workspace_size(int64_t n, int64_t adapters, int rank) {
+    if (n <= 0 || n > kMaxRows || adapters < 1 || adapters > VCE_MAX_ADAPTERS || rank < 1 || rank > VCE_MAX_ADAPTER_RANK)
+        return 0;
+    return adapter_ws_bytes(n, adapters, rank);
+}
+
+vce_status adapter_linear(const void* y, int y_dtype, int64_t n, int64_t vocab, int64_t y_stride, const void* x,
+                          int x_dtype, int64_t hidden, int64_t x_stride, const void* A, const void* B,
+                          int64_t adapters, int rank, const int32_t* index, const float* scale, void* out,
+                          int64_t out_stride, void* ws, size_t ws_bytes, int* dev_status, void* stream) {
+    if (!dtype_ok(y_dtype) || !dtype_ok(x_dtype)) return VCE_ERR_DTYPE;
+    if (n < 0 || n > kMaxTokens || vocab < 1 || vocab > kMaxCols || y_stride < vocab || out_stride < vocab ||
+        hidden < 1 || hidden > kMaxCols || x_stride < hidden || adapters < 1 || adapters > VCE_MAX_ADAPTERS ||
+        rank < 1 || rank > VCE_MAX_ADAPTER_RANK || rank % 8)
+        return VCE_ERR_INVALID_ARG;
+    if (n > 0 && (!y || !x || !A || !B || !index || !out)) return VCE_ERR_INVALID_ARG;
+    if (out == y && out_stride != y_stride) return VCE_ERR_INVALID_ARG;
+    const int64_t es = int64_t(elem_size(x_dtype));
+    if (!aligned(y, elem_size(y_dtype)) || !aligned(out, elem_size(y_dtype)) || !aligned(x, 16) || !aligned(A, 16) ||
+        !aligned(B, 16) || !aligned(index, 4) || !aligned(scale, 4) || !aligned(ws, 256) || hidden % 8 ||
+        (n > 1 && x_stride * es % 16))
+        return VCE_ERR_ALIGN;
+    if (n > 0 && (!ws || ws_bytes < adapter_workspace_size(n, adapters, rank))) return VCE_ERR_WORKSPACE;
+    DeviceInfo dev;
+    if (vce_status st = current_device(dev)) return st;
+    return launch_adapter_linear(y, y_dtype, n, vocab, y_stride, x, x_dtype, hidden, x_stride, A, B, adapters, rank, index,
+                                 scale, out, out_stride, ws, dev_status, static_cast<cudaStream_t>(stream), dev);
 }
 
 }  // extern "C"
