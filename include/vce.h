@@ -306,8 +306,9 @@ size_t ce_beam_workspace_size(int64_t batch, int beams, int count);
  *     one that has ended offers itself: token ``end``, c = s, length l.
  * The best ``count`` of a request by c / max(length, 1)^length_penalty are taken, in that
  * order, the lowest (beam, token) first among equal ones.  (Within a beam that is the order of
- * the logits.)  Sums and comparisons are FP64 but for the sum of the exponentials, whose error
- * is a few 1e-9; equal rows give equal sums bit for bit.
+ * the logits.)  Sums and comparisons are FP64 but for the sum of the exponentials, whose
+ * logarithm is within 1e-6 at worst and about 2e-8 off, mostly the same for all rows; equal
+ * rows give equal sums bit for bit.
  *
  *   logits   as in ce_forward, rows request by request, 1 <= vocab <= VCE_SAMPLE_MAX_VOCAB;
  *            -inf marks a token that is not allowed.
