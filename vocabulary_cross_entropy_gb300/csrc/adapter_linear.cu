@@ -4,14 +4,15 @@
 // Three kernels.  One sorts the tokens by their adapters, in tiles of at most 64 of one
 // adapter.  The second computes t_n = A_i x_n, a tile shared by a cluster of blocks that
 // divide the hidden dimension.  The third adds s_i B_i t_n to y: it reads each adapter's B
-// once per tile and y once.
+// once per tile and y once.  Each starts while the one before still runs, up to its wait for it.
 //
-// The last one carries the work, and its bytes bound it: a token's 2 r operations per
+// The last one carries the work, and its bytes are the floor: a token's 2 r operations per
 // logit are few beside the logit's read and write (r = 64: 32 per byte, where the memory takes
-// as long as 290).  So the products go through the warp-level tensor instruction with operands
-// straight from global memory to registers: B is used by the warp that loads it alone, and
-// staging it for the block-level instruction would cost a pass through shared memory and
-// tensor memory for each logit.
+// as long as 290).  So the products go through the warp-level tensor instruction, whose results
+// lie in the registers of the lanes that hold the logits; the block-level one would take each logit
+// through tensor memory as well.  There are two forms of it, for few and for many tokens per
+// adapter: adapter_expand_few and adapter_expand_many.  They add the same products in the same order, and
+// a token's result does not depend on which one takes it.
 //
 // Precision.  t is FP32 and is multiplied as a sum of BF16 terms, three (all 24 bits) for FP32
 // logits, two (16 bits: 2^-17 of the adapter's part) for BF16 logits, whose own rounding is
@@ -22,6 +23,7 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 namespace vce {
 namespace {
@@ -34,8 +36,15 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSlices = 8;            // blocks of a cluster that divide the hidden dimension
 constexpr int kRankBlock = 32;        // ranks per block of the second kernel
-constexpr int kVWarp = 32;            // logits per warp and step of the third
-constexpr int kVBlock = kWarps * kVWarp;
+constexpr int kVWarp = 32;            // logits of a warp, and
+constexpr int kVBlock = kWarps * kVWarp;  // of a block of adapter_expand_many
+constexpr int kRun = 512;             // logits of a unit that is handed out, or a multiple
+constexpr int kMaxStages = 6;         // of adapter_expand_few's ring
+constexpr int kRingBytes = 208 << 10;
+constexpr int64_t kMany = 24;         // tokens per adapter from which adapter_expand_many takes them
+constexpr int kMaxBlock = 1024;       // logits of a stage, at most
+constexpr int kStageRows = 32 << 10;  // bytes of y in a stage, and
+constexpr int kStageB = 32 << 10;     // of B
 constexpr int kPlanThreads = 1024;
 constexpr int kMaxAdapters = VCE_MAX_ADAPTERS;
 
@@ -45,6 +54,7 @@ struct Tile {
 
 struct Plan {
     int n_work, n_all;  // tiles with an adapter, and all
+    int next;           // the next unit of work of the third kernel
 };
 
 // ---------------------------------------------------------------------------
@@ -83,6 +93,7 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan(const PlanArgs a) {
     __shared__ int count[kMaxAdapters + 1];  // the last: no adapter; then the places of the next tokens
     __shared__ int2 warp_sum[kPlanThreads / 32];
     const int tid = threadIdx.x;
+    cudaTriggerProgrammaticLaunchCompletion();  // the next kernel starts, up to its wait for this one
     constexpr int kPer = kMaxAdapters / kPlanThreads;
     for (int i = tid; i <= a.adapters; i += kPlanThreads) count[i] = 0;
     __syncthreads();
@@ -114,7 +125,7 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan(const PlanArgs a) {
         at += c[k];
     }
     if (tid == kPlanThreads - 1) {  // the sums of all
-        *a.plan = {upto.y, upto.y + (a.copy ? (none + kTile - 1) / kTile : 0)};
+        *a.plan = {upto.y, upto.y + (a.copy ? (none + kTile - 1) / kTile : 0), 0};
         if (a.copy)
             for (int j = 0; j < none; j += kTile) a.tiles[upto.y + j / kTile] = {-1, upto.x + j, min(kTile, none - j)};
         count[a.adapters] = upto.x;
@@ -140,6 +151,14 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {  // c = the product
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // x as a sum of BF16 terms, exactly where there are three: each term takes the leading bits of
@@ -190,6 +209,7 @@ __global__ void __launch_bounds__(kThreads) adapter_shrink(const ShrinkArgs a) {
     extern __shared__ __align__(16) float red[];  // [warps][tile][kRankBlock]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
     const int slice = int(cluster_ctarank());
+    cudaTriggerProgrammaticLaunchCompletion();
     cudaGridDependencySynchronize();
     const int id = int(blockIdx.x) / kSlices;
     if (id >= a.plan->n_work) return;  // the whole cluster
@@ -294,13 +314,334 @@ struct ExpandArgs {
     const void* y;
     void* out;
     int64_t y_stride, out_stride;
-    int vocab, rank, n;
-    int vectors;  // rows start at 16-byte boundaries
-    const Plan* plan;
+    int vocab, rank;
+    int stages, stage_bytes, y_bytes;  // of the ring; of a stage; of its rows of y
+    int block[4];                      // logits of a stage, by class_of a tile
+    Plan* plan;
     const Tile* tiles;
     const int* perm;
     int* dev_status;
 };
+
+// The first of the four neighbouring ranks that lane q holds in step s of KS.
+template <int KS>
+__device__ __forceinline__ int rank_of(int s, int q) { return KS == 1 ? 4 * q : 32 * (s / 2) + 8 * q + 4 * (s & 1); }
+
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void put(float* p, float x) { *p = x; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+// Four neighbouring logits at an address that is a multiple of their size.
+__device__ __forceinline__ void load4(float (&x)[4], const float* p) {
+    const float4 w = *reinterpret_cast<const float4*>(p);
+    x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
+}
+__device__ __forceinline__ void load4(float (&x)[4], const __nv_bfloat16* p) {
+    const uint2 w = *reinterpret_cast<const uint2*>(p);
+    x[0] = __uint_as_float(w.x << 16), x[1] = __uint_as_float(w.x & 0xffff0000u);
+    x[2] = __uint_as_float(w.y << 16), x[3] = __uint_as_float(w.y & 0xffff0000u);
+}
+__device__ __forceinline__ void store4(float* p, const float (&x)[4]) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&x)[4]) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+// By the logits' type and the steps of 16 ranks: terms of t, and warps that multiply (t's operands stay in
+// registers).
+template <typename Y, int KS>
+struct Shape {
+    static constexpr int kTerms = sizeof(Y) == 2 ? 2 : 3;
+    static constexpr int kWarps = KS * kTerms >= 12 ? 8 : 16;
+};
+
+// Tiles by how many tokens they have: up to 4, 16, 32, 64.
+__host__ __device__ __forceinline__ int class_of(int count) { return count > 32 ? 3 : count > 16 ? 2 : count > 4 ? 1 : 0; }
+
+struct Ring {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    int4 what[kMaxStages];  // tile (-1: the end), first logit, number of logits
+    int abort;
+};
+
+// Tiles of few tokens, or rows that start anywhere.  Logits are the rows of the products (16) and tokens the
+// columns (8): a tile of one token costs no more than one of eight.  A warp takes 16 tokens and 32 logits at a time;
+// what warps the tokens leave divide the logits.  A further warp copies y's rows and B, some logits at a
+// time, through a ring in shared memory.  Units of work are handed out by a counter, the larger ones first: tiles
+// differ by a factor of 64.
+//
+// Rows that start off 16-byte boundaries are copied with what shares their first and last 16 bytes, except
+// at a row's ends, whose odd elements are copied one by one; results go back through shared memory, so
+// that a warp writes neighbours of one row.
+//
+// 64 tokens with 35 adapters of rank 16, 128256 FP32 logits: 47 us (4.3 TB/s), of which the copies alone take
+// 40; the others are the multiplying warps' instructions, about 160 for 32 logits of a token.  257 x 32001
+// BF16 logits (odd rows), 20 adapters of rank 8: 30 us; with a unit of work for each block from the start
+// 41, and with elements loaded one by one 90.
+//
+// What bounds it for larger tiles is its copies, one for each row and stage: 66 cycles each.
+template <typename Y, int KS, bool VEC>
+__global__ void __launch_bounds__(Shape<Y, KS>::kWarps * 32 + 32, 1) adapter_expand_few(const __grid_constant__ ExpandArgs a) {
+    using S = Shape<Y, KS>;
+    constexpr int TERMS = S::kTerms, kMulWarps = S::kWarps, ES = int(sizeof(Y));
+    extern __shared__ __align__(128) uint8_t smem[];  // stages: rows of y, then B
+    __shared__ Ring ring;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
+    if (tid == 0) {
+        for (int i = 0; i < a.stages; ++i) {
+            mbar_init(&ring.full[i], 32);
+            mbar_init(&ring.empty[i], kMulWarps);
+        }
+        fence_mbar_init();
+        ring.abort = 0;
+    }
+    __syncthreads();
+    cudaGridDependencySynchronize();
+    int stage = 0;
+    bool ok = true;
+    if (warp == kMulWarps) {
+        // Unit u: a run of logits of tile tiles - 1 - u / runs (those without an adapter come first).
+        const int tiles = a.plan->n_all;
+        const int run = kRun * int(max(int64_t(1), min(int64_t(16), int64_t(tiles) * a.vocab / (int64_t(gridDim.x) * (3 * kRun)))));
+        const int runs = (a.vocab + run - 1) / run;
+        const int64_t units = int64_t(tiles) * runs;
+        int issued = 0, id = -1, block = 0, pitch = 0;
+        uint32_t parity = 1;  // of the ring's previous round, which the first one need not wait for
+        uintptr_t row[2] = {0, 0};  // this lane's; 0: none
+        Tile tile{};
+        auto take = [&]() { return lane == 0 ? atomicAdd(&a.plan->next, 1) : 0; };
+        int coming = take();
+        for (;;) {
+            const int unit = __shfl_sync(0xffffffffu, coming, 0);
+            const bool end = unit >= units;
+            if (!end) coming = take();
+            if (!end && tiles - 1 - unit / runs != id) {
+                id = tiles - 1 - unit / runs;
+                tile = a.tiles[id];
+                block = a.block[class_of(tile.count)], pitch = block * ES + 32;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int p = lane + 32 * h;
+                    row[h] = p < tile.count ? reinterpret_cast<uintptr_t>(static_cast<const Y*>(a.y) + a.perm[tile.start + p] * a.y_stride) : 0;
+                }
+            }
+            const int v0 = end ? 0 : unit % runs * run, v1 = end ? 1 : min(v0 + run, a.vocab);
+            for (int v = v0; v < v1; v += end ? 1 : block) {
+                if (issued >= a.stages) {
+                    ok = mbar_wait(&ring.empty[stage], parity, &ring.abort, kPipeTimeoutNs);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                }
+                const int ve = min(v + block, v1);
+                uint8_t* const to = smem + size_t(stage) * a.stage_bytes;
+                uintptr_t from[2] = {0, 0};
+                uint32_t bytes[2] = {0, 0}, b_bytes = 0;
+                if (!end) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (row[h] == 0) continue;
+                        const uintptr_t s = row[h] + int64_t(v) * ES, e = row[h] + int64_t(ve) * ES, low = s & ~uintptr_t(15);
+                        uintptr_t f = low, l = (e + 15) & ~uintptr_t(15);
+                        if (f < row[h]) f += 16;
+                        if (l > row[h] + int64_t(a.vocab) * ES) l -= 16;
+                        if (f > l) f = l;
+                        from[h] = f, bytes[h] = uint32_t(l - f);
+                        if (f > s || l < e) {  // odd elements at the row's ends
+                            Y* const at = reinterpret_cast<Y*>(to + (lane + 32 * h) * pitch + (s - low));
+                            for (uintptr_t x = s; x < e; x += ES) {
+                                if (x >= f && x < l) x = l;
+                                if (x < e) at[(x - s) / ES] = *reinterpret_cast<const Y*>(x);
+                            }
+                            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before a later round's copies
+                        }
+                    }
+                    if (lane == 0 && tile.adapter >= 0) b_bytes = uint32_t((ve - v) * a.rank * 2);
+                }
+                if (lane == 0) ring.what[stage] = make_int4(end ? -1 : id, v, ve - v, 0);
+                mbar_arrive_expect_tx(&ring.full[stage], bytes[0] + bytes[1] + b_bytes);
+                auto copy = [&](uint8_t* dst, const void* src, uint32_t n) {
+                    if (VCE_BOUNDS(aligned16(src) && aligned16(dst) && n % 16 == 0 && dst + n <= to + a.stage_bytes, a.dev_status))
+                        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                                         smem_u32(dst)),
+                                     "l"(src), "r"(n), "r"(smem_u32(&ring.full[stage]))
+                                     : "memory");
+                };
+                if (b_bytes) copy(to + a.y_bytes, a.b + (int64_t(tile.adapter) * a.vocab + v) * a.rank, b_bytes);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (bytes[h]) {
+                        const uintptr_t low = (row[h] + int64_t(v) * ES) & ~uintptr_t(15);
+                        copy(to + (lane + 32 * h) * pitch + (from[h] - low), reinterpret_cast<const void*>(from[h]), bytes[h]);
+                    }
+                ++issued;
+                if (++stage == a.stages) stage = 0, parity ^= 1;
+            }
+            if (end || !ok) break;
+        }
+        if (!ok) {  // copies on their way still write to shared memory
+            if (lane == 0) report(a.dev_status, VCE_DEVSTATUS_TIMEOUT);
+            for (int i = max(0, issued - a.stages); i < issued; ++i) {
+                const uint64_t t0 = globaltimer();
+                while (!mbar_try_wait(&ring.full[i % a.stages], (i / a.stages) & 1) && globaltimer() - t0 < kDrainTimeoutNs) {}
+            }
+        }
+        __syncthreads();
+        return;
+    }
+    uint32_t parity = 0;
+    int id = -1, pitch = 0, p0 = 0, part = 0, parts = 1, count = 0;
+    Tile tile{};
+    // column 2 q + e of product j is token p0 + 8 j + 2 q + e: its row in a stage, and in memory
+    int place[2][2];
+    Y* to[2][2];
+    uint32_t t[2][TERMS][KS][2];  // operands
+    const int b_row = a.rank * 2;
+    // The products of 32 logits, whose rows of B start at ``b``; EVERY: all 16 KS ranks are there.
+    auto multiply = [&](float (&c)[2][2][4], const uint8_t* b, auto every) {
+#pragma unroll
+        for (int s = 0; s < KS; s += 2) {
+            const int r = rank_of<KS>(s, q);
+            uint32_t w[2][2][4];  // product, row, words: row g of product i is logit 4 g + 2 i, row g + 8 the next
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint8_t* const from = b + (2 * i + h) * b_row + r * 2;
+                    if constexpr (KS == 1) {
+                        const uint2 x = decltype(every)::value || r < a.rank ? *reinterpret_cast<const uint2*>(from) : make_uint2(0, 0);
+                        w[i][h][0] = x.x, w[i][h][1] = x.y;
+                    } else {
+                        const uint4 x = decltype(every)::value || r < a.rank ? *reinterpret_cast<const uint4*>(from) : make_uint4(0, 0, 0, 0);
+                        w[i][h][0] = x.x, w[i][h][1] = x.y, w[i][h][2] = x.z, w[i][h][3] = x.w;
+                    }
+                }
+            auto step = [&](int j) {
+#pragma unroll
+                for (int e = 0; e < (KS == 1 ? 1 : 2); ++e)
+#pragma unroll
+                    for (int k = TERMS - 1; k >= 0; --k)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t x[4] = {w[i][0][2 * e], w[i][1][2 * e], w[i][0][2 * e + 1], w[i][1][2 * e + 1]};
+                            if (s + e == 0 && k == TERMS - 1) mma_first(c[i][j], x, t[j][k][s + e][0], t[j][k][s + e][1]);
+                            else mma(c[i][j], x, t[j][k][s + e][0], t[j][k][s + e][1]);
+                        }
+            };
+            step(0);
+            if (count > 8) step(1);
+        }
+    };
+    for (;;) {
+        ok = mbar_wait(&ring.full[stage], parity, &ring.abort, kPipeTimeoutNs);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const int4 what = ring.what[stage];
+        if (what.x < 0) break;
+        if (what.x != id) {
+            id = what.x;
+            tile = a.tiles[id];
+            const int across_log2 = max(class_of(tile.count) - 1, 0);  // warps across the tokens
+            pitch = a.block[class_of(tile.count)] * ES + 32;
+            p0 = (warp & ((1 << across_log2) - 1)) * 16, part = warp >> across_log2, parts = kMulWarps >> across_log2;
+            count = min(16, tile.count - p0);  // of this warp's tokens; none if not positive
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int p = 8 * j + 2 * q + e;
+                    to[j][e] = nullptr, place[j][e] = 0;
+                    if (p < count) {
+                        const int64_t n = a.perm[tile.start + p0 + p];
+                        to[j][e] = static_cast<Y*>(a.out) + n * a.out_stride;
+                        place[j][e] = (p0 + p) * pitch + int(reinterpret_cast<uintptr_t>(static_cast<const Y*>(a.y) + n * a.y_stride) & 15);
+                    }
+                }
+            if (tile.adapter >= 0) {
+                const float scale = a.scale ? a.scale[tile.adapter] : 1.f;
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int s = 0; s < KS; ++s) {
+                        const int p = 8 * j + g, r = rank_of<KS>(s, q);
+                        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (p < count && r < a.rank)
+                            x = *reinterpret_cast<const float4*>(a.t + int64_t(tile.start + p0 + p) * a.rank + r);
+                        uint32_t w[2][TERMS];
+                        split2<TERMS>(x.x * scale, x.y * scale, w[0]);
+                        split2<TERMS>(x.z * scale, x.w * scale, w[1]);
+#pragma unroll
+                        for (int k = 0; k < TERMS; ++k) t[j][k][s][0] = w[0][k], t[j][k][s][1] = w[1][k];
+                    }
+            }
+        }
+        uint8_t* const y = smem + size_t(stage) * a.stage_bytes;
+        const int here = what.z;
+#pragma unroll 1
+        for (int vc = part * 32; vc < here && count > 0; vc += parts * 32) {
+            uint8_t* const yc = y + vc * ES;
+            const int64_t vo = what.y + vc;
+            if (tile.adapter >= 0) {
+                float c[2][2][4];
+                const uint8_t* const b = y + a.y_bytes + (vc + 4 * g) * b_row;
+                if (a.rank == KS * 16) multiply(c, b, std::true_type{});
+                else multiply(c, b, std::false_type{});
+                const int left = here - vc - 4 * g;  // of this lane's four logits
+                const bool whole = vc + 32 <= here;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (8 * j >= count) break;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        if (to[j][e] == nullptr) continue;
+                        const float sum[4] = {c[0][j][e], c[0][j][2 + e], c[1][j][e], c[1][j][2 + e]};
+                        Y* const at = reinterpret_cast<Y*>(yc + place[j][e]) + 4 * g;
+                        if constexpr (VEC) {
+                            float x[4];
+                            load4(x, at);  // (past the end: of the stage, not used)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) x[i] += sum[i];
+                            Y* const out = to[j][e] + vo + 4 * g;
+                            if (whole || left >= 4) {
+                                store4(out, x);
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 3; ++i)
+                                    if (i < left) put(out + i, x[i]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (whole || i < left) put(at + i, to_float(at[i]) + sum[i]);
+                        }
+                    }
+                }
+            }
+            if (!VEC || tile.adapter < 0) {
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (8 * j >= count) break;
+#pragma unroll
+                    for (int p = 0; p < 8; ++p) {  // token 8 j + p is lane p / 2's, its (p % 2)-th
+                        if (8 * j + p >= count) break;
+                        const int where = __shfl_sync(0xffffffffu, place[j][p & 1], p >> 1);
+                        Y* const out = reinterpret_cast<Y*>(
+                            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to[j][p & 1]), p >> 1));
+                        if (vc + lane < here) out[vo + lane] = (reinterpret_cast<const Y*>(yc + where))[lane];
+                    }
+                }
+            }
+        }
+        if constexpr (!VEC) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the next copy
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ring.empty[stage]);
+        if (++stage == a.stages) stage = 0, parity ^= 1;
+    }
+    __syncthreads();
+}
 
 template <typename Y>
 struct Eight;  // eight neighbouring logits of a row
@@ -361,26 +702,34 @@ struct Eight<float> {
     }
 };
 
-// The first of the four neighbouring ranks that lane q holds in step s of KS.
-template <int KS>
-__device__ __forceinline__ int rank_of(int s, int q) { return KS == 1 ? 4 * q : 32 * (s / 2) + 8 * q + 4 * (s & 1); }
-
-// Tokens are the rows of the products and logits the columns: column 2 q + e of tile j is logit
-// 8 q + 2 j + e of the warp's 32, so that a lane ends up with eight neighbours of a row.
+// Many tokens to an adapter, in rows that start at 16-byte boundaries.  Tokens are the rows of the products (16)
+// and logits the columns (8): column 2 q + e of product j is logit 8 q + 2 j + e of the warp's 32, so that
+// a lane ends up with eight neighbours of a row.  A warp loads B's operands once for all tokens of a tile, and the
+// next 16 rows of y while it multiplies.
+//
+// Units are blocks of kVBlock logits of a tile, tiles of the same logits next to each other: blocks that
+// work at the same time read the same part of B.  Where tiles are few a block stays with its tile.
+//
+// 2048 tokens with 6 adapters of rank 64, 128256 BF16 logits: 266 us (4.2 TB/s); 417 with FP32 logits (5.3).  It is
+// bound by what 16 warps per SM keep on its way between their instructions.  512 x 128256, rank 16, this
+// form / the other one in us: 16 tokens per adapter 110 / 96 (BF16), 137 / 128 (FP32); 32 tokens 89 / 103 and
+// 118 / 163; hence kMany.
 template <typename Y, int KS>
-__global__ void __launch_bounds__(kThreads) adapter_expand(const ExpandArgs a) {
+__global__ void __launch_bounds__(kThreads, KS <= 4 ? 2 : 1) adapter_expand_many(const __grid_constant__ ExpandArgs a) {
     constexpr int TERMS = sizeof(Y) == 2 ? 2 : 3;
     extern __shared__ __align__(16) uint4 frag[];  // [TERMS][kMTiles][KS][32]: operands of t
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
     cudaGridDependencySynchronize();
     const int vblocks = (a.vocab + kVBlock - 1) / kVBlock;
     const int64_t units = int64_t(a.plan->n_all) * vblocks;
-    const int64_t first = units * blockIdx.x / gridDim.x, last = units * (blockIdx.x + 1) / gridDim.x;
+    const int tiles = a.plan->n_all;
+    const int step = tiles * 4 <= int(gridDim.x) ? int(gridDim.x) / max(tiles, 1) * tiles : int(gridDim.x);
+    if (int(blockIdx.x) >= step) return;
     int id = -1;
     Tile tile{};
     int64_t token[kMTiles][2];
-    for (int64_t unit = first; unit < last; ++unit) {
-        const int now = int(unit / vblocks);
+    for (int64_t unit = blockIdx.x; unit < units; unit += step) {
+        const int now = int(unit % tiles), vb = int(unit / tiles);
         if (now != id) {
             id = now;
             tile = a.tiles[id];
@@ -414,7 +763,7 @@ __global__ void __launch_bounds__(kThreads) adapter_expand(const ExpandArgs a) {
                 }
             __syncthreads();
         }
-        const int v0 = int(unit - int64_t(id) * vblocks) * kVBlock + warp * kVWarp;
+        const int v0 = vb * kVBlock + warp * kVWarp;
         if (v0 >= a.vocab) continue;
         uint32_t b[4][KS][2];
 #pragma unroll
@@ -439,7 +788,7 @@ __global__ void __launch_bounds__(kThreads) adapter_expand(const ExpandArgs a) {
             }
         }
         const int v = v0 + 8 * q, left = a.vocab - v;  // this lane's eight logits
-        const bool whole = a.vectors && left >= 8;
+        const bool whole = left >= 8;
         auto fetch = [&](Eight<Y>& e, int64_t n) {
             e.clear();
             if (n < 0 || left <= 0) return;
@@ -461,9 +810,9 @@ __global__ void __launch_bounds__(kThreads) adapter_expand(const ExpandArgs a) {
             float c[4][4] = {};
             if (tile.adapter >= 0) {
 #pragma unroll
-                for (int k = TERMS - 1; k >= 0; --k)
+                for (int s = 0; s < KS; ++s)
 #pragma unroll
-                    for (int s = 0; s < KS; ++s) {
+                    for (int k = TERMS - 1; k >= 0; --k) {
                         const uint4 f = frag[((k * kMTiles + m) * KS + s) * 32 + lane];
                         const uint32_t w[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
@@ -486,9 +835,17 @@ __global__ void __launch_bounds__(kThreads) adapter_expand(const ExpandArgs a) {
     }
 }
 
+template <typename Y, bool VEC>
+auto expand_kernel(int ks, int* threads) {
+    *threads = 32 + 32 * (ks == 1 ? Shape<Y, 1>::kWarps : ks == 2 ? Shape<Y, 2>::kWarps : ks == 4 ? Shape<Y, 4>::kWarps : Shape<Y, 8>::kWarps);
+    return ks == 1 ? adapter_expand_few<Y, 1, VEC> : ks == 2 ? adapter_expand_few<Y, 2, VEC> : ks == 4 ? adapter_expand_few<Y, 4, VEC>
+                                                                                          : adapter_expand_few<Y, 8, VEC>;
+}
+
 template <typename Y>
-auto expand_kernel(int ks) {
-    return ks == 1 ? adapter_expand<Y, 1> : ks == 2 ? adapter_expand<Y, 2> : ks == 4 ? adapter_expand<Y, 4> : adapter_expand<Y, 8>;
+auto many_kernel(int ks) {
+    return ks == 1 ? adapter_expand_many<Y, 1> : ks == 2 ? adapter_expand_many<Y, 2> : ks == 4 ? adapter_expand_many<Y, 4>
+                                                                                     : adapter_expand_many<Y, 8>;
 }
 
 struct Carved {
@@ -553,12 +910,33 @@ vce_status launch_adapter_linear(const void* y, int y_dtype, int64_t n, int64_t 
     auto shrink = x_dtype == VCE_BF16 ? adapter_shrink<__nv_bfloat16> : adapter_shrink<float>;
     const size_t shrink_smem = size_t(kWarps) * kTile * kRankBlock * 4;
     const int ks = rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8;
-    auto expand = y_dtype == VCE_BF16 ? expand_kernel<__nv_bfloat16>(ks) : expand_kernel<float>(ks);
-    const size_t expand_smem = size_t(y_dtype == VCE_BF16 ? 2 : 3) * kMTiles * ks * 32 * sizeof(uint4);
+    const int es = y_dtype == VCE_BF16 ? 2 : 4;
+    const bool vectors = reinterpret_cast<uintptr_t>(y) % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0 &&
+                         (n == 1 || (y_stride * es % 16 == 0 && out_stride * es % 16 == 0));
+    int threads;
+    auto expand = y_dtype == VCE_BF16
+                      ? (vectors ? expand_kernel<__nv_bfloat16, true>(ks, &threads) : expand_kernel<__nv_bfloat16, false>(ks, &threads))
+                      : (vectors ? expand_kernel<float, true>(ks, &threads) : expand_kernel<float, false>(ks, &threads));
+    ExpandArgs ea{static_cast<const __nv_bfloat16*>(b), scale, w.t, y, out, y_stride, out_stride, int(vocab), rank, 0, 0, 0,
+                  {}, w.plan, w.tiles, w.perm, dev_status};
+    int b_bytes = 0;
+    for (int rows : {4, 16, 32, 64}) {
+        int& block = ea.block[class_of(rows)];
+        block = std::min({kMaxBlock, kStageRows / (rows * es), kStageB / (rank * 2)}) / 32 * 32;
+        ea.y_bytes = std::max(ea.y_bytes, rows * (block * es + 32));
+        b_bytes = std::max(b_bytes, block * rank * 2);
+    }
+    ea.stage_bytes = ea.y_bytes + b_bytes;  // multiples of 64 both
+    ea.stages = std::min(kMaxStages, kRingBytes / ea.stage_bytes);
+    const size_t expand_smem = size_t(ea.stages) * ea.stage_bytes;
     static std::mutex mu;
-    static bool ready[64];
+    static bool ready[64], ready_expand[64][2][2][4];
     {
         std::lock_guard<std::mutex> lock(mu);
+        bool& done = ready_expand[dev.ordinal][y_dtype == VCE_BF16][vectors][ks == 8 ? 3 : ks / 2];
+        if (!done && cudaFuncSetAttribute(expand, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes) != cudaSuccess)
+            return VCE_ERR_CUDA;
+        done = true;
         if (!ready[dev.ordinal]) {
             for (auto k : {adapter_shrink<__nv_bfloat16>, adapter_shrink<float>})
                 if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(shrink_smem)) != cudaSuccess)
@@ -572,13 +950,16 @@ vce_status launch_adapter_linear(const void* y, int y_dtype, int64_t n, int64_t 
     count_launch();
     if (cudaLaunchKernelEx(&cfg, shrink, sa) != cudaSuccess) return VCE_ERR_CUDA;
 
-    const int es = y_dtype == VCE_BF16 ? 2 : 4;
-    const bool vectors = reinterpret_cast<uintptr_t>(y) % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0 &&
-                         (n == 1 || (y_stride * es % 16 == 0 && out_stride * es % 16 == 0));
-    const ExpandArgs ea{static_cast<const __nv_bfloat16*>(b), scale, w.t, y, out, y_stride, out_stride, int(vocab), rank,
-                        int(n), vectors, w.plan, w.tiles, w.perm, dev_status};
-    const int64_t vblocks = (vocab + kVBlock - 1) / kVBlock;
-    cfg.gridDim = dim3(unsigned(std::min<int64_t>(most_tiles(n, adapters) * vblocks, int64_t(dev.num_sms) * 4)));
+    if (vectors && n >= kMany * std::min(n, adapters)) {
+        auto many = y_dtype == VCE_BF16 ? many_kernel<__nv_bfloat16>(ks) : many_kernel<float>(ks);
+        cfg.gridDim = dim3(unsigned(dev.num_sms * (ks <= 4 ? 2 : 1)));
+        cfg.dynamicSmemBytes = size_t(y_dtype == VCE_BF16 ? 2 : 3) * kMTiles * ks * 32 * sizeof(uint4);
+        cfg.numAttrs = 1;
+        count_launch();
+        return cudaLaunchKernelEx(&cfg, many, ea) == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
+    }
+    cfg.gridDim = dim3(unsigned(std::min<int64_t>(most_tiles(n, adapters) * ((vocab + kRun - 1) / kRun), int64_t(dev.num_sms))));
+    cfg.blockDim = dim3(unsigned(threads));
     cfg.dynamicSmemBytes = expand_smem;
     cfg.numAttrs = 1;
     count_launch();
