@@ -4,7 +4,7 @@ are those of ``_head``.
 """
 from __future__ import annotations
 
-import ctypes
+from array import array
 from collections import namedtuple
 from functools import lru_cache
 
@@ -245,26 +245,32 @@ def beam_reorder(states, parent, *, lengths=None, position_dim=None, out=None, d
     batch = rows // beams
     if lengths is not None:
         _vector(lengths, "lengths", batch, torch.int32, index)
-    packed = []
+    packed, last = [], None  # (a cache's tensors are mostly alike: what was found out of one holds for the next)
     for src, dst, dim in zip(srcs, dsts, dims):
         if lengths is not None and dim is None:
             raise ValueError("lengths need the position_dim of every state")
-        row, apart = _state_layout(src, dim, rows, index, "a state")
+        kind = (src.shape, src.stride(), src.dtype, dim, src.get_device())
+        if kind != last:
+            (row, parts, part, positions, each), apart = _state_layout(src, dim, rows, index, "a state")
+            last = kind
         at = to = src.data_ptr()
-        to_row = row
-        if dst is not src:
-            if dst.shape != src.shape or dst.dtype is not src.dtype:
-                raise ValueError(f"out must match the states: {dst.dtype}, {tuple(dst.shape)} for {src.dtype}, {tuple(src.shape)}")
-            to_row, apart = _state_layout(dst, dim, rows, index, "out")
-            to = dst.data_ptr()
-            if row[1] != to_row[1] or row[3:] != to_row[3:]:
-                raise ValueError("a state and its out must divide into the same contiguous runs")
-            if to == at and row != to_row:
-                raise ValueError("out shares memory with its state")
-        if not apart:
-            raise ValueError("a tensor that is written has elements that share memory")
-        packed += (at, to, row[0], to_row[0], row[1], row[2], to_row[2], row[3], row[4])
-    lib = b.library()
-    _launch("beam_reorder", dev, lib.beam_reorder, (ctypes.c_int64 * len(packed))(*packed), len(srcs), parent.data_ptr(),
+        if dst is src:
+            if not apart:
+                raise ValueError("a state that is written has elements that share memory")
+            packed += (at, to, row, row, parts, part, part, positions, each)
+            continue
+        if dst.shape != src.shape or dst.dtype is not src.dtype:
+            raise ValueError(f"out must match the states: {dst.dtype}, {tuple(dst.shape)} for {src.dtype}, {tuple(src.shape)}")
+        (to_row, to_parts, to_part, *run), to_apart = _state_layout(dst, dim, rows, index, "out")
+        to = dst.data_ptr()
+        if parts != to_parts or run != [positions, each]:
+            raise ValueError("a state and its out must divide into the same contiguous runs")
+        if to == at and (row, part) != (to_row, to_part):
+            raise ValueError("out shares memory with its state")
+        if not to_apart:
+            raise ValueError("an out has elements that share memory")
+        packed += (at, to, row, to_row, parts, part, to_part, positions, each)
+    states_of = array("q", packed)  # vce_state: nine 64-bit words
+    _launch("beam_reorder", dev, b.library().beam_reorder, states_of.buffer_info()[0], len(srcs), parent.data_ptr(),
             batch, beams, b._ptr(lengths), _status(dev_status, index))
     return dsts[0] if single else dsts
