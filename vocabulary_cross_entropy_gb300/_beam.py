@@ -19,6 +19,7 @@ BEAM_MAX_BEAMS, BEAM_MAX_COUNT = 32, 64
 CEBeam = namedtuple("CEBeam", "token parent score ended length dev_status")
 
 
+@lru_cache(maxsize=1024)
 def ce_beam_workspace_size(batch: int, beams: int, count: int) -> int:
     return int(b.library().ce_beam_workspace_size(batch, beams, count))
 
@@ -83,7 +84,7 @@ def _choose(logits, code, vocab, stride, args, score, ended, length, length_pena
     token, parent, out_score, out_ended, out_length = out
     lib, ptr = b.library(), b._ptr
     if workspace is None:
-        workspace = torch.empty(max(1, lib.ce_beam_workspace_size(batch, beams, count)), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(ce_beam_workspace_size(batch, beams, count) or 1, dtype=torch.uint8, device=dev)
     elif workspace.get_device() != logits.get_device() or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the logits' device")
     _launch("ce_beam", dev, lib.ce_beam, logits.data_ptr(), code, batch, beams, vocab, stride, score.data_ptr(),

@@ -10,6 +10,7 @@ only behind its kernels.
 from __future__ import annotations
 
 from collections import namedtuple
+from functools import lru_cache
 
 import torch
 
@@ -453,6 +454,7 @@ def _check_adapters(a, b_, scale, row, n, hidden, vocab, index):
     return count, rank
 
 
+@lru_cache(maxsize=1024)
 def adapter_workspace_size(n: int, adapters: int, rank: int) -> int:
     return int(b.library().adapter_workspace_size(n, adapters, rank))
 
@@ -486,7 +488,7 @@ def adapter_linear(y, x, a, b_, index, scale=None, *, out=None, workspace=None, 
         raise ValueError("the rows of a tensor overlap")
     lib = b.library()
     if workspace is None:
-        workspace = torch.empty(max(1, lib.adapter_workspace_size(n, count, rank)), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(adapter_workspace_size(n, count, rank) or 1, dtype=torch.uint8, device=dev)
     elif workspace.get_device() != device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the inputs' device")
     _launch("adapter_linear", dev, lib.adapter_linear, y.data_ptr(), code, n, vocab, stride, x.data_ptr(), xcode, hidden, xs,

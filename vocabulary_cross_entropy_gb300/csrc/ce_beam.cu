@@ -24,11 +24,12 @@
 // the survivors while the others add up the weights).
 //
 // What bounds it: the chain of a block's steps, of which five blocks per SM cover each other.
-// 64 x 8 x 128256 BF16 (85% of the beams go on): 36 us and 9 for the merge, where the copies alone take
+// 64 x 8 x 128256 BF16 (85% of the beams go on): 36 us and 7 for the merge, where the copies alone take
 // 20 and the memory's rate allows 17.  Parts of 32 KB, 256 threads; 64 KB and 512: 37; 24 KB: 46.  With a
 // row's parts in a cluster of blocks that agreed on a maximum and joined their lists 76 + 10, most of
 // it waits at barriers; with the parts in registers, which take many more instructions and leave
-// room for two blocks, 61 + 14; with each thread looking for its survivors by itself 59 + 8.
+// room for two blocks, 61 + 14; with each thread looking for its survivors by itself 59 + 8; with as many
+// blocks as run at once, each taking one part after the other, 44 + 7 (uneven ends, and registers).
 
 #include "head_internal.cuh"
 #include "sm100_ptx.cuh"
@@ -53,7 +54,8 @@ constexpr int kFew = 128;             // as many are sorted by a warp
 constexpr int kMaxParts = 16;
 constexpr int kMaxCount = VCE_BEAM_MAX_COUNT;
 constexpr int kMaxBeams = VCE_BEAM_MAX_BEAMS;
-constexpr int kMergeThreads = 256;
+constexpr int kRowWarps = 8;          // of the merge; one more takes logarithms meanwhile
+constexpr int kMergeThreads = kRowWarps * 32 + 32;
 constexpr int kMergeBytes = 200 << 10;  // of shared memory, at most
 
 // What the first kernel leaves of a part of a row, beside its keys (descending).
@@ -580,12 +582,17 @@ __global__ void __launch_bounds__(kMergeThreads) ce_beam_merge(const __grid_cons
     }
     __syncthreads();
     cudaGridDependencySynchronize();
+    auto head_of = [&](int r) {
+        if (r < a.beams && lane < a.parts && rows[r].read) return a.heads[(request * a.beams + r) * a.parts + lane];
+        return PartHead{-INFINITY, 0, 0};
+    };
+    PartHead coming = warp < kRowWarps ? head_of(warp) : PartHead{-INFINITY, 0, 0};  // on its way with the keys
     for (int i = tid; i < all; i += kMergeThreads)
         keys[i] = a.keys[request * all + i];  // (those past a list's number are not looked at)
-    for (int r = warp; r < a.beams; r += kMergeThreads / 32) {  // a row's parts
+    for (int r = warp; r < a.beams && warp < kRowWarps; r += kRowWarps) {  // a row's parts
         const bool read = rows[r].read;
-        PartHead head{-INFINITY, 0, 0};
-        if (read && lane < a.parts) head = a.heads[(request * a.beams + r) * a.parts + lane];
+        const PartHead head = coming;
+        coming = head_of(r + kRowWarps);
         const bool broken = __any_sync(0xffffffffu, head.n < 0);
         float m = head.m;
 #pragma unroll
@@ -610,10 +617,10 @@ __global__ void __launch_bounds__(kMergeThreads) ce_beam_merge(const __grid_cons
         }
     }
     __syncthreads();
-    if (tid < a.beams) rows[tid].log_s = log(double(rows[tid].mass)) - a.q_bits * 0.69314718055994530942;
-    __syncthreads();
-    if (!at_once) {
-        for (int r = warp; r < a.beams; r += kMergeThreads / 32) {
+    if (warp == kRowWarps) {
+        if (lane < a.beams) rows[lane].log_s = log(double(rows[lane].mass)) - a.q_bits * 0.69314718055994530942;
+    } else if (!at_once) {
+        for (int r = warp; r < a.beams; r += kRowWarps) {
             int at = (r * a.parts + lane) * a.count, n = 0;
             const int end = lane < a.parts ? at + part_n[r * a.parts + lane] : 0;
             uint64_t key = at < end ? keys[at] : 0;
@@ -633,8 +640,8 @@ __global__ void __launch_bounds__(kMergeThreads) ce_beam_merge(const __grid_cons
             }
             if (lane == 0) list_n[r] = n;
         }
-        __syncthreads();
     }
+    __syncthreads();
     for (int i = tid; i < joined * a.count; i += kMergeThreads) {
         const int list = i / a.count, n = at_once ? part_n[list] : list_n[list];
         if (i - list * a.count >= n) continue;
