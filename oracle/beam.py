@@ -16,12 +16,12 @@ def beam_step(z, score, ended=None, length=None, end=-1, penalty=0.0, count=None
     token, parent = np.full((bs, count), -1), np.tile(np.arange(count) % k, (bs, 1))
     out, done, size = np.full((bs, count), -np.inf), np.zeros((bs, count), bool), np.zeros((bs, count), np.int64)
     for b in range(bs):
-        beam, tok, c = [], [], []
+        beam, tok, c, logit = [], [], [], []
         for j in range(k):
             if not np.isfinite(score[b, j]):
                 continue
             if ended[b, j]:
-                beam.append([j]), tok.append([end]), c.append([score[b, j]])
+                beam.append([j]), tok.append([end]), c.append([score[b, j]]), logit.append([0.0])
                 continue
             m = z[b, j].max()
             if not np.isfinite(m):
@@ -30,13 +30,14 @@ def beam_step(z, score, ended=None, length=None, end=-1, penalty=0.0, count=None
                 lp = (z[b, j] - m) - np.log(np.exp(z[b, j] - m).sum())
             allowed = np.flatnonzero(z[b, j] > -np.inf)
             beam.append(np.full(len(allowed), j)), tok.append(allowed), c.append(score[b, j] + lp[allowed])
+            logit.append(z[b, j][allowed])
         size[b] = length[b][parent[b]]
         if not c:
             continue
-        beam, tok, c = (np.concatenate(x) for x in (beam, tok, c))
+        beam, tok, c, logit = (np.concatenate(x) for x in (beam, tok, c, logit))
         after = length[b][beam] + ~ended[b][beam]
         value = c / np.maximum(after, 1).astype(np.float64) ** penalty
-        order = np.lexsort((tok, beam, -value))[:count]
+        order = np.lexsort((tok, -logit, beam, -value))[:count]  # (within a beam: the logits' order)
         places = list(range(len(order)))
         if keep:
             free, places = list(range(k)), [None] * len(order)

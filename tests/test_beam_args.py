@@ -122,7 +122,9 @@ def test_python_refusals():
                      ((x, parent), dict(out=torch.zeros(1, 3, 8, 2).expand(4, 3, 8, 2))),
                      ((x[:, :, ::2], parent), dict(position_dim=2)), ((x[:, :, :, :1], parent), dict(position_dim=2)),
                      ((torch.zeros(4, 4, 3, 8, 2)[:, :, ::2, :5], parent), dict(position_dim=3)),
-                     ((x[:1].expand(4, 3, 8, 2), parent), {})):
+                     ((x[:1].expand(4, 3, 8, 2), parent), {}), (([x, x], parent), {}),
+                     (([x, x.clone()], parent), dict(out=[x.clone(), x])),
+                     (([x, x.clone()], parent), dict(out=[y := x.clone(), y]))):
         with pytest.raises(ValueError):
             vce.beam_reorder(*args, **kw)
     y, h = torch.zeros(4, 10), torch.zeros(4, 16)

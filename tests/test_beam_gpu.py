@@ -107,6 +107,21 @@ def test_equal_logits(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+def test_logits_that_fp64_does_not_tell_apart(dtype):
+    """0 and 1e-30 beside a logit of 5: the same sum, but the order of the logits, in any part of the row."""
+    v = 40000
+    z = torch.zeros(2, v, dtype=dtype, device=DEV)
+    z[0, 100], z[1, 5] = 5.0, 5.0
+    z[0, 39000], z[0, 17], z[0, 20000] = 2e-30, 1e-30, 1e-30
+    z[1, 39999], z[1, 38000] = 1e-30, -1e-30
+    for shape in ((1, 2), (2, 1)):
+        for count in (3, 6, 40):
+            check(z, torch.zeros(shape, device=DEV), count=count)
+    wide = z.repeat(16, 1)
+    check(wide, torch.zeros(1, 32, device=DEV), count=64)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_masks(dtype):
     """-inf and the type's lowest value as masks; fewer allowed tokens than wanted; no allowed ones."""
     g = torch.Generator().manual_seed(2)

@@ -246,6 +246,7 @@ def beam_reorder(states, parent, *, lengths=None, position_dim=None, out=None, d
     batch = rows // beams
     if lengths is not None:
         _vector(lengths, "lengths", batch, torch.int32, index)
+    written, read = set(), set()
     packed, last = [], None  # (a cache's tensors are mostly alike: what was found out of one holds for the next)
     for src, dst, dim in zip(srcs, dsts, dims):
         if lengths is not None and dim is None:
@@ -254,11 +255,13 @@ def beam_reorder(states, parent, *, lengths=None, position_dim=None, out=None, d
         if kind != last:
             (row, parts, part, positions, each), apart = _state_layout(src, dim, rows, index, "a state")
             last = kind
-        at = to = src.data_ptr()
+        at = src.data_ptr()
         if dst is src:
-            if not apart:
-                raise ValueError("a state that is written has elements that share memory")
-            packed += (at, to, row, row, parts, part, part, positions, each)
+            if not apart or at in written:
+                raise ValueError("a state that is written has elements that share memory, or is there twice")
+            if positions:
+                written.add(at)
+            packed += (at, at, row, row, parts, part, part, positions, each)
             continue
         if dst.shape != src.shape or dst.dtype is not src.dtype:
             raise ValueError(f"out must match the states: {dst.dtype}, {tuple(dst.shape)} for {src.dtype}, {tuple(src.shape)}")
@@ -268,9 +271,15 @@ def beam_reorder(states, parent, *, lengths=None, position_dim=None, out=None, d
             raise ValueError("a state and its out must divide into the same contiguous runs")
         if to == at and (row, part) != (to_row, to_part):
             raise ValueError("out shares memory with its state")
-        if not to_apart:
-            raise ValueError("an out has elements that share memory")
+        if not to_apart or to in written:
+            raise ValueError("an out has elements that share memory, or is there twice")
+        if positions:
+            written.add(to)
+            if at != to:
+                read.add(at)
         packed += (at, to, row, to_row, parts, part, to_part, positions, each)
+    if not written.isdisjoint(read):
+        raise ValueError("out shares memory with the states")
     states_of = array("q", packed)  # vce_state: nine 64-bit words
     _launch("beam_reorder", dev, b.library().beam_reorder, states_of.buffer_info()[0], len(srcs), parent.data_ptr(),
             batch, beams, b._ptr(lengths), _status(dev_status, index))

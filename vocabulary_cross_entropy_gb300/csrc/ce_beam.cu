@@ -530,12 +530,11 @@ __device__ __forceinline__ uint64_t order_bits(double z) {  // monotone in z; -0
     return b ^ (uint64_t(int64_t(b) >> 63) | 0x8000000000000000ull);
 }
 
-// The lane with the largest value, the lowest among equal ones; -1 when all are 0.
-__device__ __forceinline__ int best_lane(uint64_t value) {
+// The lanes with the largest value; none when all are 0.
+__device__ __forceinline__ uint32_t best_lanes(uint64_t value) {
     const uint32_t high = __reduce_max_sync(0xffffffffu, uint32_t(value >> 32));
     const uint32_t low = __reduce_max_sync(0xffffffffu, uint32_t(value >> 32) == high ? uint32_t(value) : 0u);
-    if ((high | low) == 0) return -1;
-    return __ffs(int(__ballot_sync(0xffffffffu, value == (uint64_t(high) << 32 | low)))) - 1;
+    return (high | low) == 0 ? 0u : __ballot_sync(0xffffffffu, value == (uint64_t(high) << 32 | low));
 }
 
 struct Row {  // of a request
@@ -629,9 +628,9 @@ __global__ void __launch_bounds__(kMergeThreads) ce_beam_merge(const __grid_cons
                 if (lane == 0) merged[r * a.count] = at;
             } else {
                 for (; n < a.count; ++n) {
-                    const int best = best_lane(key);
-                    if (best < 0) break;
-                    if (lane == best) {
+                    const uint32_t best = best_lanes(key);
+                    if (best == 0) break;
+                    if (best >> lane & 1) {  // (no two keys are equal)
                         merged[r * a.count + n] = at;
                         ++at;
                         key = at < end ? keys[at] : 0;
@@ -660,7 +659,12 @@ __global__ void __launch_bounds__(kMergeThreads) ce_beam_merge(const __grid_cons
     uint32_t taken = 0;
     uint64_t deferred = 0;  // chosen ones without a place of their own
     for (int i = 0; i < a.count; ++i) {
-        const int best = best_lane(value);
+        uint32_t equal = best_lanes(value);
+        int best = __ffs(int(equal)) - 1;
+        if (equal & (equal - 1)) {  // the lowest beam, and in it the larger logit, which FP64 did not tell apart
+            const bool mine = (equal >> lane & 1) && lane / per == best / per;
+            best = __ffs(int(best_lanes(mine && at_once ? keys[at] + 1 : mine))) - 1;
+        }
         if (best < 0) {
             if (lane == 0) chosen_parent[i] = -1;
             deferred |= uint64_t(1) << i;
