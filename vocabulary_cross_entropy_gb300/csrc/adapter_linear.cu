@@ -702,21 +702,49 @@ struct Eight<float> {
     }
 };
 
+// Operands of B for logits v0 .. v0 + 31 of adapter_expand_many.
+template <int KS>
+__device__ __forceinline__ void load_b(uint32_t (&b)[4][KS][2], const ExpandArgs& a, int adapter, int v0) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int v = v0 + 8 * (g >> 1) + 2 * j + (g & 1);
+        const __nv_bfloat16* const at = a.b + (int64_t(adapter) * a.vocab + v) * a.rank;
+        if constexpr (KS == 1) {
+            uint2 w = make_uint2(0, 0);
+            if (v < a.vocab && 4 * q < a.rank && VCE_BOUNDS((reinterpret_cast<uintptr_t>(at) & 7) == 0, a.dev_status))
+                w = __ldg(reinterpret_cast<const uint2*>(at + 4 * q));
+            b[j][0][0] = w.x, b[j][0][1] = w.y;
+        } else {
+#pragma unroll
+            for (int s = 0; s < KS; s += 2) {
+                const int r = rank_of<KS>(s, q);
+                uint4 w = make_uint4(0, 0, 0, 0);
+                if (v < a.vocab && r < a.rank && VCE_BOUNDS(aligned16(at + r), a.dev_status))
+                    w = __ldg(reinterpret_cast<const uint4*>(at + r));
+                b[j][s][0] = w.x, b[j][s][1] = w.y, b[j][s + 1][0] = w.z, b[j][s + 1][1] = w.w;
+            }
+        }
+    }
+}
+
 // Many tokens to an adapter, in rows that start at 16-byte boundaries.  Tokens are the rows of the products (16)
 // and logits the columns (8): column 2 q + e of product j is logit 8 q + 2 j + e of the warp's 32, so that
-// a lane ends up with eight neighbours of a row.  A warp loads B's operands once for all tokens of a tile, and the
-// next 16 rows of y while it multiplies.
+// a lane ends up with eight neighbours of a row.  A warp loads B's operands once for all tokens of a tile, and
+// the next rows of y while it multiplies.
 //
 // Units are blocks of kVBlock logits of a tile, tiles of the same logits next to each other: blocks that
 // work at the same time read the same part of B.  Where tiles are few a block stays with its tile.
 //
-// 2048 tokens with 6 adapters of rank 64, 128256 BF16 logits: 266 us (4.2 TB/s); 417 with FP32 logits (5.3).  It is
-// bound by what 16 warps per SM keep on its way between their instructions.  512 x 128256, rank 16, this
-// form / the other one in us: 16 tokens per adapter 110 / 96 (BF16), 137 / 128 (FP32); 32 tokens 89 / 103 and
-// 118 / 163; hence kMany.
+// 2048 tokens with 6 adapters of rank 64, 128256 BF16 logits: 266 us (4.2 TB/s); FP32 logits 390 (5.7).  It is
+// bound by what 16 warps per SM keep on its way between their instructions.  More rows on their way help small
+// ranks (512 x 128256, rank 16, BF16: 86 -> 76 us in all) and cost as much with large ones (2048 tokens of rank
+// 64: 291 -> 318).  512 x 128256, rank 16, this form / the other one in us in all: 16 tokens per adapter
+// 110 / 96 (BF16), 137 / 128 (FP32); 32 tokens 80 / 103 and 117 / 163; hence kMany.
 template <typename Y, int KS>
 __global__ void __launch_bounds__(kThreads, KS <= 4 ? 2 : 1) adapter_expand_many(const __grid_constant__ ExpandArgs a) {
-    constexpr int TERMS = sizeof(Y) == 2 ? 2 : 3;
+    constexpr int TERMS = sizeof(Y) == 2 ? 2 : 3, kAhead = KS > 2 ? 1 : sizeof(Y) == 2 ? 4 : 3;  // groups of 16 rows on their way
+    constexpr int kSlots = kAhead < kMTiles ? kAhead + 1 : kMTiles;
     extern __shared__ __align__(16) uint4 frag[];  // [TERMS][kMTiles][KS][32]: operands of t
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
     cudaGridDependencySynchronize();
@@ -727,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, KS <= 4 ? 2 : 1) adapter_expand_many
     if (int(blockIdx.x) >= step) return;
     int id = -1;
     Tile tile{};
-    int64_t token[kMTiles][2];
+    int token[kMTiles][2];
     for (int64_t unit = blockIdx.x; unit < units; unit += step) {
         const int now = int(unit % tiles), vb = int(unit / tiles);
         if (now != id) {
@@ -765,47 +793,30 @@ __global__ void __launch_bounds__(kThreads, KS <= 4 ? 2 : 1) adapter_expand_many
         }
         const int v0 = vb * kVBlock + warp * kVWarp;
         if (v0 >= a.vocab) continue;
-        uint32_t b[4][KS][2];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int v = v0 + 8 * (g >> 1) + 2 * j + (g & 1);
-            const __nv_bfloat16* const at = a.b + (int64_t(tile.adapter) * a.vocab + v) * a.rank;
-            const bool ok = tile.adapter >= 0 && v < a.vocab;
-            if constexpr (KS == 1) {
-                uint2 w = make_uint2(0, 0);
-                if (ok && 4 * q < a.rank && VCE_BOUNDS((reinterpret_cast<uintptr_t>(at) & 7) == 0, a.dev_status))
-                    w = __ldg(reinterpret_cast<const uint2*>(at + 4 * q));
-                b[j][0][0] = w.x, b[j][0][1] = w.y;
-            } else {
-#pragma unroll
-                for (int s = 0; s < KS; s += 2) {
-                    const int r = rank_of<KS>(s, q);
-                    uint4 w = make_uint4(0, 0, 0, 0);
-                    if (ok && r < a.rank && VCE_BOUNDS(aligned16(at + r), a.dev_status))
-                        w = __ldg(reinterpret_cast<const uint4*>(at + r));
-                    b[j][s][0] = w.x, b[j][s][1] = w.y, b[j][s + 1][0] = w.z, b[j][s + 1][1] = w.w;
-                }
-            }
-        }
         const int v = v0 + 8 * q, left = a.vocab - v;  // this lane's eight logits
         const bool whole = left >= 8;
-        auto fetch = [&](Eight<Y>& e, int64_t n) {
-            e.clear();
+        auto fetch = [&](Eight<Y>& e, int n) {
+            e.clear();  // (a load that may not be made would wait for what the registers held)
             if (n < 0 || left <= 0) return;
             const Y* const p = static_cast<const Y*>(a.y) + n * a.y_stride + v;
             if (whole) e.load(p);
             else e.load_some(p, left);
         };
-        Eight<Y> e[2];
-        fetch(e[0], token[0][0]);
-        fetch(e[1], token[0][1]);
+        uint32_t b[4][KS][2];
+        if (tile.adapter >= 0) load_b<KS>(b, a, tile.adapter, v0);
+        Eight<Y> e[kSlots][2];
+#pragma unroll
+        for (int m = 0; m < kAhead; ++m) {
+            fetch(e[m][0], token[m][0]);
+            fetch(e[m][1], token[m][1]);
+        }
 #pragma unroll
         for (int m = 0; m < kMTiles; ++m) {
             if (m * 16 >= tile.count) break;
-            Eight<Y> next[2];
-            if (m + 1 < kMTiles) {  // on their way while this tile is multiplied
-                fetch(next[0], token[m + 1 < kMTiles ? m + 1 : m][0]);
-                fetch(next[1], token[m + 1 < kMTiles ? m + 1 : m][1]);
+            if (m + kAhead < kMTiles) {  // before the products: a load behind their stores would wait for them
+                const int next = m + kAhead < kMTiles ? m + kAhead : 0;
+                fetch(e[next % kSlots][0], token[next][0]);
+                fetch(e[next % kSlots][1], token[next][1]);
             }
             float c[4][4] = {};
             if (tile.adapter >= 0) {
@@ -816,20 +827,23 @@ __global__ void __launch_bounds__(kThreads, KS <= 4 ? 2 : 1) adapter_expand_many
                         const uint4 f = frag[((k * kMTiles + m) * KS + s) * 32 + lane];
                         const uint32_t w[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) mma(c[j], w, b[j][s][0], b[j][s][1]);
+                        for (int j = 0; j < 4; ++j) {
+                            if (s == 0 && k == TERMS - 1) mma_first(c[j], w, b[j][s][0], b[j][s][1]);
+                            else mma(c[j], w, b[j][s][0], b[j][s][1]);
+                        }
                     }
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int64_t n = token[m][h];
+                Eight<Y>& x = e[m % kSlots][h];
+                const int n = token[m][h];
                 if (n >= 0 && left > 0) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) e[h].add(j, c[j][2 * h], c[j][2 * h + 1]);
+                    for (int j = 0; j < 4; ++j) x.add(j, c[j][2 * h], c[j][2 * h + 1]);
                     Y* const p = static_cast<Y*>(a.out) + n * a.out_stride + v;
-                    if (whole) e[h].store(p);
-                    else e[h].store_some(p, left);
+                    if (whole) x.store(p);
+                    else x.store_some(p, left);
                 }
-                e[h] = next[h];
             }
         }
     }
