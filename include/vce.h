@@ -23,10 +23,11 @@
  *       "Implementation": forward GEMM fused with NLL/LSE, backward = logits
  *       recomputation, dX and dW).
  *
- *   output head  rms_norm_*, mx_*, ce_sample
+ *   output head  rms_norm_*, mx_*, adapter_linear, ce_sample, ce_beam, beam_reorder
  *       What surrounds the loss in a model: the norm before the classifier (forward,
  *       8-bit, backward), microscaled tensors and the product that gives a quantised
- *       classifier's logits, and the draw of a token from logits.
+ *       classifier's logits, adapters beside it, and what follows from logits: the draw of a
+ *       token, or a beam search's next hypotheses and its states after them.
  *
  * Common conventions
  *   - Every pointer argument is a DEVICE pointer unless said otherwise; the
@@ -95,7 +96,8 @@ typedef enum vce_dtype {
 #define VCE_DEVSTATUS_BOUNDS 4
 
 /* ce_sample: a row from which no token can be drawn (every logit -inf, a NaN or +inf
- * among the logits, or a NaN parameter); its token is -1. */
+ * among the logits, or a NaN parameter); its token is -1.  ce_beam: a beam that offers
+ * nothing for such a reason. */
 #define VCE_DEVSTATUS_BAD_ROW 8
 
 /* beam_reorder, adapter_linear: an index outside its range; what it names counts as absent. */
@@ -324,8 +326,8 @@ size_t ce_beam_workspace_size(int64_t batch, int beams, int count);
  *            places in their order, so that beam_reorder moves no beam that has a child.
  *   token, parent  int64 [batch, count]; out_score F32; out_ended uint8 (required when ended is
  *            given or end >= 0, else may be NULL); out_length int32 (required when length is
- *            given, else NULL).  out_score, out_ended and out_length may be score, ended and
- *            length themselves.
+ *            given, else NULL).  With count == beams out_score, out_ended and out_length may be
+ *            score, ended and length themselves.
  *   ws       ce_beam_workspace_size bytes, 256-byte aligned.
  * Where a request offers fewer than ``count`` candidates the rest have token -1, score -inf,
  * ended 0, and the beam at their own place (modulo beams) as parent, with its length.  A beam
@@ -358,7 +360,7 @@ typedef struct vce_state {
  *
  *   states   HOST array of ``count`` states (read before the call returns).
  *   parent   int64 [batch, beams], as ce_beam writes it.  An entry outside [0, beams) counts as
- *            the beam itself and sets VCE_DEVSTATUS_BAD_INDEX.
+ *            the beam itself and sets VCE_DEVSTATUS_BAD_INDEX.  batch is at most 2^23.
  *   lengths  int32 [batch] or NULL; below 0 counts as 0, above a state's positions as all.
  */
 vce_status beam_reorder(const vce_state* states, int count, const int64_t* parent, int64_t batch, int beams,

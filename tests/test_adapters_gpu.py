@@ -132,6 +132,13 @@ def test_values_beyond_finite():
         assert torch.equal(out[6], clean[6]) and torch.isfinite(out[8]).all()
 
 
+def test_a_nan_whose_leading_half_is_an_infinity():
+    y, x, a, b, index, scale = make(6, 3, 64, 40, 8, 1, F32, F32, 0.0)
+    x[1, 9:10] = torch.tensor([0x7f800001], dtype=torch.int32, device="cuda").view(F32)
+    out = vce.adapter_linear(y, x, a, b, index, scale)
+    assert torch.isnan(out[1]).all() and torch.isfinite(out[::2]).all()
+
+
 def test_captured_and_on_another_stream():
     y, x, a, b, index, scale = make(6, 33, 128, 700, 16, 3, BF16, BF16)
     want = vce.adapter_linear(y, x, a, b, index, scale)

@@ -33,7 +33,9 @@ def test_beam_refusals():
                 dict(stride=99), dict(count=0), dict(count=65), dict(keep=1, count=3), dict(end=-2), dict(end=100),
                 dict(ended=FAKE, done=FAKE), dict(end=5), dict(ended=FAKE, end=5), dict(pen=17.0, length=FAKE, size=FAKE),
                 dict(pen=float("nan"), length=FAKE, size=FAKE), dict(pen=1.0), dict(length=FAKE), dict(size=FAKE),
-                dict(z=None), dict(score=None), dict(tok=None), dict(par=None), dict(sc=None), dict(batch=1 << 30)):
+                dict(z=None), dict(score=None), dict(tok=None), dict(par=None), dict(sc=None), dict(batch=1 << 30),
+                dict(count=3), dict(count=3, sc=FAKE + 64, ended=FAKE, end=5, done=FAKE),
+                dict(count=3, sc=FAKE + 64, length=FAKE, size=FAKE)):
         assert call(**bad) == INVALID, bad
     for bad in (dict(z=FAKE + 1), dict(score=FAKE + 2), dict(tok=FAKE + 4), dict(par=FAKE + 4), dict(sc=FAKE + 2),
                 dict(ws=FAKE + 128), dict(length=FAKE + 2, size=FAKE), dict(length=FAKE, size=FAKE + 2)):
@@ -63,7 +65,8 @@ def test_reorder_refusals():
     for bad in (dict(batch=-1), dict(beams=0), dict(beams=33), dict(parent=None), dict(count=-1), dict(states=False),
                 dict(src=None), dict(dst=None), dict(parts=-1), dict(positions=-1), dict(position_bytes=-1),
                 dict(src_row=-1), dict(dst_part=-5), dict(src_row=1 << 50), dict(positions=1 << 40, position_bytes=1 << 20),
-                dict(positions=1 << 62), dict(parts=1 << 46, positions=2), dict(dst_row=2048), dict(dst_part=1024)):
+                dict(positions=1 << 62), dict(parts=1 << 46, positions=2), dict(dst_row=2048), dict(dst_part=1024),
+                dict(batch=(1 << 23) + 1)):
         assert call(**bad) == INVALID, bad
     for bad in (dict(parent=FAKE + 4), dict(lengths=FAKE + 2)):
         assert call(**bad) == ALIGN, bad

@@ -109,7 +109,7 @@ def ce_beam(logits, score, *, ended=None, length=None, end=-1, length_penalty=0.
     Returns (token int64, parent int64, score, ended, length, dev_status), shaped like score with
     ``count`` in the last place; parent is an index among the request's beams.  ended is None
     where neither ``ended`` nor ``end`` is given, length where ``length`` is not.  The state of
-    a search can be updated in place: out_score=score, out_ended=ended, out_length=length.
+    a search can be updated in place where count is beams: out_score=score, out_ended=ended, out_length=length.
     Places for which nothing is offered get token -1 and score -inf.  A beam whose logits give
     no distribution offers nothing and sets a bit of ``dev_status`` (int32 [1]) where passed."""
     if stream is not None:

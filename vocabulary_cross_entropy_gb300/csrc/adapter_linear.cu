@@ -64,6 +64,7 @@ struct Plan {
 struct PlanArgs {
     const int* index;
     int n, adapters, copy;  // copy: tokens without an adapter get tiles too
+    int tiles_cap;          // how many tiles there is room for
     Plan* plan;
     Tile* tiles;
     int* perm;
@@ -120,14 +121,17 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan(const PlanArgs a) {
     for (int k = 0; k < kPer; ++k) {
         const int i = tid * kPer + k;
         if (i >= a.adapters) break;
-        for (int j = 0; j < c[k]; j += kTile) a.tiles[tile++] = {i, at + j, min(kTile, c[k] - j)};
+        for (int j = 0; j < c[k]; j += kTile, ++tile)
+            if (VCE_BOUNDS(tile < a.tiles_cap, a.dev_status)) a.tiles[tile] = {i, at + j, min(kTile, c[k] - j)};
         count[i] = at;
         at += c[k];
     }
     if (tid == kPlanThreads - 1) {  // the sums of all
         *a.plan = {upto.y, upto.y + (a.copy ? (none + kTile - 1) / kTile : 0), 0};
         if (a.copy)
-            for (int j = 0; j < none; j += kTile) a.tiles[upto.y + j / kTile] = {-1, upto.x + j, min(kTile, none - j)};
+            for (int j = 0; j < none; j += kTile)
+                if (VCE_BOUNDS(upto.y + j / kTile < a.tiles_cap, a.dev_status))
+                    a.tiles[upto.y + j / kTile] = {-1, upto.x + j, min(kTile, none - j)};
         count[a.adapters] = upto.x;
     }
     __syncthreads();
@@ -136,6 +140,13 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan(const PlanArgs a) {
         const int p = atomicAdd(&count[i >= 0 && i < a.adapters ? i : a.adapters], 1);
         if (VCE_BOUNDS(p >= 0 && p < a.n, a.dev_status)) a.perm[p] = n;
     }
+}
+
+// The token at a place of the order.
+__device__ __forceinline__ int token_at(const int* perm, int at, int n, int* dev_status) {
+    if (!VCE_BOUNDS(at >= 0 && at < n, dev_status)) return 0;
+    const int token = perm[at];
+    return VCE_BOUNDS(token >= 0 && token < n, dev_status) ? token : 0;
 }
 
 // ---------------------------------------------------------------------------
@@ -172,7 +183,7 @@ __device__ __forceinline__ void split(float x, uint32_t (&t)[TERMS]) {  // BF16 
         const uint32_t bits = __float_as_uint(rest);
         t[i] = last ? uint32_t(__bfloat16_as_ushort(__float2bfloat16_rn(rest))) : bits >> 16;
         const float d = rest - __uint_as_float(bits & 0xffff0000u);
-        rest = fabsf(rest) <= 3.402823466e38f ? d : 0.f;  // (an infinity or a NaN is the first term)
+        rest = fabsf(rest) == INFINITY ? 0.f : d;  // (a NaN's later terms are NaN: its first one's bits may be an infinity's)
     }
 }
 
@@ -222,7 +233,8 @@ __global__ void __launch_bounds__(kThreads) adapter_shrink(const ShrinkArgs a) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int p = m * 16 + h * 8 + g;
-            row[m][h] = p < tile.count ? static_cast<const X*>(a.x) + a.perm[tile.start + p] * a.x_stride : nullptr;
+            row[m][h] = p < tile.count ? static_cast<const X*>(a.x) + token_at(a.perm, tile.start + p, a.n, a.dev_status) * a.x_stride
+                                       : nullptr;
         }
     float c[kMTiles][kRankBlock / 8][4] = {};
     const __nv_bfloat16* const base = a.a + (int64_t(tile.adapter) * a.rank + r0) * a.hidden;
@@ -298,7 +310,8 @@ __global__ void __launch_bounds__(kThreads) adapter_shrink(const ShrinkArgs a) {
             s += v;
         }
         const int p = e / kRankBlock, r = r0 + e % kRankBlock;
-        if (p < tile.count && r < a.rank) a.t[int64_t(tile.start + p) * a.rank + r] = s;
+        if (p < tile.count && r < a.rank && VCE_BOUNDS(tile.start + p < a.n, a.dev_status))
+            a.t[int64_t(tile.start + p) * a.rank + r] = s;
     }
     cluster_sync();  // nobody leaves while its shared memory is read
 }
@@ -314,7 +327,7 @@ struct ExpandArgs {
     const void* y;
     void* out;
     int64_t y_stride, out_stride;
-    int vocab, rank;
+    int n, vocab, rank;
     int stages, stage_bytes, y_bytes;  // of the ring; of a stage; of its rows of y
     int block[4];                      // logits of a stage, by class_of a tile
     Plan* plan;
@@ -425,7 +438,9 @@ __global__ void __launch_bounds__(Shape<Y, KS>::kWarps * 32 + 32, 1) adapter_exp
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int p = lane + 32 * h;
-                    row[h] = p < tile.count ? reinterpret_cast<uintptr_t>(static_cast<const Y*>(a.y) + a.perm[tile.start + p] * a.y_stride) : 0;
+                    row[h] = p < tile.count ? reinterpret_cast<uintptr_t>(static_cast<const Y*>(a.y) +
+                                                                          token_at(a.perm, tile.start + p, a.n, a.dev_status) * a.y_stride)
+                                            : 0;
                 }
             }
             const int v0 = end ? 0 : unit % runs * run, v1 = end ? 1 : min(v0 + run, a.vocab);
@@ -453,7 +468,8 @@ __global__ void __launch_bounds__(Shape<Y, KS>::kWarps * 32 + 32, 1) adapter_exp
                             Y* const at = reinterpret_cast<Y*>(to + (lane + 32 * h) * pitch + (s - low));
                             for (uintptr_t x = s; x < e; x += ES) {
                                 if (x >= f && x < l) x = l;
-                                if (x < e) at[(x - s) / ES] = *reinterpret_cast<const Y*>(x);
+                                if (x < e && VCE_BOUNDS(lane + 32 * h < tile.count && x - low + ES <= uintptr_t(pitch), a.dev_status))
+                                    at[(x - s) / ES] = *reinterpret_cast<const Y*>(x);
                             }
                             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before a later round's copies
                         }
@@ -554,7 +570,7 @@ __global__ void __launch_bounds__(Shape<Y, KS>::kWarps * 32 + 32, 1) adapter_exp
                     const int p = 8 * j + 2 * q + e;
                     to[j][e] = nullptr, place[j][e] = 0;
                     if (p < count) {
-                        const int64_t n = a.perm[tile.start + p0 + p];
+                        const int64_t n = token_at(a.perm, tile.start + p0 + p, a.n, a.dev_status);
                         to[j][e] = static_cast<Y*>(a.out) + n * a.out_stride;
                         place[j][e] = (p0 + p) * pitch + int(reinterpret_cast<uintptr_t>(static_cast<const Y*>(a.y) + n * a.y_stride) & 15);
                     }
@@ -567,7 +583,7 @@ __global__ void __launch_bounds__(Shape<Y, KS>::kWarps * 32 + 32, 1) adapter_exp
                     for (int s = 0; s < KS; ++s) {
                         const int p = 8 * j + g, r = rank_of<KS>(s, q);
                         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (p < count && r < a.rank)
+                        if (p < count && r < a.rank && VCE_BOUNDS(tile.start + p0 + p < a.n, a.dev_status))
                             x = *reinterpret_cast<const float4*>(a.t + int64_t(tile.start + p0 + p) * a.rank + r);
                         uint32_t w[2][TERMS];
                         split2<TERMS>(x.x * scale, x.y * scale, w[0]);
@@ -583,6 +599,10 @@ __global__ void __launch_bounds__(Shape<Y, KS>::kWarps * 32 + 32, 1) adapter_exp
         for (int vc = part * 32; vc < here && count > 0; vc += parts * 32) {
             uint8_t* const yc = y + vc * ES;
             const int64_t vo = what.y + vc;
+            if (!VCE_BOUNDS(vo >= 0 && what.y + here <= a.vocab && (vc + 32) * ES + 16 <= pitch &&
+                                (vc + 32) * b_row <= a.stage_bytes - a.y_bytes && tile.count * pitch <= a.y_bytes,
+                            a.dev_status))
+                break;
             if (tile.adapter >= 0) {
                 float c[2][2][4];
                 const uint8_t* const b = y + a.y_bytes + (vc + 4 * g) * b_row;
@@ -771,7 +791,7 @@ __global__ void __launch_bounds__(kThreads, KS <= 4 ? 2 : 1) adapter_expand_many
                     for (int h = 0; h < 2; ++h) {
                         const int p = m * 16 + h * 8 + (l >> 2);
                         v[h] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (p < tile.count && r < a.rank)
+                        if (p < tile.count && r < a.rank && VCE_BOUNDS(tile.start + p < a.n, a.dev_status))
                             v[h] = *reinterpret_cast<const float4*>(a.t + int64_t(tile.start + p) * a.rank + r);
                     }
                     uint32_t w[4][TERMS];
@@ -787,7 +807,7 @@ __global__ void __launch_bounds__(kThreads, KS <= 4 ? 2 : 1) adapter_expand_many
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int p = m * 16 + h * 8 + g;
-                    token[m][h] = p < tile.count ? a.perm[tile.start + p] : -1;
+                    token[m][h] = p < tile.count ? token_at(a.perm, tile.start + p, a.n, a.dev_status) : -1;
                 }
             __syncthreads();
         }
@@ -799,6 +819,7 @@ __global__ void __launch_bounds__(kThreads, KS <= 4 ? 2 : 1) adapter_expand_many
             e.clear();  // (a load that may not be made would wait for what the registers held)
             if (n < 0 || left <= 0) return;
             const Y* const p = static_cast<const Y*>(a.y) + n * a.y_stride + v;
+            if (!VCE_BOUNDS(aligned16(p) && v >= 0, a.dev_status)) return;
             if (whole) e.load(p);
             else e.load_some(p, left);
         };
@@ -841,6 +862,7 @@ __global__ void __launch_bounds__(kThreads, KS <= 4 ? 2 : 1) adapter_expand_many
 #pragma unroll
                     for (int j = 0; j < 4; ++j) x.add(j, c[j][2 * h], c[j][2 * h + 1]);
                     Y* const p = static_cast<Y*>(a.out) + n * a.out_stride + v;
+                    if (!VCE_BOUNDS(aligned16(p), a.dev_status)) continue;
                     if (whole) x.store(p);
                     else x.store_some(p, left);
                 }
@@ -903,7 +925,7 @@ vce_status launch_adapter_linear(const void* y, int y_dtype, int64_t n, int64_t 
     if (n == 0) return VCE_OK;
     const Carved w = carve(ws, n, adapters, rank);
     const bool in_place = out == y;
-    const PlanArgs pa{index, int(n), int(adapters), !in_place, w.plan, w.tiles, w.perm, dev_status};
+    const PlanArgs pa{index, int(n), int(adapters), !in_place, int(most_tiles(n, adapters)), w.plan, w.tiles, w.perm, dev_status};
     count_launch();
     adapter_plan<<<1, kPlanThreads, 0, s>>>(pa);
     if (cudaGetLastError() != cudaSuccess) return VCE_ERR_CUDA;
@@ -931,7 +953,7 @@ vce_status launch_adapter_linear(const void* y, int y_dtype, int64_t n, int64_t 
     auto expand = y_dtype == VCE_BF16
                       ? (vectors ? expand_kernel<__nv_bfloat16, true>(ks, &threads) : expand_kernel<__nv_bfloat16, false>(ks, &threads))
                       : (vectors ? expand_kernel<float, true>(ks, &threads) : expand_kernel<float, false>(ks, &threads));
-    ExpandArgs ea{static_cast<const __nv_bfloat16*>(b), scale, w.t, y, out, y_stride, out_stride, int(vocab), rank, 0, 0, 0,
+    ExpandArgs ea{static_cast<const __nv_bfloat16*>(b), scale, w.t, y, out, y_stride, out_stride, int(n), int(vocab), rank, 0, 0, 0,
                   {}, w.plan, w.tiles, w.perm, dev_status};
     int b_bytes = 0;
     for (int rows : {4, 16, 32, 64}) {

@@ -67,6 +67,7 @@ bool mx_ok(int fmt) { return fmt == VCE_MX_E4M3 || fmt == VCE_MX_E2M1; }
 constexpr int64_t kMaxRows = 0x7fffff00;
 constexpr int64_t kMaxCols = int64_t(1) << 28;
 constexpr int64_t kMaxTokens = int64_t(1) << 27;  // of adapter_linear, whose grid has eight blocks for each
+constexpr int64_t kMaxReorder = int64_t(1) << 23;  // requests of beam_reorder: a grid dimension of groups of 256
 
 vce_status check_norm(int dtype, int64_t n, int64_t hidden, const void* x, int64_t x_stride, const void* residual,
                       int64_t residual_stride, const void* weight, int weight_dtype, float eps, const void* h,
@@ -403,6 +404,9 @@ vce_status ce_beam(const void* logits, int dtype, int64_t batch, int beams, int6
                       (length && !out_length)))
         return VCE_ERR_INVALID_ARG;
     if (!length && out_length) return VCE_ERR_INVALID_ARG;
+    // a request's results over another one's state
+    if (batch > 0 && count != beams && (out_score == score || (ended && out_ended == ended) || (length && out_length == length)))
+        return VCE_ERR_INVALID_ARG;
     if (!aligned(logits, elem_size(dtype)) || !aligned(score, 4) || !aligned(length, 4) || !aligned(token, 8) ||
         !aligned(parent, 8) || !aligned(out_score, 4) || !aligned(out_length, 4) || !aligned(ws, 256))
         return VCE_ERR_ALIGN;
@@ -418,7 +422,7 @@ vce_status beam_reorder(const vce_state* states, int count, const int64_t* paren
                         const int32_t* lengths, int* dev_status, void* stream) {
     constexpr int64_t kMost = int64_t(1) << 46;  // bytes; keeps every product below in 63 bits
     if (count < 0 || (count > 0 && !states) || batch < 0 || batch > kMaxRows || beams < 1 ||
-        beams > VCE_BEAM_MAX_BEAMS || batch * beams > kMaxRows)
+        beams > VCE_BEAM_MAX_BEAMS || batch * beams > kMaxRows || batch > kMaxReorder)
         return VCE_ERR_INVALID_ARG;
     for (int i = 0; i < count; ++i) {
         const vce_state& s = states[i];
