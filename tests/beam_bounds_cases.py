@@ -83,7 +83,8 @@ def main():
         r = status_of(lambda st: vce.ce_beam(same, torch.zeros(2, 1, device=DEV), count=5, dev_status=st))
         assert r.token.tolist() == [[0, 1, 2, 3, 4]] * 2
         for n, h, v, r, count in ((1, 64, 9, 8, 1), (70, 136, 1001, 16, 3), (300, 256, 4096, 64, 2), (40, 72, 333, 128, 9),
-                                  (257, 2056, 2001, 24, 20), (900, 64, 640, 32, 1), (5, 8, 100000, 16, 5)):
+                                  (257, 2056, 2001, 24, 20), (900, 64, 640, 32, 1), (5, 8, 100000, 16, 5),
+                                  (40, 264, 32001, 8, 40), (150, 72, 32000, 32, 50)):
             for pad, offset in ((0, 0), (3, 1), (8 - v % 8, 0)):
                 for xt in (torch.bfloat16, torch.float32):
                     adapters(n, h, v, r, count, xt, dtype, pad, offset)

@@ -85,6 +85,39 @@ def test_rows_anywhere(pad, offset, yt):
     assert torch.equal(around, y._base)
 
 
+@pytest.mark.parametrize("yt", [BF16, F32])
+@pytest.mark.parametrize("n,v,r,count,none,pad,offset", [(40, 32001, 8, 40, 0.0, 0, 0), (70, 32000, 16, 40, 0.0, 0, 0),
+                                                         (150, 32004, 32, 50, 0.3, 3, 1), (600, 16001, 24, 60, 0.1, 0, 3),
+                                                         (600, 16000, 32, 60, 0.1, 8, 8), (128, 40000, 8, 33, 0.5, 8, 0)])
+def test_much_work_of_few_tokens(n, v, r, count, none, pad, offset, yt):
+    """More logits of more adapters than there are blocks for at once, half of the tokens with one adapter."""
+    y, x, a, b, index, scale = make(n + r, n, 264, v, r, count, F32 if n == 128 else BF16, yt, none, pad, offset)
+    index[:n // 2:2] = 1
+    out = vce.adapter_linear(y, x, a, b, index, scale)
+    check(out, y, x, a, b, index, scale)
+    for i in (0, 1, n - 1):  # by itself, which is little work
+        assert torch.equal(vce.adapter_linear(y[i:i + 1], x[i:i + 1], a, b, index[i:i + 1], scale)[0], out[i])
+    base = y.storage_offset(), y._base if y._base is not None else y
+    around = base[1].clone()
+    place = around[:, offset:offset + v] if pad or offset else around
+    vce.adapter_linear(place, x, a, b, index, scale, out=place)
+    assert torch.equal(place, out)
+    if pad or offset:  # what lies between rows stays
+        assert torch.equal(around[:, :offset], base[1][:, :offset]) and torch.equal(around[:, offset + v:], base[1][:, offset + v:])
+
+
+@pytest.mark.parametrize("n", [127, 128, 129])
+def test_tokens_of_one_adapter_and_of_none(n):
+    """Tiles that are full, and the border at which the tokens are sorted in another kernel."""
+    y, x, a, b, index, scale = make(n, n, 64, 300, 16, 3, BF16, F32, 0.0)
+    for which in (torch.full_like(index, 2), torch.full_like(index, -1),
+                  torch.where(torch.arange(n, device=DEV) < 65, 1, -1).int(), torch.where(torch.arange(n, device=DEV) < 64, -1, 0).int()):
+        out = vce.adapter_linear(y, x, a, b, which, scale)
+        check(out, y, x, a, b, which, scale)
+        place = y.clone()
+        assert torch.equal(vce.adapter_linear(place, x, a, b, which, scale, out=place), out)
+
+
 def test_a_token_does_not_depend_on_its_neighbours():
     y, x, a, b, index, scale = make(3, 300, 264, 1003, 16, 4, BF16, F32)
     out = vce.adapter_linear(y, x, a, b, index, scale)

@@ -2,16 +2,16 @@
 //     out_n = y_n + s_i B_i (A_i x_n),   i = index[n],   A_i [r, H], B_i [V, r].
 //
 // Three kernels.  One sorts the tokens by their adapters, in tiles of at most 64 of one
-// adapter.  The second computes t_n = A_i x_n, a tile shared by a cluster of blocks that
-// divide the hidden dimension.  The third adds s_i B_i t_n to y: it reads each adapter's B
+// adapter (few tokens are sorted by each block of the second).  The second computes t_n = A_i x_n, a
+// tile shared by a cluster of blocks that divide the hidden dimension.  The third adds s_i B_i t_n to y: it reads each adapter's B
 // once per tile and y once.  Each starts while the one before still runs, up to its wait for it.
 //
 // The last one carries the work, and its bytes are the floor: a token's 2 r operations per
 // logit are few beside the logit's read and write (r = 64: 32 per byte, where the memory takes
 // as long as 290).  So the products go through the warp-level tensor instruction, whose results
 // lie in the registers of the lanes that hold the logits; the block-level one would take each logit
-// through tensor memory as well.  There are two forms of it, for few and for many tokens per
-// adapter: adapter_expand_few and adapter_expand_many.  They add the same products in the same order, and
+// through tensor memory as well.  There are two forms of it: adapter_expand_few for much work of few tokens
+// per adapter and small ranks, adapter_expand_many for the others.  They add the same products in the same order, and
 // a token's result does not depend on which one takes it.
 //
 // Precision.  t is FP32 and is multiplied as a sum of BF16 terms, three (all 24 bits) for FP32
@@ -22,6 +22,7 @@
 #include "sm100_ptx.cuh"
 
 #include <algorithm>
+#include <climits>
 #include <mutex>
 #include <type_traits>
 
@@ -34,14 +35,18 @@ constexpr int kTile = 64;             // tokens of a tile
 constexpr int kMTiles = kTile / 16;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kSlices = 8;            // blocks of a cluster that divide the hidden dimension
+constexpr int kSlices = 8;            // blocks of a cluster that divide the hidden dimension, at most
+constexpr int kSelf = 128;            // tokens that the second kernel sorts by itself
 constexpr int kRankBlock = 32;        // ranks per block of the second kernel
 constexpr int kVWarp = 32;            // logits of a warp, and
 constexpr int kVBlock = kWarps * kVWarp;  // of a block of adapter_expand_many
 constexpr int kRun = 512;             // logits of a unit that is handed out, or a multiple
 constexpr int kMaxStages = 6;         // of adapter_expand_few's ring
 constexpr int kRingBytes = 208 << 10;
-constexpr int64_t kMany = 24;         // tokens per adapter from which adapter_expand_many takes them
+constexpr int64_t kMany = 24;         // tokens per adapter from which adapter_expand_many takes them, and
+constexpr int kShort = 13, kShortAny = 7;  // units of its work per block up to which it does (any alignment)
+constexpr int kMulWarps = 16;         // warps of adapter_expand_few that multiply
+constexpr int kCellPitch = 292;       // floats: a row of kVBlock products, one unused behind every eight (no bank conflicts)
 constexpr int kMaxBlock = 1024;       // logits of a stage, at most
 constexpr int kStageRows = 32 << 10;  // bytes of y in a stage, and
 constexpr int kStageB = 32 << 10;     // of B
@@ -201,6 +206,8 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t (&t)[TERMS]) {
 // ---------------------------------------------------------------------------
 
 struct ShrinkArgs {
+    PlanArgs plan_args;
+    int slices;  // blocks of a cluster
     const void* x;
     int64_t x_stride;
     const __nv_bfloat16* a;  // [adapters, rank, hidden]
@@ -212,19 +219,89 @@ struct ShrinkArgs {
     int* dev_status;
 };
 
-// A warp takes every 64th run of 32 hidden values: sums of at most hidden / 64 products stay in
+// The order of up to kSelf tokens, which every block finds for itself: a token's place is the number of those
+// before it.  The first block leaves it to the next kernel.  Returns this block's tile (count 0: none).
+struct Sorted {
+    int key[kSelf], order[kSelf];
+    uint32_t starts[kSelf / 32];  // a bit for each place at which a tile starts
+    int none;                     // tokens without an adapter, which come last
+    Tile tile;
+};
+
+__device__ __forceinline__ Tile plan_here(const PlanArgs& a, Sorted& sh, int id, bool first) {
+    const int tid = threadIdx.x;
+    int adapter = 0;
+    if (tid < kSelf) {
+        if (tid < a.n) {
+            adapter = a.index[tid];
+            if (adapter < 0 || adapter >= a.adapters) {
+                if (adapter != -1 && first) report(a.dev_status, VCE_DEVSTATUS_BAD_INDEX);
+                adapter = a.adapters;
+            }
+        }
+        sh.key[tid] = tid < a.n ? adapter * kSelf + tid : INT_MAX;
+    }
+    if (tid < kSelf / 32) sh.starts[tid] = 0;
+    if (tid == 0) sh.none = 0, sh.tile.count = 0;
+    __syncthreads();
+    int place = 0, less = 0, same = 0;
+    if (tid < a.n) {
+        const int low = adapter * kSelf, high = low + kSelf, mine = low + tid;
+        for (int j = 0; j < a.n; j += 4) {  // (what is behind the last token is above every key)
+            const int4 k = *reinterpret_cast<const int4*>(&sh.key[j]);
+            place += (k.x < mine) + (k.y < mine) + (k.z < mine) + (k.w < mine);
+            less += (k.x < low) + (k.y < low) + (k.z < low) + (k.w < low);
+            same += (k.x < high) + (k.y < high) + (k.z < high) + (k.w < high);
+        }
+        same -= less;
+        sh.order[place] = tid;
+        if ((place - less) % kTile == 0) atomicOr(&sh.starts[place / 32], 1u << place % 32);
+        if (adapter == a.adapters && place == less) sh.none = same;
+    }
+    __syncthreads();
+    if (tid < a.n && (place - less) % kTile == 0) {
+        int which = __popc(sh.starts[place / 32] & ((1u << place % 32) - 1));
+        for (int w = 0; w < place / 32; ++w) which += __popc(sh.starts[w]);
+        const bool has = adapter < a.adapters;
+        const Tile tile{has ? adapter : -1, place, min(kTile, same - (place - less))};
+        if (has && which == id) sh.tile = tile;
+        if (first && (has || a.copy) && VCE_BOUNDS(which < a.tiles_cap, a.dev_status)) a.tiles[which] = tile;
+    }
+    if (first) {
+        if (tid < a.n) a.perm[place] = tid;
+        if (tid == 0) {
+            int all = 0;
+            for (uint32_t w : sh.starts) all += __popc(w);
+            const int none = (sh.none + kTile - 1) / kTile;
+            *a.plan = {all - none, a.copy ? all : all - none, 0};
+        }
+    }
+    __syncthreads();
+    return sh.tile;
+}
+
+// A warp takes every (8 slices)-th run of 32 hidden values: sums of few products stay in
 // the instruction's accumulator, what is left is added up in FP32, in a fixed order.
-template <typename X>
-__global__ void __launch_bounds__(kThreads) adapter_shrink(const ShrinkArgs a) {
+template <typename X, bool SELF>
+__global__ void __launch_bounds__(kThreads, 2) adapter_shrink(const ShrinkArgs a) {
     constexpr int TERMS = sizeof(X) == 2 ? 1 : 3;
     extern __shared__ __align__(16) float red[];  // [warps][tile][kRankBlock]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
     const int slice = int(cluster_ctarank());
     cudaTriggerProgrammaticLaunchCompletion();
     cudaGridDependencySynchronize();
-    const int id = int(blockIdx.x) / kSlices;
-    if (id >= a.plan->n_work) return;  // the whole cluster
-    const Tile tile = a.tiles[id];
+    const int id = int(blockIdx.x) / a.slices;
+    Tile tile;
+    __shared__ __align__(16) char sorted_mem[SELF ? sizeof(Sorted) : 16];
+    Sorted& sorted = *reinterpret_cast<Sorted*>(sorted_mem);
+    if constexpr (SELF) {
+        tile = plan_here(a.plan_args, sorted, id, blockIdx.x == 0 && blockIdx.y == 0);
+        if (tile.count == 0) return;  // the whole cluster
+    } else {
+        if (id >= a.plan->n_work) return;
+        tile = a.tiles[id];
+    }
+    auto token = [&](int p) { return SELF ? sorted.order[tile.start + p] : token_at(a.perm, tile.start + p, a.n, a.dev_status); };
     const int r0 = int(blockIdx.y) * kRankBlock, mtiles = (tile.count + 15) / 16;
 
     const X* row[kMTiles][2];
@@ -233,12 +310,11 @@ __global__ void __launch_bounds__(kThreads) adapter_shrink(const ShrinkArgs a) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int p = m * 16 + h * 8 + g;
-            row[m][h] = p < tile.count ? static_cast<const X*>(a.x) + token_at(a.perm, tile.start + p, a.n, a.dev_status) * a.x_stride
-                                       : nullptr;
+            row[m][h] = p < tile.count ? static_cast<const X*>(a.x) + token(p) * a.x_stride : nullptr;
         }
     float c[kMTiles][kRankBlock / 8][4] = {};
     const __nv_bfloat16* const base = a.a + (int64_t(tile.adapter) * a.rank + r0) * a.hidden;
-    for (int k = (slice * kWarps + warp) * 32 + q * 8; k - q * 8 < a.hidden; k += kSlices * kWarps * 32) {
+    for (int k = (slice * kWarps + warp) * 32 + q * 8; k - q * 8 < a.hidden; k += a.slices * kWarps * 32) {
         uint4 b[kRankBlock / 8];
 #pragma unroll
         for (int j = 0; j < kRankBlock / 8; ++j) {
@@ -300,11 +376,12 @@ __global__ void __launch_bounds__(kThreads) adapter_shrink(const ShrinkArgs a) {
         red[e] = s;
     }
     cluster_sync();
-    const int share = entries / kSlices;  // entries are a multiple of 512
+    const int share = entries / a.slices;  // entries are a multiple of 512
     for (int e = slice * share + tid; e < (slice + 1) * share; e += kThreads) {
         float s = 0.f;
 #pragma unroll
         for (int k = 0; k < kSlices; ++k) {
+            if (k >= a.slices) break;
             float v;
             asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(smem_u32(&red[e]), k)) : "memory");
             s += v;
@@ -363,14 +440,6 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&x)[4]) {
     *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-// By the logits' type and the steps of 16 ranks: terms of t, and warps that multiply (t's operands stay in
-// registers).
-template <typename Y, int KS>
-struct Shape {
-    static constexpr int kTerms = sizeof(Y) == 2 ? 2 : 3;
-    static constexpr int kWarps = KS * kTerms >= 12 ? 8 : 16;
-};
-
 // Tiles by how many tokens they have: up to 4, 16, 32, 64.
 __host__ __device__ __forceinline__ int class_of(int count) { return count > 32 ? 3 : count > 16 ? 2 : count > 4 ? 1 : 0; }
 
@@ -380,7 +449,7 @@ struct Ring {
     int abort;
 };
 
-// Tiles of few tokens, or rows that start anywhere.  Logits are the rows of the products (16) and tokens the
+// Tiles of few tokens, where there are many or many logits, and ranks up to 32.  Logits are the rows of the products (16) and tokens the
 // columns (8): a tile of one token costs no more than one of eight.  A warp takes 16 tokens and 32 logits at a time;
 // what warps the tokens leave divide the logits.  A further warp copies y's rows and B, some logits at a
 // time, through a ring in shared memory.  Units of work are handed out by a counter, the larger ones first: tiles
@@ -391,15 +460,15 @@ struct Ring {
 // that a warp writes neighbours of one row.
 //
 // 64 tokens with 35 adapters of rank 16, 128256 FP32 logits: 47 us (4.3 TB/s), of which the copies alone take
-// 40; the others are the multiplying warps' instructions, about 160 for 32 logits of a token.  257 x 32001
-// BF16 logits (odd rows), 20 adapters of rank 8: 30 us; with a unit of work for each block from the start
-// 41, and with elements loaded one by one 90.
+// 40; the others are the multiplying warps' instructions, about 160 for 32 logits of a token.  256 tokens with 64
+// adapters, rank 16, BF16, all three kernels, this form / the other one: 128256 logits 91 / 160 us, 128257
+// (rows off 16-byte boundaries) 129 / 222.
 //
-// What bounds it for larger tiles is its copies, one for each row and stage: 66 cycles each.
+// What bounds it for larger tiles is its copies, one for each row and stage: 66 cycles each.  Larger ranks are the other
+// one's because t's operands no longer fit this one's registers (rank 64, the same: 407 / 225).
 template <typename Y, int KS, bool VEC>
-__global__ void __launch_bounds__(Shape<Y, KS>::kWarps * 32 + 32, 1) adapter_expand_few(const __grid_constant__ ExpandArgs a) {
-    using S = Shape<Y, KS>;
-    constexpr int TERMS = S::kTerms, kMulWarps = S::kWarps, ES = int(sizeof(Y));
+__global__ void __launch_bounds__(kMulWarps * 32 + 32, 1) adapter_expand_few(const __grid_constant__ ExpandArgs a) {
+    constexpr int TERMS = sizeof(Y) == 2 ? 2 : 3, ES = int(sizeof(Y));
     extern __shared__ __align__(128) uint8_t smem[];  // stages: rows of y, then B
     __shared__ Ring ring;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
@@ -722,6 +791,71 @@ struct Eight<float> {
     }
 };
 
+// Up to kVBlock neighbouring logits of a row that starts anywhere, held by a warp: whole vectors by the address that is
+// written, and an element per lane of what comes before and behind them.
+template <typename Y>
+struct SomeRow {
+    static constexpr int VE = 16 / int(sizeof(Y)), kChunks = kVBlock / VE / 32;
+    uint32_t v[kChunks][4];
+    Y single;
+
+    // Elements of a row before its first 16-byte boundary.
+    __device__ __forceinline__ static int before(const Y* p) {
+        return int((16 - (reinterpret_cast<uintptr_t>(p) & 15)) % 16 / sizeof(Y));
+    }
+    // This lane's single element of ``n``, or -1.
+    __device__ __forceinline__ static int one(int head, int n) {
+        const int lane = threadIdx.x & 31, i = lane < VE ? lane : ((n - head) & ~(VE - 1)) + head + lane - VE;
+        return i < (lane < VE ? head : n) ? i : -1;
+    }
+    __device__ __forceinline__ static uint32_t word(const float* p) { return __float_as_uint(*p); }
+    __device__ __forceinline__ static uint32_t word(const __nv_bfloat16* p) {
+        return uint32_t(__bfloat16_as_ushort(p[0])) | uint32_t(__bfloat16_as_ushort(p[1])) << 16;
+    }
+    // ``head`` (at most n) elements lie before out's vectors; ``alike``: and before y's.
+    __device__ __forceinline__ void load(const Y* y, int head, bool alike, int n) {
+        const int lane = threadIdx.x & 31, whole = (n - head) / VE;
+        const Y* const at = y + head + lane * VE;
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k) {
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (lane + 32 * k < whole) {
+                const Y* const x = at + 32 * VE * k;
+                if (alike) w = *reinterpret_cast<const uint4*>(x);
+                else w = make_uint4(word(x), word(x + VE / 4), word(x + VE / 2), word(x + 3 * VE / 4));
+            }
+            v[k][0] = w.x, v[k][1] = w.y, v[k][2] = w.z, v[k][3] = w.w;
+        }
+        const int i = one(head, n);
+        single = Y(0.f);
+        if (i >= 0) single = y[i];
+    }
+    // ``sums``: of logit i at i + i / 8.
+    __device__ __forceinline__ void add(Y* out, int head, int n, const float* sums) {
+        const int lane = threadIdx.x & 31, whole = (n - head) / VE;
+        auto sum = [&](int i) { return sums[i + (i >> 3)]; };
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k) {
+            if (lane + 32 * k >= whole) continue;
+            const int i0 = head + (lane + 32 * k) * VE;
+            if constexpr (VE == 4) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[k][i] = __float_as_uint(__uint_as_float(v[k][i]) + sum(i0 + i));
+            } else {
+                const float* const at = sums + 9 * lane + head;
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = at[i + (head + i >= 8)];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[k][i] = Eight<__nv_bfloat16>::sum(v[k][i], x[2 * i], x[2 * i + 1]);
+            }
+            *reinterpret_cast<uint4*>(out + i0) = make_uint4(v[k][0], v[k][1], v[k][2], v[k][3]);
+        }
+        const int i = one(head, n);
+        if (i >= 0) put(out + i, to_float(single) + sum(i));
+    }
+};
+
 // Operands of B for logits v0 .. v0 + 31 of adapter_expand_many.
 template <int KS>
 __device__ __forceinline__ void load_b(uint32_t (&b)[4][KS][2], const ExpandArgs& a, int adapter, int v0) {
@@ -748,36 +882,56 @@ __device__ __forceinline__ void load_b(uint32_t (&b)[4][KS][2], const ExpandArgs
     }
 }
 
-// Many tokens to an adapter, in rows that start at 16-byte boundaries.  Tokens are the rows of the products (16)
+// Many tokens to an adapter, large ranks, or little work.  Tokens are the rows of the products (16)
 // and logits the columns (8): column 2 q + e of product j is logit 8 q + 2 j + e of the warp's 32, so that
 // a lane ends up with eight neighbours of a row.  A warp loads B's operands once for all tokens of a tile, and
 // the next rows of y while it multiplies.
 //
 // Units are blocks of kVBlock logits of a tile, tiles of the same logits next to each other: blocks that
-// work at the same time read the same part of B.  Where tiles are few a block stays with its tile.
+// work at the same time read the same part of B.  Where tiles are few a block stays with its tile; where they hold few
+// tokens a unit has several blocks of logits, so that the tile's operands of t are put together less often.
 //
-// 2048 tokens with 6 adapters of rank 64, 128256 BF16 logits: 266 us (4.2 TB/s); FP32 logits 390 (5.7).  It is
+// Rows that start anywhere (VEC false): the products of 16 tokens go through shared memory, from which each warp
+// adds them to two rows, in the vectors that lie at 16-byte boundaries of the row; what is left at the ends of
+// its kVBlock logits takes an element per lane.
+//
+// 2048 tokens with 6 adapters of rank 64, 128256 BF16 logits: 266 us (4.2 TB/s).  It is
 // bound by what 16 warps per SM keep on its way between their instructions.  More rows on their way help small
 // ranks (512 x 128256, rank 16, BF16: 86 -> 76 us in all) and cost as much with large ones (2048 tokens of rank
-// 64: 291 -> 318).  512 x 128256, rank 16, this form / the other one in us in all: 16 tokens per adapter
-// 110 / 96 (BF16), 137 / 128 (FP32); 32 tokens 80 / 103 and 117 / 163; hence kMany.
-template <typename Y, int KS>
+// 64: 291 -> 318).  Rows of 128257 logits take 460 (element by element through the warps' own shared memory 660).
+//
+// All three kernels in us, this form / the other one: 512 x 128256, rank 16, 16 tokens per adapter
+// 110 / 96 (BF16), 137 / 128 (FP32); 32 tokens 80 / 103 and 117 / 163; hence kMany.  16 tokens with 16 adapters, rank 16,
+// BF16: 8000 logits 13 / 15, 32000 17 / 21, 128256 29 / 27; 32 with 32: 15 / 17, 21 / 22, 52 / 41; hence kShort.
+// Off 16-byte boundaries 257 with 20, 32001 logits 45 / 37; 16 with 16 19 / 21; hence kShortAny.
+// 1024 with 64, 128256 FP32: rank 32 398 / 346, rank 64 504 / 451, in BF16 319 / 245 and 368 / 680.
+template <typename Y, int KS, bool VEC>
 __global__ void __launch_bounds__(kThreads, KS <= 4 ? 2 : 1) adapter_expand_many(const __grid_constant__ ExpandArgs a) {
-    constexpr int TERMS = sizeof(Y) == 2 ? 2 : 3, kAhead = KS > 2 ? 1 : sizeof(Y) == 2 ? 4 : 3;  // groups of 16 rows on their way
+    constexpr int TERMS = sizeof(Y) == 2 ? 2 : 3;
+    constexpr int kAhead = KS > 2 || !VEC ? 1 : sizeof(Y) == 2 ? 4 : 3;  // groups of 16 rows on their way
     constexpr int kSlots = kAhead < kMTiles ? kAhead + 1 : kMTiles;
-    extern __shared__ __align__(16) uint4 frag[];  // [TERMS][kMTiles][KS][32]: operands of t
+    extern __shared__ __align__(16) uint4 frag[];  // [TERMS][kMTiles][KS][32]: operands of t; then each warp's products
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
     cudaGridDependencySynchronize();
-    const int vblocks = (a.vocab + kVBlock - 1) / kVBlock;
-    const int64_t units = int64_t(a.plan->n_all) * vblocks;
-    const int tiles = a.plan->n_all;
+    const int vblocks = (a.vocab + kVBlock - 1) / kVBlock, tiles = a.plan->n_all;
+    const int run = int64_t(tiles) * 32 <= a.n ? 1 : int(max(int64_t(1), min(int64_t(8), int64_t(tiles) * vblocks / (3 * int64_t(gridDim.x)))));
+    const int64_t units = int64_t(tiles) * ((vblocks + run - 1) / run);
     const int step = tiles * 4 <= int(gridDim.x) ? int(gridDim.x) / max(tiles, 1) * tiles : int(gridDim.x);
     if (int(blockIdx.x) >= step) return;
     int id = -1;
     Tile tile{};
-    int token[kMTiles][2];
+    int token[kMTiles][2];  // VEC
+    struct Place {  // of a token's row
+        const Y* y;
+        Y* out;
+        int head, alike;  // as of SomeRow
+    };
+    __shared__ __align__(16) char place_mem[VEC ? 16 : kTile * sizeof(Place)];
+    Place* const place = reinterpret_cast<Place*>(place_mem);
+    float* const cells = reinterpret_cast<float*>(frag + TERMS * kMTiles * KS * 32);  // two of them, in turn
+    int turn = 0;
     for (int64_t unit = blockIdx.x; unit < units; unit += step) {
-        const int now = int(unit % tiles), vb = int(unit / tiles);
+        const int now = int(unit % tiles), vb0 = int(unit / tiles) * run;
         if (now != id) {
             id = now;
             tile = a.tiles[id];
@@ -802,8 +956,15 @@ __global__ void __launch_bounds__(kThreads, KS <= 4 ? 2 : 1) adapter_expand_many
 #pragma unroll
                     for (int k = 0; k < TERMS; ++k) frag[k * (kMTiles * KS * 32) + i] = make_uint4(w[0][k], w[1][k], w[2][k], w[3][k]);
                 }
+            if constexpr (!VEC)
+                if (tid < tile.count) {
+                    const int64_t n = token_at(a.perm, tile.start + tid, a.n, a.dev_status);
+                    const Y* const y = static_cast<const Y*>(a.y) + n * a.y_stride;
+                    Y* const out = static_cast<Y*>(a.out) + n * a.out_stride;
+                    place[tid] = {y, out, SomeRow<Y>::before(out), SomeRow<Y>::before(y) == SomeRow<Y>::before(out)};
+                }
 #pragma unroll
-            for (int m = 0; m < kMTiles; ++m)
+            for (int m = 0; m < (VEC ? kMTiles : 0); ++m)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int p = m * 16 + h * 8 + g;
@@ -811,36 +972,12 @@ __global__ void __launch_bounds__(kThreads, KS <= 4 ? 2 : 1) adapter_expand_many
                 }
             __syncthreads();
         }
-        const int v0 = vb * kVBlock + warp * kVWarp;
-        if (v0 >= a.vocab) continue;
-        const int v = v0 + 8 * q, left = a.vocab - v;  // this lane's eight logits
-        const bool whole = left >= 8;
-        auto fetch = [&](Eight<Y>& e, int n) {
-            e.clear();  // (a load that may not be made would wait for what the registers held)
-            if (n < 0 || left <= 0) return;
-            const Y* const p = static_cast<const Y*>(a.y) + n * a.y_stride + v;
-            if (!VCE_BOUNDS(aligned16(p) && v >= 0, a.dev_status)) return;
-            if (whole) e.load(p);
-            else e.load_some(p, left);
-        };
-        uint32_t b[4][KS][2];
-        if (tile.adapter >= 0) load_b<KS>(b, a, tile.adapter, v0);
-        Eight<Y> e[kSlots][2];
-#pragma unroll
-        for (int m = 0; m < kAhead; ++m) {
-            fetch(e[m][0], token[m][0]);
-            fetch(e[m][1], token[m][1]);
-        }
-#pragma unroll
-        for (int m = 0; m < kMTiles; ++m) {
-            if (m * 16 >= tile.count) break;
-            if (m + kAhead < kMTiles) {  // before the products: a load behind their stores would wait for them
-                const int next = m + kAhead < kMTiles ? m + kAhead : 0;
-                fetch(e[next % kSlots][0], token[next][0]);
-                fetch(e[next % kSlots][1], token[next][1]);
-            }
-            float c[4][4] = {};
-            if (tile.adapter >= 0) {
+        for (int vb = vb0; vb < min(vb0 + run, vblocks); ++vb) {
+            const int v0 = vb * kVBlock + warp * kVWarp;
+            if (VEC && v0 >= a.vocab) continue;
+            uint32_t b[4][KS][2];
+            if (tile.adapter >= 0) load_b<KS>(b, a, tile.adapter, v0);
+            auto multiply = [&](float (&c)[4][4], int m) {
 #pragma unroll
                 for (int s = 0; s < KS; ++s)
 #pragma unroll
@@ -853,18 +990,83 @@ __global__ void __launch_bounds__(kThreads, KS <= 4 ? 2 : 1) adapter_expand_many
                             else mma(c[j], w, b[j][s][0], b[j][s][1]);
                         }
                     }
-            }
+            };
+            if constexpr (VEC) {
+                const int v = v0 + 8 * q, left = a.vocab - v;  // this lane's eight logits
+                const bool whole = left >= 8;
+                auto fetch = [&](Eight<Y>& e, int n) {
+                    e.clear();  // (a load that may not be made would wait for what the registers held)
+                    if (n < 0 || left <= 0) return;
+                    const Y* const p = static_cast<const Y*>(a.y) + n * a.y_stride + v;
+                    if (!VCE_BOUNDS(aligned16(p) && v >= 0, a.dev_status)) return;
+                    if (whole) e.load(p);
+                    else e.load_some(p, left);
+                };
+                Eight<Y> e[kSlots][2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                Eight<Y>& x = e[m % kSlots][h];
-                const int n = token[m][h];
-                if (n >= 0 && left > 0) {
+                for (int m = 0; m < kAhead; ++m) {
+                    fetch(e[m][0], token[m][0]);
+                    fetch(e[m][1], token[m][1]);
+                }
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) x.add(j, c[j][2 * h], c[j][2 * h + 1]);
-                    Y* const p = static_cast<Y*>(a.out) + n * a.out_stride + v;
-                    if (!VCE_BOUNDS(aligned16(p), a.dev_status)) continue;
-                    if (whole) x.store(p);
-                    else x.store_some(p, left);
+                for (int m = 0; m < kMTiles; ++m) {
+                    if (m * 16 >= tile.count) break;
+                    if (m + kAhead < kMTiles) {  // before the products: a load behind their stores would wait for them
+                        const int next = m + kAhead < kMTiles ? m + kAhead : 0;
+                        fetch(e[next % kSlots][0], token[next][0]);
+                        fetch(e[next % kSlots][1], token[next][1]);
+                    }
+                    float c[4][4] = {};
+                    if (tile.adapter >= 0) multiply(c, m);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        Eight<Y>& x = e[m % kSlots][h];
+                        const int n = token[m][h];
+                        if (n >= 0 && left > 0) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) x.add(j, c[j][2 * h], c[j][2 * h + 1]);
+                            Y* const p = static_cast<Y*>(a.out) + n * a.out_stride + v;
+                            if (!VCE_BOUNDS(aligned16(p), a.dev_status)) continue;
+                            if (whole) x.store(p);
+                            else x.store_some(p, left);
+                        }
+                    }
+                }
+            } else {
+                const int base = vb * kVBlock, here = min(kVBlock, a.vocab - base);
+                SomeRow<Y> e[kSlots][2];
+                auto fetch = [&](SomeRow<Y>(&x)[2], int m) {
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const int p = m * 16 + 2 * warp + r;
+                        const Place at = place[p];
+                        const bool is = p < tile.count;
+                        x[r].load(at.y + base, is ? min(at.head, here) : 0, at.alike, is ? here : 0);
+                    }
+                };
+#pragma unroll
+                for (int m = 0; m < kAhead; ++m) fetch(e[m], m);
+#pragma unroll
+                for (int m = 0; m < kMTiles; ++m) {
+                    if (m * 16 >= tile.count) break;
+                    if (m + kAhead < kMTiles) fetch(e[(m + kAhead) % kSlots], m + kAhead);
+                    float c[4][4] = {};
+                    if (tile.adapter >= 0) multiply(c, m);
+                    float* const cell = cells + turn * (16 * kCellPitch);
+                    turn ^= 1;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float* const at = cell + (h * 8 + g) * kCellPitch + 9 * (4 * warp + q);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) at[2 * j] = c[j][2 * h], at[2 * j + 1] = c[j][2 * h + 1];
+                    }
+                    __syncthreads();  // (the next one comes before this cell's next turn)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const int p = m * 16 + 2 * warp + r;
+                        if (p < tile.count)
+                            e[m % kSlots][r].add(place[p].out + base, min(place[p].head, here), here, cell + (2 * warp + r) * kCellPitch);
+                    }
                 }
             }
         }
@@ -872,16 +1074,14 @@ __global__ void __launch_bounds__(kThreads, KS <= 4 ? 2 : 1) adapter_expand_many
 }
 
 template <typename Y, bool VEC>
-auto expand_kernel(int ks, int* threads) {
-    *threads = 32 + 32 * (ks == 1 ? Shape<Y, 1>::kWarps : ks == 2 ? Shape<Y, 2>::kWarps : ks == 4 ? Shape<Y, 4>::kWarps : Shape<Y, 8>::kWarps);
-    return ks == 1 ? adapter_expand_few<Y, 1, VEC> : ks == 2 ? adapter_expand_few<Y, 2, VEC> : ks == 4 ? adapter_expand_few<Y, 4, VEC>
-                                                                                          : adapter_expand_few<Y, 8, VEC>;
+auto few_kernel(int ks) {
+    return ks == 1 ? adapter_expand_few<Y, 1, VEC> : adapter_expand_few<Y, 2, VEC>;
 }
 
-template <typename Y>
+template <typename Y, bool VEC>
 auto many_kernel(int ks) {
-    return ks == 1 ? adapter_expand_many<Y, 1> : ks == 2 ? adapter_expand_many<Y, 2> : ks == 4 ? adapter_expand_many<Y, 4>
-                                                                                     : adapter_expand_many<Y, 8>;
+    return ks == 1 ? adapter_expand_many<Y, 1, VEC> : ks == 2 ? adapter_expand_many<Y, 2, VEC>
+                                                  : ks == 4 ? adapter_expand_many<Y, 4, VEC> : adapter_expand_many<Y, 8, VEC>;
 }
 
 struct Carved {
@@ -926,33 +1126,45 @@ vce_status launch_adapter_linear(const void* y, int y_dtype, int64_t n, int64_t 
     const Carved w = carve(ws, n, adapters, rank);
     const bool in_place = out == y;
     const PlanArgs pa{index, int(n), int(adapters), !in_place, int(most_tiles(n, adapters)), w.plan, w.tiles, w.perm, dev_status};
-    count_launch();
-    adapter_plan<<<1, kPlanThreads, 0, s>>>(pa);
-    if (cudaGetLastError() != cudaSuccess) return VCE_ERR_CUDA;
+    const bool self = n <= kSelf;
+    if (!self) {
+        count_launch();
+        adapter_plan<<<1, kPlanThreads, 0, s>>>(pa);
+        if (cudaGetLastError() != cudaSuccess) return VCE_ERR_CUDA;
+    }
+    // by the hidden dimension alone: a token's sums are divided in the same way in every batch
+    const int slices = hidden > 1024 ? 8 : hidden > 512 ? 4 : hidden > 256 ? 2 : 1;
 
     cudaLaunchAttribute attr[2]{};
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = kSlices;
+    attr[1].val.clusterDim.x = unsigned(slices);
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
     cfg.attrs = attr;
 
-    const ShrinkArgs sa{x, x_stride, static_cast<const __nv_bfloat16*>(a), int(hidden), rank, int(n), w.plan, w.tiles,
+    const ShrinkArgs sa{pa, slices, x, x_stride, static_cast<const __nv_bfloat16*>(a), int(hidden), rank, int(n), w.plan, w.tiles,
                         w.perm, w.t, dev_status};
-    auto shrink = x_dtype == VCE_BF16 ? adapter_shrink<__nv_bfloat16> : adapter_shrink<float>;
+    auto shrink = x_dtype == VCE_BF16 ? (self ? adapter_shrink<__nv_bfloat16, true> : adapter_shrink<__nv_bfloat16, false>)
+                                      : (self ? adapter_shrink<float, true> : adapter_shrink<float, false>);
     const size_t shrink_smem = size_t(kWarps) * kTile * kRankBlock * 4;
     const int ks = rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8;
     const int es = y_dtype == VCE_BF16 ? 2 : 4;
     const bool vectors = reinterpret_cast<uintptr_t>(y) % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0 &&
                          (n == 1 || (y_stride * es % 16 == 0 && out_stride * es % 16 == 0));
-    int threads;
-    auto expand = y_dtype == VCE_BF16
-                      ? (vectors ? expand_kernel<__nv_bfloat16, true>(ks, &threads) : expand_kernel<__nv_bfloat16, false>(ks, &threads))
-                      : (vectors ? expand_kernel<float, true>(ks, &threads) : expand_kernel<float, false>(ks, &threads));
+    const int64_t used = std::min(n, adapters), vblocks = (vocab + kVBlock - 1) / kVBlock;
+    const int many_blocks = dev.num_sms * (ks <= 4 ? 2 : 1);
+    const bool many = ks > 2 || n >= kMany * used || (used + n / kTile) * vblocks <= (vectors ? kShort : kShortAny) * many_blocks;
+    const size_t many_smem = size_t(y_dtype == VCE_BF16 ? 2 : 3) * kMTiles * ks * 32 * sizeof(uint4) +
+                             (vectors ? 0 : size_t(2) * 16 * kCellPitch * sizeof(float));
+    auto expand = many ? y_dtype == VCE_BF16
+                             ? (vectors ? many_kernel<__nv_bfloat16, true>(ks) : many_kernel<__nv_bfloat16, false>(ks))
+                             : (vectors ? many_kernel<float, true>(ks) : many_kernel<float, false>(ks))
+                  : y_dtype == VCE_BF16 ? (vectors ? few_kernel<__nv_bfloat16, true>(ks) : few_kernel<__nv_bfloat16, false>(ks))
+                                        : (vectors ? few_kernel<float, true>(ks) : few_kernel<float, false>(ks));
     ExpandArgs ea{static_cast<const __nv_bfloat16*>(b), scale, w.t, y, out, y_stride, out_stride, int(n), int(vocab), rank, 0, 0, 0,
                   {}, w.plan, w.tiles, w.perm, dev_status};
     int b_bytes = 0;
@@ -966,36 +1178,37 @@ vce_status launch_adapter_linear(const void* y, int y_dtype, int64_t n, int64_t 
     ea.stages = std::min(kMaxStages, kRingBytes / ea.stage_bytes);
     const size_t expand_smem = size_t(ea.stages) * ea.stage_bytes;
     static std::mutex mu;
-    static bool ready[64], ready_expand[64][2][2][4];
+    static bool ready[64], ready_expand[64][2][2][2][4];
     {
         std::lock_guard<std::mutex> lock(mu);
-        bool& done = ready_expand[dev.ordinal][y_dtype == VCE_BF16][vectors][ks == 8 ? 3 : ks / 2];
-        if (!done && cudaFuncSetAttribute(expand, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes) != cudaSuccess)
+        bool& done = ready_expand[dev.ordinal][many][y_dtype == VCE_BF16][vectors][ks == 8 ? 3 : ks / 2];
+        if (!done && cudaFuncSetAttribute(expand, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          int(many ? many_smem : size_t(kRingBytes))) != cudaSuccess)
             return VCE_ERR_CUDA;
         done = true;
         if (!ready[dev.ordinal]) {
-            for (auto k : {adapter_shrink<__nv_bfloat16>, adapter_shrink<float>})
+            for (auto k : {adapter_shrink<__nv_bfloat16, true>, adapter_shrink<__nv_bfloat16, false>, adapter_shrink<float, true>,
+                           adapter_shrink<float, false>})
                 if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(shrink_smem)) != cudaSuccess)
                     return VCE_ERR_CUDA;
             ready[dev.ordinal] = true;
         }
     }
-    cfg.gridDim = dim3(unsigned(std::min(n, adapters) + n / kTile) * kSlices, unsigned((rank + kRankBlock - 1) / kRankBlock));
+    cfg.gridDim = dim3(unsigned(used + n / kTile) * slices, unsigned((rank + kRankBlock - 1) / kRankBlock));
     cfg.dynamicSmemBytes = shrink_smem;
     cfg.numAttrs = 2;
     count_launch();
     if (cudaLaunchKernelEx(&cfg, shrink, sa) != cudaSuccess) return VCE_ERR_CUDA;
 
-    if (vectors && n >= kMany * std::min(n, adapters)) {
-        auto many = y_dtype == VCE_BF16 ? many_kernel<__nv_bfloat16>(ks) : many_kernel<float>(ks);
-        cfg.gridDim = dim3(unsigned(dev.num_sms * (ks <= 4 ? 2 : 1)));
-        cfg.dynamicSmemBytes = size_t(y_dtype == VCE_BF16 ? 2 : 3) * kMTiles * ks * 32 * sizeof(uint4);
+    if (many) {
+        cfg.gridDim = dim3(unsigned(many_blocks));
+        cfg.dynamicSmemBytes = many_smem;
         cfg.numAttrs = 1;
         count_launch();
-        return cudaLaunchKernelEx(&cfg, many, ea) == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
+        return cudaLaunchKernelEx(&cfg, expand, ea) == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
     }
     cfg.gridDim = dim3(unsigned(std::min<int64_t>(most_tiles(n, adapters) * ((vocab + kRun - 1) / kRun), int64_t(dev.num_sms))));
-    cfg.blockDim = dim3(unsigned(threads));
+    cfg.blockDim = dim3(kMulWarps * 32 + 32);
     cfg.dynamicSmemBytes = expand_smem;
     cfg.numAttrs = 1;
     count_launch();
