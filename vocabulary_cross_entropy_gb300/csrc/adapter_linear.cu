@@ -280,8 +280,8 @@ __device__ __forceinline__ Tile plan_here(const PlanArgs& a, Sorted& sh, int id,
     return sh.tile;
 }
 
-// A warp takes every (8 slices)-th run of 32 hidden values: sums of few products stay in
-// the instruction's accumulator, what is left is added up in FP32, in a fixed order.
+// Sums of the products of every (8 slices)-th run of 32 hidden values stay in the instruction's accumulator, what is
+// left is added up in FP32, in an order that the hidden dimension alone determines.
 template <typename X, bool SELF>
 __global__ void __launch_bounds__(kThreads, 2) adapter_shrink(const ShrinkArgs a) {
     constexpr int TERMS = sizeof(X) == 2 ? 1 : 3;
@@ -304,70 +304,93 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_shrink(const ShrinkArgs a
     auto token = [&](int p) { return SELF ? sorted.order[tile.start + p] : token_at(a.perm, tile.start + p, a.n, a.dev_status); };
     const int r0 = int(blockIdx.y) * kRankBlock, mtiles = (tile.count + 15) / 16;
 
-    const X* row[kMTiles][2];
+    // The runs of 32 hidden values (slice kWarps + c), and every (slices kWarps)-th after it, are chain c of the slice,
+    // one sum.  The warps divide the groups of 16 tokens and, for each, the chains.
+    const int across = mtiles > 2 ? 4 : mtiles;  // warps across the tokens
+    const int m = warp % across, kw = warp / across, per = kWarps / across;
+    const int stride = a.slices * kWarps * 32, runs = (a.hidden + stride - 1) / stride;  // of a chain
+    const int items = m < mtiles ? kWarps / per * runs : 0;
+    const X* row[2];
 #pragma unroll
-    for (int m = 0; m < kMTiles; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int p = m * 16 + h * 8 + g;
-            row[m][h] = p < tile.count ? static_cast<const X*>(a.x) + token(p) * a.x_stride : nullptr;
-        }
-    float c[kMTiles][kRankBlock / 8][4] = {};
+    for (int h = 0; h < 2; ++h) {
+        const int p = m * 16 + h * 8 + g;
+        row[h] = p < tile.count ? static_cast<const X*>(a.x) + token(p) * a.x_stride : nullptr;
+    }
     const __nv_bfloat16* const base = a.a + (int64_t(tile.adapter) * a.rank + r0) * a.hidden;
-    for (int k = (slice * kWarps + warp) * 32 + q * 8; k - q * 8 < a.hidden; k += a.slices * kWarps * 32) {
-        uint4 b[kRankBlock / 8];
+    struct Item {
+        uint4 b[kRankBlock / 8], x[2][sizeof(X) / 2];
+    };
+    constexpr int kItems = TERMS == 1 ? 3 : 2;  // on their way
+    Item item[kItems];
+    int chain = kw, run = 0;  // of the next item to load
+    auto load = [&](Item& it) {
+        const int k = (slice * kWarps + chain) * 32 + run * stride + q * 8;
+        const bool in = chain < kWarps && k < a.hidden && items > 0;
 #pragma unroll
         for (int j = 0; j < kRankBlock / 8; ++j) {
-            b[j] = make_uint4(0, 0, 0, 0);
-            if (k < a.hidden && r0 + j * 8 + g < a.rank &&
-                VCE_BOUNDS(aligned16(base + k) && k + 8 <= a.hidden, a.dev_status))
-                b[j] = __ldg(reinterpret_cast<const uint4*>(base + int64_t(j * 8 + g) * a.hidden + k));
+            it.b[j] = make_uint4(0, 0, 0, 0);
+            if (in && r0 + j * 8 + g < a.rank && VCE_BOUNDS(aligned16(base + k) && k + 8 <= a.hidden, a.dev_status))
+                it.b[j] = __ldg(reinterpret_cast<const uint4*>(base + int64_t(j * 8 + g) * a.hidden + k));
         }
 #pragma unroll
-        for (int m = 0; m < kMTiles; ++m) {
-            if (m >= mtiles) break;
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < int(sizeof(X)) / 2; ++i) {
+                it.x[h][i] = make_uint4(0, 0, 0, 0);
+                if (in && row[h] && VCE_BOUNDS(aligned16(row[h] + k), a.dev_status))
+                    it.x[h][i] = __ldg(reinterpret_cast<const uint4*>(row[h] + k) + i);
+            }
+        if (++run == runs) run = 0, chain += per;
+    };
+    float c[kRankBlock / 8][4] = {};
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) load(item[i]);
+    for (int done = 0, left = runs, to = kw; done < items;) {
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            if (done >= items) break;
+            Item& it = item[i];
             uint32_t x[TERMS][2][4];  // term, half of the run, operand words
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 if constexpr (TERMS == 1) {
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (k < a.hidden && row[m][h] && VCE_BOUNDS(aligned16(row[m][h] + k), a.dev_status))
-                        v = __ldg(reinterpret_cast<const uint4*>(row[m][h] + k));
+                    const uint4 v = it.x[h][0];
                     x[0][0][h] = v.x, x[0][0][2 + h] = v.y, x[0][1][h] = v.z, x[0][1][2 + h] = v.w;
                 } else {
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
-                        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (k < a.hidden && row[m][h] && VCE_BOUNDS(aligned16(row[m][h] + k), a.dev_status))
-                            v = __ldg(reinterpret_cast<const float4*>(row[m][h] + k) + s);
+                        const uint4 v = it.x[h][s];
                         uint32_t lo[TERMS], hi[TERMS];
-                        split2<TERMS>(v.x, v.y, lo);
-                        split2<TERMS>(v.z, v.w, hi);
+                        split2<TERMS>(__uint_as_float(v.x), __uint_as_float(v.y), lo);
+                        split2<TERMS>(__uint_as_float(v.z), __uint_as_float(v.w), hi);
 #pragma unroll
-                        for (int i = 0; i < TERMS; ++i) x[i][s][h] = lo[i], x[i][s][2 + h] = hi[i];
+                        for (int t = 0; t < TERMS; ++t) x[t][s][h] = lo[t], x[t][s][2 + h] = hi[t];
                     }
                 }
             }
 #pragma unroll
-            for (int i = TERMS - 1; i >= 0; --i)
+            for (int t = TERMS - 1; t >= 0; --t)
 #pragma unroll
                 for (int j = 0; j < kRankBlock / 8; ++j) {
-                    mma(c[m][j], x[i][0], b[j].x, b[j].y);
-                    mma(c[m][j], x[i][1], b[j].z, b[j].w);
+                    mma(c[j], x[t][0], it.b[j].x, it.b[j].y);
+                    mma(c[j], x[t][1], it.b[j].z, it.b[j].w);
                 }
+            load(it);
+            ++done;
+            if (--left == 0) {  // the chain's sum is complete
+#pragma unroll
+                for (int j = 0; j < kRankBlock / 8; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        *reinterpret_cast<float2*>(&red[to * (kTile * kRankBlock) + (m * 16 + h * 8 + g) * kRankBlock + j * 8 + 2 * q]) =
+                            make_float2(c[j][2 * h], c[j][2 * h + 1]);
+                        c[j][2 * h] = c[j][2 * h + 1] = 0.f;
+                    }
+                left = runs, to += per;
+            }
         }
     }
     const int entries = mtiles * 16 * kRankBlock;
-#pragma unroll
-    for (int m = 0; m < kMTiles; ++m) {
-        if (m >= mtiles) break;
-#pragma unroll
-        for (int j = 0; j < kRankBlock / 8; ++j)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                *reinterpret_cast<float2*>(&red[warp * (kTile * kRankBlock) + (m * 16 + h * 8 + g) * kRankBlock + j * 8 + 2 * q]) =
-                    make_float2(c[m][j][2 * h], c[m][j][2 * h + 1]);
-    }
     __syncthreads();
     for (int e = tid; e < entries; e += kThreads) {
         float s = 0.f;
@@ -1196,9 +1219,11 @@ vce_status launch_adapter_linear(const void* y, int y_dtype, int64_t n, int64_t 
     }
     cfg.gridDim = dim3(unsigned(used + n / kTile) * slices, unsigned((rank + kRankBlock - 1) / kRankBlock));
     cfg.dynamicSmemBytes = shrink_smem;
-    cfg.numAttrs = 2;
+    if (self) cfg.attrs = attr + 1;  // the first kernel of the call: what runs before it is not ours
+    cfg.numAttrs = self ? 1 : 2;
     count_launch();
     if (cudaLaunchKernelEx(&cfg, shrink, sa) != cudaSuccess) return VCE_ERR_CUDA;
+    cfg.attrs = attr;
 
     if (many) {
         cfg.gridDim = dim3(unsigned(many_blocks));
