@@ -42,14 +42,14 @@ constexpr int kVWarp = 32;            // logits of a warp, and
 constexpr int kVBlock = kWarps * kVWarp;  // of a block of adapter_expand_many
 constexpr int kRun = 512;             // logits of a unit that is handed out, or a multiple
 constexpr int kMaxStages = 6;         // of adapter_expand_few's ring
-constexpr int kRingBytes = 208 << 10;
+constexpr int kRingBytes = 216 << 10;
 constexpr int64_t kMany = 24;         // tokens per adapter from which adapter_expand_many takes them, and
 constexpr int kShort = 13, kShortAny = 7;  // units of its work per block up to which it does (any alignment)
 constexpr int kMulWarps = 16;         // warps of adapter_expand_few that multiply
 constexpr int kCellPitch = 292;       // floats: a row of kVBlock products, one unused behind every eight (no bank conflicts)
 constexpr int kMaxBlock = 1024;       // logits of a stage, at most
 constexpr int kStageRows = 32 << 10;  // bytes of y in a stage, and
-constexpr int kStageB = 32 << 10;     // of B
+constexpr int kStageB = 32 << 10;     // of B, at most
 constexpr int kPlanThreads = 1024;
 constexpr int kMaxAdapters = VCE_MAX_ADAPTERS;
 
@@ -428,7 +428,7 @@ struct ExpandArgs {
     void* out;
     int64_t y_stride, out_stride;
     int n, vocab, rank;
-    int stages, stage_bytes, y_bytes;  // of the ring; of a stage; of its rows of y
+    int stages, stage_bytes, y_bytes, b_bytes;  // of the ring; of a stage, of its rows of y, of its part of B
     int block[4];                      // logits of a stage, by class_of a tile
     Plan* plan;
     const Tile* tiles;
@@ -468,15 +468,24 @@ __host__ __device__ __forceinline__ int class_of(int count) { return count > 32 
 
 struct Ring {
     uint64_t full[kMaxStages], empty[kMaxStages];
-    int4 what[kMaxStages];  // tile (-1: the end), first logit, number of logits
+    int4 what[kMaxStages];  // 0 (-1: the end), first logit, number of logits, whether its tile is another one
     int abort;
 };
 
-// Tiles of few tokens, where there are many or many logits, and ranks up to 32.  Logits are the rows of the products (16) and tokens the
-// columns (8): a tile of one token costs no more than one of eight.  A warp takes 16 tokens and 32 logits at a time;
-// what warps the tokens leave divide the logits.  A further warp copies y's rows and B, some logits at a
-// time, through a ring in shared memory.  Units of work are handed out by a counter, the larger ones first: tiles
-// differ by a factor of 64.
+// What the multiplying warps have to know of a tile, beside t.
+template <typename Y>
+struct TileInfo {
+    int adapter, count;
+    float scale;
+    Y* out[kTile];   // the tokens' rows
+    int off[kTile];  // bytes of y's rows behind a 16-byte boundary
+};
+
+// Tiles of few tokens, where there are many or many logits, and ranks up to 32.  Logits are the rows of the
+// products (16) and tokens the columns (8): a tile of one token costs no more than one of eight.  A warp takes 16
+// tokens and 32 logits at a time; what warps the tokens leave divide the logits.  A further warp copies y's rows and B,
+// some logits at a time, through a ring in shared memory, and with a tile's first logits t and what else belongs to the
+// tile.  Units of work are handed out by a counter, the larger ones first: tiles differ by a factor of 64.
 //
 // Rows that start off 16-byte boundaries are copied with what shares their first and last 16 bytes, except
 // at a row's ends, whose odd elements are copied one by one; results go back through shared memory, so
@@ -484,16 +493,18 @@ struct Ring {
 //
 // 64 tokens with 35 adapters of rank 16, 128256 FP32 logits: 47 us (4.3 TB/s), of which the copies alone take
 // 40; the others are the multiplying warps' instructions, about 160 for 32 logits of a token.  256 tokens with 64
-// adapters, rank 16, BF16, all three kernels, this form / the other one: 128256 logits 91 / 160 us, 128257
-// (rows off 16-byte boundaries) 129 / 222.
+// adapters, rank 16, BF16, all three kernels, this form / the other one: 128256 logits 85 / 150 us, 128257
+// (rows off 16-byte boundaries) 124 / 207.  Before the ring carried t and the tiles, each warp waited for a chain of three
+// loads with each tile: 91 and 129.
 //
 // What bounds it for larger tiles is its copies, one for each row and stage: 66 cycles each.  Larger ranks are the other
 // one's because t's operands no longer fit this one's registers (rank 64, the same: 407 / 225).
 template <typename Y, int KS, bool VEC>
 __global__ void __launch_bounds__(kMulWarps * 32 + 32, 1) adapter_expand_few(const __grid_constant__ ExpandArgs a) {
     constexpr int TERMS = sizeof(Y) == 2 ? 2 : 3, ES = int(sizeof(Y));
-    extern __shared__ __align__(128) uint8_t smem[];  // stages: rows of y, then B
+    extern __shared__ __align__(128) uint8_t smem[];  // stages: rows of y, then B, then t
     __shared__ Ring ring;
+    __shared__ TileInfo<Y> infos[kMaxStages];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
     if (tid == 0) {
         for (int i = 0; i < a.stages; ++i) {
@@ -510,31 +521,42 @@ __global__ void __launch_bounds__(kMulWarps * 32 + 32, 1) adapter_expand_few(con
     if (warp == kMulWarps) {
         // Unit u: a run of logits of tile tiles - 1 - u / runs (those without an adapter come first).
         const int tiles = a.plan->n_all;
-        const int run = kRun * int(max(int64_t(1), min(int64_t(16), int64_t(tiles) * a.vocab / (int64_t(gridDim.x) * (3 * kRun)))));
+        // Three to five units for each block: a unit costs a chain of loads, which few tokens' work does not cover.
+        const int share = 3 + min(a.n / max(tiles, 1), 16) / 6;
+        const int run = kRun * int(max(int64_t(1), min(int64_t(16), int64_t(tiles) * a.vocab / (int64_t(gridDim.x) * share * kRun))));
         const int runs = (a.vocab + run - 1) / run;
         const int64_t units = int64_t(tiles) * runs;
-        int issued = 0, id = -1, block = 0, pitch = 0;
+        int issued = 0, block = 0, pitch = 0;
         uint32_t parity = 1;  // of the ring's previous round, which the first one need not wait for
-        uintptr_t row[2] = {0, 0};  // this lane's; 0: none
         Tile tile{};
+        float scale = 1.f;
+        int64_t token[2] = {-1, -1};  // this lane's
+        uintptr_t row[2] = {0, 0};    // 0: none
+        bool fresh = false;           // the tile's first logits are still to come
+        asm volatile("fence.proxy.async.global;" ::: "memory");  // t was written by ordinary stores, and is copied from here
         auto take = [&]() { return lane == 0 ? atomicAdd(&a.plan->next, 1) : 0; };
-        int coming = take();
-        for (;;) {
-            const int unit = __shfl_sync(0xffffffffu, coming, 0);
-            const bool end = unit >= units;
-            if (!end) coming = take();
-            if (!end && tiles - 1 - unit / runs != id) {
-                id = tiles - 1 - unit / runs;
-                tile = a.tiles[id];
-                block = a.block[class_of(tile.count)], pitch = block * ES + 32;
+        auto enter = [&](const Tile& t) {
+            tile = t, fresh = true;
+            block = a.block[class_of(tile.count)], pitch = block * ES + 32;
+            scale = a.scale && tile.adapter >= 0 ? a.scale[tile.adapter] : 1.f;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int p = lane + 32 * h;
-                    row[h] = p < tile.count ? reinterpret_cast<uintptr_t>(static_cast<const Y*>(a.y) +
-                                                                          token_at(a.perm, tile.start + p, a.n, a.dev_status) * a.y_stride)
-                                            : 0;
-                }
+            for (int h = 0; h < 2; ++h) {
+                const int p = lane + 32 * h;
+                token[h] = p < tile.count ? token_at(a.perm, tile.start + p, a.n, a.dev_status) : -1;
+                row[h] = p < tile.count ? reinterpret_cast<uintptr_t>(static_cast<const Y*>(a.y) + token[h] * a.y_stride) : 0;
             }
+        };
+        // The next unit is known while one is copied, and the one after it on its way.
+        int unit = __shfl_sync(0xffffffffu, take(), 0);
+        int coming = take();
+        if (unit < units) enter(a.tiles[tiles - 1 - unit / runs]);
+        for (;;) {
+            const bool end = unit >= units;
+            const int next = end ? unit : __shfl_sync(0xffffffffu, coming, 0);
+            if (!end) coming = take();
+            const bool other = next < units && next / runs != unit / runs;
+            Tile next_tile{};
+            if (other) next_tile = a.tiles[tiles - 1 - next / runs];
             const int v0 = end ? 0 : unit % runs * run, v1 = end ? 1 : min(v0 + run, a.vocab);
             for (int v = v0; v < v1; v += end ? 1 : block) {
                 if (issued >= a.stages) {
@@ -545,7 +567,8 @@ __global__ void __launch_bounds__(kMulWarps * 32 + 32, 1) adapter_expand_few(con
                 const int ve = min(v + block, v1);
                 uint8_t* const to = smem + size_t(stage) * a.stage_bytes;
                 uintptr_t from[2] = {0, 0};
-                uint32_t bytes[2] = {0, 0}, b_bytes = 0;
+                uint32_t bytes[2] = {0, 0}, b_bytes = 0, t_bytes = 0;
+                const bool first = fresh && !end;
                 if (!end) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -566,10 +589,24 @@ __global__ void __launch_bounds__(kMulWarps * 32 + 32, 1) adapter_expand_few(con
                             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before a later round's copies
                         }
                     }
-                    if (lane == 0 && tile.adapter >= 0) b_bytes = uint32_t((ve - v) * a.rank * 2);
+                    if (lane == 0 && tile.adapter >= 0) {
+                        b_bytes = uint32_t((ve - v) * a.rank * 2);
+                        if (first) t_bytes = uint32_t(tile.count * a.rank * 4);
+                    }
                 }
-                if (lane == 0) ring.what[stage] = make_int4(end ? -1 : id, v, ve - v, 0);
-                mbar_arrive_expect_tx(&ring.full[stage], bytes[0] + bytes[1] + b_bytes);
+                if (lane == 0) ring.what[stage] = make_int4(end ? -1 : 0, v, ve - v, first);
+                if (first) {
+                    TileInfo<Y>& info = infos[stage];
+                    if (lane == 0) info.adapter = tile.adapter, info.count = tile.count, info.scale = scale;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (row[h] != 0) {
+                            info.out[lane + 32 * h] = static_cast<Y*>(a.out) + token[h] * a.out_stride;
+                            info.off[lane + 32 * h] = int(row[h] & 15);
+                        }
+                    fresh = false;
+                }
+                mbar_arrive_expect_tx(&ring.full[stage], bytes[0] + bytes[1] + b_bytes + t_bytes);
                 auto copy = [&](uint8_t* dst, const void* src, uint32_t n) {
                     if (VCE_BOUNDS(aligned16(src) && aligned16(dst) && n % 16 == 0 && dst + n <= to + a.stage_bytes, a.dev_status))
                         asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -577,6 +614,7 @@ __global__ void __launch_bounds__(kMulWarps * 32 + 32, 1) adapter_expand_few(con
                                      "l"(src), "r"(n), "r"(smem_u32(&ring.full[stage]))
                                      : "memory");
                 };
+                if (t_bytes) copy(to + a.y_bytes + a.b_bytes, a.t + int64_t(tile.start) * a.rank, t_bytes);
                 if (b_bytes) copy(to + a.y_bytes, a.b + (int64_t(tile.adapter) * a.vocab + v) * a.rank, b_bytes);
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
@@ -588,6 +626,8 @@ __global__ void __launch_bounds__(kMulWarps * 32 + 32, 1) adapter_expand_few(con
                 if (++stage == a.stages) stage = 0, parity ^= 1;
             }
             if (end || !ok) break;
+            if (other) enter(next_tile);
+            unit = next;
         }
         if (!ok) {  // copies on their way still write to shared memory
             if (lane == 0) report(a.dev_status, VCE_DEVSTATUS_TIMEOUT);
@@ -600,8 +640,7 @@ __global__ void __launch_bounds__(kMulWarps * 32 + 32, 1) adapter_expand_few(con
         return;
     }
     uint32_t parity = 0;
-    int id = -1, pitch = 0, p0 = 0, part = 0, parts = 1, count = 0;
-    Tile tile{};
+    int adapter = -1, pitch = 0, p0 = 0, part = 0, parts = 1, count = 0;
     // column 2 q + e of product j is token p0 + 8 j + 2 q + e: its row in a stage, and in memory
     int place[2][2];
     Y* to[2][2];
@@ -648,35 +687,32 @@ __global__ void __launch_bounds__(kMulWarps * 32 + 32, 1) adapter_expand_few(con
         if (!ok) break;
         const int4 what = ring.what[stage];
         if (what.x < 0) break;
-        if (what.x != id) {
-            id = what.x;
-            tile = a.tiles[id];
-            const int across_log2 = max(class_of(tile.count) - 1, 0);  // warps across the tokens
-            pitch = a.block[class_of(tile.count)] * ES + 32;
+        uint8_t* const y = smem + size_t(stage) * a.stage_bytes;
+        if (what.w) {
+            const TileInfo<Y>& info = infos[stage];
+            adapter = info.adapter;
+            const int all = info.count, across_log2 = max(class_of(all) - 1, 0);  // warps across the tokens
+            pitch = a.block[class_of(all)] * ES + 32;
             p0 = (warp & ((1 << across_log2) - 1)) * 16, part = warp >> across_log2, parts = kMulWarps >> across_log2;
-            count = min(16, tile.count - p0);  // of this warp's tokens; none if not positive
+            count = min(16, all - p0);  // of this warp's tokens; none if not positive
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int p = 8 * j + 2 * q + e;
                     to[j][e] = nullptr, place[j][e] = 0;
-                    if (p < count) {
-                        const int64_t n = token_at(a.perm, tile.start + p0 + p, a.n, a.dev_status);
-                        to[j][e] = static_cast<Y*>(a.out) + n * a.out_stride;
-                        place[j][e] = (p0 + p) * pitch + int(reinterpret_cast<uintptr_t>(static_cast<const Y*>(a.y) + n * a.y_stride) & 15);
-                    }
+                    if (p < count) to[j][e] = info.out[p0 + p], place[j][e] = (p0 + p) * pitch + info.off[p0 + p];
                 }
-            if (tile.adapter >= 0) {
-                const float scale = a.scale ? a.scale[tile.adapter] : 1.f;
+            if (adapter >= 0) {
+                const float scale = info.scale;
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
                     for (int s = 0; s < KS; ++s) {
                         const int p = 8 * j + g, r = rank_of<KS>(s, q);
                         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (p < count && r < a.rank && VCE_BOUNDS(tile.start + p0 + p < a.n, a.dev_status))
-                            x = *reinterpret_cast<const float4*>(a.t + int64_t(tile.start + p0 + p) * a.rank + r);
+                        if (p < count && r < a.rank)
+                            x = *reinterpret_cast<const float4*>(y + a.y_bytes + a.b_bytes + ((p0 + p) * a.rank + r) * 4);
                         uint32_t w[2][TERMS];
                         split2<TERMS>(x.x * scale, x.y * scale, w[0]);
                         split2<TERMS>(x.z * scale, x.w * scale, w[1]);
@@ -685,17 +721,16 @@ __global__ void __launch_bounds__(kMulWarps * 32 + 32, 1) adapter_expand_few(con
                     }
             }
         }
-        uint8_t* const y = smem + size_t(stage) * a.stage_bytes;
         const int here = what.z;
 #pragma unroll 1
         for (int vc = part * 32; vc < here && count > 0; vc += parts * 32) {
             uint8_t* const yc = y + vc * ES;
             const int64_t vo = what.y + vc;
             if (!VCE_BOUNDS(vo >= 0 && what.y + here <= a.vocab && (vc + 32) * ES + 16 <= pitch &&
-                                (vc + 32) * b_row <= a.stage_bytes - a.y_bytes && tile.count * pitch <= a.y_bytes,
+                                (vc + 32) * b_row <= a.b_bytes && (p0 + count) * pitch <= a.y_bytes,
                             a.dev_status))
                 break;
-            if (tile.adapter >= 0) {
+            if (adapter >= 0) {
                 float c[2][2][4];
                 const uint8_t* const b = y + a.y_bytes + (vc + 4 * g) * b_row;
                 if (a.rank == KS * 16) multiply(c, b, std::true_type{});
@@ -731,7 +766,7 @@ __global__ void __launch_bounds__(kMulWarps * 32 + 32, 1) adapter_expand_few(con
                     }
                 }
             }
-            if (!VEC || tile.adapter < 0) {
+            if (!VEC || adapter < 0) {
                 __syncwarp();
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -1188,18 +1223,19 @@ vce_status launch_adapter_linear(const void* y, int y_dtype, int64_t n, int64_t 
                              : (vectors ? many_kernel<float, true>(ks) : many_kernel<float, false>(ks))
                   : y_dtype == VCE_BF16 ? (vectors ? few_kernel<__nv_bfloat16, true>(ks) : few_kernel<__nv_bfloat16, false>(ks))
                                         : (vectors ? few_kernel<float, true>(ks) : few_kernel<float, false>(ks));
-    ExpandArgs ea{static_cast<const __nv_bfloat16*>(b), scale, w.t, y, out, y_stride, out_stride, int(n), int(vocab), rank, 0, 0, 0,
+    ExpandArgs ea{static_cast<const __nv_bfloat16*>(b), scale, w.t, y, out, y_stride, out_stride, int(n), int(vocab), rank, 0, 0, 0, 0,
                   {}, w.plan, w.tiles, w.perm, dev_status};
-    int b_bytes = 0;
-    for (int rows : {4, 16, 32, 64}) {
-        int& block = ea.block[class_of(rows)];
-        block = std::min({kMaxBlock, kStageRows / (rows * es), kStageB / (rank * 2)}) / 32 * 32;
-        ea.y_bytes = std::max(ea.y_bytes, rows * (block * es + 32));
-        b_bytes = std::max(b_bytes, block * rank * 2);
+    if (!many) {  // three stages at least
+        const int t_bytes = kTile * rank * 4, b_most = std::min(kStageB, kRingBytes / 3 - (kStageRows + kTile * 32) - t_bytes);
+        for (int rows : {4, 16, 32, 64}) {
+            int& block = ea.block[class_of(rows)];
+            block = std::min({kMaxBlock, kStageRows / (rows * es), b_most / (rank * 2)}) / 32 * 32;
+            ea.y_bytes = std::max(ea.y_bytes, rows * (block * es + 32));
+            ea.b_bytes = std::max(ea.b_bytes, block * rank * 2);
+        }
+        ea.stage_bytes = ea.y_bytes + ea.b_bytes + t_bytes;  // multiples of 64 all
+        ea.stages = std::min(kMaxStages, kRingBytes / ea.stage_bytes);
     }
-    ea.stage_bytes = ea.y_bytes + b_bytes;  // multiples of 64 both
-    ea.stages = std::min(kMaxStages, kRingBytes / ea.stage_bytes);
-    const size_t expand_smem = size_t(ea.stages) * ea.stage_bytes;
     static std::mutex mu;
     static bool ready[64], ready_expand[64][2][2][2][4];
     {
@@ -1234,7 +1270,7 @@ vce_status launch_adapter_linear(const void* y, int y_dtype, int64_t n, int64_t 
     }
     cfg.gridDim = dim3(unsigned(std::min<int64_t>(most_tiles(n, adapters) * ((vocab + kRun - 1) / kRun), int64_t(dev.num_sms))));
     cfg.blockDim = dim3(kMulWarps * 32 + 32);
-    cfg.dynamicSmemBytes = expand_smem;
+    cfg.dynamicSmemBytes = size_t(ea.stages) * ea.stage_bytes;
     cfg.numAttrs = 1;
     count_launch();
     return cudaLaunchKernelEx(&cfg, expand, ea) == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
