@@ -596,7 +596,7 @@ size_t adapter_workspace_size(int64_t n, int64_t adapters, int rank);
  * FP32; the product with B takes 24 bits of it for F32 logits and 16 for BF16 ones, sums
  * are FP32, and y enters before the one rounding to out's type.
  *
- *   y       [n, vocab], BF16 or F32, rows y_stride elements apart.
+ *   y       [n, vocab], BF16 or F32, rows y_stride elements apart; n at most 2^27.
  *   x       [n, hidden], BF16 or F32, rows x_stride elements apart; 16-byte aligned, hidden a
  *           multiple of 8, rows a multiple of 16 bytes apart.
  *   A       BF16 [adapters, rank, hidden], B BF16 [adapters, vocab, rank]; 16-byte aligned.

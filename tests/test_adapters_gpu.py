@@ -193,6 +193,23 @@ def test_captured_and_on_another_stream():
         assert torch.equal(out, vce.adapter_linear(y, x, a, b, idx, scale))
 
 
+@pytest.mark.parametrize("n,v,r,count", [(5, 300, 16, 3), (200, 1001, 64, 3), (300, 32001, 16, 70)])
+def test_workspace_of_two_graphs(n, v, r, count):
+    """Two captured calls of different sizes in one workspace, whatever it holds, replayed in turn."""
+    calls = [make(n + i, n - i, 264, v, r, count, BF16, F32) for i in (0, 2)]
+    want = [vce.adapter_linear(*c) for c in calls]
+    ws = torch.full((vce.adapter_workspace_size(n, count, r),), 255, dtype=torch.uint8, device=DEV)
+    outs, graphs = [torch.empty_like(w) for w in want], [torch.cuda.CUDAGraph() for _ in calls]
+    for c, o, g in zip(calls, outs, graphs):
+        with torch.cuda.graph(g):
+            vce.adapter_linear(*c, out=o, workspace=ws)
+    for which in (0, 1, 1, 0):
+        ws.random_(0, 255)
+        outs[which].zero_()
+        graphs[which].replay()
+        assert torch.equal(outs[which], want[which])
+
+
 def test_beyond_2_31_elements():
     """Logits and factors of more than 2^31 elements: their last rows."""
     n, v = 17000, 128264

@@ -253,6 +253,24 @@ def test_streams_and_workspace():
     assert out.token.shape == (0, 3)
 
 
+@pytest.mark.parametrize("shapes", [((2, 4, 3001), (1, 4, 2000)), ((20, 6, 32001), (3, 8, 128256)), ((1, 1, 300000), (2, 32, 513))])
+def test_workspace_of_two_graphs(shapes):
+    """Two captured calls in one workspace, whatever it holds, replayed in turn."""
+    g = torch.Generator().manual_seed(8)
+    calls = [(logits(g, b * k, v, t), torch.randn(b, k, generator=g).to(DEV)) for (b, k, v), t in zip(shapes, (BF16, F32))]
+    want = [vce.ce_beam(*c) for c in calls]
+    ws = torch.empty(max(vce.ce_beam_workspace_size(*c[1].shape, c[1].shape[1]) for c in calls), dtype=torch.uint8, device=DEV)
+    got, graphs = [], [torch.cuda.CUDAGraph() for _ in calls]
+    for c, graph in zip(calls, graphs):
+        with torch.cuda.graph(graph):
+            got.append(vce.ce_beam(*c, workspace=ws))
+    for which in (0, 1, 1, 0):
+        ws.random_(0, 255)
+        got[which].token.zero_(), got[which].parent.zero_(), got[which].score.zero_()
+        graphs[which].replay()
+        assert all(torch.equal(p, q) for p, q in zip(want[which][:3], got[which][:3]))
+
+
 # ---------------------------------------------------------------------------
 # states
 # ---------------------------------------------------------------------------
