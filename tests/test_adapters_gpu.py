@@ -106,12 +106,13 @@ def test_much_work_of_few_tokens(n, v, r, count, none, pad, offset, yt):
         assert torch.equal(around[:, :offset], base[1][:, :offset]) and torch.equal(around[:, offset + v:], base[1][:, offset + v:])
 
 
-@pytest.mark.parametrize("n", [127, 128, 129])
+@pytest.mark.parametrize("n", [1, 2, 31, 127, 128, 129, 255, 256, 257])
 def test_tokens_of_one_adapter_and_of_none(n):
     """Tiles that are full, and the border at which the tokens are sorted in another kernel."""
     y, x, a, b, index, scale = make(n, n, 64, 300, 16, 3, BF16, F32, 0.0)
     for which in (torch.full_like(index, 2), torch.full_like(index, -1),
-                  torch.where(torch.arange(n, device=DEV) < 65, 1, -1).int(), torch.where(torch.arange(n, device=DEV) < 64, -1, 0).int()):
+                  torch.where(torch.arange(n, device=DEV) < 65, 1, -1).int(), torch.where(torch.arange(n, device=DEV) < 64, -1, 0).int(),
+                  (torch.arange(n, device=DEV) % 4 - 1).int()):
         out = vce.adapter_linear(y, x, a, b, which, scale)
         check(out, y, x, a, b, which, scale)
         place = y.clone()
