@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(kMergeThreads) ce_beam_merge(const __grid_cons
     };
     PartHead coming = warp < kRowWarps ? head_of(warp) : PartHead{-INFINITY, 0, 0};  // on its way with the keys
     for (int i = tid; i < all; i += kMergeThreads)
-        keys[i] = a.keys[request * all + i];  // (those past a list's number are not looked at)
+        keys[i] = a.keys[request * all + i];  // (those past a list's number, and an ended beam's, are not looked at)
     for (int r = warp; r < a.beams && warp < kRowWarps; r += kRowWarps) {  // a row's parts
         const bool read = rows[r].read;
         const PartHead head = coming;
@@ -663,7 +663,9 @@ __global__ void __launch_bounds__(kMergeThreads) ce_beam_merge(const __grid_cons
         int best = __ffs(int(equal)) - 1;
         if (equal & (equal - 1)) {  // the lowest beam, and in it the larger logit, which FP64 did not tell apart
             const bool mine = (equal >> lane & 1) && lane / per == best / per;
-            best = __ffs(int(best_lanes(mine && at_once ? keys[at] + 1 : mine))) - 1;
+            uint64_t key = mine;  // (an ended beam has no key, and one list; no key is 0)
+            if (mine && at_once && !rows[lane / per].ended) key = keys[at];
+            best = __ffs(int(best_lanes(key))) - 1;
         }
         if (best < 0) {
             if (lane == 0) chosen_parent[i] = -1;
