@@ -77,3 +77,35 @@ def test_what_the_workspace_holds(shape, dtype):
     for what in (0, 127, 128, 255, None):
         ws.random_(0, 256) if what is None else ws.fill_(what)
         check(z, score, **kw, workspace=ws)
+
+
+SHIFTS = [3e4, -3e4, 1e5, -1e5, 1e6, -1e6, 1e7, -1e7, 3e7, -3e7, 1e8, 2.6e8, -2.6e8, 2.0 ** 30, -2.0 ** 31, 1e20]
+
+
+@pytest.mark.parametrize("shift", SHIFTS)
+def test_logits_far_from_zero(shift):
+    """The sum's logarithm is as good where all logits of a row share a large offset (FP32 rows: a mask that is
+    added, a bias), and beams whose rows differ by an offset alone are ranked by their scores.  Without a score the
+    result is what the row's sum is made of: one rounding of it and the 1e-6 of the module's derivation."""
+    g = torch.Generator().manual_seed(7)
+    for v in (4000, 128256):
+        z = (torch.randn(4, v, generator=g) * 2 + shift).to(DEV)
+        z[3] = shift
+        z[3, v // 2] = float(np.nextafter(np.float32(shift), np.float32(np.inf)))
+        check(z, torch.zeros(4, 1, device=DEV), count=1)
+        zd = z.double()
+        lp = -torch.log(torch.exp(zd - zd.amax(1, keepdim=True)).sum(1))
+        s = -lp.float()
+        st = torch.zeros(1, dtype=torch.int32, device=DEV)
+        r = vce.ce_beam(z, s[:, None].contiguous(), count=1, dev_status=st)
+        # the score that remains is small: what is wrong with it is wrong with the sum
+        err = (r.score[:, 0].double() - (s.double() + lp)).abs().max().item()
+        assert err <= 1e-6 and int(st) == 0, err
+    # differences of whole steps of the shifted logits: the shift is exact
+    step = max(2.0 ** -10, 2.0 ** (math.frexp(abs(shift))[1] - 24))
+    base = (torch.randn(1, 4000, generator=g) * 2 / step).round() * step
+    far = base.double() + math.trunc(shift / step) * step
+    assert (far.float().double() == far).all()
+    z = torch.cat([base, far.float(), base, far.float()]).to(DEV)
+    for score in ([-1.0, -1.00001, -1.00002, -1.00003], [-1.00003, -1.00002, -1.00001, -1.0], [-1.00002, -1.0, -1.00003, -1.00001]):
+        check(z, torch.tensor([score], device=DEV), count=8)

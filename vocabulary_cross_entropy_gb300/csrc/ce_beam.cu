@@ -14,7 +14,8 @@
 //     a division of the row that goes by the index of the token alone, never by the address,
 //     and the threads' sums are joined as whole numbers, in any order.
 // What is wrong with ln S is mostly common to all rows: 3e-8 from the rounding of log2(e), 5e-9
-// of it differing from row to row (128256 tokens).
+// of it differing from row to row (128256 tokens).  The FP32 exponent is one FMA, z log2(e) - m log2(e), whose
+// second term is rounded once for the row: 2^r, r the remainder of that rounding, multiplies the row's sum.
 //
 // A part is copied into a block's shared memory at once, asynchronously: its maximum and the bound
 // are found, and the sum and the survivors come from there.  The bound is the n-th largest of
@@ -220,6 +221,14 @@ struct Part {
         return i >= 0 && VCE_BOUNDS(i < vocab, dev_status) ? one(row + i) : -INFINITY;
     }
 };
+
+// 2^r for the remainder r of neg = -m log2(e) rounded to FP32, |r| <= 2^6 where |m| < 2^30.  The linear term of 2^r
+// alone, which is enough near 0, is 1e-5 off at logits of 1e5 and has nothing to do with it at 3e7.
+__device__ __forceinline__ float offset_factor(float m, float neg) {
+    const float r = fmaf(-m, kLog2e, -neg), n = rintf(r);  // exact
+    const float f = 1.f + expm1f((r - n) * kLn2);
+    return f * __int_as_float((127 + int(n)) << 23);
+}
 
 // make_scale of the temperature 1
 __device__ __forceinline__ Scale natural(float m) { return {m, 1.44269502162933349609375f, 1.92596299e-8f}; }
@@ -431,12 +440,15 @@ __global__ void __launch_bounds__(kThreads + 32, kBlocks) ce_beam_rows(const __g
     __syncthreads();
     const int found = int(sh.n_hot) * (kHold * VE);
     // ---- the sum of the weights below it ----
-    // (of a largest logit so far from 0 every other one is 2^36 away: only those equal to it count)
-    const Exp2Offset offset = fabsf(part_max) < 0x1p60f ? exp2_offset(part_max) : Exp2Offset{-INFINITY, 1.f};
-    const float2 log2e = make_float2(kLog2e, kLog2e), shift = make_float2(offset.neg, offset.neg);
+    // (so far from 0 FP32 numbers are 64 apart, which no weight survives: only logits equal to the largest count)
+    const bool near = fabsf(part_max) < 0x1p30f;
+    const float neg = near ? -part_max * kLog2e : -INFINITY;
+    const float2 log2e = make_float2(kLog2e, kLog2e), shift = make_float2(neg, neg);
     uint64_t* const keys = a.keys + id * a.count;
     float2 sum[2] = {};
     uint64_t mass = 0;  // of the serving warp
+    float factor = 1.f;
+    if (serves && near) factor = offset_factor(part_max, neg);
 #pragma unroll 1
     for (int c = chunks - 1;;) {
         for (int j = tid; j < found; j += kThreads + 32) {
@@ -474,10 +486,10 @@ __global__ void __launch_bounds__(kThreads + 32, kBlocks) ce_beam_rows(const __g
     }
     if (!serves) {
         const float2 s = __fadd2_rn(sum[0], sum[1]);
-        float total = s.x + s.y + ex2f(fmaf(z1, kLog2e, offset.neg));
+        float total = s.x + s.y + ex2f(fmaf(z1, kLog2e, neg));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-        if (lane == 0) sh.warp_sum[warp] = total * offset.fix;
+        if (lane == 0) sh.warp_sum[warp] = total;
     }
     __syncthreads();
     uint32_t n = sh.n_list;
@@ -499,7 +511,7 @@ __global__ void __launch_bounds__(kThreads + 32, kBlocks) ce_beam_rows(const __g
     }
     if (!serves) return;
     // the light sums, as whole numbers
-    if (lane < kWarps) mass += __float2ull_rn(sh.warp_sum[lane] * __int_as_float((127 + a.q_bits) << 23));
+    if (lane < kWarps) mass += __float2ull_rn(sh.warp_sum[lane] * factor * __int_as_float((127 + a.q_bits) << 23));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
     if (lane == 0) *head = {part_max, min(int(n), a.count), sh.mass + mass};
