@@ -319,7 +319,7 @@ size_t ce_beam_workspace_size(int64_t batch, int beams, int count);
  *   ended    uint8 [batch, beams] (0 or not 0) or NULL: none.
  *   length   int32 [batch, beams] or NULL (then length_penalty must be 0).
  *   end      the token that ends a hypothesis, or -1 (then ended must be NULL).
- *   length_penalty  between -16 and 16; 0 compares scores.
+ *   length_penalty  between -16 and 16; 0 compares scores.  FP64, as what it orders.
  *   beams    1 to VCE_BEAM_MAX_BEAMS;  count  1 to VCE_BEAM_MAX_COUNT.
  *   keep_places  0: hypotheses come in their order.  Not 0 (count must equal beams): the first
  *            child of every beam is put at its parent's place and the others at the free
@@ -336,7 +336,7 @@ size_t ce_beam_workspace_size(int64_t batch, int beams, int count);
  */
 vce_status ce_beam(const void* logits, int dtype, int64_t batch, int beams, int64_t vocab, int64_t row_stride,
                    const float* score, const uint8_t* ended, const int32_t* length, int64_t end,
-                   float length_penalty, int count, int keep_places, int64_t* token, int64_t* parent,
+                   double length_penalty, int count, int keep_places, int64_t* token, int64_t* parent,
                    float* out_score, uint8_t* out_ended, int32_t* out_length, void* ws, size_t ws_bytes,
                    int* dev_status, void* stream);
 

@@ -109,3 +109,23 @@ def test_logits_far_from_zero(shift):
     z = torch.cat([base, far.float(), base, far.float()]).to(DEV)
     for score in ([-1.0, -1.00001, -1.00002, -1.00003], [-1.00003, -1.00002, -1.00001, -1.0], [-1.00002, -1.0, -1.00003, -1.00001]):
         check(z, torch.tensor([score], device=DEV), count=8)
+
+
+def test_length_penalty_in_64_bits():
+    """Two hypotheses whose order is another one under the penalty's nearest 32-bit number."""
+    penalty, a, b = 0.8, 10, 200
+    near = float(np.float32(penalty))
+    pairs = []
+    for i in range(400000):
+        low = np.float32(-30.0 - i * 1e-5)
+        high = np.float32(float(low) * (a / b) ** penalty)
+        exact = float(high) / a ** penalty - float(low) / b ** penalty
+        if exact * (float(high) / a ** near - float(low) / b ** near) < 0 and abs(exact) > 1e-10:
+            pairs.append((high, low))
+        if len(pairs) == 8:
+            break
+    assert len(pairs) == 8
+    score = torch.tensor(np.array(pairs), device=DEV)
+    length = torch.tensor([[a, b]] * 8, dtype=torch.int32, device=DEV)
+    ended = torch.ones(8, 2, dtype=torch.bool, device=DEV)
+    check(torch.zeros(16, 5, device=DEV), score, ended=ended, end=1, length=length, length_penalty=penalty)

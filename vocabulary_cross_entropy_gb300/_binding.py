@@ -28,6 +28,7 @@ REDUCE_NONE, REDUCE_MEAN, REDUCE_SUM = 0, 1, 2
 _c_i64 = ctypes.c_int64
 _c_int = ctypes.c_int
 _c_f32 = ctypes.c_float
+_c_f64 = ctypes.c_double
 _c_p = ctypes.c_void_p
 _c_size = ctypes.c_size_t
 
@@ -112,7 +113,7 @@ def library() -> ctypes.CDLL:
     lib.adapter_linear.restype = _c_int
     lib.ce_beam_workspace_size.argtypes = [_c_i64, _c_int, _c_int]
     lib.ce_beam_workspace_size.restype = _c_size
-    lib.ce_beam.argtypes = [_c_p, _c_int, _c_i64, _c_int, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_i64, _c_f32, _c_int,
+    lib.ce_beam.argtypes = [_c_p, _c_int, _c_i64, _c_int, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_i64, _c_f64, _c_int,
                             _c_int, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_size, _c_p, _c_p]
     lib.ce_beam.restype = _c_int
     lib.beam_reorder.argtypes = [_c_p, _c_int, _c_p, _c_i64, _c_int, _c_p, _c_p, _c_p]

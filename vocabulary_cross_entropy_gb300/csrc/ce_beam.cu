@@ -524,7 +524,8 @@ __global__ void __launch_bounds__(kThreads + 32, kBlocks) ce_beam_rows(const __g
 struct MergeArgs {
     int64_t batch;
     int beams, count, parts, end, keep, q_bits;
-    float penalty, least_log2;
+    double penalty;
+    float least_log2;
     const PartHead* heads;
     const uint64_t* keys;
     const float* score;
@@ -588,7 +589,7 @@ __global__ void __launch_bounds__(kMergeThreads) ce_beam_merge(const __grid_cons
         row.read = row.score != -INFINITY && !row.ended;
         row.bad = row.score != -INFINITY && !(row.score < INFINITY && row.score > -INFINITY);
         row.norm = 1.0;
-        if (a.penalty != 0.f) row.norm = pow(double(max(row.ended ? row.length : row.length + 1, 1)), double(a.penalty));
+        if (a.penalty != 0.0) row.norm = pow(double(max(row.ended ? row.length : row.length + 1, 1)), a.penalty);
         rows[tid] = row;
     }
     __syncthreads();
@@ -658,7 +659,7 @@ __global__ void __launch_bounds__(kMergeThreads) ce_beam_merge(const __grid_cons
         if (i - list * a.count >= n) continue;
         const Row& row = rows[at_once ? list / a.parts : list];
         const double c = row.ended ? double(row.score) : total_of(row, keys[at_once ? i : merged[i]]);
-        values[i] = order_bits(a.penalty != 0.f ? c / row.norm : c);
+        values[i] = order_bits(a.penalty != 0.0 ? c / row.norm : c);
     }
     __syncthreads();
     if (warp > 0) return;
@@ -741,7 +742,7 @@ size_t ce_beam_ws_bytes(int64_t rows, int count) {
 }
 
 vce_status launch_ce_beam(const void* logits, int dtype, int64_t batch, int beams, int64_t vocab, int64_t stride,
-                          const float* score, const uint8_t* ended, const int* length, int64_t end, float penalty,
+                          const float* score, const uint8_t* ended, const int* length, int64_t end, double penalty,
                           int count, int keep, int64_t* token, int64_t* parent, float* out_score,
                           uint8_t* out_ended, int* out_length, void* ws, int* dev_status, cudaStream_t s,
                           const DeviceInfo& dev) {

@@ -14,7 +14,7 @@ vce_status launch_ce_sample(const void* logits, int dtype, int64_t n, int64_t vo
 // ---- beam search (ce_beam.cu, beam_reorder.cu) ----
 size_t ce_beam_ws_bytes(int64_t rows, int count);
 vce_status launch_ce_beam(const void* logits, int dtype, int64_t batch, int beams, int64_t vocab, int64_t stride,
-                          const float* score, const uint8_t* ended, const int* length, int64_t end, float penalty,
+                          const float* score, const uint8_t* ended, const int* length, int64_t end, double penalty,
                           int count, int keep, int64_t* token, int64_t* parent, float* out_score,
                           uint8_t* out_ended, int* out_length, void* ws, int* dev_status, cudaStream_t s,
                           const DeviceInfo& dev);

@@ -391,14 +391,14 @@ size_t ce_beam_workspace_size(int64_t batch, int beams, int count) {
 
 vce_status ce_beam(const void* logits, int dtype, int64_t batch, int beams, int64_t vocab, int64_t row_stride,
                    const float* score, const uint8_t* ended, const int32_t* length, int64_t end,
-                   float length_penalty, int count, int keep_places, int64_t* token, int64_t* parent,
+                   double length_penalty, int count, int keep_places, int64_t* token, int64_t* parent,
                    float* out_score, uint8_t* out_ended, int32_t* out_length, void* ws, size_t ws_bytes,
                    int* dev_status, void* stream) {
     if (!dtype_ok(dtype)) return VCE_ERR_DTYPE;
     if (batch < 0 || batch > kMaxRows || beams < 1 || beams > VCE_BEAM_MAX_BEAMS || batch * beams > kMaxRows ||
         vocab < 1 || vocab > VCE_SAMPLE_MAX_VOCAB || row_stride < vocab || count < 1 || count > VCE_BEAM_MAX_COUNT ||
         (keep_places && count != beams) || end < -1 || end >= vocab || (ended && end < 0) ||
-        !(length_penalty >= -16.f && length_penalty <= 16.f) || (length_penalty != 0.f && !length))
+        !(length_penalty >= -16.0 && length_penalty <= 16.0) || (length_penalty != 0.0 && !length))
         return VCE_ERR_INVALID_ARG;
     if (batch > 0 && (!logits || !score || !token || !parent || !out_score || ((ended || end >= 0) && !out_ended) ||
                       (length && !out_length)))
