@@ -317,7 +317,8 @@ size_t ce_beam_workspace_size(int64_t batch, int beams, int count);
  *   score    F32 [batch, beams]; -inf marks a beam that offers nothing (a request's first
  *            step has one live beam).  Its logits, and those of an ended beam, are not read.
  *   ended    uint8 [batch, beams] (0 or not 0) or NULL: none.
- *   length   int32 [batch, beams] or NULL (then length_penalty must be 0).
+ *   length   int32 [batch, beams] or NULL (then length_penalty must be 0).  One of 2^31 - 1 is compared as l + 1
+ *            and stays what it is.
  *   end      the token that ends a hypothesis, or -1 (then ended must be NULL).
  *   length_penalty  between -16 and 16; 0 compares scores.  FP64, as what it orders.
  *   beams    1 to VCE_BEAM_MAX_BEAMS;  count  1 to VCE_BEAM_MAX_COUNT.

@@ -129,3 +129,17 @@ def test_length_penalty_in_64_bits():
     length = torch.tensor([[a, b]] * 8, dtype=torch.int32, device=DEV)
     ended = torch.ones(8, 2, dtype=torch.bool, device=DEV)
     check(torch.zeros(16, 5, device=DEV), score, ended=ended, end=1, length=length, length_penalty=penalty)
+
+
+@pytest.mark.parametrize("penalty", [0.0, 0.9, -0.5])
+def test_the_longest_lengths(penalty):
+    """A length of 2^31 - 1 is compared as one more than it is, and stays there."""
+    most = 2 ** 31 - 1
+    z = torch.linspace(0, 1, 10, device=DEV).repeat(4, 1)
+    score = torch.tensor([[-3.0, -3.5], [-3.0, -2.0]], device=DEV)
+    length = torch.tensor([[most, 4], [most - 1, most]], dtype=torch.int32, device=DEV)
+    token, parent, out, _, size = ref.beam_step(z.double().cpu().numpy().reshape(2, 2, 10), score.cpu().numpy(), None,
+                                                length.cpu().numpy(), penalty=penalty, count=4)
+    r = vce.ce_beam(z, score, length=length, length_penalty=penalty, count=4)
+    assert np.array_equal(r.token.cpu().numpy(), token) and np.array_equal(r.parent.cpu().numpy(), parent)
+    assert np.array_equal(r.length.cpu().numpy(), np.minimum(size, most))

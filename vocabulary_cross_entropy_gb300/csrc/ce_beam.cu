@@ -37,6 +37,7 @@
 #include "token_order.cuh"
 
 #include <algorithm>
+#include <climits>
 #include <math.h>
 #include <mutex>
 
@@ -589,7 +590,7 @@ __global__ void __launch_bounds__(kMergeThreads) ce_beam_merge(const __grid_cons
         row.read = row.score != -INFINITY && !row.ended;
         row.bad = row.score != -INFINITY && !(row.score < INFINITY && row.score > -INFINITY);
         row.norm = 1.0;
-        if (a.penalty != 0.0) row.norm = pow(double(max(row.ended ? row.length : row.length + 1, 1)), a.penalty);
+        if (a.penalty != 0.0) row.norm = pow(fmax(double(row.length) + !row.ended, 1.0), a.penalty);
         rows[tid] = row;
     }
     __syncthreads();
@@ -717,7 +718,7 @@ __global__ void __launch_bounds__(kMergeThreads) ce_beam_merge(const __grid_cons
         a.parent[out] = parent;
         a.out_score[out] = float(c);
         if (a.out_ended) a.out_ended[out] = valid && (row.ended || token == a.end);
-        if (a.out_length) a.out_length[out] = row.length + (valid && !row.ended);
+        if (a.out_length) a.out_length[out] = row.length + (valid && !row.ended && row.length < INT_MAX);
     }
 }
 
