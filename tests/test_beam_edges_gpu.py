@@ -143,3 +143,18 @@ def test_the_longest_lengths(penalty):
     r = vce.ce_beam(z, score, length=length, length_penalty=penalty, count=4)
     assert np.array_equal(r.token.cpu().numpy(), token) and np.array_equal(r.parent.cpu().numpy(), parent)
     assert np.array_equal(r.length.cpu().numpy(), np.minimum(size, most))
+
+
+@pytest.mark.parametrize("length", [2 ** 31 - 1, 1, 0])
+def test_reorder_positions_beyond_4_gb(length):
+    """Positions of more than 2^32 bytes, whose product with a length does not fit 63 bits."""
+    size = 2 ** 32 + 64
+    assert (2 ** 31 - 1) * size >= 1 << 63
+    x = torch.empty(2, 1, size, dtype=torch.uint8, device=DEV)
+    x[0], x[1] = 3, 5
+    parent = torch.tensor([[1, 1]], device=DEV)
+    lengths = torch.tensor([length], dtype=torch.int32, device=DEV)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    vce.beam_reorder(x, parent, lengths=lengths, position_dim=1, dev_status=st)
+    want = 5 if length else 3
+    assert int(st) == 0 and int(x[0].min()) == int(x[0].max()) == want and int(x[1].min()) == int(x[1].max()) == 5

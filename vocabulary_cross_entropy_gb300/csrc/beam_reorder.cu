@@ -31,7 +31,8 @@ struct State {
     const char* src;
     char* dst;
     int64_t src_stride, dst_stride, src_part, dst_part;  // bytes
-    int64_t parts, run, each;  // runs of ``run`` bytes per row; ``each`` bytes per position
+    int64_t parts, run;        // runs of ``run`` bytes per row,
+    int64_t positions, each;   // of positions of ``each`` bytes
     int width;                 // bytes of a column
 };
 
@@ -107,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, blocks_of<kMany>()) beam_reorder_ker
             ++n;
         }
         int64_t bytes = st.run;
-        if (a.lengths) bytes = min(bytes, max(int64_t(a.lengths[b0 + tid]), int64_t(0)) * st.each);
+        if (a.lengths) bytes = min(st.positions, max(int64_t(a.lengths[b0 + tid]), int64_t(0))) * st.each;
         const int64_t columns = bytes / st.width;
         sh.n[tid] = uint8_t(n), sh.columns[tid] = columns;
         if (n) units = (columns + U * 32 - 1) / (U * 32) * st.parts;
@@ -178,7 +179,7 @@ vce_status launch_beam_reorder(const vce_state* states, int count, const int64_t
             if (x.parts == 0 || x.positions == 0 || x.position_bytes == 0) continue;
             State& st = a.state[a.states++];
             st = {static_cast<const char*>(x.src), static_cast<char*>(x.dst), x.src_row_stride, x.dst_row_stride,
-                  x.src_part_stride, x.dst_part_stride, x.parts, x.positions * x.position_bytes, x.position_bytes,
+                  x.src_part_stride, x.dst_part_stride, x.parts, x.positions * x.position_bytes, x.positions, x.position_bytes,
                   column_width(x, lengths != nullptr)};
             const int64_t units = (st.run / st.width + per_unit - 1) / per_unit * st.parts * std::min<int64_t>(batch, kGroup);
             most = std::max(most, (units + kWarps - 1) / kWarps);
