@@ -603,7 +603,7 @@ size_t adapter_workspace_size(int64_t n, int64_t adapters, int rank);
  *   A       BF16 [adapters, rank, hidden], B BF16 [adapters, vocab, rank]; 16-byte aligned.
  *           rank is a multiple of 8 up to VCE_MAX_ADAPTER_RANK (adapters of smaller rank are
  *           padded with zeros), adapters 1 to VCE_MAX_ADAPTERS.
- *   index   int32 [n]; -1: no adapter.  Any other number outside [0, adapters) counts as -1 and
+ *   index   int32 [n]; -1: no adapter, out is y, every bit of it.  Any other number outside [0, adapters) counts as -1 and
  *           sets VCE_DEVSTATUS_BAD_INDEX.
  *   scale   F32 [adapters] or NULL (1).
  *   out     like y, rows out_stride apart; y itself (same stride) or without overlap.

@@ -1,0 +1,42 @@
+"""adapter_linear where it can go wrong at the edges: the bits of tokens without an adapter, the terms that
+t = A x is multiplied in, what a workspace holds; and a search with adapters, step by step."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import vocabulary_cross_entropy_gb300 as vce
+from oracle import beam as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def make(seed, n, h, v, r, count, xt, yt, none=0.2, pad=0, offset=0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(n, h, generator=g).to(xt).to(DEV)
+    a = (torch.randn(count, r, h, generator=g) * h ** -0.5).to(BF16).to(DEV)
+    b = (torch.randn(count, v, r, generator=g) * r ** -0.5).to(BF16).to(DEV)
+    full = (torch.randn(n, v + pad + offset, generator=g) * 2).to(yt).to(DEV)
+    index = torch.randint(0, count, (n,), generator=g, dtype=torch.int32)
+    index[torch.rand(n, generator=g) < none] = -1
+    scale = (0.25 + torch.rand(count, generator=g)).to(DEV)
+    return full[:, offset:offset + v], x, a, b, index.to(DEV), scale
+
+
+@pytest.mark.parametrize("yt", [BF16, F32])
+@pytest.mark.parametrize("n,v,r,count,pad,offset", [(9, 300, 16, 3, 4, 0), (70, 517, 64, 3, 0, 1), (300, 264, 8, 2, 0, 0),
+                                                    (70, 32000, 16, 40, 0, 0), (150, 32004, 8, 50, 3, 1)])
+def test_tokens_without_an_adapter_keep_their_bits(n, v, r, count, pad, offset, yt):
+    """Every bit: -0 stays -0, a NaN keeps its payload, in either form, in place or not."""
+    y, x, a, b, index, scale = make(n, n, 64, v, r, count, BF16, yt, 0.0, pad, offset)
+    index[::3] = -1
+    bits = torch.int16 if yt is BF16 else torch.int32
+    y[:, ::5] = -0.0
+    y[:, 1::7] = torch.tensor([0x7f81 if yt is BF16 else 0x7f800001], dtype=bits, device=DEV).view(yt)
+    want = y.contiguous().view(bits).clone()
+    none = index < 0
+    for out in (vce.adapter_linear(y, x, a, b, index, scale), vce.adapter_linear(y, x, a, b, index, scale, out=y)):
+        assert torch.equal(out.contiguous().view(bits)[none], want[none])

@@ -896,6 +896,15 @@ struct SomeRow {
         single = Y(0.f);
         if (i >= 0) single = y[i];
     }
+    __device__ __forceinline__ void copy(Y* out, int head, int n) const {
+        const int lane = threadIdx.x & 31, whole = (n - head) / VE;
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k)
+            if (lane + 32 * k < whole)
+                *reinterpret_cast<uint4*>(out + head + (lane + 32 * k) * VE) = make_uint4(v[k][0], v[k][1], v[k][2], v[k][3]);
+        const int i = one(head, n);
+        if (i >= 0) out[i] = single;
+    }
     // ``sums``: of logit i at i + i / 8.
     __device__ __forceinline__ void add(Y* out, int head, int n, const float* sums) {
         const int lane = threadIdx.x & 31, whole = (n - head) / VE;
@@ -1038,11 +1047,47 @@ __global__ void __launch_bounds__(kThreads, KS <= 4 ? 2 : 1) adapter_expand_many
                 }
             __syncthreads();
         }
+        // Tokens without an adapter: y as it is, every bit (the sum with +0 would make +0 of -0).
+        if constexpr (VEC) {
+            if (tile.adapter < 0) {
+                for (int vb = vb0; vb < min(vb0 + run, vblocks); ++vb) {
+                    const int v = vb * kVBlock + warp * kVWarp + 8 * q, left = a.vocab - v;
+                    if (left <= 0) continue;
+                    Eight<Y> e[kMTiles][2];
+#pragma unroll
+                    for (int m = 0; m < kMTiles; ++m)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            e[m][h].clear();  // (what a load may leave undefined is spilled, in the loop below too: 1182 us instead of 446)
+                            if (token[m][h] < 0) continue;
+                            const Y* const p = static_cast<const Y*>(a.y) + token[m][h] * a.y_stride + v;
+                            if (!VCE_BOUNDS(aligned16(p), a.dev_status)) continue;
+                            if (left >= 8) e[m][h].load(p);
+                            else e[m][h].load_some(p, left);
+                        }
+#pragma unroll
+                    for (int m = 0; m < kMTiles; ++m)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (token[m][h] < 0) continue;
+                            Y* const p = static_cast<Y*>(a.out) + token[m][h] * a.out_stride + v;
+                            if (!VCE_BOUNDS(aligned16(p), a.dev_status)) continue;
+                            if (left >= 8) e[m][h].store(p);
+                            else e[m][h].store_some(p, left);
+                        }
+                }
+                continue;
+            }
+        }
         for (int vb = vb0; vb < min(vb0 + run, vblocks); ++vb) {
             const int v0 = vb * kVBlock + warp * kVWarp;
             if (VEC && v0 >= a.vocab) continue;
             uint32_t b[4][KS][2];
-            if (tile.adapter >= 0) load_b<KS>(b, a, tile.adapter, v0);
+            // (a condition that the compiler does not see through: without it the loads of y wait, 512 x 128256, rank 16,
+            // BF16, 92 us in all instead of 83)
+            int adapter = tile.adapter;
+            asm volatile("" : "+r"(adapter));
+            if (adapter >= 0) load_b<KS>(b, a, adapter, v0);
             auto multiply = [&](float (&c)[4][4], int m) {
 #pragma unroll
                 for (int s = 0; s < KS; ++s)
@@ -1082,8 +1127,8 @@ __global__ void __launch_bounds__(kThreads, KS <= 4 ? 2 : 1) adapter_expand_many
                         fetch(e[next % kSlots][0], token[next][0]);
                         fetch(e[next % kSlots][1], token[next][1]);
                     }
-                    float c[4][4] = {};
-                    if (tile.adapter >= 0) multiply(c, m);
+                    float c[4][4];
+                    multiply(c, m);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         Eight<Y>& x = e[m % kSlots][h];
@@ -1100,7 +1145,6 @@ __global__ void __launch_bounds__(kThreads, KS <= 4 ? 2 : 1) adapter_expand_many
                 }
             } else {
                 const int base = vb * kVBlock, here = min(kVBlock, a.vocab - base);
-                SomeRow<Y> e[kSlots][2];
                 auto fetch = [&](SomeRow<Y>(&x)[2], int m) {
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
@@ -1110,14 +1154,28 @@ __global__ void __launch_bounds__(kThreads, KS <= 4 ? 2 : 1) adapter_expand_many
                         x[r].load(at.y + base, is ? min(at.head, here) : 0, at.alike, is ? here : 0);
                     }
                 };
+                if (tile.adapter < 0) {  // (not before the loop, as above: 600 x 32001 FP32 57 us instead of 51)
+                    SomeRow<Y> e[kMTiles][2];
+#pragma unroll
+                    for (int m = 0; m < kMTiles; ++m) fetch(e[m], m);
+#pragma unroll
+                    for (int m = 0; m < kMTiles; ++m)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const int p = m * 16 + 2 * warp + r;
+                            if (p < tile.count) e[m][r].copy(place[p].out + base, min(place[p].head, here), here);
+                        }
+                    continue;
+                }
+                SomeRow<Y> e[kSlots][2];
 #pragma unroll
                 for (int m = 0; m < kAhead; ++m) fetch(e[m], m);
 #pragma unroll
                 for (int m = 0; m < kMTiles; ++m) {
                     if (m * 16 >= tile.count) break;
                     if (m + kAhead < kMTiles) fetch(e[(m + kAhead) % kSlots], m + kAhead);
-                    float c[4][4] = {};
-                    if (tile.adapter >= 0) multiply(c, m);
+                    float c[4][4];
+                    multiply(c, m);
                     float* const cell = cells + turn * (16 * kCellPitch);
                     turn ^= 1;
 #pragma unroll
