@@ -594,8 +594,8 @@ size_t adapter_workspace_size(int64_t n, int64_t adapters, int rank);
  * of them share (mx_linear's logits, for instance):
  *     out[n, :] = y[n, :] + scale[i] B[i] (A[i] x[n, :]),   i = index[n].
  * A token's result depends on its own row and adapter alone, not on its neighbours.  A[i] x is
- * FP32; the product with B takes 24 bits of it for F32 logits and 16 for BF16 ones, sums
- * are FP32, and y enters before the one rounding to out's type.
+ * FP32; the product with B takes all of it for F32 logits and, rounded by 2^-17 at most, 16 bits and
+ * a sign for BF16 ones, sums are FP32, and y enters before the one rounding to out's type.
  *
  *   y       [n, vocab], BF16 or F32, rows y_stride elements apart; n at most 2^27.
  *   x       [n, hidden], BF16 or F32, rows x_stride elements apart; 16-byte aligned, hidden a

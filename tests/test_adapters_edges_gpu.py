@@ -40,3 +40,26 @@ def test_tokens_without_an_adapter_keep_their_bits(n, v, r, count, pad, offset, 
     none = index < 0
     for out in (vce.adapter_linear(y, x, a, b, index, scale), vce.adapter_linear(y, x, a, b, index, scale, out=y)):
         assert torch.equal(out.contiguous().view(bits)[none], want[none])
+
+
+@pytest.mark.parametrize("n,v,r,count,pad,offset", [(40, 264, 8, 1, 0, 0), (40, 261, 64, 2, 0, 1), (70, 32000, 16, 40, 0, 0),
+                                                    (150, 32004, 8, 50, 3, 1)])
+def test_two_terms_hold_17_bits(n, v, r, count, pad, offset):
+    """BF16 logits take t = A x as two BF16 terms, the first rounded to 8 bits: what is left of a t of 17 bits is at
+    most half of the first term's last place, 2^8 units, which 8 bits and a sign hold.  With y = -(the first term)
+    that is the result, and exact."""
+    y, x, a, b, index, scale = make(n, n, 64, v, r, count, F32, BF16, 0.0, pad, offset)
+    g = torch.Generator().manual_seed(1)
+    t = torch.randint(1 << 16, 1 << 17, (n,), generator=g) * (1 - 2 * torch.randint(0, 2, (n,), generator=g))
+    t[:4] = torch.tensor([(1 << 16) + 511, -(1 << 16) - 511, (1 << 17) - 1, (1 << 16) + 257])
+    t = (t.float() * 2.0 ** -16).to(DEV)
+    x.zero_(), a.zero_(), b.zero_()
+    x[:, 9], a[:, 3, 9], b[:, :, 3] = t, 1.0, 1.0
+    y.copy_((-t.to(BF16))[:, None].expand(n, v))
+    out = vce.adapter_linear(y, x, a, b, index)
+    assert torch.equal(out, (t - t.to(BF16).float()).to(BF16)[:, None].expand(n, v))
+    # the largest finite values do not round to an infinity
+    x[:, 9] = torch.finfo(F32).max
+    b[:, :, 3] = 2.0 ** -120
+    out = vce.adapter_linear(torch.zeros_like(y), x, a, b, index)
+    assert torch.equal(out, torch.full_like(out, 256.0))

@@ -15,8 +15,8 @@
 // a token's result does not depend on which one takes it.
 //
 // Precision.  t is FP32 and is multiplied as a sum of BF16 terms, three (all 24 bits) for FP32
-// logits, two (16 bits: 2^-17 of the adapter's part) for BF16 logits, whose own rounding is
-// 2^-9.  FP32 hidden states enter as three terms too.
+// logits, two (2^-17 of the adapter's part) for BF16 logits, whose own rounding is
+// 2^-8.  FP32 hidden states enter as three terms too.
 
 #include "head_internal.cuh"
 #include "sm100_ptx.cuh"
@@ -193,8 +193,19 @@ __device__ __forceinline__ void split(float x, uint32_t (&t)[TERMS]) {  // BF16 
     }
 }
 
+// Pairs.  The first of two terms is rounded, too, where it cannot overflow: 2^-17 of x is left at most (2^-16 if it were
+// cut off).
 template <int TERMS>
-__device__ __forceinline__ void split2(float x, float y, uint32_t (&t)[TERMS]) {  // pairs
+__device__ __forceinline__ void split2(float x, float y, uint32_t (&t)[TERMS]) {
+    if constexpr (TERMS == 2) {
+        if (fmaxf(fabsf(x), fabsf(y)) < 0x1.ffp127f) {
+            const __nv_bfloat162 a = __floats2bfloat162_rn(x, y);
+            t[0] = *reinterpret_cast<const uint32_t*>(&a);
+            const __nv_bfloat162 b = __floats2bfloat162_rn(x - __uint_as_float(t[0] << 16), y - __uint_as_float(t[0] & 0xffff0000u));
+            t[1] = *reinterpret_cast<const uint32_t*>(&b);
+            return;
+        }
+    }
     uint32_t u[TERMS], v[TERMS];
     split<TERMS>(x, u);
     split<TERMS>(y, v);
