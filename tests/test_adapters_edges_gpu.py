@@ -63,3 +63,52 @@ def test_two_terms_hold_17_bits(n, v, r, count, pad, offset):
     b[:, :, 3] = 2.0 ** -120
     out = vce.adapter_linear(torch.zeros_like(y), x, a, b, index)
     assert torch.equal(out, torch.full_like(out, 256.0))
+
+
+@pytest.mark.parametrize("n,v,r,count", [(5, 300, 16, 3), (200, 1001, 64, 3), (300, 32001, 16, 70)])
+def test_what_the_workspace_holds(n, v, r, count):
+    """Results do not depend on the workspace's contents, bytes up to 255 among them."""
+    call = make(n, n, 264, v, r, count, BF16, F32)
+    want = vce.adapter_linear(*call)
+    ws = torch.empty(vce.adapter_workspace_size(n, count, r), dtype=torch.uint8, device=DEV)
+    for what in (0, 255, None):
+        ws.random_(0, 256) if what is None else ws.fill_(what)
+        assert torch.equal(vce.adapter_linear(*call, workspace=ws), want)
+
+
+@pytest.mark.parametrize("keep", [False, True])
+def test_every_step_of_a_search_against_the_definitions(keep):
+    """A search with adapters whose every choice, and every history after it, is the definition's for that step's
+    logits: product and adapters by this package, choice and reordering in FP64."""
+    g = torch.Generator().manual_seed(31)
+    b, k, h, v, steps = 3, 4, 128, 403, 7
+    table = torch.randn(v, h, generator=g).to(BF16).to(DEV)
+    w4 = vce.mx_quantize(table.float() * h ** -0.5, "e2m1")
+    _, _, a, bb, _, scale = make(32, b * k, h, v, 8, 2, BF16, F32)
+    index = torch.tensor([0] * k + [-1] * k + [1] * k, dtype=torch.int32, device=DEV)
+    score = torch.full((b, k), -math.inf, device=DEV)
+    score[:, 0] = 0
+    ended = torch.zeros(b, k, dtype=torch.bool, device=DEV)
+    length = torch.zeros(b, k, dtype=torch.int32, device=DEV)
+    last = torch.arange(1, b + 1, device=DEV)[:, None].repeat(1, k)
+    history = torch.zeros(b * k, steps, dtype=torch.int64, device=DEV)
+    state = torch.zeros(b * k, h, device=DEV)
+    for i in range(steps):
+        state.mul_(0.5).add_(table[last.view(-1)].float())
+        x = state.to(BF16)
+        z = vce.adapter_linear(vce.mx_linear(vce.mx_quantize(x, "e4m3"), w4, F32), x, a, bb, index, scale)
+        want = ref.beam_step(z.double().cpu().numpy().reshape(b, k, v), score.cpu().numpy(), ended.cpu().numpy(),
+                             length.cpu().numpy(), 0, 0.7, None, keep)
+        before = history.cpu().numpy(), state.cpu().numpy()
+        r = vce.linear_beam(x.view(b, k, h), w4, score, ended=ended, length=length, end=0, length_penalty=0.7,
+                            keep_places=keep, adapters=vce.Adapters(a, bb, scale), adapter_index=index, out_score=score,
+                            out_ended=ended, out_length=length)
+        assert int(r.dev_status) == 0
+        for got, right in zip((r.token, r.parent, r.ended, r.length), (want[0], want[1], want[3], want[4])):
+            assert np.array_equal(got.cpu().numpy(), right)
+        assert np.allclose(r.score.cpu().numpy(), want[2], rtol=2.0 ** -24, atol=1e-6)
+        vce.beam_reorder([history, state], r.parent)
+        for got, was in zip((history, state), before):
+            assert np.array_equal(got.cpu().numpy(), ref.reorder(was, want[1]))
+        last.copy_(r.token)
+        history[:, i] = r.token.view(-1)
