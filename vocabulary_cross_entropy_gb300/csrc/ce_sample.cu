@@ -330,6 +330,64 @@ __device__ __forceinline__ int first_at_least(const V* s, int n, V target) {
     return lo;
 }
 
+// Sorts list[0 .. n), n <= kCap, descending (all keys differ); ``tmp`` is scratch.
+__device__ __forceinline__ void sort_list(uint64_t* list, int n, uint64_t* tmp) {
+    const int t = threadIdx.x;
+    if (n <= kThreads / 2) {  // each key counts those before it, two threads to a key
+        const int i = t >> 1, half = (n + 1) >> 1;
+        const uint64_t k = i < n ? list[i] : 0;
+        int r = 0;
+        const int end = t & 1 ? n : half;
+#pragma unroll 4
+        for (int j = t & 1 ? half : 0; j < end; ++j) r += list[j] > k;
+        r += __shfl_xor_sync(0xffffffffu, r, 1);
+        if (i < n && !(t & 1)) tmp[r] = k;
+        __syncthreads();
+        if (t < n) list[t] = tmp[t];
+        __syncthreads();
+        return;
+    }
+    int size = kThreads;
+    while (size < n) size *= 2;
+    for (int i = n + t; i < size; i += kThreads) list[i] = 0;  // after every key
+    __syncthreads();
+    if (size == kThreads) {  // one key per thread: partners within a warp need no barrier
+        uint64_t key = list[t];
+#pragma unroll 1
+        for (int len = 2; len <= size; len *= 2)
+#pragma unroll 1
+            for (int step = len / 2; step > 0; step /= 2) {
+                uint64_t other;
+                if (step >= 32) {
+                    __syncthreads();
+                    list[t] = key;
+                    __syncthreads();
+                    other = list[t ^ step];
+                } else {
+                    other = __shfl_xor_sync(0xffffffffu, key, step);
+                }
+                const bool larger = ((t & len) == 0) == ((t & step) == 0);  // this place keeps the larger
+                key = (other > key) == larger ? other : key;
+            }
+        __syncthreads();
+        list[t] = key;
+        __syncthreads();
+        return;
+    }
+#pragma unroll 1
+    for (int len = 2; len <= size; len *= 2)
+#pragma unroll 1
+        for (int step = len / 2; step > 0; step /= 2) {
+            for (int i = t; i < size / 2; i += kThreads) {
+                const int lo = (i / step) * step * 2 + i % step, hi = lo + step;
+                const bool desc = (lo & len) == 0;
+                const uint64_t a = list[lo], b = list[hi];
+                if ((a < b) == desc) list[lo] = b, list[hi] = a;
+            }
+            __syncthreads();
+        }
+}
+
 template <typename T>
 struct Sampler {
     const SampleArgs& a;
@@ -773,7 +831,7 @@ __global__ void __launch_bounds__(kThreads, 2) ce_sample_kernel(const SampleArgs
                 int n;
                 cmd.flag = s.join_lists(n);
                 if (cmd.flag) {
-                    sort_list<kThreads>(sh.list, n, sh.sums);
+                    sort_list(sh.list, n, sh.sums);
                     auto weight = [&](int i) {
                         return weight_of(sc, key_logit(sh.list[i]), sh.table, a.q_bits) + (i == 0 ? base : 0);
                     };

@@ -126,66 +126,5 @@ __device__ __forceinline__ float element<__nv_bfloat16>(uint4 v, int e) {
 __device__ __forceinline__ float one(const float* p) { return *p; }
 __device__ __forceinline__ float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
-// Sorts list[0 .. n) descending (all keys differ) in a block of kThreads threads, a power of two
-// below which n is counted and above which it is rounded up to one (list has that many entries);
-// ``tmp`` is scratch of kThreads / 2.
-template <int kThreads>
-__device__ __forceinline__ void sort_list(uint64_t* list, int n, uint64_t* tmp) {
-    const int t = threadIdx.x;
-    if (n <= kThreads / 2) {  // each key counts those before it, two threads to a key
-        const int i = t >> 1, half = (n + 1) >> 1;
-        const uint64_t k = i < n ? list[i] : 0;
-        int r = 0;
-        const int end = t & 1 ? n : half;
-#pragma unroll 4
-        for (int j = t & 1 ? half : 0; j < end; ++j) r += list[j] > k;
-        r += __shfl_xor_sync(0xffffffffu, r, 1);
-        if (i < n && !(t & 1)) tmp[r] = k;
-        __syncthreads();
-        if (t < n) list[t] = tmp[t];
-        __syncthreads();
-        return;
-    }
-    int size = kThreads;
-    while (size < n) size *= 2;
-    for (int i = n + t; i < size; i += kThreads) list[i] = 0;  // after every key
-    __syncthreads();
-    if (size == kThreads) {  // one key per thread: partners within a warp need no barrier
-        uint64_t key = list[t];
-#pragma unroll 1
-        for (int len = 2; len <= size; len *= 2)
-#pragma unroll 1
-            for (int step = len / 2; step > 0; step /= 2) {
-                uint64_t other;
-                if (step >= 32) {
-                    __syncthreads();
-                    list[t] = key;
-                    __syncthreads();
-                    other = list[t ^ step];
-                } else {
-                    other = __shfl_xor_sync(0xffffffffu, key, step);
-                }
-                const bool larger = ((t & len) == 0) == ((t & step) == 0);  // this place keeps the larger
-                key = (other > key) == larger ? other : key;
-            }
-        __syncthreads();
-        list[t] = key;
-        __syncthreads();
-        return;
-    }
-#pragma unroll 1
-    for (int len = 2; len <= size; len *= 2)
-#pragma unroll 1
-        for (int step = len / 2; step > 0; step /= 2) {
-            for (int i = t; i < size / 2; i += kThreads) {
-                const int lo = (i / step) * step * 2 + i % step, hi = lo + step;
-                const bool desc = (lo & len) == 0;
-                const uint64_t a = list[lo], b = list[hi];
-                if ((a < b) == desc) list[lo] = b, list[hi] = a;
-            }
-            __syncthreads();
-        }
-}
-
 }  // namespace
 }  // namespace vce
