@@ -36,15 +36,16 @@ constexpr int kMTiles = kTile / 16;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSlices = 8;            // blocks of a cluster that divide the hidden dimension, at most
-constexpr int kSelf = kThreads;       // tokens that a block of the second kernel can sort by itself, and up to which it
-constexpr int kSelfMost = 128;        // does: 256 with 64 adapters, 128256 logits 96.6 us against 92.6 by adapter_plan; with 16 equal
+constexpr int kSelf = 128;            // tokens up to which each block of the second kernel sorts them by itself: 256 with 64
+                                      // adapters, 128256 logits took 96.6 us so, 92.6 by adapter_plan; with 16 adapters equal
 constexpr int kRankBlock = 32;        // ranks per block of the second kernel
 constexpr int kVWarp = 32;            // logits of a warp, and
 constexpr int kVBlock = kWarps * kVWarp;  // of a block of adapter_expand_many
 constexpr int kRun = 512;             // logits of a unit that is handed out, or a multiple
 constexpr int kMaxStages = 6;         // of adapter_expand_few's ring
 constexpr int kRingBytes = 216 << 10;
-constexpr int64_t kMany = 24;         // tokens per adapter from which adapter_expand_many takes them, and
+constexpr int64_t kMany = 24;         // tokens per adapter (of the table: the host does not know which are used) from which
+                                      // adapter_expand_many takes them, and
 constexpr int kShort = 13, kShortAny = 7;  // units of its work per block up to which it does (any alignment)
 constexpr int kMulWarps = 16;         // warps of adapter_expand_few that multiply
 constexpr int kCellPitch = 292;       // floats: a row of kVBlock products, one unused behind every eight (no bank conflicts)
@@ -251,7 +252,7 @@ __device__ __forceinline__ Tile plan_here(const PlanArgs& a, Sorted& sh, int id,
         }
     }
     const int low = adapter * kSelf, mine = low + tid;
-    sh.key[tid] = tid < a.n ? mine : INT_MAX;
+    if (tid < kSelf) sh.key[tid] = tid < a.n ? mine : INT_MAX;
     if (tid < kSelf / 32) sh.starts[tid] = 0;
     if (tid == 0) sh.none = 0, sh.tile.count = 0;
     __syncthreads();
@@ -1261,7 +1262,7 @@ vce_status launch_adapter_linear(const void* y, int y_dtype, int64_t n, int64_t 
     const Carved w = carve(ws, n, adapters, rank);
     const bool in_place = out == y;
     const PlanArgs pa{index, int(n), int(adapters), !in_place, int(most_tiles(n, adapters)), w.plan, w.tiles, w.perm, dev_status};
-    const bool self = n <= kSelfMost;
+    const bool self = n <= kSelf;
     if (!self) {
         count_launch();
         adapter_plan<<<1, kPlanThreads, 0, s>>>(pa);

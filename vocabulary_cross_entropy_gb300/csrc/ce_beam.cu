@@ -106,7 +106,7 @@ __device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {  // of tw
 // which both lie in the row for any address, [1, vocab / VE - 1), are divided among the parts,
 // [g0, g1) to this one; the elements before them go one to a thread of the first part, those
 // behind, fewer than 3 VE, of the last.  So a part's tokens come before the next one's.
-// The groups are copied to ``data`` a chunk of kHold kThreads at a time (parts of up to 64 KB have
+// The groups are copied to ``data`` a chunk of kHold kThreads at a time (parts of up to 32 KB have
 // one chunk, which stays).  A BF16 thread takes whole groups; an FP32 thread elements that are
 // kThreads apart, which it reads without cutting.
 template <typename T>

@@ -420,7 +420,7 @@ vce_status ce_beam(const void* logits, int dtype, int64_t batch, int beams, int6
 
 vce_status beam_reorder(const vce_state* states, int count, const int64_t* parent, int64_t batch, int beams,
                         const int32_t* lengths, int* dev_status, void* stream) {
-    constexpr int64_t kMost = int64_t(1) << 46;  // bytes; keeps every product below in 63 bits
+    constexpr int64_t kMost = int64_t(1) << 46;  // bytes of a row, and of a stride
     if (count < 0 || (count > 0 && !states) || batch < 0 || batch > kMaxRows || beams < 1 ||
         beams > VCE_BEAM_MAX_BEAMS || batch * beams > kMaxRows || batch > kMaxReorder)
         return VCE_ERR_INVALID_ARG;
