@@ -349,7 +349,7 @@ vce_status ce_beam(const void* logits, int dtype, int64_t batch, int beams, int6
  */
 typedef struct vce_state {
     const void* src;
-    void* dst; /* src itself (with its strides): in place; otherwise no overlap with any src */
+    void* dst; /* src itself (with its strides): in place; otherwise no overlap with any src.  No two dst overlap. */
     int64_t src_row_stride, dst_row_stride;
     int64_t parts, src_part_stride, dst_part_stride;
     int64_t positions, position_bytes;

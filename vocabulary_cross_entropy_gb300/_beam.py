@@ -223,7 +223,8 @@ def beam_reorder(states, parent, *, lengths=None, position_dim=None, out=None, d
     row for each beam in their first dimension, request by request; ``parent`` int64 [..., beams].
 
     In place (beams that keep their place are not touched), or into ``out``, tensors like the
-    states that share no memory with them.  With ``lengths`` (int32, one per request) only the first so many
+    states that share no memory with them.  What is written shares none with another state, parent or
+    lengths either.  With ``lengths`` (int32, one per request) only the first so many
     positions move, along ``position_dim`` (a number, or one for each state): for keys
     [rows, heads, T, D] it is 2, for [rows, T, heads, D] it is 1.  Positions must follow one another in
     memory, and the dimensions before them have one stride.  An entry of parent that names no beam

@@ -462,10 +462,10 @@ def adapter_workspace_size(n: int, adapters: int, rank: int) -> int:
 def adapter_linear(y, x, a, b_, index, scale=None, *, out=None, workspace=None, dev_status=None, stream=None):
     """``y`` [..., V] plus each token's adapter: y + scale[i] B[i] (A[i] x), i = ``index`` (int32, one
     per token; -1: none), for the outputs y of a projection of ``x`` [..., H] that all tokens
-    share.  y and x are bfloat16 or float32; ``a`` [adapters, rank, H] and ``b_`` [adapters, V,
-    rank] bfloat16, the rank a multiple of 8 up to 128; ``scale`` float32 [adapters] or None.
-    Returns ``out`` (y itself may be given), like y.  An index outside the adapters counts as
-    -1 and sets a bit of ``dev_status`` (int32 [1])."""
+    share.  y and x are bfloat16 or float32, x's rows 16-byte aligned; ``a`` [adapters, rank, H] and
+    ``b_`` [adapters, V, rank] bfloat16, the rank a multiple of 8 up to 128; ``scale`` float32 [adapters]
+    or None.  Returns ``out`` (y itself may be given, otherwise it shares no memory with y), like y.  An index
+    outside the adapters counts as -1 and sets a bit of ``dev_status`` (int32 [1])."""
     if stream is not None:
         return _under(stream, adapter_linear, y, x, a, b_, index, scale, out=out, workspace=workspace,
                       dev_status=dev_status)

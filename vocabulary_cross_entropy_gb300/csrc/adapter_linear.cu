@@ -982,10 +982,10 @@ __device__ __forceinline__ void load_b(uint32_t (&b)[4][KS][2], const ExpandArgs
 // adds them to two rows, in the vectors that lie at 16-byte boundaries of the row; what is left at the ends of
 // its kVBlock logits takes an element per lane.
 //
-// 2048 tokens with 6 adapters of rank 64, 128256 BF16 logits: 266 us (4.2 TB/s).  It is
+// 2048 tokens with 6 adapters of rank 64, 128256 BF16 logits: 263 us (4.3 TB/s; under the profiler).  It is
 // bound by what 16 warps per SM keep on its way between their instructions.  More rows on their way help small
 // ranks (512 x 128256, rank 16, BF16: 86 -> 76 us in all) and cost as much with large ones (2048 tokens of rank
-// 64: 291 -> 318).  Rows of 128257 logits take 445 us (element by element through the warps' own shared memory 630).
+// 64: 291 -> 318).  Rows of 128257 logits take 455 us in all (element by element through the warps' own shared memory 660).
 //
 // All three kernels in us, this form / the other one: 512 x 128256, rank 16, 16 tokens per adapter
 // 110 / 96 (BF16), 137 / 128 (FP32); 32 tokens 80 / 103 and 117 / 163; hence kMany.  16 tokens with 16 adapters, rank 16,

@@ -11,9 +11,9 @@
 // lengths are spread evenly.  (Shares of a block each leave most threads idle where a part has few
 // columns: 53 x 11 beams of 17 heads, 2 positions of 192 bytes each, 35 us instead of 14.)
 //
-// 8 caches of 256 x 8 x 1024 x 128 BF16, half filled on average, half of the beams replaced by others of the
-// same request: 290 us for 2.15 GB, where some beams are read for several.  24 x 5 beams of odd FP32 caches
-// into other buffers: 61 us (6.6 TB/s).
+// 8 caches of 256 x 8 x 1024 x 128 BF16, half filled on average, four of eight beams replaced by others of the
+// same request, some of which are read for several: 283 us for 1.8 GB (6.4 TB/s).  24 x 5 beams of odd FP32 caches
+// into other buffers: 60 us (6.7 TB/s).
 
 #include "head_internal.cuh"
 
